@@ -1,0 +1,471 @@
+"""The operators around the products on the GPU against plain 64-bit forms.
+
+Tolerances count roundings: half a step of the output's type, and for fp32 sums the
+worst case of one rounding (2^-24 of the terms' magnitudes) per term on the longest way."""
+import pytest
+import torch
+
+from gpu_util import DEV, say
+from ops_util import (DT, U32, f8_64, f8_cut, norm64, norm_bwd64, norm_steps, off, padded, rounding, untouched, w4_64)
+from tiled_stage_software_amd import libgemm as lg, ops
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    lg.load()  # fails loudly if the library is missing
+    torch.zeros(1, device=DEV)
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def code(t):
+    return {torch.float32: lg.GEMM_F32, torch.bfloat16: lg.GEMM_BF16, torch.float16: lg.GEMM_F16,
+            torch.float8_e4m3fn: lg.GEMM_F8E4M3}[t.dtype]
+
+
+# ------------------------------------------------------------------ norm
+
+def run_norm(x, r, w, out, pad=0, lead=0, eps=EPS, want_h=True):
+    """gemm_rmsnorm on rows `pad` elements apart; checks that nothing else is written."""
+    rows, cols = x.shape
+    X, _ = padded(x, pad, DEV, lead=lead)
+    R = padded(r, pad, DEV, lead=lead)[0] if r is not None else None
+    W = w.to(DEV) if w is not None else None
+    y, yw = padded(torch.zeros(rows, cols, dtype=out), pad, DEV, lead=lead)
+    h, hw = padded(torch.zeros(rows, cols, dtype=x.dtype), pad, DEV, lead=lead)
+    scale = torch.full((rows,), -7.0, device=DEV)
+    rstd = torch.full((rows,), -7.0, device=DEV)
+    lg.check(lg.gemm_rmsnorm(code(X), code(W) if W is not None else 0, code(y), rows, cols, eps, X.data_ptr(), X.stride(0),
+                             R.data_ptr() if R is not None else 0, X.stride(0), W.data_ptr() if W is not None else 0,
+                             h.data_ptr() if want_h else 0, h.stride(0), y.data_ptr(), y.stride(0), scale.data_ptr(),
+                             rstd.data_ptr(), torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert untouched(y, yw) and untouched(h, hw)
+    if out != torch.float8_e4m3fn:
+        assert bool((scale == -7.0).all())
+    if not want_h:
+        assert bool((h.float() == 0).all())
+    return y.cpu(), scale.cpu(), h.cpu(), rstd.cpu()
+
+
+def check_norm(x, r, w, out, **kw):
+    y, scale, h, rstd = run_norm(x, r, w, out, **kw)
+    h64, rstd64, y64 = norm64(x, r, w, kw.get("eps", EPS))
+    if kw.get("want_h", True):
+        assert torch.equal(h.view(torch.uint8), h64.view(torch.uint8))
+    # the sum is off by at most `steps` roundings, the root halves that; a few more for the
+    # division, the root, the products by rstd and by w
+    rel = (norm_steps(x.shape[1]) / 2 + 8) * U32
+    assert off(rstd, rstd64, rel * rstd64) <= 1
+    if out == torch.float8_e4m3fn:
+        s64 = (y64.abs().amax(1) / ops.F8_MAX).clamp_min(ops.TINY)
+        assert off(scale, s64, (rel + 4 * U32) * s64) <= 1
+        q64 = y64 / s64[:, None]
+        back, allowed = y.double(), rounding(q64, out) + (2 * rel + 8 * U32) * q64.abs()
+        e = off(back, q64, allowed)
+    else:
+        e = off(y, y64, rounding(y64, out) + rel * y64.abs())
+    assert e <= 1, e
+    return e
+
+
+NORM_SHAPES = [(1, 1), (1, 4096), (3, 7), (5, 64), (4, 512), (7, 513), (9, 1000), (3, 1025), (2, 2048), (6, 2049),
+               (3, 4001), (2, 8192), (1, 8200), (2, 16385), (2, 33000)]
+
+
+@pytest.mark.parametrize("rows,cols", NORM_SHAPES)
+@pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
+def test_norm(rows, cols, t):
+    g = gen(rows * 100003 + cols)
+    x = torch.randn(rows, cols, generator=g).to(DT[t])
+    r = (2 * torch.randn(rows, cols, generator=g)).to(DT[t])
+    w = (1 + 0.1 * torch.randn(cols, generator=g)).to(DT[t])
+    worst = [check_norm(x, r, w, DT[t]), check_norm(x, r, w, DT["f8"], pad=3, lead=1),
+             check_norm(x, None, w.float(), DT["f8"]), check_norm(x, None, None, DT["f32"], pad=8, want_h=False),
+             check_norm(x, r, w.float(), DT["bf16"], pad=1, lead=3)]
+    say(f"[norm] {t} {rows}x{cols}: {max(worst):.3f} of the tolerance")
+
+
+@pytest.mark.parametrize("cols", [40, 1000, 4096, 40000])
+def test_norm_special_rows(cols):
+    """Zeros, one value, values near the type's ends, infinities and NaN stay in their rows."""
+    t = torch.bfloat16
+    g = gen(cols)
+    x = torch.randn(9, cols, generator=g).to(t)
+    x[1] = 0
+    x[2] = 0
+    x[2, cols // 2] = -3.0
+    x[3] = 2.0 ** -100                 # its square underflows: rstd is 1 / sqrt(eps)
+    x[4, cols - 1] = float("nan")
+    x[5, 0] = float("inf")
+    x[6] = 2.0 ** 60
+    x[7, cols // 3] = -float("inf")
+    w = torch.ones(cols, dtype=t)
+    y, scale, h, rstd = run_norm(x, None, w, torch.float8_e4m3fn)
+    assert torch.equal(h.view(torch.int16), x.view(torch.int16))
+    assert bool((y[1].float() == 0).all()) and float(scale[1]) == ops.TINY
+    assert float(y[2].float().min()) == -448.0 and int((y[2].float() != 0).sum()) == 1
+    for bad in (4, 5, 7):
+        assert not bool(torch.isfinite(y[bad].float() * scale[bad]).any())
+    for fine in (0, 1, 2, 3, 6, 8):
+        assert bool(torch.isfinite(y[fine].float()).all()) and bool(torch.isfinite(scale[fine]))
+    keep = [0, 1, 2, 6, 8]
+    check_norm(x[keep], None, w, torch.float8_e4m3fn)
+    check_norm(x[keep], None, w, torch.float32)
+    y32, _, _, r32 = run_norm(x, None, w, torch.float32)
+    assert bool(torch.isnan(y32[4]).all()) and bool(torch.isnan(y32[5, 0])) and bool((y32[5, 1:] == 0).all())
+    assert off(r32[3:4], torch.tensor([1e3]), torch.tensor([1.0])) <= 1
+
+
+def test_norm_of_a_kept_sum_is_the_same():
+    """Adding the residual first and norming the kept h later gives the same bits."""
+    g = gen(5)
+    x = torch.randn(33, 4096, generator=g).bfloat16().to(DEV)
+    r = torch.randn(33, 4096, generator=g).bfloat16().to(DEV)
+    w = torch.randn(4096, generator=g).bfloat16().to(DEV)
+    one = ops.rmsnorm(x, w, r, out_dtype=torch.float8_e4m3fn)
+    two = ops.rmsnorm(one.h, w, out_dtype=torch.float8_e4m3fn)
+    assert torch.equal(one.y.view(torch.uint8), two.y.view(torch.uint8))
+    assert torch.equal(one.scale, two.scale) and torch.equal(one.rstd, two.rstd)
+    assert two.h.data_ptr() == one.h.data_ptr()
+
+
+@pytest.mark.parametrize("cols", [300, 5000, 40000])
+def test_norm_in_place(cols):
+    g = gen(cols)
+    x0 = torch.randn(17, cols, generator=g).bfloat16()
+    r0 = torch.randn(17, cols, generator=g).bfloat16()
+    w = torch.randn(cols, generator=g).bfloat16().to(DEV)
+    want = ops.rmsnorm(x0.to(DEV), w, r0.to(DEV))
+    x, r = x0.to(DEV), r0.to(DEV)
+    rstd = torch.empty(17, device=DEV)
+    lg.check(lg.gemm_rmsnorm(lg.GEMM_BF16, lg.GEMM_BF16, lg.GEMM_BF16, 17, cols, EPS, x.data_ptr(), cols, r.data_ptr(), cols,
+                             w.data_ptr(), r.data_ptr(), cols, x.data_ptr(), cols, 0, rstd.data_ptr(),
+                             torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert torch.equal(r, want.h) and torch.equal(x, want.y) and torch.equal(rstd, want.rstd)
+
+
+# ------------------------------------------------------------------ norm, backward
+
+def check_bwd(dy, h, w, rstd, dh, pad=0, lead=0, workspace="auto", need_dw=True):
+    rows, cols = h.shape
+    view = lambda t: padded(t, pad, DEV, lead=lead)[0] if t is not None else None  # noqa: E731
+    dx, dw = ops.rmsnorm_backward(view(dy), view(h), w.to(DEV) if w is not None else None, rstd.to(DEV), view(dh), need_dw,
+                                  workspace)
+    torch.cuda.synchronize()
+    dx64, dw64, dx_size, dw_size = norm_bwd64(dy, h, w, rstd, dh)
+    e = off(dx, dx64, rounding(dx64, h.dtype) + (norm_steps(cols) + 12) * U32 * dx_size)
+    assert e <= 1, e
+    if not need_dw:
+        assert dw is None
+        return e, 0.0
+    f = off(dw, dw64, (rows + 8) * U32 * dw_size + 2.0 ** -149)
+    assert f <= 1, f
+    return e, f
+
+
+@pytest.mark.parametrize("rows,cols", NORM_SHAPES + [(700, 96), (1301, 640), (600, 2050), (70, 40000)])
+@pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
+def test_norm_backward(rows, cols, t):
+    g = gen(rows * 7919 + cols)
+    h = torch.randn(rows, cols, generator=g).to(DT[t])
+    dy = torch.randn(rows, cols, generator=g).to(DT[t])
+    dh = torch.randn(rows, cols, generator=g).to(DT[t])
+    w = (1 + 0.1 * torch.randn(cols, generator=g)).to(DT[t])
+    _, rstd, _ = norm64(h, None, None, EPS)
+    rstd = rstd.float()
+    r = [check_bwd(dy, h, w, rstd, dh), check_bwd(dy, h, w.float(), rstd, None, pad=5, lead=1),
+         check_bwd(dy, h, None, rstd, dh, workspace=None) if rows < 100 else (0, 0),
+         check_bwd(dy, h, w, rstd, dh, workspace=torch.empty(5 * cols * 4, dtype=torch.uint8, device=DEV)),
+         check_bwd(dy, h, w, rstd, dh, need_dw=False)]
+    say(f"[norm backward] {t} {rows}x{cols}: dx {max(a for a, _ in r):.3f}, dw {max(b for _, b in r):.3f} of the tolerance")
+
+
+def test_norm_backward_against_differences():
+    """The gradient of sum(dy * y) + sum(dh * h) by central differences in 64 bits."""
+    g = gen(3)
+    rows, cols = 3, 37
+    x, r = torch.randn(rows, cols, generator=g).double(), torch.randn(rows, cols, generator=g).double()
+    x, r = x.float().double(), r.float().double()
+    w = torch.randn(cols, generator=g).float().double()
+    dy, dh = torch.randn(rows, cols, generator=g), torch.randn(rows, cols, generator=g)
+
+    def f(x, w):
+        h = x + r
+        y = h / torch.sqrt((h * h).mean(1, keepdim=True) + EPS) * w
+        return float((dy.double() * y).sum() + (dh.double() * h).sum())
+
+    fwd = ops.rmsnorm(x.float().to(DEV), w.float().to(DEV), r.float().to(DEV))
+    dx, dw = ops.rmsnorm_backward(dy.to(DEV), fwd.h, w.float().to(DEV), fwd.rstd, dh.to(DEV))
+    step = 1e-5
+    for i in range(rows):
+        for j in range(0, cols, 5):
+            d = torch.zeros_like(x)
+            d[i, j] = step
+            # the difference is off by step^2 and 64-bit noise / step, h by its rounding to fp32
+            assert abs((f(x + d, w) - f(x - d, w)) / (2 * step) - float(dx[i, j])) < 2e-5
+    for j in range(0, cols, 3):
+        d = torch.zeros_like(w)
+        d[j] = step
+        assert abs((f(x, w + d) - f(x, w - d)) / (2 * step) - float(dw[j])) < 2e-5
+
+
+def test_norm_backward_of_no_rows_and_in_place():
+    dw = torch.full((70,), 3.0, device=DEV)
+    lg.check(lg.gemm_rmsnorm_bwd(lg.GEMM_BF16, 0, 0, 70, 0, 70, 0, 70, 0, 0, 0, 0, 0, 70, dw.data_ptr(), 0, 0,
+                                 torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert bool((dw == 0).all())
+    g = gen(9)
+    for cols in (400, 5000, 40000):
+        h, dy, dh = (torch.randn(12, cols, generator=g).bfloat16().to(DEV) for _ in range(3))
+        rstd = torch.rand(12, generator=g).to(DEV) + 0.5
+        want = ops.rmsnorm_backward(dy, h, None, rstd, dh)
+        ws = torch.empty(1 << 22, dtype=torch.uint8, device=DEV)
+        for place in (0, 1, 2):
+            t = [dy.clone(), h.clone(), dh.clone()]
+            got = torch.empty(cols, device=DEV)
+            lg.check(lg.gemm_rmsnorm_bwd(lg.GEMM_BF16, 0, 12, cols, t[0].data_ptr(), cols, t[1].data_ptr(), cols, 0,
+                                         rstd.data_ptr(), t[2].data_ptr(), cols, t[place].data_ptr(), cols, got.data_ptr(),
+                                         ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream))
+            torch.cuda.synchronize()
+            assert torch.equal(t[place], want[0]) and torch.equal(got, want[1])
+
+
+# ------------------------------------------------------------------ products
+
+def run_product(call, M, N, out, beta, pad, seed):
+    """C = call(C's pointer, its type, its leading dimension) into rows `pad` apart; (C, its old values)."""
+    old = torch.randn(M, N, generator=gen(seed)).to(out) if beta else torch.zeros(M, N, dtype=out)
+    if not beta and M * N:
+        old.view(torch.uint8).fill_(0xFF)   # NaN: must not be read
+    C, whole = padded(old, pad, DEV)
+    lg.check(call(C.data_ptr(), code(C), C.stride(0)))
+    torch.cuda.synchronize()
+    assert untouched(C, whole)
+    return C.cpu(), old
+
+
+def close(C, old, p64, size, steps, alpha, beta, cut=0.0):
+    want = alpha * p64 + (beta * old.double() if beta else 0.0)
+    allowed = rounding(want, C.dtype) + abs(alpha) * cut + U32 * (abs(alpha) * steps * size + 4 * want.abs()
+                                               + (4 * abs(beta) * old.double().abs() if beta else 0.0))
+    return off(C, want, allowed)
+
+
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def f8_operands(M, N, K, seed):
+    g = gen(seed)
+    a, sa = ops.quantize_f8(torch.randn(M, K, generator=g))
+    b, sb = ops.quantize_f8(torch.randn(N, K, generator=g))
+    return a, sa, b, sb
+
+
+WS = 16 << 20
+
+
+def check_f8(M, N, K, out, alpha=1.0, beta=0.0, pads=(0, 0, 0), scales=True, ws=WS):
+    a, sa, b, sb = f8_operands(M, N, K, M * 31 + N * 17 + K)
+    if not scales:
+        sa = sb = None
+    A, B = padded(a, pads[0], DEV)[0], padded(b, pads[1], DEV)[0]
+    SA, SB = (sa.to(DEV), sb.to(DEV)) if scales else (None, None)
+    W = torch.full((max(ws, 1),), 0xFF, dtype=torch.uint8, device=DEV)
+    C, old = run_product(lambda c, t, ld: lg.gemm_f8(M, N, K, alpha, A.data_ptr(), A.stride(0), SA.data_ptr() if scales else 0,
+                                                     B.data_ptr(), B.stride(0), SB.data_ptr() if scales else 0, beta, c, t, ld,
+                                                     W.data_ptr() if ws else 0, ws, stream()), M, N, DT[out], beta, pads[2], K)
+    p64, size = f8_64(a, b, sa, sb)
+    cut = 0.0 if out == "f32" else f8_cut(a, b, sa, sb)
+    e = close(C, old, p64, size, K + 4, alpha, beta, cut)   # K terms, three products by scales and alpha
+    assert e <= 1, e
+    return e
+
+
+F8_SHAPES = [(1, 1, 1), (1, 5, 16), (3, 5, 15), (2, 17, 33), (16, 16, 128), (17, 33, 129), (64, 64, 255), (65, 70, 256),
+             (1, 1000, 2048), (5, 321, 4100), (48, 257, 1024), (128, 128, 512), (130, 200, 2049), (256, 256, 256),
+             (300, 520, 384), (257, 300, 1040), (512, 768, 640)]
+
+
+@pytest.mark.parametrize("M,N,K", F8_SHAPES)
+def test_f8(M, N, K):
+    r = [check_f8(M, N, K, "f32"), check_f8(M, N, K, "bf16", ws=0), check_f8(M, N, K, "f16", 0.5, -1.5, (16, 32, 4)),
+         check_f8(M, N, K, "f32", -2.0, 1.0, (1, 7, 3)), check_f8(M, N, K, "bf16", 1.0, 0.0, (0, 5, 1), scales=False),
+         check_f8(M, N, K, "f32", 1.0, 0.0, (48, 16, 0), ws=4096)]
+    say(f"[f8] {M}x{N}x{K}: {max(r):.3f} of the tolerance")
+
+
+def test_f8_exact_integers():
+    """Small whole numbers: every sum is exact, so every bit has to be right."""
+    g = gen(1)
+    for M, N, K in ((1, 96, 4096), (40, 33, 200), (256, 512, 1024)):
+        a = torch.randint(-3, 4, (M, K), generator=g).float().to(torch.float8_e4m3fn)
+        b = torch.randint(-3, 4, (N, K), generator=g).float().to(torch.float8_e4m3fn)
+        C = ops.matmul_f8(a.to(DEV), b.to(DEV), out_dtype=torch.float32)
+        assert torch.equal(C.cpu(), a.float() @ b.float().t())
+
+
+def test_f8_nan_and_zero_stay_in_their_rows():
+    M, N, K = 70, 90, 300
+    a, sa, b, sb = f8_operands(M, N, K, 4)
+    a[3, K - 1] = float("nan")
+    b[7, 0] = float("nan")
+    sa[5] = float("inf")
+    a[9] = 0
+    C = ops.matmul_f8(a.to(DEV), b.to(DEV), sa.to(DEV), sb.to(DEV), out_dtype=torch.float32).cpu()
+    p64, size = f8_64(a, b, sa, sb)
+    bad = torch.isnan(C)
+    assert bool(bad[3].all()) and bool(bad[:, 7].all()) and int(bad.sum()) == M + N - 1
+    fine = torch.ones(M, N, dtype=torch.bool)
+    fine[3], fine[5], fine[:, 7] = False, False, False
+    assert bool((C[9][torch.arange(N) != 7] == 0).all())
+    assert float(((C.double() - p64).abs() / (U32 * (K + 4) * size + 2.0 ** -149))[fine].max()) <= 1
+    assert bool(torch.isinf(C[5][torch.arange(N) != 7]).all())
+
+
+def w4_operands(M, N, K, group, t, zeros, seed):
+    g = gen(seed)
+    a = torch.randn(M, K, generator=g).to(DT[t])
+    codes, s, z = ops.quantize_w4(torch.randn(N, K, generator=g), group, DT[t], zeros)
+    return a, codes, s, z
+
+
+def check_w4(M, N, K, group, t, out, zeros, alpha=1.0, beta=0.0, pads=(0, 0, 0, 0), ws=WS):
+    a, codes, s, z = w4_operands(M, N, K, group, t, zeros, M * 31 + N * 17 + K)
+    A, Q = padded(a, pads[0], DEV)[0], padded(codes, pads[1], DEV)[0]
+    S = padded(s, pads[2], DEV)[0]
+    Z = padded(z, pads[2], DEV)[0] if zeros else None
+    W = torch.full((max(ws, 1),), 0xFF, dtype=torch.uint8, device=DEV)
+    C, old = run_product(lambda c, ct, ld: lg.gemm_w4(code(A), M, N, K, group, alpha, A.data_ptr(), A.stride(0), Q.data_ptr(),
+                                                      Q.stride(0), S.data_ptr(), Z.data_ptr() if zeros else 0, S.stride(0),
+                                                      beta, c, ct, ld, W.data_ptr() if ws else 0, ws, stream()),
+                         M, N, DT[out], beta, pads[3], K)
+    p64, size = w4_64(a, codes, s, z, group)
+    e = close(C, old, p64, size, min(group, K) + s.shape[1] + 16, alpha, beta)
+    assert e <= 1, e
+    return e
+
+
+W4_SHAPES = [(1, 1, 1, 32), (1, 5, 31, 32), (2, 17, 33, 32), (3, 16, 64, 64), (1, 300, 1024, 128), (5, 70, 1000, 64),
+             (16, 48, 2048, 128), (17, 33, 520, 32), (33, 100, 640, 96), (64, 65, 768, 256), (65, 130, 1025, 128),
+             (128, 256, 512, 128), (200, 320, 1100, 64), (300, 257, 2048, 32), (256, 512, 1024, 1024)]
+
+
+@pytest.mark.parametrize("M,N,K,group", W4_SHAPES)
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_w4(M, N, K, group, t):
+    r = [check_w4(M, N, K, group, t, t, False), check_w4(M, N, K, group, t, "f32", True, ws=0),
+         check_w4(M, N, K, group, t, t, True, -0.5, 1.0, (8, 16, 0, 4)),
+         check_w4(M, N, K, group, t, "f32", False, 2.0, -1.0, (1, 3, 1, 1)),
+         check_w4(M, N, K, group, t, t, True, 1.0, 0.0, (0, 1, 5, 0), ws=4096)]
+    say(f"[w4] {t} {M}x{N}x{K} by {group}: {max(r):.3f} of the tolerance")
+
+
+def test_w4_every_code_and_zero_point():
+    """One element of A against every code and zero point: nothing is rounded before the end."""
+    K = 32
+    a = torch.zeros(2, K, dtype=torch.bfloat16)
+    a[0, 5], a[1, 30] = 1.0, -2.0
+    q = torch.arange(16, dtype=torch.uint8)
+    q = (q | q << 4)[:, None].expand(16, K // 2)
+    codes = q.repeat(16, 1).contiguous()                       # row 16 z + q: code q everywhere
+    zeros = torch.arange(16).repeat_interleave(16)[:, None].to(torch.bfloat16)
+    scales = torch.full((256, 1), 0.5, dtype=torch.bfloat16)
+    C = ops.matmul_w4(a.to(DEV), codes.to(DEV), scales.to(DEV), zeros.to(DEV), group=32, out_dtype=torch.float32).cpu()
+    want = 0.5 * (torch.arange(16).repeat(16) - zeros[:, 0].float())
+    assert torch.equal(C, torch.stack([want, -2.0 * want]))
+
+
+def test_w4_nan_stays_in_its_row_and_column():
+    a, codes, s, _ = w4_operands(20, 50, 200, 64, "bf16", False, 8)
+    a[3, 199] = float("nan")
+    s[11, 2] = float("nan")
+    a[4, 7] = float("inf")
+    C = ops.matmul_w4(a.to(DEV), codes.to(DEV), s.to(DEV), group=64, out_dtype=torch.float32).cpu()
+    bad = ~torch.isfinite(C)
+    want = torch.zeros(20, 50, dtype=torch.bool)
+    want[3], want[4], want[:, 11] = True, True, True
+    assert torch.equal(bad, want)
+
+
+@pytest.mark.parametrize("alpha,K", [(0.0, 64), (1.0, 0)])
+def test_products_that_only_scale_c(alpha, K):
+    C0 = torch.randn(5, 7, device=DEV)
+    for beta, want in ((0.0, torch.zeros_like(C0)), (-2.0, -2.0 * C0)):
+        for op in ("f8", "w4"):
+            C = C0.clone()
+            if op == "f8":
+                q = torch.zeros(8, K, dtype=torch.float8_e4m3fn, device=DEV)
+                ops.matmul_f8(q[:5], q[:7], C=C, alpha=alpha, beta=beta)
+            else:
+                ops.matmul_w4(torch.zeros(5, K, dtype=torch.float16, device=DEV),
+                              torch.zeros(7, K // 2, dtype=torch.uint8, device=DEV),
+                              torch.ones(7, K // 32, dtype=torch.float16, device=DEV), group=32, C=C, alpha=alpha, beta=beta)
+            assert torch.equal(C, want)
+
+
+# ------------------------------------------------------------------ together
+
+def chain(x, r, w, b, sb, codes, s, dy):
+    n = ops.rmsnorm(x, w, r, out_dtype=torch.float8_e4m3fn)
+    c = ops.matmul_f8(n.y, b, n.scale, sb)
+    d = ops.matmul_w4(c, codes, s, group=64)
+    dx, dw = ops.rmsnorm_backward(dy, n.h, w, n.rstd)
+    return n.y.view(torch.uint8), n.scale, n.h, c, d, dx, dw
+
+
+def chain_inputs(rows, seed):
+    g = gen(seed)
+    K, N = 512, 640
+    x, r, dy = (torch.randn(rows, K, generator=g).bfloat16().to(DEV) for _ in range(3))
+    w = (1 + 0.1 * torch.randn(K, generator=g)).bfloat16().to(DEV)
+    b, sb = ops.quantize_f8(torch.randn(N, K, generator=g))
+    codes, s, _ = ops.quantize_w4(torch.randn(K, N, generator=g), 64, torch.bfloat16)
+    return x, r, w, b.to(DEV), sb.to(DEV), codes.to(DEV), s.to(DEV), dy
+
+
+@pytest.mark.parametrize("rows", [1, 33, 300])
+def test_same_bits_again_and_on_another_stream(rows):
+    args = chain_inputs(rows, rows)
+    want = chain(*args)
+    again = chain(*args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = chain(*args)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    for a, b, c in zip(want, again, other):
+        assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("rows", [1, 65])
+def test_graph_replays(rows):
+    """Captured once, replayed with new inputs and eager work between: the eager results."""
+    args = chain_inputs(rows, 1)
+    chain(*args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain(*args)
+    for seed in (2, 3, 4):
+        for t, v in zip(args, chain_inputs(rows, seed)):
+            t.copy_(v)
+        want = chain(*args)
+        torch.cuda.synchronize()
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b), seed

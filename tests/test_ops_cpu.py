@@ -1,0 +1,163 @@
+"""The operators around the products, on the CPU: refusals before anything is launched, quick
+returns, workspace sizes, and the quantisers."""
+import pytest
+import torch
+
+from tiled_stage_software_amd import libgemm as lg, ops
+from ops_util import unpack4
+
+P = 0x10000  # a fake device address: nothing here launches
+F32, BF16, F16, F8 = lg.GEMM_F32, lg.GEMM_BF16, lg.GEMM_F16, lg.GEMM_F8E4M3
+BAD = lg.GEMM_ERR_INVALID_ARG
+
+
+def norm(**kw):
+    a = dict(in_type=BF16, w_type=BF16, y_type=F8, rows=3, cols=40, eps=1e-6, x=P, ldx=40, r=P, ldr=40, w=P, h=P, ldh=40,
+             y=P, ldy=40, scale=P, rstd=P)
+    a.update(kw)
+    return lg.gemm_rmsnorm(**a)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(in_type=F8), dict(in_type=9), dict(w_type=F16), dict(w_type=F8), dict(y_type=7), dict(y_type=-1),
+    dict(rows=-1), dict(cols=-1), dict(cols=(1 << 30) + 1), dict(rows=1 << 40), dict(eps=-1.0), dict(eps=float("nan")),
+    dict(eps=float("inf")), dict(ldx=39), dict(ldr=39), dict(ldh=0), dict(ldy=39), dict(x=0), dict(y=0), dict(scale=0),
+])
+def test_norm_refuses(kw):
+    assert norm(**kw) == BAD
+    assert lg.gemm_last_error() != ""
+
+
+@pytest.mark.parametrize("kw", [dict(rows=0, x=0, y=0, scale=0), dict(cols=0, x=0, y=0), dict(rows=0, cols=0)])
+def test_norm_of_nothing(kw):
+    assert norm(**kw) == lg.GEMM_OK
+
+
+def bwd(**kw):
+    a = dict(in_type=BF16, w_type=F32, rows=3, cols=40, dy=P, lddy=40, h=P, ldh=40, w=P, rstd=P, dh=P, lddh=40, dx=P,
+             lddx=40, dw=P, workspace=P, workspace_bytes=1 << 20)
+    a.update(kw)
+    return lg.gemm_rmsnorm_bwd(**a)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(in_type=F8), dict(w_type=F16), dict(rows=-2), dict(cols=-2), dict(lddy=39), dict(ldh=39), dict(lddh=39),
+    dict(lddx=39), dict(dy=0), dict(h=0), dict(rstd=0), dict(dx=0), dict(workspace=P + 16),
+])
+def test_norm_backward_refuses(kw):
+    assert bwd(**kw) == BAD
+    assert lg.gemm_last_error() != ""
+
+
+def test_norm_backward_of_nothing():
+    assert bwd(cols=0) == lg.GEMM_OK
+    assert bwd(rows=0, dw=0, dy=0, h=0, rstd=0, dx=0) == lg.GEMM_OK
+
+
+def test_norm_backward_workspace():
+    assert lg.gemm_rmsnorm_bwd_workspace_size(BF16, 1, 4096) == (lg.GEMM_OK, 0)       # one row: nothing to join
+    s, n = lg.gemm_rmsnorm_bwd_workspace_size(BF16, 16384, 4096)
+    assert s == lg.GEMM_OK and n % (4096 * 4) == 0 and 0 < n <= 64 << 20
+    assert lg.gemm_rmsnorm_bwd_workspace_size(BF16, 5, 0) == (lg.GEMM_OK, 0)
+    assert lg.gemm_rmsnorm_bwd_workspace_size(F8, 5, 8)[0] == BAD
+    assert lg.gemm_rmsnorm_bwd_workspace_size(BF16, -1, 8)[0] == BAD
+
+
+def f8(**kw):
+    a = dict(M=4, N=5, K=24, alpha=1.0, A=P, lda=24, scale_a=P, B=P, ldb=24, scale_b=P, beta=0.0, C=P, c_type=BF16, ldc=5,
+             workspace=P, workspace_bytes=0)
+    a.update(kw)
+    return lg.gemm_f8(**a)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(M=-1), dict(N=-1), dict(K=-1), dict(K=1 << 31), dict(lda=23), dict(ldb=23), dict(ldc=4), dict(A=0), dict(B=0),
+    dict(C=0), dict(c_type=F8), dict(c_type=5), dict(workspace=P + 8),
+])
+def test_f8_refuses(kw):
+    assert f8(**kw) == BAD
+    assert lg.gemm_last_error() != ""
+
+
+def w4(**kw):
+    a = dict(in_type=BF16, M=4, N=5, K=96, group=32, alpha=1.0, A=P, lda=96, codes=P, ldw=48, scales=P, zeros=P, lds=3,
+             beta=0.0, C=P, c_type=BF16, ldc=5, workspace=P, workspace_bytes=0)
+    a.update(kw)
+    return lg.gemm_w4(**a)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(in_type=F32), dict(in_type=F8), dict(c_type=F16), dict(M=-1), dict(N=-1), dict(K=-1), dict(group=0),
+    dict(group=16), dict(group=48), dict(group=-32), dict(lda=95), dict(ldw=47), dict(lds=2), dict(ldc=4), dict(A=0),
+    dict(codes=0), dict(scales=0), dict(C=0), dict(workspace=P + 8), dict(K=97, lda=97, lds=4),
+])
+def test_w4_refuses(kw):
+    assert w4(**kw) == BAD
+    assert lg.gemm_last_error() != ""
+
+
+def test_products_of_nothing():
+    assert f8(M=0, A=0, C=0) == lg.GEMM_OK
+    assert f8(N=0, B=0, C=0, ldc=1) == lg.GEMM_OK
+    assert w4(M=0, A=0, C=0) == lg.GEMM_OK
+    assert w4(N=0, codes=0, scales=0, C=0, ldc=1) == lg.GEMM_OK
+
+
+def test_product_workspaces():
+    for s, n in (lg.gemm_f8_workspace_size(1, 4096, 4096), lg.gemm_w4_workspace_size(BF16, 1, 4096, 4096, 128)):
+        assert s == lg.GEMM_OK and 0 <= n <= 64 << 20
+    assert lg.gemm_f8_workspace_size(-1, 1, 1)[0] == BAD
+    assert lg.gemm_w4_workspace_size(F32, 1, 1, 1, 32)[0] == BAD
+    assert lg.gemm_w4_workspace_size(BF16, 1, 1, 1, 33)[0] == BAD
+
+
+def test_wrappers_refuse_other_shapes_and_types():
+    x = torch.zeros(2, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        ops.rmsnorm(x, torch.ones(7, dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        ops.rmsnorm(x, torch.ones(8, dtype=torch.float16))
+    with pytest.raises(ValueError):
+        ops.rmsnorm(x, residual=torch.zeros(2, 7, dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        ops.rmsnorm(x.t())
+    with pytest.raises(ValueError):
+        ops.rmsnorm(x, out_dtype=torch.int8)
+    with pytest.raises(ValueError):
+        ops.rmsnorm_backward(x, x, None, torch.zeros(3))
+    q = torch.zeros(2, 8, dtype=torch.float8_e4m3fn)
+    with pytest.raises(ValueError):
+        ops.matmul_f8(q, x)
+    with pytest.raises(ValueError):
+        ops.matmul_f8(q, q[:, :7])
+    with pytest.raises(ValueError):
+        ops.matmul_f8(q, q, scale_a=torch.ones(3))
+    with pytest.raises(ValueError):
+        ops.matmul_f8(q, q, beta=1.0)
+    with pytest.raises(ValueError):
+        ops.matmul_w4(x, torch.zeros(3, 5, dtype=torch.uint8), torch.ones(3, 1, dtype=torch.bfloat16), group=32)
+    with pytest.raises(ValueError):
+        ops.matmul_f8(q, q, C=torch.zeros(1, 2).expand(2, 2))  # rows that lie on each other
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("k", [64, 97])
+def test_quantize_w4_is_half_a_step_off(k, zeros):
+    g = torch.Generator().manual_seed(k)
+    w = torch.randn(6, k, generator=g) + (0.5 if zeros else 0.0)
+    codes, s, z = ops.quantize_w4(w, 32, torch.float32, zeros)
+    assert codes.shape == (6, (k + 1) // 2) and s.shape == (6, -(-k // 32)) and (z is not None) == zeros
+    each = lambda t: t.repeat_interleave(32, 1)[:, :k]  # noqa: E731
+    back = each(s) * (unpack4(codes, k).float() - (each(z) if zeros else 8.0))
+    # codes are rounded (half a step) and clamped: the largest value may lie half a step past 15
+    # (centred: 8 + 7.5; with zeros the rounding of the zero point)
+    assert bool(((back - w).abs() <= 1.01 * each(s)).all())
+    assert float(((back - w).abs() <= 0.51 * each(s)).float().mean()) > 0.9
+
+
+def test_quantize_f8():
+    t = torch.tensor([[0.0, 0.0], [448.0, -1.0], [1e-3, 2e-3]])
+    q, s = ops.quantize_f8(t)
+    assert s[0] == ops.TINY and s[1] == 1.0
+    assert torch.equal(q[:2].float(), t[:2])
+    assert bool(((q.float() * s[:, None] - t).abs() <= 2.0 ** -4 * t.abs()).all())

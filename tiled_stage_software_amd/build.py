@@ -27,7 +27,9 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.hip"))) + [os.path.join(CSRC, "libgemm.cpp")]
+    ops = os.path.join(CSRC, "ops")
+    return (sorted(glob.glob(os.path.join(CSRC, "*.hip"))) + [os.path.join(CSRC, "libgemm.cpp")] +
+            sorted(glob.glob(os.path.join(ops, "*.hip"))) + [os.path.join(ops, "ops.cpp")])
 
 
 def _compile(src: str, extra) -> str:

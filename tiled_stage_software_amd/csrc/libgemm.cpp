@@ -13,6 +13,7 @@
 
 #include "libgemm.h"
 #include "launch.hpp"
+#include "ops/ops.hpp"
 #include "schedule.hpp"
 
 namespace {
@@ -623,6 +624,22 @@ bool rec_staged_ks(Recorder& r, int ks, int numK) {
 }
 
 }  // namespace
+
+// The error state of this file, for the operators' entry points.
+namespace gemm {
+
+gemm_status_t op_fail(gemm_status_t s, const char* fmt, ...) {
+    char text[sizeof(g_err)];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(text, sizeof(text), fmt, ap);
+    va_end(ap);
+    return fail(s, "%s", text);
+}
+void op_clear_error() { g_err[0] = 0; }
+bool op_debug_on() { return debug_on(); }
+
+}  // namespace gemm
 
 extern "C" {
 

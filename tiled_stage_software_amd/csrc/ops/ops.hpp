@@ -1,0 +1,84 @@
+// ops.hpp -- parameters and launchers of the operators around the products: the
+// root-mean-square norm, its backward pass, the product of 8-bit operands with scales and
+// the product with 4-bit weights (internal to the library; the entry points are in ops.cpp).
+#pragma once
+
+#include "common.hpp"
+#include "launch.hpp"
+#include "libgemm.h"
+
+namespace gemm {
+
+enum : int { DT_F8E4M3 = 3 };   // continues common.hpp's DT_*: OCP 8-bit floats, 4 exponent bits
+
+// Records a status and its text for gemm_last_error() and returns it (libgemm.cpp).
+gemm_status_t op_fail(gemm_status_t s, const char* fmt, ...);
+void op_clear_error();
+bool op_debug_on();
+
+// ---------------------------------------------------------------- norm
+struct NormParams {
+    const char* x;
+    const char* r;       // residual added to x, or NULL
+    const char* w;       // NULL: ones
+    char* h;             // x + r as it is kept, or NULL
+    char* y;
+    float* scale;        // per row, y_type DT_F8E4M3 only
+    float* rstd;         // per row, or NULL
+    int64_t ldx, ldr, ldh, ldy;   // elements
+    int64_t rows;
+    int cols;
+    int w_type, y_type;
+    float eps;
+};
+hipError_t launch_norm(int in_type, const NormParams& p, hipStream_t st);
+
+struct NormBwdParams {
+    const char* dy;
+    const char* h;
+    const char* w;       // NULL: ones
+    const float* rstd;
+    const char* dh;      // gradient added to dx, or NULL
+    char* dx;
+    float* dw;           // NULL: not computed
+    float* part;         // parts x cols partial sums of dw (parts > 1)
+    int64_t lddy, ldh, lddh, lddx;
+    int64_t rows;
+    int cols;
+    int w_type;
+    int parts;           // workgroups, each a fixed set of rows and one partial row of dw
+};
+// Rows that one workgroup of the backward kernel works on at a time, and the number of
+// workgroups it would like for this problem (its partial sums need parts * cols floats).
+int norm_bwd_parts(int in_type, int64_t rows, int cols);
+hipError_t launch_norm_bwd(int in_type, const NormBwdParams& p, hipStream_t st);
+
+// ---------------------------------------------------------------- 8-bit product
+struct F8Params {
+    const uint8_t* A;    // M x K, K contiguous
+    const uint8_t* B;    // N x K, K contiguous
+    char* C;
+    const float* sa;     // per row of A, or NULL (ones)
+    const float* sb;     // per row of B, or NULL (ones)
+    int64_t lda, ldb, ldc;
+    int M, N, K;
+    float alpha, beta;
+    int out_type;
+};
+hipError_t launch_f8_staged(const F8Params& p, hipStream_t st);
+
+// ---------------------------------------------------------------- 4-bit weights
+struct W4Params {
+    const char* A;       // M x K, bf16 or f16
+    const uint8_t* W;    // N rows of ceil(K/2) bytes
+    const char* scales;  // N x groups, A's type
+    const char* zeros;   // the same, or NULL (8)
+    char* C;
+    int64_t lda, ldw, lds, ldc;   // elements; ldw in bytes
+    int M, N, K, group;
+    float alpha, beta;
+    int out_type;
+};
+hipError_t launch_w4_skinny(int in_type, const W4Params& p, hipStream_t st);
+
+}  // namespace gemm

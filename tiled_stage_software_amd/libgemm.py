@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(PKG, "lib", "libgemm.so")
 
 GEMM_OK, GEMM_ERR_INVALID_ARG, GEMM_ERR_UNSUPPORTED, GEMM_ERR_HIP = 0, 1, 2, 3
 GEMM_ROW_MAJOR, GEMM_COL_MAJOR = 0, 1
-GEMM_F32, GEMM_BF16, GEMM_F16 = 0, 1, 2
+GEMM_F32, GEMM_BF16, GEMM_F16, GEMM_F8E4M3 = 0, 1, 2, 3
 (GEMM_KERNEL_AUTO, GEMM_KERNEL_VALU_RING, GEMM_KERNEL_VALU_STAGED, GEMM_KERNEL_MFMA_RING,
  GEMM_KERNEL_MFMA_STAGED, GEMM_KERNEL_SCALE) = range(6)
 GEMM_FLAG_NO_XCD_REMAP = 1
@@ -39,7 +39,8 @@ KERNEL_NAMES = {0: "none", 1: "valu_ring", 2: "valu_staged", 3: "mfma_ring", 4: 
 EXPORTS = ("gemm_f32", "gemm_bf16", "gemm_f16", "gemm_f32_ex", "gemm_bf16_ex", "gemm_f16_ex",
            "gemm_bf16_ws", "gemm_f16_ws", "gemm_ws_static", "gemm_workspace_size", "gemm_plan", "gemm_tune", "gemm_tune_ws",
            "gemm_schedule", "gemm_pipe_copy", "gemm_mfma_ceiling", "gemm_h2d_staged", "gemm_h2d_staged_async", "gemm_status_string",
-           "gemm_last_error")
+           "gemm_last_error", "gemm_rmsnorm", "gemm_rmsnorm_bwd", "gemm_rmsnorm_bwd_workspace_size", "gemm_f8",
+           "gemm_f8_workspace_size", "gemm_w4", "gemm_w4_workspace_size")
 
 
 class GemmOpts(ctypes.Structure):
@@ -115,6 +116,17 @@ def load():
         lib.gemm_mfma_ceiling.restype = i32
         for name in ("gemm_h2d_staged", "gemm_h2d_staged_async"):
             getattr(lib, name).argtypes = [vp, vp, i64, vp, i64, i32, vp]
+            getattr(lib, name).restype = i32
+        sz, szp = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+        lib.gemm_rmsnorm.argtypes = [i32, i32, i32, i64, i64, f32, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp]
+        lib.gemm_rmsnorm_bwd.argtypes = [i32, i32, i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp, sz, vp]
+        lib.gemm_rmsnorm_bwd_workspace_size.argtypes = [i32, i64, i64, szp]
+        lib.gemm_f8.argtypes = [i64, i64, i64, f32, vp, i64, vp, vp, i64, vp, f32, vp, i32, i64, vp, sz, vp]
+        lib.gemm_f8_workspace_size.argtypes = [i64, i64, i64, szp]
+        lib.gemm_w4.argtypes = [i32, i64, i64, i64, i64, f32, vp, i64, vp, i64, vp, vp, i64, f32, vp, i32, i64, vp, sz, vp]
+        lib.gemm_w4_workspace_size.argtypes = [i32, i64, i64, i64, i64, szp]
+        for name in ("gemm_rmsnorm", "gemm_rmsnorm_bwd", "gemm_rmsnorm_bwd_workspace_size", "gemm_f8",
+                     "gemm_f8_workspace_size", "gemm_w4", "gemm_w4_workspace_size"):
             getattr(lib, name).restype = i32
         lib.gemm_status_string.argtypes = [i32]
         lib.gemm_status_string.restype = ctypes.c_char_p
@@ -247,6 +259,53 @@ def gemm_h2d_staged_async(dst: int, src: int, nbytes: int, staging: int, chunk_b
                           stream: int = 0) -> int:
     """gemm_h2d_staged returning before the last DMAs finish (sync `stream` before reusing staging)."""
     return load().gemm_h2d_staged_async(dst, src, nbytes, staging, chunk_bytes, nstage, stream)
+
+
+def gemm_rmsnorm(in_type, w_type, y_type, rows, cols, eps, x, ldx, r, ldr, w, h, ldh, y, ldy, scale, rstd, stream=0) -> int:
+    """h = x + r; y = h * rstd * w, for GEMM_F8E4M3 with a scale per row (see include/libgemm.h)."""
+    return load().gemm_rmsnorm(in_type, w_type, y_type, rows, cols, eps, x, ldx, r, ldr, w, h, ldh, y, ldy, scale, rstd,
+                               stream)
+
+
+def gemm_rmsnorm_bwd(in_type, w_type, rows, cols, dy, lddy, h, ldh, w, rstd, dh, lddh, dx, lddx, dw, workspace=0,
+                     workspace_bytes=0, stream=0) -> int:
+    return load().gemm_rmsnorm_bwd(in_type, w_type, rows, cols, dy, lddy, h, ldh, w, rstd, dh, lddh, dx, lddx, dw,
+                                   workspace, workspace_bytes, stream)
+
+
+def gemm_f8(M, N, K, alpha, A, lda, scale_a, B, ldb, scale_b, beta, C, c_type, ldc, workspace=0, workspace_bytes=0,
+            stream=0) -> int:
+    """C = alpha * diag(scale_a) A B^T diag(scale_b) + beta * C, A and B e4m3."""
+    return load().gemm_f8(M, N, K, alpha, A, lda, scale_a, B, ldb, scale_b, beta, C, c_type, ldc, workspace,
+                          workspace_bytes, stream)
+
+
+def gemm_w4(in_type, M, N, K, group, alpha, A, lda, codes, ldw, scales, zeros, lds, beta, C, c_type, ldc, workspace=0,
+            workspace_bytes=0, stream=0) -> int:
+    """C = alpha * A W^T + beta * C, W in 4-bit codes with group scales."""
+    return load().gemm_w4(in_type, M, N, K, group, alpha, A, lda, codes, ldw, scales, zeros, lds, beta, C, c_type, ldc,
+                          workspace, workspace_bytes, stream)
+
+
+def _size_of(fn, *args):
+    n = ctypes.c_size_t(0)
+    s = fn(*args, ctypes.byref(n))
+    return s, n.value
+
+
+def gemm_rmsnorm_bwd_workspace_size(in_type, rows, cols):
+    """(status, bytes)"""
+    return _size_of(load().gemm_rmsnorm_bwd_workspace_size, in_type, rows, cols)
+
+
+def gemm_f8_workspace_size(M, N, K):
+    """(status, bytes)"""
+    return _size_of(load().gemm_f8_workspace_size, M, N, K)
+
+
+def gemm_w4_workspace_size(in_type, M, N, K, group):
+    """(status, bytes)"""
+    return _size_of(load().gemm_w4_workspace_size, in_type, M, N, K, group)
 
 
 def gemm_status_string(s: int) -> str:
