@@ -315,6 +315,25 @@ def test_f8_exact_integers():
         assert torch.equal(C.cpu(), a.float() @ b.float().t())
 
 
+@pytest.mark.parametrize("M,N,K,pad", [(4096, 4096, 512, 0), (4096, 4096, 128, 16), (4099, 4111, 650, 0), (4357, 3840, 255, 5),
+                                       (2560, 12160, 384, 3), (640, 700, 8200, 0), (129, 260, 16000, 7)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_f8_exact_integers_large(M, N, K, pad, out):
+    """The same on shapes that take the large tiles and the splits of K, from any pitch."""
+    g = torch.Generator(DEV).manual_seed(M + K)
+    draw = lambda rows: torch.randint(-3, 4, (rows, K), generator=g, device=DEV).float()  # noqa: E731
+    a, b = draw(M), draw(N)
+    A = padded(a.to(torch.float8_e4m3fn), pad, DEV)[0]
+    B = padded(b.to(torch.float8_e4m3fn), pad, DEV)[0]
+    want = a @ b.t()                                   # whole numbers below 2^24: exact in fp32
+    C, whole = padded(torch.full((M, N), float("nan"), device=DEV).to(DT[out]), pad, DEV)
+    ops.matmul_f8(A, B, C=C)
+    assert untouched(C, whole)
+    assert torch.equal(C, want.to(DT[out]))
+    ops.matmul_f8(A, B, C=C, alpha=-2.0, beta=1.0, workspace=None)
+    assert torch.equal(C, (-2.0 * want + want.to(DT[out]).float()).to(DT[out]))
+
+
 def test_f8_nan_and_zero_stay_in_their_rows():
     M, N, K = 70, 90, 300
     a, sa, b, sb = f8_operands(M, N, K, 4)

@@ -185,8 +185,8 @@ gemm_status_t gemm_f8(int64_t M, int64_t N, int64_t K, float alpha, const void* 
     p.M = (int)M; p.N = (int)N; p.K = (int)K;
     p.alpha = alpha; p.beta = beta;
     p.out_type = c_type;
-    (void)workspace_bytes;
-    return launched(launch_f8_staged(p, stream));
+    if (M <= kF8SkinnyRows) return launched(launch_f8_skinny(p, stream));
+    return launched(f8_tile_fits(p) ? launch_f8_tile(p, workspace, workspace_bytes, stream) : launch_f8_staged(p, stream));
 }
 
 gemm_status_t gemm_f8_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
@@ -196,6 +196,10 @@ gemm_status_t gemm_f8_workspace_size(int64_t M, int64_t N, int64_t K, size_t* by
     TRY(check_size("M", M));
     TRY(check_size("N", N));
     TRY(check_size("K", K));
+    if (M > kF8SkinnyRows && N > 0 && K > 0) {   // (the type of C is not known here: the larger of its two)
+        const size_t a = f8_tile_workspace(M, N, K, false), b = f8_tile_workspace(M, N, K, true);
+        *bytes = a > b ? a : b;
+    }
     return GEMM_OK;
 }
 

@@ -65,6 +65,11 @@ struct F8Params {
     float alpha, beta;
     int out_type;
 };
+constexpr int kF8SkinnyRows = 32;   // rows of A that launch_f8_skinny takes
+hipError_t launch_f8_skinny(const F8Params& p, hipStream_t st);
+bool f8_tile_fits(const F8Params& p);
+size_t f8_tile_workspace(int64_t M, int64_t N, int64_t K, bool wide);
+hipError_t launch_f8_tile(const F8Params& p, void* ws, size_t ws_bytes, hipStream_t st);
 hipError_t launch_f8_staged(const F8Params& p, hipStream_t st);
 
 // ---------------------------------------------------------------- 4-bit weights
