@@ -1,0 +1,78 @@
+// w4_common.hpp -- the arithmetic of 4-bit weights.
+//
+// W[n][k] = s * (q - z) with a scale s and zero point z for each row n and group of k.  By groups:
+//   sum_k a * s * (q - z) = s * (sum_k a * q - z * sum_k a),
+// the sums on the matrix cores in fp32.  A code becomes a 16-bit float by placing it at the
+// top of the mantissa of 1.0, which is exactly 1 + q/16, so
+//   sum a*(q - z) = 16 * (sum a*(1 + q/16) - (1 + z/16) * sum a).
+// No weight is rounded: the scale multiplies the fp32 sum of its group.
+#pragma once
+
+#include "ops_common.hpp"
+
+namespace gemm {
+
+template <int T> struct Half;
+template <> struct Half<DT_BF16> {
+    typedef __bf16 type;
+    static constexpr uint32_t ONES = 0x3F803F80u;   // 1.0, twice
+    static constexpr int TOP = 3;                   // the code's place at the top of the mantissa
+    static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+};
+template <> struct Half<DT_F16> {
+    typedef _Float16 type;
+    static constexpr uint32_t ONES = 0x3C003C00u;
+    static constexpr int TOP = 6;
+    static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    }
+};
+
+// Eight codes (code i in bits 4 i .. 4 i + 3) as eight 1 + q/16 in their order.  Two rotations put
+// every even and every odd code at bit TOP of some byte; a byte permute then pairs codes 2 i and
+// 2 i + 1 in the halves of a word: ten operations for eight codes.
+template <int T>
+__device__ __forceinline__ u32x4 spread(uint32_t w) {
+    constexpr int TOP = Half<T>::TOP;
+    constexpr uint32_t MASK = 0x000F000Fu << TOP;
+    const uint32_t even = __builtin_amdgcn_alignbit(w, w, 32 - TOP);          // left by TOP
+    const uint32_t odd = __builtin_amdgcn_alignbit(w, w, (36 - TOP) & 31);    // left by TOP - 4
+    u32x4 v;
+    v[0] = (__builtin_amdgcn_perm(odd, even, 0x05040100u) & MASK) | Half<T>::ONES;
+    v[1] = (__builtin_amdgcn_perm(odd, even, 0x06050201u) & MASK) | Half<T>::ONES;
+    v[2] = (__builtin_amdgcn_perm(odd, even, 0x07060302u) & MASK) | Half<T>::ONES;
+    v[3] = (__builtin_amdgcn_perm(odd, even, 0x04070003u) & MASK) | Half<T>::ONES;
+    return v;
+}
+
+// 16 s and 1 + z/16 of a group.
+template <int T>
+__device__ __forceinline__ float scale16(uint16_t s) { return 16.0f * to_f32<T>(s); }
+template <int T>
+__device__ __forceinline__ float zero16(uint16_t z) { return 1.0f + to_f32<T>(z) * 0.0625f; }
+constexpr float kZero16 = 1.5f;   // of z = 8
+
+// Eight elements of a row of K from k, zeros past its end.
+__device__ __forceinline__ u32x4 load_a(const char* row, int k, int K) {
+    if (k + 8 <= K) return load16(row + (int64_t)k * 2);
+    u32x4 v = {0u, 0u, 0u, 0u};
+    for (int i = 0; i < 8; ++i)
+        if (k + i < K) v[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[k + i] << ((i & 1) * 16);
+    return v;
+}
+// Eight codes (four bytes) from k; what lies past the row's bytes is not read.  (Codes past
+// K meet zeros of A.)
+__device__ __forceinline__ uint32_t load_q(const uint8_t* row, int k, int K) {
+    uint32_t v = 0;
+    if (k + 8 <= K) {
+        __builtin_memcpy(&v, row + (k >> 1), 4);
+        return v;
+    }
+    for (int i = 0; i < 4; ++i)
+        if (k + 2 * i < K) v |= (uint32_t)row[(k >> 1) + i] << (8 * i);
+    return v;
+}
+
+}  // namespace gemm

@@ -1,139 +1,169 @@
-// w4_skinny.hip -- C = alpha * A * W^T + beta * C with W[n][k] = s * (q - z): 4-bit codes q,
-// two to a byte, and a scale s and zero point z for each row n and group of k.
+// w4_skinny.hip -- C = alpha * A * W^T + beta * C with 4-bit weights for few rows of A: the
+// codes' bytes bound it.
 //
-// By groups:  sum_k a * s * (q - z) = s * (sum_k a * q - z * sum_k a), the sums on the matrix
-// cores in fp32.  A code becomes a 16-bit float with two operations a pair: q placed at the
-// top of the mantissa of 1.0 is exactly 1 + q/16, so
-//   sum a*(q - z) = 16 * (sum a*(1 + q/16) - (1 + z/16) * sum a),
-// and the sum of a, one instruction against ones, serves every column.  No weight is rounded:
-// the scale multiplies the fp32 sum of its group.
-//
-// Few rows of A: the codes' bytes bound it.  A workgroup computes 16 columns, its eight waves
-// share K; every lane loads its own 16 bytes (32 codes) of a row straight into registers as
-// the matrix instruction's second operand, with no LDS between.
-#include "ops_common.hpp"
+// A workgroup computes 16 columns; its waves share K, each taking every WAVES-th step of 128
+// codes.  Every lane loads 16 bytes (32 codes) of a row of W straight into registers: the four
+// lane groups take 64 whole bytes of a row.  An instruction's k have to lie in one group of
+// scales, which may be 32 long, so the four words of a lane change places with those of the other lane
+// groups (a 4 x 4 transpose, four lane swaps) until instruction t holds k = 32 t .. 32 t + 31.
+// The sum of a, which the zero points multiply, is one more instruction, against ones.
+#include "w4_common.hpp"
 
 namespace gemm {
 namespace {
 
-template <int T> struct Half;
-template <> struct Half<DT_BF16> {
-    static constexpr uint32_t ONES = 0x3F803F80u;   // 1.0, twice
-    static constexpr int TOP = 3;                   // the code's place at the top of the mantissa
-    static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-    }
-};
-template <> struct Half<DT_F16> {
-    static constexpr uint32_t ONES = 0x3C003C00u;
-    static constexpr int TOP = 6;
-    static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-    }
-};
+constexpr int kStep = 128;
 
-// Eight codes as 1 + q/16: result i holds codes i and i + 4 in its halves.
-template <int T>
-__device__ __forceinline__ u32x4 spread(uint32_t w) {
-    constexpr int TOP = Half<T>::TOP;
-    constexpr uint32_t MASK = 0x000F000Fu << TOP;
-    u32x4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int s = 4 * i - TOP;
-        v[i] = ((s < 0 ? w << -s : w >> s) & MASK) | Half<T>::ONES;
-    }
-    return v;
-}
-// Eight elements of A in the order spread() gives the codes: 0, 4, 1, 5, 2, 6, 3, 7.
-__device__ __forceinline__ u32x4 shuffle8(u32x4 a) {
-    u32x4 v;
-    v[0] = __builtin_amdgcn_perm(a[2], a[0], 0x05040100u);
-    v[1] = __builtin_amdgcn_perm(a[2], a[0], 0x07060302u);
-    v[2] = __builtin_amdgcn_perm(a[3], a[1], 0x05040100u);
-    v[3] = __builtin_amdgcn_perm(a[3], a[1], 0x07060302u);
-    return v;
+// v[i] of lane group g becomes v[g] of lane group i.
+__device__ __forceinline__ u32x4 transpose_groups(u32x4 v) {
+    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+    const u2 a = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+    const u2 b = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+    const u2 c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const u2 d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    return u32x4{c[0], c[1], d[0], d[1]};
 }
 
-// Eight elements of a row of K from k, zeros past its end.
-__device__ __forceinline__ u32x4 load_a(const char* row, int k, int K) {
-    if (k + 8 <= K) return load16(row + (int64_t)k * 2);
-    u32x4 v = {0u, 0u, 0u, 0u};
-    for (int i = 0; i < 8; ++i)
-        if (k + i < K) v[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[k + i] << ((i & 1) * 16);
-    return v;
-}
-// Eight codes (four bytes) from k; what lies past the row's bytes is not read.  (Codes past
-// K meet zeros of A.)
-__device__ __forceinline__ uint32_t load_q(const uint8_t* row, int k, int K) {
-    uint32_t v = 0;
-    if (k + 8 <= K) {
-        __builtin_memcpy(&v, row + (k >> 1), 4);
-        return v;
-    }
-    for (int i = 0; i < 4; ++i)
-        if (k + 2 * i < K) v |= (uint32_t)row[(k >> 1) + i] << (8 * i);
-    return v;
-}
-
-// 16 columns and MT x 16 rows per workgroup; a step is 32 k, which one group holds.
-constexpr int kWaves = 8;
-template <int T, int MT>
-__global__ __launch_bounds__(64 * kWaves) void w4_simple_kernel(const W4Params p, int tiles_n) {
-    __shared__ float part[kWaves][MT][64][4];
+// MT x 16 rows.  CHAIN: instructions of 32 codes that are sure to share a scale (groups are multiples of 32 * CHAIN).
+template <int T, int MT, int WAVES, int CHAIN>
+__global__ __launch_bounds__(64 * WAVES) void w4_skinny_kernel(const W4Params p, int tiles_n) {
+    constexpr int NS = 4 / CHAIN, DEPTH = MT == 1 && (WAVES == 8 || NS < 4) ? 4 : 2;   // (what the registers hold)
+    __shared__ float part[WAVES][MT][64][4];
     const int lane = lane_id(), w = wave_id(), r = lane % 16, g = lane / 16;
-    const int n0 = (int)(blockIdx.x % tiles_n) * 16, m0 = (int)(blockIdx.x / tiles_n) * 16 * MT;
-    const int nc = min(n0 + r, p.N - 1);
-    const uint8_t* qrow = p.W + (int64_t)nc * p.ldw;
+    const int64_t n0 = (int64_t)(blockIdx.x % tiles_n) * 16;
+    const int m0 = (int)(blockIdx.x / tiles_n) * 16 * MT;
+    const int64_t nc = min(n0 + r, (int64_t)p.N - 1);
+    const uint8_t* qrow = p.W + nc * p.ldw;
+    const uint16_t* srow = reinterpret_cast<const uint16_t*>(p.scales) + nc * p.lds;
+    const uint16_t* zrow = reinterpret_cast<const uint16_t*>(p.zeros) + nc * p.lds;
     const char* arow[MT];
+    bool has[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) arow[i] = p.A + (int64_t)min(m0 + 16 * i + r, p.M - 1) * p.lda * 2;
-    const u32x4 ones = {Half<T>::ONES, Half<T>::ONES, Half<T>::ONES, Half<T>::ONES};
+    for (int i = 0; i < MT; ++i) {
+        has[i] = m0 + 16 * i + r < p.M;
+        arow[i] = p.A + (int64_t)min(m0 + 16 * i + r, p.M - 1) * p.lda * 2;
+    }
+    const u32x4 none = {0u, 0u, 0u, 0u}, ones = {Half<T>::ONES, Half<T>::ONES, Half<T>::ONES, Half<T>::ONES};
     f32x4 total[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) total[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int steps = (p.K + 31) / 32;
-    for (int s = w; s < steps; s += kWaves) {
-        const int k = s * 32 + 8 * g;
-        const u32x4 b = spread<T>(load_q(qrow, k, p.K));
-        const int64_t gi = (int64_t)nc * p.lds + s * 32 / p.group;
-        const float sc = 16.0f * load_elem(p.scales, T, gi);
-        const float z1 = -1.0f - (p.zeros ? load_elem(p.zeros, T, gi) : 8.0f) * 0.0625f;
+
+    // 128 codes: words q of this lane in instruction order, a[i][t] the matching elements of A, and NS scales
+    auto multiply = [&](const u32x4& q, const u32x4 (*a)[4], const float* s, const float* z) {
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        f32x4 dot[MT], sum[MT];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const u32x4 a = shuffle8(load_a(arow[i], k, p.K));
-            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-            const f32x4 dot = Half<T>::mfma(a, b, zero), sum = Half<T>::mfma(a, ones, zero);
+        for (int t = 0; t < 4; ++t) {
+            const u32x4 b = spread<T>(q[t]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) total[i][e] = __builtin_fmaf(sc, __builtin_fmaf(z1, sum[e], dot[e]), total[i][e]);
+            for (int i = 0; i < MT; ++i) {
+                const bool first = t % CHAIN == 0;
+                dot[i] = Half<T>::mfma(a[i][t], b, first ? zero : dot[i]);
+                sum[i] = Half<T>::mfma(a[i][t], ones, first ? zero : sum[i]);
+                if (t % CHAIN == CHAIN - 1) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        total[i][e] = __builtin_fmaf(s[t / CHAIN], __builtin_fmaf(-z[t / CHAIN], sum[i][e], dot[i][e]), total[i][e]);
+                }
+            }
         }
+    };
+    const int full = p.K / kStep;
+    // D steps from s, every WAVES-th.  LAST: those past the last whole step repeat it with zeros in A and scales.
+    auto steps = [&](int s, auto depth, auto last) {
+        constexpr int D = decltype(depth)::value;
+        constexpr bool LAST = decltype(last)::value;
+        u32x4 q[D], a[D][MT][4];
+        uint16_t sb[D][NS], zb[D][NS];
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const int st = LAST ? min(s + d * WAVES, full - 1) : s + d * WAVES;
+            q[d] = load16(qrow + (int64_t)st * (kStep / 2) + 16 * g);
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                const int64_t gi = (st * kStep + 32 * CHAIN * j) / p.group;
+                sb[d][j] = srow[gi];
+                zb[d][j] = p.zeros ? zrow[gi] : (uint16_t)0;
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const bool in = !LAST || s + d * WAVES < full;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    a[d][i][t] = none;
+                    if (has[i] && in) a[d][i][t] = load16(arow[i] + ((int64_t)(s + d * WAVES) * kStep + 32 * t + 8 * g) * 2);
+                }
+        }
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            float sc[NS], ze[NS];
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                sc[j] = !LAST || s + d * WAVES < full ? scale16<T>(sb[d][j]) : 0.0f;
+                ze[j] = p.zeros ? zero16<T>(zb[d][j]) : kZero16;
+                if (LAST && s + d * WAVES >= full) ze[j] = 0.0f;
+            }
+            multiply(transpose_groups(q[d]), a[d], sc, ze);
+        }
+    };
+    int s = w;
+    for (; s + (DEPTH - 1) * WAVES < full; s += DEPTH * WAVES)
+        steps(s, std::integral_constant<int, DEPTH>(), std::false_type());
+    if (s < full) steps(s, std::integral_constant<int, DEPTH>(), std::true_type());
+    if (full % WAVES == w && full * kStep < p.K) {   // the last, partial step
+        u32x4 q, a[MT][4];
+        float sc[NS], ze[NS];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int k = full * kStep + 32 * t + 8 * g;
+            q[t] = load_q(qrow, k, p.K);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) a[i][t] = has[i] ? load_a(arow[i], k, p.K) : none;
+        }
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            const int64_t k = full * kStep + 32 * CHAIN * j;
+            const bool in = k < p.K;
+            sc[j] = in ? scale16<T>(srow[k / p.group]) : 0.0f;
+            ze[j] = !in ? 0.0f : p.zeros ? zero16<T>(zrow[k / p.group]) : kZero16;
+        }
+        multiply(q, a, sc, ze);
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) part[w][i][lane][e] = total[i][e];
+    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(part[w][i][lane]) = total[i];
     __syncthreads();
-    for (int t = threadIdx.x; t < MT * 256; t += 64 * kWaves) {
-        const int i = t / 256, l = t % 64, e = t / 64 % 4;
-        const int m = m0 + 16 * i + 4 * (l / 16) + e, col = n0 + l % 16;
+    // lane l, element e holds row 4 * (l / 16) + e and column l % 16; the waves' sums meet in wave order
+    for (int t = threadIdx.x; t < MT * 256; t += 64 * WAVES) {
+        const int n = t % 16, row = t / 16, m = m0 + row;
+        if (m >= p.M || n0 + n >= p.N) continue;
         float v = 0.0f;
 #pragma unroll
-        for (int q = 0; q < kWaves; ++q) v += part[q][i][l][e];
-        if (m < p.M && col < p.N) store_c1(p.C, p.out_type, (int64_t)m * p.ldc + col, v, p.alpha, p.beta);
+        for (int q = 0; q < WAVES; ++q) v += part[q][row / 16][row % 16 / 4 * 16 + n][row % 4];
+        store_c1(p.C, p.out_type, m * p.ldc + n0 + n, v, p.alpha, p.beta);
     }
 }
 
-template <int T, int MT>
+template <int T, int MT, int WAVES>
 hipError_t go(const W4Params& p, hipStream_t st) {
     const int64_t tn = ((int64_t)p.N + 15) / 16, tm = ((int64_t)p.M + 16 * MT - 1) / (16 * MT);
-    if (tm * tn > INT32_MAX / (64 * kWaves)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((w4_simple_kernel<T, MT>), dim3((unsigned)(tm * tn)), dim3(64 * kWaves), 0, st, p, (int)tn);
+    if (tm * tn > INT32_MAX / (64 * WAVES)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(tm * tn)), block(64 * WAVES);
+    if (p.group % 128 == 0) hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 4>), grid, block, 0, st, p, (int)tn);
+    else if (p.group % 64 == 0) hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 2>), grid, block, 0, st, p, (int)tn);
+    else hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 1>), grid, block, 0, st, p, (int)tn);
     return hipGetLastError();
 }
 
+// Sixteen waves where eight would leave most of the card's wave slots empty and each still has steps to take.
 template <int T>
 hipError_t skinny_of(const W4Params& p, hipStream_t st) {
-    return p.M <= 16 ? go<T, 1>(p, st) : go<T, 4>(p, st);
+    const int64_t tn = ((int64_t)p.N + 15) / 16;
+    const bool deep = tn <= 2 * num_compute_units() && p.K >= 2048;
+    if (p.M <= 16) return deep ? go<T, 1, 16>(p, st) : go<T, 1, 8>(p, st);
+    return go<T, 4, 8>(p, st);
 }
 
 }  // namespace
