@@ -1,169 +1,178 @@
 // w4_skinny.hip -- C = alpha * A * W^T + beta * C with 4-bit weights for few rows of A: the
 // codes' bytes bound it.
 //
-// A workgroup computes 16 columns; its waves share K, each taking every WAVES-th step of 128
-// codes.  Every lane loads 16 bytes (32 codes) of a row of W straight into registers: the four
-// lane groups take 64 whole bytes of a row.  An instruction's k have to lie in one group of
-// scales, which may be 32 long, so the four words of a lane change places with those of the other lane
-// groups (a 4 x 4 transpose, four lane swaps) until instruction t holds k = 32 t .. 32 t + 31.
-// The sum of a, which the zero points multiply, is one more instruction, against ones.
+// A workgroup computes 16 columns (MT x 16 rows); its waves share K, each taking every WAVES-th
+// step of 128 codes, DEPTH steps of loads ahead of the one it multiplies.
+//
+// The address unit takes four neighbouring lanes a cycle only if they lie in one cache line, so
+// no load follows the matrix instruction's layout (lane l holds row l % 16): four lanes load 64
+// consecutive bytes of codes of a row, sixteen lanes 256 bytes of A, and a slot of LDS that belongs to the
+// wave turns them (no barrier: a wave's LDS operations run in order).  Instruction t of a step
+// takes k = 32 t .. 32 t + 31, which one group of scales holds.  The scales and zero points of the 16
+// columns are brought into LDS by the whole workgroup before it starts: gathered step by step
+// they took as many cycles of the address unit as all the rest (16 rows of A, groups of 64: 33 us of
+// 4096 x 14336, of which the codes' bytes take 7).
 #include "w4_common.hpp"
 
 namespace gemm {
 namespace {
 
-constexpr int kStep = 128;
+constexpr int kStep = 128, kFewRows = 4;
+constexpr int kGroups = 256;           // groups of 16 columns in LDS at a time
+constexpr int kGroupRow = kGroups + 2; // words apart: rows start on different banks
 
-// v[i] of lane group g becomes v[g] of lane group i.
-__device__ __forceinline__ u32x4 transpose_groups(u32x4 v) {
-    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-    const u2 a = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
-    const u2 b = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
-    const u2 c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-    const u2 d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-    return u32x4{c[0], c[1], d[0], d[1]};
+__device__ __forceinline__ void wave_fence() {   // for the compiler; the hardware keeps a wave's LDS order
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
 }
 
-// MT x 16 rows.  CHAIN: instructions of 32 codes that are sure to share a scale (groups are multiples of 32 * CHAIN).
-template <int T, int MT, int WAVES, int CHAIN>
-__global__ __launch_bounds__(64 * WAVES) void w4_skinny_kernel(const W4Params p, int tiles_n) {
-    constexpr int NS = 4 / CHAIN, DEPTH = MT == 1 && (WAVES == 8 || NS < 4) ? 4 : 2;   // (what the registers hold)
-    __shared__ float part[WAVES][MT][64][4];
+// CHAIN: instructions of 32 codes that are sure to share a scale (groups are multiples of 32 * CHAIN).
+template <int T, int MT, int WAVES, int CHAIN, bool FEW>
+__global__ __launch_bounds__(64 * WAVES) void w4_skinny_kernel(const W4Params p) {
+    constexpr int DEPTH = FEW ? 4 : MT == 1 && WAVES == 8 ? 3 : 2;   // what the registers hold
+    constexpr int AL = FEW ? 1 : 4 * MT;                 // 16-byte loads of A per step, four rows each
+    constexpr int QB = 16 * 64, SLOT = QB + AL * 4 * 256;
+    static_assert(!FEW || MT == 1, "few rows are one block");
+    constexpr int GROUPS = 16 * kGroupRow * 4;           // a scale and a zero point to a word
+    __shared__ __attribute__((aligned(1024))) char smem_raw[WAVES * (SLOT > MT * 1024 ? SLOT : MT * 1024) + GROUPS];
+    LDS_AS char* slot = (LDS_AS char*)smem_raw + wave_id() * SLOT;
+    LDS_AS uint32_t* groups = reinterpret_cast<LDS_AS uint32_t*>((LDS_AS char*)smem_raw + sizeof(smem_raw) - GROUPS);
     const int lane = lane_id(), w = wave_id(), r = lane % 16, g = lane / 16;
-    const int64_t n0 = (int64_t)(blockIdx.x % tiles_n) * 16;
-    const int m0 = (int)(blockIdx.x / tiles_n) * 16 * MT;
-    const int64_t nc = min(n0 + r, (int64_t)p.N - 1);
-    const uint8_t* qrow = p.W + nc * p.ldw;
-    const uint16_t* srow = reinterpret_cast<const uint16_t*>(p.scales) + nc * p.lds;
-    const uint16_t* zrow = reinterpret_cast<const uint16_t*>(p.zeros) + nc * p.lds;
-    const char* arow[MT];
-    bool has[MT];
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int m0 = (int)blockIdx.y * 16 * MT;
+    const uint8_t* qsrc = p.W + min(n0 + lane / 4, (int64_t)p.N - 1) * p.ldw + 16 * (lane % 4);
+    const char* asrc[AL];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        has[i] = m0 + 16 * i + r < p.M;
-        arow[i] = p.A + (int64_t)min(m0 + 16 * i + r, p.M - 1) * p.lda * 2;
-    }
-    const u32x4 none = {0u, 0u, 0u, 0u}, ones = {Half<T>::ONES, Half<T>::ONES, Half<T>::ONES, Half<T>::ONES};
+    for (int h = 0; h < AL; ++h) asrc[h] = p.A + ((int64_t)min(m0 + g + 4 * h, p.M - 1) * p.lda + 8 * r) * 2;   // rows past the end are not stored
+    const u32x4 ones = {Half<T>::ONES, Half<T>::ONES, Half<T>::ONES, Half<T>::ONES};
     f32x4 total[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) total[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    u32x4 q[DEPTH], a[DEPTH][AL];
 
-    // 128 codes: words q of this lane in instruction order, a[i][t] the matching elements of A, and NS scales
-    auto multiply = [&](const u32x4& q, const u32x4 (*a)[4], const float* s, const float* z) {
+    const int full = p.K / kStep;
+    auto load = [&](int d, int s) {
+        q[d] = load16(qsrc + (int64_t)s * (kStep / 2));
+#pragma unroll
+        for (int h = 0; h < AL; ++h) a[d][h] = load16(asrc[h] + (int64_t)s * (kStep * 2));
+    };
+    // Chunk c of A's row `row` of the slot: 16 lanes of one chunk and 16 rows meet 16 different ones.
+    auto a_at = [&](int row, int c) { return reinterpret_cast<LDS_AS u32x4*>(slot + QB + row * 256 + ((c ^ (row & 15)) << 4)); };
+    int g0 = 0;   // the first group in LDS
+    auto multiply = [&](int s, const uint32_t* word, auto&& chunk) {
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
         f32x4 dot[MT], sum[MT];
+        float sc = 0.0f, ze = 0.0f;
+        int gi = s * kStep / p.group, in = s * kStep - gi * p.group;   // the group of this instruction, and k's place in it
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const u32x4 b = spread<T>(q[t]);
+            const bool first = t % CHAIN == 0, last = t % CHAIN == CHAIN - 1;
+            if (first) {
+                const bool past = s * kStep + 32 * t >= p.K;   // then A is zero and the group may not exist
+                const uint32_t v = groups[r * kGroupRow + (past ? 0 : gi - g0)];
+                sc = past ? 0.0f : scale16<T>((uint16_t)v);
+                ze = past ? 0.0f : p.zeros ? zero16<T>((uint16_t)(v >> 16)) : kZero16;
+                in += 32 * CHAIN;
+                if (in >= p.group) { in = 0; ++gi; }
+            }
+            const u32x4 b = spread<T>(word[t]);
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                const bool first = t % CHAIN == 0;
-                dot[i] = Half<T>::mfma(a[i][t], b, first ? zero : dot[i]);
-                sum[i] = Half<T>::mfma(a[i][t], ones, first ? zero : sum[i]);
-                if (t % CHAIN == CHAIN - 1) {
+                const u32x4 f = chunk(i, t);
+                dot[i] = Half<T>::mfma(f, b, first ? zero : dot[i]);
+                sum[i] = Half<T>::mfma(f, ones, first ? zero : sum[i]);
+                if (last) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        total[i][e] = __builtin_fmaf(s[t / CHAIN], __builtin_fmaf(-z[t / CHAIN], sum[i][e], dot[i][e]), total[i][e]);
+                        total[i][e] = __builtin_fmaf(sc, __builtin_fmaf(-ze, sum[i][e], dot[i][e]), total[i][e]);
                 }
             }
         }
     };
-    const int full = p.K / kStep;
-    // D steps from s, every WAVES-th.  LAST: those past the last whole step repeat it with zeros in A and scales.
-    auto steps = [&](int s, auto depth, auto last) {
-        constexpr int D = decltype(depth)::value;
-        constexpr bool LAST = decltype(last)::value;
-        u32x4 q[D], a[D][MT][4];
-        uint16_t sb[D][NS], zb[D][NS];
+    auto step = [&](int d, int s) {
+        wave_fence();
+        const int row = lane / 4;
+        *reinterpret_cast<LDS_AS u32x4*>(slot + row * 64 + (((lane % 4) ^ swz<4>(row)) << 4)) = q[d];
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const int st = LAST ? min(s + d * WAVES, full - 1) : s + d * WAVES;
-            q[d] = load16(qrow + (int64_t)st * (kStep / 2) + 16 * g);
+        for (int h = 0; h < AL; ++h) *a_at(g + 4 * h, r) = a[d][h];
+        wave_fence();
+        uint32_t word[4];
 #pragma unroll
-            for (int j = 0; j < NS; ++j) {
-                const int64_t gi = (st * kStep + 32 * CHAIN * j) / p.group;
-                sb[d][j] = srow[gi];
-                zb[d][j] = p.zeros ? zrow[gi] : (uint16_t)0;
-            }
-        }
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            const bool in = !LAST || s + d * WAVES < full;
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    a[d][i][t] = none;
-                    if (has[i] && in) a[d][i][t] = load16(arow[i] + ((int64_t)(s + d * WAVES) * kStep + 32 * t + 8 * g) * 2);
-                }
-        }
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            float sc[NS], ze[NS];
-#pragma unroll
-            for (int j = 0; j < NS; ++j) {
-                sc[j] = !LAST || s + d * WAVES < full ? scale16<T>(sb[d][j]) : 0.0f;
-                ze[j] = p.zeros ? zero16<T>(zb[d][j]) : kZero16;
-                if (LAST && s + d * WAVES >= full) ze[j] = 0.0f;
-            }
-            multiply(transpose_groups(q[d]), a[d], sc, ze);
-        }
+        for (int t = 0; t < 4; ++t) word[t] = *reinterpret_cast<LDS_AS uint32_t*>(slot + r * 64 + ((t ^ swz<4>(r)) << 4) + 4 * g);
+        multiply(s, word, [&](int i, int t) -> u32x4 {
+            return *a_at(FEW ? r % kFewRows : 16 * i + r, 4 * t + g);
+        });
+        __builtin_amdgcn_sched_barrier(0);   // steps mixed by the scheduler would not fit the registers
     };
-    int s = w;
-    for (; s + (DEPTH - 1) * WAVES < full; s += DEPTH * WAVES)
-        steps(s, std::integral_constant<int, DEPTH>(), std::false_type());
-    if (s < full) steps(s, std::integral_constant<int, DEPTH>(), std::true_type());
-    if (full % WAVES == w && full * kStep < p.K) {   // the last, partial step
-        u32x4 q, a[MT][4];
-        float sc[NS], ze[NS];
+    // Groups that LDS holds at a time are whole steps; their steps are dealt to the waves.
+    const int64_t span = (int64_t)p.group * kGroups;   // codes (a multiple of 128: kGroups is one of 4)
+    for (int64_t k0 = 0; k0 < p.K; k0 += span) {
+        const int s0 = (int)(k0 / kStep), s1 = (int)min((k0 + span) / kStep, (int64_t)full);   // whole steps
+        if (s1 > s0)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int k = full * kStep + 32 * t + 8 * g;
-            q[t] = load_q(qrow, k, p.K);
-#pragma unroll
-            for (int i = 0; i < MT; ++i) a[i][t] = has[i] ? load_a(arow[i], k, p.K) : none;
+            for (int d = 0; d < DEPTH; ++d) load(d, min(s0 + w + d * WAVES, s1 - 1));
+        if (k0 > 0) __syncthreads();   // every wave is done with the last groups
+        g0 = (int)(k0 / p.group);
+        const int ng = min(kGroups, (p.K + p.group - 1) / p.group - g0);
+        for (int i = threadIdx.x; i < 16 * ng; i += 64 * WAVES) {
+            const int row = i / ng, c = i % ng;
+            const int64_t at = min(n0 + row, (int64_t)p.N - 1) * p.lds + g0 + c;
+            uint32_t v = reinterpret_cast<const uint16_t*>(p.scales)[at];
+            if (p.zeros) v |= (uint32_t)reinterpret_cast<const uint16_t*>(p.zeros)[at] << 16;
+            groups[row * kGroupRow + c] = v;
         }
+        __syncthreads();
+        // (loads stand outside of branches: behind one, a wait for an older load would wait for them all)
+        for (int s = s0 + w; s < s1; s += DEPTH * WAVES)
 #pragma unroll
-        for (int j = 0; j < NS; ++j) {
-            const int64_t k = full * kStep + 32 * CHAIN * j;
-            const bool in = k < p.K;
-            sc[j] = in ? scale16<T>(srow[k / p.group]) : 0.0f;
-            ze[j] = !in ? 0.0f : p.zeros ? zero16<T>(zrow[k / p.group]) : kZero16;
+            for (int d = 0; d < DEPTH; ++d) {
+                if (s + d * WAVES < s1) step(d, s + d * WAVES);
+                load(d, min(s + (d + DEPTH) * WAVES, s1 - 1));
+            }
+        if (k0 + span >= p.K && full * kStep < p.K && full % WAVES == w) {   // the last, partial step, as its instructions want it
+            const uint8_t* qrow = p.W + min(n0 + r, (int64_t)p.N - 1) * p.ldw;
+            uint32_t word[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) word[t] = load_q(qrow, full * kStep + 32 * t + 8 * g, p.K);
+            multiply(full, word, [&](int i, int t) -> u32x4 {
+                return load_a(p.A + (int64_t)min(m0 + 16 * i + r, p.M - 1) * p.lda * 2, full * kStep + 32 * t + 8 * g, p.K);
+            });
         }
-        multiply(q, a, sc, ze);
     }
+    __syncthreads();   // the slots are free
+    auto part = [&](int v, int i, int l) { return reinterpret_cast<LDS_AS f32x4*>((LDS_AS char*)smem_raw + ((v * MT + i) * 64 + l) * 16); };
 #pragma unroll
-    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(part[w][i][lane]) = total[i];
+    for (int i = 0; i < MT; ++i) *part(w, i, lane) = total[i];
     __syncthreads();
     // lane l, element e holds row 4 * (l / 16) + e and column l % 16; the waves' sums meet in wave order
     for (int t = threadIdx.x; t < MT * 256; t += 64 * WAVES) {
-        const int n = t % 16, row = t / 16, m = m0 + row;
-        if (m >= p.M || n0 + n >= p.N) continue;
+        const int n = t % 16, m = t / 16;
+        if (m0 + m >= p.M || n0 + n >= p.N) continue;
         float v = 0.0f;
 #pragma unroll
-        for (int q = 0; q < WAVES; ++q) v += part[q][row / 16][row % 16 / 4 * 16 + n][row % 4];
-        store_c1(p.C, p.out_type, m * p.ldc + n0 + n, v, p.alpha, p.beta);
+        for (int x = 0; x < WAVES; ++x) v += reinterpret_cast<LDS_AS float*>(part(x, m / 16, m % 16 / 4 * 16 + n))[m % 4];
+        store_c1(p.C, p.out_type, (m0 + m) * p.ldc + n0 + n, v, p.alpha, p.beta);
     }
 }
 
-template <int T, int MT, int WAVES>
+template <int T, int MT, int WAVES, bool FEW>
 hipError_t go(const W4Params& p, hipStream_t st) {
     const int64_t tn = ((int64_t)p.N + 15) / 16, tm = ((int64_t)p.M + 16 * MT - 1) / (16 * MT);
-    if (tm * tn > INT32_MAX / (64 * WAVES)) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)(tm * tn)), block(64 * WAVES);
-    if (p.group % 128 == 0) hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 4>), grid, block, 0, st, p, (int)tn);
-    else if (p.group % 64 == 0) hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 2>), grid, block, 0, st, p, (int)tn);
-    else hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 1>), grid, block, 0, st, p, (int)tn);
+    if (tn > INT32_MAX / (64 * WAVES) || tm > 65535) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)tn, (unsigned)tm), block(64 * WAVES);
+    if (p.group % 128 == 0) hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 4, FEW>), grid, block, 0, st, p);
+    else if (p.group % 64 == 0) hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 2, FEW>), grid, block, 0, st, p);
+    else hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 1, FEW>), grid, block, 0, st, p);
     return hipGetLastError();
 }
 
 // Sixteen waves where eight would leave most of the card's wave slots empty and each still has steps to take.
 template <int T>
 hipError_t skinny_of(const W4Params& p, hipStream_t st) {
-    const int64_t tn = ((int64_t)p.N + 15) / 16;
-    const bool deep = tn <= 2 * num_compute_units() && p.K >= 2048;
-    if (p.M <= 16) return deep ? go<T, 1, 16>(p, st) : go<T, 1, 8>(p, st);
-    return go<T, 4, 8>(p, st);
+    const bool deep = ((int64_t)p.N + 15) / 16 <= 2 * num_compute_units() && p.K >= 2048;
+    if (p.M <= kFewRows) return deep ? go<T, 1, 16, true>(p, st) : go<T, 1, 8, true>(p, st);
+    if (p.M <= 16) return deep ? go<T, 1, 16, false>(p, st) : go<T, 1, 8, false>(p, st);
+    return go<T, 2, 8, false>(p, st);
 }
 
 }  // namespace
