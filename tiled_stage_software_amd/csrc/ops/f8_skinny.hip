@@ -19,12 +19,6 @@ namespace {
 
 constexpr int kStep = 128, kFewRows = 4;
 
-// Orders a wave's own LDS writes and reads for the compiler (the hardware keeps their order).
-__device__ __forceinline__ void wave_fence() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_wave_barrier();
-}
-
 template <int MT, int WAVES, bool WIDE, bool FEW>
 __global__ __launch_bounds__(64 * WAVES) void f8_skinny_kernel(const F8Params p) {
     constexpr int DEPTH = MT == 1 || WAVES == 8 ? 4 : 2;   // what the registers hold
@@ -103,11 +97,11 @@ __global__ __launch_bounds__(64 * WAVES) void f8_skinny_kernel(const F8Params p)
             acc[i] = mfma_f8<WIDE>(fb, join16(load_chunk(arow, 16 * g, p.K), load_chunk(arow, 64 + 16 * g, p.K)), acc[i]);
         }
     }
-    __syncthreads();   // the slots are free
+    lds_barrier();   // the slots are free
     auto part = [&](int q, int i, int l) { return reinterpret_cast<LDS_AS f32x4*>((LDS_AS char*)smem_raw + ((q * MT + i) * 64 + l) * 16); };
 #pragma unroll
     for (int i = 0; i < MT; ++i) *part(w, i, lane) = acc[i];
-    __syncthreads();
+    lds_barrier();
     for (int t = threadIdx.x; t < MT * 256; t += 64 * WAVES) {
         const int n = t % 16, m = t / 16;
         if (m >= p.M || n0 + n >= p.N) continue;

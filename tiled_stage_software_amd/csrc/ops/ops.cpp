@@ -230,6 +230,7 @@ gemm_status_t gemm_w4(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, int
     p.alpha = alpha; p.beta = beta;
     p.out_type = c_type;
     (void)workspace_bytes;
+    if (M <= kW4VectorRows) return launched(launch_w4_vector(in_type, p, stream));
     return launched(launch_w4_skinny(in_type, p, stream));
 }
 

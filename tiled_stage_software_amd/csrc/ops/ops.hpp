@@ -84,6 +84,8 @@ struct W4Params {
     float alpha, beta;
     int out_type;
 };
+constexpr int kW4VectorRows = 4;    // rows of A that launch_w4_vector takes
+hipError_t launch_w4_vector(int in_type, const W4Params& p, hipStream_t st);
 hipError_t launch_w4_skinny(int in_type, const W4Params& p, hipStream_t st);
 
 }  // namespace gemm

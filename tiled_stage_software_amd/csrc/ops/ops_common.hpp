@@ -14,6 +14,17 @@ __device__ __forceinline__ u32x4 load16(const void* p) {
 }
 __device__ __forceinline__ void store16(void* p, u32x4 v) { __builtin_memcpy(p, &v, 16); }
 
+// Orders a wave's own LDS writes and reads for the compiler (the hardware keeps their order).
+__device__ __forceinline__ void wave_fence() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+// Barrier for what the workgroup shares in LDS; unlike __syncthreads() it leaves loads from memory in flight.
+__device__ __forceinline__ void lds_barrier() {
+    wait_lgkm0();
+    barrier();
+}
+
 template <int T>
 __device__ __forceinline__ float to_f32(uint16_t b) {
     return T == DT_BF16 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b);

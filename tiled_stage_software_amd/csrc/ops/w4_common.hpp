@@ -30,26 +30,40 @@ template <> struct Half<DT_F16> {
     }
 };
 
-// Eight codes (code i in bits 4 i .. 4 i + 3) as eight 1 + q/16 in their order.  Two rotations put
-// every even and every odd code at bit TOP of some byte; a byte permute then pairs codes 2 i and
-// 2 i + 1 in the halves of a word: ten operations for eight codes.
+// Turns codes into operands.  The mask and the ones sit in registers, out of the compiler's sight, so that
+// masking and joining are one v_and_or_b32 (as literals they are two instructions).
 template <int T>
-__device__ __forceinline__ u32x4 spread(uint32_t w) {
-    constexpr int TOP = Half<T>::TOP;
-    constexpr uint32_t MASK = 0x000F000Fu << TOP;
-    const uint32_t even = __builtin_amdgcn_alignbit(w, w, 32 - TOP);          // left by TOP
-    const uint32_t odd = __builtin_amdgcn_alignbit(w, w, (36 - TOP) & 31);    // left by TOP - 4
-    u32x4 v;
-    v[0] = (__builtin_amdgcn_perm(odd, even, 0x05040100u) & MASK) | Half<T>::ONES;
-    v[1] = (__builtin_amdgcn_perm(odd, even, 0x06050201u) & MASK) | Half<T>::ONES;
-    v[2] = (__builtin_amdgcn_perm(odd, even, 0x07060302u) & MASK) | Half<T>::ONES;
-    v[3] = (__builtin_amdgcn_perm(odd, even, 0x04070003u) & MASK) | Half<T>::ONES;
-    return v;
+struct Spread {
+    static constexpr int TOP = Half<T>::TOP;
+    uint32_t mask, ones;
+    __device__ __forceinline__ Spread() : mask(0x000F000Fu << TOP), ones(Half<T>::ONES) {
+        asm("" : "+s"(mask));
+        asm("" : "+v"(ones));
+    }
+    __device__ __forceinline__ uint32_t place(uint32_t v) const { return (v & mask) | ones; }
+    // Eight codes (code i in bits 4 i .. 4 i + 3) in their order.  Two rotations put every even and every odd
+    // code at bit TOP of some byte; a byte permute then pairs codes 2 i and 2 i + 1: ten operations.
+    __device__ __forceinline__ u32x4 in_order(uint32_t w) const {
+        const uint32_t even = __builtin_amdgcn_alignbit(w, w, 32 - TOP);          // left by TOP
+        const uint32_t odd = __builtin_amdgcn_alignbit(w, w, (36 - TOP) & 31);    // left by TOP - 4
+        return u32x4{place(__builtin_amdgcn_perm(odd, even, 0x05040100u)), place(__builtin_amdgcn_perm(odd, even, 0x06050201u)),
+                     place(__builtin_amdgcn_perm(odd, even, 0x07060302u)), place(__builtin_amdgcn_perm(odd, even, 0x04070003u))};
+    }
+    // The same as pairs (0, 4), (1, 5), (2, 6), (3, 7), for an A whose eight elements lie so: eight operations.
+    __device__ __forceinline__ u32x4 in_pairs(uint32_t w) const {
+        u32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = place(4 * i < TOP ? w << (TOP - 4 * i) : w >> (4 * i - TOP));
+        return v;
+    }
+};
+// Eight 16-bit elements in the order of in_pairs().
+__device__ __forceinline__ u32x4 pairs_of(u32x4 a) {
+    return u32x4{__builtin_amdgcn_perm(a[2], a[0], 0x05040100u), __builtin_amdgcn_perm(a[2], a[0], 0x07060302u),
+                 __builtin_amdgcn_perm(a[3], a[1], 0x05040100u), __builtin_amdgcn_perm(a[3], a[1], 0x07060302u)};
 }
 
-// 16 s and 1 + z/16 of a group.
-template <int T>
-__device__ __forceinline__ float scale16(uint16_t s) { return 16.0f * to_f32<T>(s); }
+// 1 + z/16 of a group.
 template <int T>
 __device__ __forceinline__ float zero16(uint16_t z) { return 1.0f + to_f32<T>(z) * 0.0625f; }
 constexpr float kZero16 = 1.5f;   // of z = 8

@@ -17,26 +17,20 @@
 namespace gemm {
 namespace {
 
-constexpr int kStep = 128, kFewRows = 4;
-constexpr int kGroups = 256;           // groups of 16 columns in LDS at a time
-constexpr int kGroupRow = kGroups + 2; // words apart: rows start on different banks
-
-__device__ __forceinline__ void wave_fence() {   // for the compiler; the hardware keeps a wave's LDS order
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_wave_barrier();
-}
+constexpr int kStep = 128;
+constexpr int kGroups = 128;           // groups of 16 columns in LDS at a time
+constexpr int kGroupRow = kGroups + 1; // apart: rows start on different banks
 
 // CHAIN: instructions of 32 codes that are sure to share a scale (groups are multiples of 32 * CHAIN).
-template <int T, int MT, int WAVES, int CHAIN, bool FEW>
+template <int T, int MT, int WAVES, int CHAIN>
 __global__ __launch_bounds__(64 * WAVES) void w4_skinny_kernel(const W4Params p) {
-    constexpr int DEPTH = FEW ? 4 : MT == 1 && WAVES == 8 ? 3 : 2;   // what the registers hold
-    constexpr int AL = FEW ? 1 : 4 * MT;                 // 16-byte loads of A per step, four rows each
+    constexpr int DEPTH = MT == 1 && WAVES == 8 ? 3 : 2;   // what the registers hold
+    constexpr int AL = 4 * MT;                 // 16-byte loads of A per step, four rows each
     constexpr int QB = 16 * 64, SLOT = QB + AL * 4 * 256;
-    static_assert(!FEW || MT == 1, "few rows are one block");
-    constexpr int GROUPS = 16 * kGroupRow * 4;           // a scale and a zero point to a word
+    constexpr int GROUPS = 16 * kGroupRow * 8;           // of each the scale and 1 + z/16 as floats
     __shared__ __attribute__((aligned(1024))) char smem_raw[WAVES * (SLOT > MT * 1024 ? SLOT : MT * 1024) + GROUPS];
     LDS_AS char* slot = (LDS_AS char*)smem_raw + wave_id() * SLOT;
-    LDS_AS uint32_t* groups = reinterpret_cast<LDS_AS uint32_t*>((LDS_AS char*)smem_raw + sizeof(smem_raw) - GROUPS);
+    LDS_AS f32x2* groups = reinterpret_cast<LDS_AS f32x2*>((LDS_AS char*)smem_raw + sizeof(smem_raw) - GROUPS);
     const int lane = lane_id(), w = wave_id(), r = lane % 16, g = lane / 16;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
     const int m0 = (int)blockIdx.y * 16 * MT;
@@ -45,6 +39,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_skinny_kernel(const W4Params p)
 #pragma unroll
     for (int h = 0; h < AL; ++h) asrc[h] = p.A + ((int64_t)min(m0 + g + 4 * h, p.M - 1) * p.lda + 8 * r) * 2;   // rows past the end are not stored
     const u32x4 ones = {Half<T>::ONES, Half<T>::ONES, Half<T>::ONES, Half<T>::ONES};
+    const Spread<T> spread;
     f32x4 total[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) total[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -58,24 +53,22 @@ __global__ __launch_bounds__(64 * WAVES) void w4_skinny_kernel(const W4Params p)
     };
     // Chunk c of A's row `row` of the slot: 16 lanes of one chunk and 16 rows meet 16 different ones.
     auto a_at = [&](int row, int c) { return reinterpret_cast<LDS_AS u32x4*>(slot + QB + row * 256 + ((c ^ (row & 15)) << 4)); };
-    int g0 = 0;   // the first group in LDS
-    auto multiply = [&](int s, const uint32_t* word, auto&& chunk) {
+    // at: the first instruction's group in LDS; in: k's place in it; left: codes before the end (past it A is
+    // zero and a group need not exist).
+    auto multiply = [&](int at, int in, int left, const uint32_t* word, auto&& chunk) {
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
         f32x4 dot[MT], sum[MT];
-        float sc = 0.0f, ze = 0.0f;
-        int gi = s * kStep / p.group, in = s * kStep - gi * p.group;   // the group of this instruction, and k's place in it
+        f32x2 sz = {0.f, 0.f};
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const bool first = t % CHAIN == 0, last = t % CHAIN == CHAIN - 1;
             if (first) {
-                const bool past = s * kStep + 32 * t >= p.K;   // then A is zero and the group may not exist
-                const uint32_t v = groups[r * kGroupRow + (past ? 0 : gi - g0)];
-                sc = past ? 0.0f : scale16<T>((uint16_t)v);
-                ze = past ? 0.0f : p.zeros ? zero16<T>((uint16_t)(v >> 16)) : kZero16;
+                sz = groups[r * kGroupRow + at];
+                if (left <= 32 * t) sz = f32x2{0.f, 0.f};
                 in += 32 * CHAIN;
-                if (in >= p.group) { in = 0; ++gi; }
+                if (in >= p.group && left > 32 * (t + CHAIN)) { in = 0; ++at; }
             }
-            const u32x4 b = spread<T>(word[t]);
+            const u32x4 b = spread.in_order(word[t]);
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 const u32x4 f = chunk(i, t);
@@ -84,12 +77,12 @@ __global__ __launch_bounds__(64 * WAVES) void w4_skinny_kernel(const W4Params p)
                 if (last) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        total[i][e] = __builtin_fmaf(sc, __builtin_fmaf(-ze, sum[i][e], dot[i][e]), total[i][e]);
+                        total[i][e] = __builtin_fmaf(sz[0], __builtin_fmaf(-sz[1], sum[i][e], dot[i][e]), total[i][e]);
                 }
             }
         }
     };
-    auto step = [&](int d, int s) {
+    auto step = [&](int d, int at, int in) {
         wave_fence();
         const int row = lane / 4;
         *reinterpret_cast<LDS_AS u32x4*>(slot + row * 64 + (((lane % 4) ^ swz<4>(row)) << 4)) = q[d];
@@ -99,8 +92,8 @@ __global__ __launch_bounds__(64 * WAVES) void w4_skinny_kernel(const W4Params p)
         uint32_t word[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) word[t] = *reinterpret_cast<LDS_AS uint32_t*>(slot + r * 64 + ((t ^ swz<4>(r)) << 4) + 4 * g);
-        multiply(s, word, [&](int i, int t) -> u32x4 {
-            return *a_at(FEW ? r % kFewRows : 16 * i + r, 4 * t + g);
+        multiply(at, in, kStep, word, [&](int i, int t) -> u32x4 {
+            return *a_at(16 * i + r, 4 * t + g);
         });
         __builtin_amdgcn_sched_barrier(0);   // steps mixed by the scheduler would not fit the registers
     };
@@ -111,39 +104,43 @@ __global__ __launch_bounds__(64 * WAVES) void w4_skinny_kernel(const W4Params p)
         if (s1 > s0)
 #pragma unroll
             for (int d = 0; d < DEPTH; ++d) load(d, min(s0 + w + d * WAVES, s1 - 1));
-        if (k0 > 0) __syncthreads();   // every wave is done with the last groups
-        g0 = (int)(k0 / p.group);
+        if (k0 > 0) lds_barrier();   // every wave is done with the last groups
+        const int g0 = (int)(k0 / p.group);
         const int ng = min(kGroups, (p.K + p.group - 1) / p.group - g0);
         for (int i = threadIdx.x; i < 16 * ng; i += 64 * WAVES) {
             const int row = i / ng, c = i % ng;
             const int64_t at = min(n0 + row, (int64_t)p.N - 1) * p.lds + g0 + c;
-            uint32_t v = reinterpret_cast<const uint16_t*>(p.scales)[at];
-            if (p.zeros) v |= (uint32_t)reinterpret_cast<const uint16_t*>(p.zeros)[at] << 16;
-            groups[row * kGroupRow + c] = v;
+            groups[row * kGroupRow + c] = f32x2{to_f32<T>(reinterpret_cast<const uint16_t*>(p.scales)[at]),
+                                                p.zeros ? zero16<T>(reinterpret_cast<const uint16_t*>(p.zeros)[at]) : kZero16};
         }
-        __syncthreads();
+        lds_barrier();
         // (loads stand outside of branches: behind one, a wait for an older load would wait for them all)
+        int at = w * kStep / p.group, in = w * kStep % p.group;   // this step's first group, and its place in it
         for (int s = s0 + w; s < s1; s += DEPTH * WAVES)
 #pragma unroll
             for (int d = 0; d < DEPTH; ++d) {
-                if (s + d * WAVES < s1) step(d, s + d * WAVES);
+                if (s + d * WAVES < s1) step(d, at, in);
                 load(d, min(s + (d + DEPTH) * WAVES, s1 - 1));
+                at += WAVES * kStep / p.group;
+                in += WAVES * kStep % p.group;
+                if (in >= p.group) { in -= p.group; ++at; }
             }
         if (k0 + span >= p.K && full * kStep < p.K && full % WAVES == w) {   // the last, partial step, as its instructions want it
             const uint8_t* qrow = p.W + min(n0 + r, (int64_t)p.N - 1) * p.ldw;
             uint32_t word[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) word[t] = load_q(qrow, full * kStep + 32 * t + 8 * g, p.K);
-            multiply(full, word, [&](int i, int t) -> u32x4 {
+            const int k = full * kStep, at = k / p.group;
+            multiply(at - g0, k - at * p.group, p.K - k, word, [&](int i, int t) -> u32x4 {
                 return load_a(p.A + (int64_t)min(m0 + 16 * i + r, p.M - 1) * p.lda * 2, full * kStep + 32 * t + 8 * g, p.K);
             });
         }
     }
-    __syncthreads();   // the slots are free
+    lds_barrier();   // the slots are free
     auto part = [&](int v, int i, int l) { return reinterpret_cast<LDS_AS f32x4*>((LDS_AS char*)smem_raw + ((v * MT + i) * 64 + l) * 16); };
 #pragma unroll
     for (int i = 0; i < MT; ++i) *part(w, i, lane) = total[i];
-    __syncthreads();
+    lds_barrier();
     // lane l, element e holds row 4 * (l / 16) + e and column l % 16; the waves' sums meet in wave order
     for (int t = threadIdx.x; t < MT * 256; t += 64 * WAVES) {
         const int n = t % 16, m = t / 16;
@@ -151,18 +148,18 @@ __global__ __launch_bounds__(64 * WAVES) void w4_skinny_kernel(const W4Params p)
         float v = 0.0f;
 #pragma unroll
         for (int x = 0; x < WAVES; ++x) v += reinterpret_cast<LDS_AS float*>(part(x, m / 16, m % 16 / 4 * 16 + n))[m % 4];
-        store_c1(p.C, p.out_type, (m0 + m) * p.ldc + n0 + n, v, p.alpha, p.beta);
+        store_c1(p.C, p.out_type, (m0 + m) * p.ldc + n0 + n, 16.0f * v, p.alpha, p.beta);
     }
 }
 
-template <int T, int MT, int WAVES, bool FEW>
+template <int T, int MT, int WAVES>
 hipError_t go(const W4Params& p, hipStream_t st) {
     const int64_t tn = ((int64_t)p.N + 15) / 16, tm = ((int64_t)p.M + 16 * MT - 1) / (16 * MT);
     if (tn > INT32_MAX / (64 * WAVES) || tm > 65535) return hipErrorInvalidValue;
     const dim3 grid((unsigned)tn, (unsigned)tm), block(64 * WAVES);
-    if (p.group % 128 == 0) hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 4, FEW>), grid, block, 0, st, p);
-    else if (p.group % 64 == 0) hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 2, FEW>), grid, block, 0, st, p);
-    else hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 1, FEW>), grid, block, 0, st, p);
+    if (p.group % 128 == 0) hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 4>), grid, block, 0, st, p);
+    else if (p.group % 64 == 0) hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 2>), grid, block, 0, st, p);
+    else hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 1>), grid, block, 0, st, p);
     return hipGetLastError();
 }
 
@@ -170,9 +167,8 @@ hipError_t go(const W4Params& p, hipStream_t st) {
 template <int T>
 hipError_t skinny_of(const W4Params& p, hipStream_t st) {
     const bool deep = ((int64_t)p.N + 15) / 16 <= 2 * num_compute_units() && p.K >= 2048;
-    if (p.M <= kFewRows) return deep ? go<T, 1, 16, true>(p, st) : go<T, 1, 8, true>(p, st);
-    if (p.M <= 16) return deep ? go<T, 1, 16, false>(p, st) : go<T, 1, 8, false>(p, st);
-    return go<T, 2, 8, false>(p, st);
+    if (p.M <= 16) return deep ? go<T, 1, 16>(p, st) : go<T, 1, 8>(p, st);
+    return go<T, 2, 8>(p, st);
 }
 
 }  // namespace
