@@ -23,8 +23,9 @@ constexpr int kGroupRow = kGroups + 1; // apart: rows start on different banks
 
 // CHAIN: instructions of 32 codes that are sure to share a scale (groups are multiples of 32 * CHAIN).
 template <int T, int MT, int WAVES, int CHAIN>
-__global__ __launch_bounds__(64 * WAVES) void w4_skinny_kernel(const W4Params p) {
-    constexpr int DEPTH = MT == 1 && WAVES == 8 ? 3 : 2;   // what the registers hold
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(MT == 1 ? 4 : 2)))
+void w4_skinny_kernel(const W4Params p) {
+    constexpr int DEPTH = 2;   // what the registers of four (MT 1) or two waves a SIMD hold
     constexpr int AL = 4 * MT;                 // 16-byte loads of A per step, four rows each
     constexpr int QB = 16 * 64, SLOT = QB + AL * 4 * 256;
     constexpr int GROUPS = 16 * kGroupRow * 8;           // of each the scale and 1 + z/16 as floats
@@ -163,12 +164,17 @@ hipError_t go(const W4Params& p, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Sixteen waves where eight would leave most of the card's wave slots empty and each still has steps to take.
+// Waves for 16 on each compute unit (a wave's start costs as much as some steps, so no more share K).
+template <int T, int MT>
+hipError_t rows_of(const W4Params& p, hipStream_t st) {
+    const int64_t blocks = ((int64_t)p.N + 15) / 16 * ((p.M + 16 * MT - 1) / (16 * MT)), cu = num_compute_units();
+    if (blocks >= 3 * cu || p.K < 1024) return go<T, MT, 4>(p, st);
+    if (MT > 1 || blocks >= 3 * cu / 2 || p.K < 4096) return go<T, MT, 8>(p, st);
+    return go<T, 1, 16>(p, st);
+}
 template <int T>
 hipError_t skinny_of(const W4Params& p, hipStream_t st) {
-    const bool deep = ((int64_t)p.N + 15) / 16 <= 2 * num_compute_units() && p.K >= 2048;
-    if (p.M <= 16) return deep ? go<T, 1, 16>(p, st) : go<T, 1, 8>(p, st);
-    return go<T, 2, 8>(p, st);
+    return p.M <= 16 ? rows_of<T, 1>(p, st) : rows_of<T, 2>(p, st);
 }
 
 }  // namespace
