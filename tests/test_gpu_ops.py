@@ -390,6 +390,34 @@ def test_w4(M, N, K, group, t):
     say(f"[w4] {t} {M}x{N}x{K} by {group}: {max(r):.3f} of the tolerance")
 
 
+@pytest.mark.parametrize("M,N,K,group,pad", [(2048, 2304, 1024, 128, 0), (2049, 2307, 1090, 64, 0), (1000, 1536, 640, 32, 3),
+                                             (64, 1024, 8192, 128, 0), (100, 515, 8197, 64, 1), (300, 130, 16000, 32, 0),
+                                             (257, 8200, 450, 192, 5), (33, 128, 64, 32, 0), (47, 200, 65, 64, 0)])
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_w4_exact_integers_large(M, N, K, group, pad, t):
+    """Small whole numbers: every sum is exact in fp32, so every bit has to be right, on the large tiles
+    and the splits of K, from any pitch."""
+    g = torch.Generator(DEV).manual_seed(M + K)
+    groups = -(-K // group)
+    a = torch.randint(-2, 3, (M, K), generator=g, device=DEV).float()
+    codes = torch.randint(0, 256, (N, (K + 1) // 2), generator=g, device=DEV, dtype=torch.uint8)
+    s = 2.0 ** torch.randint(-1, 2, (N, groups), generator=g, device=DEV).float()
+    z = torch.randint(0, 16, (N, groups), generator=g, device=DEV).float()
+    q = torch.stack([codes & 15, codes >> 4], 2).flatten(1)[:, :K].float()
+    each = lambda v: v.repeat_interleave(group, 1)[:, :K]  # noqa: E731
+    A, Q = padded(a.to(DT[t]), pad, DEV)[0], padded(codes, pad, DEV)[0]
+    S, Z = padded(s.to(DT[t]), pad, DEV)[0], padded(z.to(DT[t]), pad, DEV)[0]
+    want = a @ (each(s) * (q - each(z))).t()
+    C, whole = padded(torch.full((M, N), float("nan"), device=DEV), pad, DEV)
+    ops.matmul_w4(A, Q, S, Z, group, C=C)
+    assert untouched(C, whole)
+    assert torch.equal(C, want)
+    ops.matmul_w4(A, Q, S, None, group, C=C, alpha=-2.0, beta=1.0, workspace=torch.empty(1 << 16, dtype=torch.uint8, device=DEV))
+    assert torch.equal(C, -2.0 * (a @ (each(s) * (q - 8.0)).t()) + want)
+    low = ops.matmul_w4(A, Q, S, Z, group)
+    assert torch.equal(low, want.to(DT[t]))
+
+
 def test_w4_every_code_and_zero_point():
     """One element of A against every code and zero point: nothing is rounded before the end."""
     K = 32

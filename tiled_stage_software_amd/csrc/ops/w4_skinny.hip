@@ -18,8 +18,6 @@ namespace gemm {
 namespace {
 
 constexpr int kStep = 128;
-constexpr int kGroups = 128;           // groups of 16 columns in LDS at a time
-constexpr int kGroupRow = kGroups + 1; // apart: rows start on different banks
 
 // CHAIN: instructions of 32 codes that are sure to share a scale (groups are multiples of 32 * CHAIN).
 template <int T, int MT, int WAVES, int CHAIN>
@@ -28,7 +26,9 @@ void w4_skinny_kernel(const W4Params p) {
     constexpr int DEPTH = 2;   // what the registers of four (MT 1) or two waves a SIMD hold
     constexpr int AL = 4 * MT;                 // 16-byte loads of A per step, four rows each
     constexpr int QB = 16 * 64, SLOT = QB + AL * 4 * 256;
-    constexpr int GROUPS = 16 * kGroupRow * 8;           // of each the scale and 1 + z/16 as floats
+    constexpr int NG = WAVES == 16 ? 256 : 128;          // groups of each column in LDS at a time
+    constexpr int GROW = NG + 1;                         // apart: columns start on different banks
+    constexpr int GROUPS = 16 * GROW * 8;              // of each the scale and 1 + z/16 as floats
     __shared__ __attribute__((aligned(1024))) char smem_raw[WAVES * (SLOT > MT * 1024 ? SLOT : MT * 1024) + GROUPS];
     LDS_AS char* slot = (LDS_AS char*)smem_raw + wave_id() * SLOT;
     LDS_AS f32x2* groups = reinterpret_cast<LDS_AS f32x2*>((LDS_AS char*)smem_raw + sizeof(smem_raw) - GROUPS);
@@ -64,7 +64,7 @@ void w4_skinny_kernel(const W4Params p) {
         for (int t = 0; t < 4; ++t) {
             const bool first = t % CHAIN == 0, last = t % CHAIN == CHAIN - 1;
             if (first) {
-                sz = groups[r * kGroupRow + at];
+                sz = groups[r * GROW + at];
                 if (left <= 32 * t) sz = f32x2{0.f, 0.f};
                 in += 32 * CHAIN;
                 if (in >= p.group && left > 32 * (t + CHAIN)) { in = 0; ++at; }
@@ -99,7 +99,7 @@ void w4_skinny_kernel(const W4Params p) {
         __builtin_amdgcn_sched_barrier(0);   // steps mixed by the scheduler would not fit the registers
     };
     // Groups that LDS holds at a time are whole steps; their steps are dealt to the waves.
-    const int64_t span = (int64_t)p.group * kGroups;   // codes (a multiple of 128: kGroups is one of 4)
+    const int64_t span = (int64_t)p.group * NG;   // codes (a multiple of 128)
     for (int64_t k0 = 0; k0 < p.K; k0 += span) {
         const int s0 = (int)(k0 / kStep), s1 = (int)min((k0 + span) / kStep, (int64_t)full);   // whole steps
         if (s1 > s0)
@@ -107,11 +107,11 @@ void w4_skinny_kernel(const W4Params p) {
             for (int d = 0; d < DEPTH; ++d) load(d, min(s0 + w + d * WAVES, s1 - 1));
         if (k0 > 0) lds_barrier();   // every wave is done with the last groups
         const int g0 = (int)(k0 / p.group);
-        const int ng = min(kGroups, (p.K + p.group - 1) / p.group - g0);
-        for (int i = threadIdx.x; i < 16 * ng; i += 64 * WAVES) {
-            const int row = i / ng, c = i % ng;
+        const int ng = min(NG, (p.K + p.group - 1) / p.group - g0);
+        const int row = threadIdx.x / (4 * WAVES);
+        for (int c = threadIdx.x % (4 * WAVES); c < ng; c += 4 * WAVES) {
             const int64_t at = min(n0 + row, (int64_t)p.N - 1) * p.lds + g0 + c;
-            groups[row * kGroupRow + c] = f32x2{to_f32<T>(reinterpret_cast<const uint16_t*>(p.scales)[at]),
+            groups[row * GROW + c] = f32x2{to_f32<T>(reinterpret_cast<const uint16_t*>(p.scales)[at]),
                                                 p.zeros ? zero16<T>(reinterpret_cast<const uint16_t*>(p.zeros)[at]) : kZero16};
         }
         lds_barrier();

@@ -1,0 +1,490 @@
+// w4_tile.hip -- the product with 4-bit weights on large tiles: BM x 128 of C per workgroup, waves
+// of WTM x 32, slabs of 64 k in an LDS ring, v_mfma_f32_16x16x32 on 16 x 16 blocks.
+//
+// No weight is rounded, so a group's scale multiplies an fp32 sum: each accumulator has a second one
+// for the running group, and one pass of two FMAs for each joins them at the group's end.  That and
+// turning codes into operands is vector work beside the matrix cores' (per wave, 128 x 32 tile and
+// 128 k: 1024 cycles of matrix instructions; 4 x 2 x 10 operations for the codes, 2 x 64 for a group's end,
+// four cycles each).  Wide blocks of A's rows keep it below theirs: one turned code serves WTM / 16
+// instructions.  Groups shorter than 64 end with every 32 k, which makes the vector work the bound.
+//
+// A launch before prepares what the group's end needs, so that the ring brings it along with the slabs: the sum of A over
+// each unit (a group; 32 k for short groups), which the zero points multiply, in the order of the
+// accumulators; and scales with zero points, transposed to rows of columns.
+#include "../mfma.hpp"
+#include "w4_common.hpp"
+
+namespace gemm {
+namespace {
+
+constexpr int kSlabK = 64, kBN = 128, kNC = 4;   // kNC: waves that copy
+
+constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct W4Tile {
+    GemmParams g;          // A, C, sizes, tiles; B unused
+    const uint8_t* W;
+    int64_t ldw;
+    const char* sums;      // [unit][tile of M][BM] floats
+    uint32_t sz_at;        // from there: [unit][tile of N][128], scale in the low half, zero point in the high one
+    int per_unit;          // slabs of a unit (0: two units to a slab)
+    int per_split;         // slabs of a split of K
+    int64_t part;          // bytes between the splits' results
+};
+
+template <int BM>
+struct W4Layout {
+    static constexpr int A_BYTES = BM * 128, Q_BYTES = kBN * 32;
+    static constexpr int SL = BM / 16, REGION = (SL + 8) * 16;   // a copying wave's piece of a unit: SL chunks of sums, 8 of scales
+    static constexpr int UNIT = kNC * REGION;
+};
+
+// S1: units are 32 k, two to a slab.
+template <int T, int BM, int WM, bool S1>
+struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, WM, 4, 16> {
+    typedef MfmaCompute<typename Half<T>::type, BM, kBN, 64, WM, 4, 16> C;
+    typedef W4Layout<BM> Y;
+    static constexpr int TM = C::TM, TN = C::TN, AH = TM / 2, NU = S1 ? 2 : 1;
+    static constexpr int STAGE = Y::A_BYTES + Y::Q_BYTES + NU * Y::UNIT;
+    static constexpr int KS = 4;   // steps of a slab: two k-steps by two halves of A's blocks
+    static_assert(TN == 2 && TM % 2 == 0, "waves of 32 columns");
+    f32x4 dot[TM][TN];
+    u32x4 fa[2][AH], b[TN];
+    uint32_t word[TN];
+    u32x4 fsz[NU][TN];
+    f32x4 fsum[NU][TM / 4];
+    uint32_t qo, zo, so;   // LDS offsets of codes, scales and sums within a slot
+    Spread<T> spread;
+    int pos = 0, per_unit, left;   // slab within its unit; slabs left
+
+    __device__ __forceinline__ void init(LDS_AS char* smem_, const W4Tile& p, int slabs) {
+        C::init(smem_);
+        const int w = wave_id(), wm = w / 4, wn = w % 4, lane = lane_id(), r = lane % 16, g = lane / 16;
+        const int kc = (g & 1) * 2 + (g >> 1);   // the k-chunk of lane group g, as in A's fragments
+        qo = (uint32_t)(Y::A_BYTES + (wn * 32 + r) * 32 + kc * 4);
+        const int at = wm * C::WTM + r * TM;     // this lane's sums, TM of them
+        so = (uint32_t)(Y::A_BYTES + Y::Q_BYTES + at / (BM / kNC) * Y::REGION + at % (BM / kNC) * 4);
+        zo = (uint32_t)(Y::A_BYTES + Y::Q_BYTES + wn * Y::REGION + Y::SL * 16 + g * 16);
+        per_unit = p.per_unit;
+        left = slabs;
+    }
+    // Step q: half q % 2 of A's blocks at k-step q / 2, with the codes of the k-step.
+    template <int BUF>
+    __device__ __forceinline__ void frag(int, int slot, int q) {
+        LDS_AS const char* st = this->smem + slot * STAGE;
+#pragma unroll
+        for (int i = 0; i < AH; ++i)
+            fa[BUF][i] = *reinterpret_cast<LDS_AS const u32x4*>(st + this->a_off[q / 2] + (q % 2 * AH + i) * 16 * 128);
+        if (q % 2 == 0) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) word[j] = *reinterpret_cast<LDS_AS const uint32_t*>(st + qo + j * 16 * 32 + q / 2 * 16);
+        }
+        if (q == 1) {   // (before the barrier that frees the slot)
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+#pragma unroll
+                for (int j = 0; j < TN; ++j) fsz[u][j] = *reinterpret_cast<LDS_AS const u32x4*>(st + zo + u * Y::UNIT + j * 64);
+#pragma unroll
+                for (int i = 0; i < TM / 4; ++i) fsum[u][i] = *reinterpret_cast<LDS_AS const f32x4*>(st + so + u * Y::UNIT + i * 16);
+            }
+        }
+    }
+    template <int BUF, bool FIRST>
+    __device__ __forceinline__ void products(int half) {
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int i = 0; i < AH; ++i) {
+                f32x4& d = dot[half * AH + i][j];
+                d = Half<T>::mfma(b[j], fa[BUF][i], FIRST ? zero : d);
+            }
+    }
+    // acc += s * (dot - (1 + z/16) * sum)
+    __device__ __forceinline__ void finish_unit(int u) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            float s[4], z[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[e] = to_f32<T>((uint16_t)fsz[u][j][e]);
+                z[e] = -zero16<T>((uint16_t)(fsz[u][j][e] >> 16));
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    this->acc[i][j][e] = __builtin_fmaf(s[e], __builtin_fmaf(z[e], fsum[u][i / 4][i % 4], dot[i][j][e]), this->acc[i][j][e]);
+        }
+    }
+    template <int BUF>
+    __device__ __forceinline__ void step(int q) {
+        if (q % 2 == 0) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) b[j] = spread.in_order(word[j]);
+        }
+        if (S1) {
+            products<BUF, true>(q % 2);
+            if (q % 2 == 1) finish_unit(q / 2);
+        } else {
+            if (q < 2 && pos == 0) products<BUF, true>(q % 2);
+            else products<BUF, false>(q % 2);
+            if (q == KS - 1) {
+                --left;
+                if (++pos == per_unit || left == 0) {
+                    finish_unit(0);
+                    pos = 0;
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __device__ __forceinline__ void wait_lds() { wait_lgkm0(); }
+    __device__ __forceinline__ void barrier() { gemm::barrier(); }
+};
+
+// Where chunk l of a unit's piece that copying wave w brings lies, in bytes from the sums on.
+template <int BM>
+__device__ __forceinline__ uint32_t unit_chunk(const W4Tile& p, int tm, int tn, int unit, int w, int l) {
+    constexpr int SL = W4Layout<BM>::SL;
+    if (l < SL) return (((uint32_t)unit * p.g.tiles_m + tm) * BM + w * (BM / kNC)) * 4 + l * 16;
+    return p.sz_at + (((uint32_t)unit * p.g.tiles_n + tn) * kBN + w * (kBN / kNC)) * 4 + (l - SL) * 16;
+}
+// First unit of slab s of the whole K.
+__device__ __forceinline__ int unit_of(const W4Tile& p, int s) { return p.per_unit ? s / p.per_unit : 2 * s; }
+
+// Direct global -> LDS copies by the first four waves: 16-byte aligned rows, whole slabs and tiles.
+template <int T, int BM, int WM, bool S1, bool COPY>
+struct W4RingOps : W4Compute<T, BM, WM, S1> {
+    typedef W4Compute<T, BM, WM, S1> F;
+    DirectLoader<BM, 128, kNC, true> la;
+    DirectLoader<kBN, 32, kNC, false> lq;
+    static constexpr int L = decltype(la)::IPW + decltype(lq)::IPW + F::NU;
+    const W4Tile* p;
+    int tm, tn, s0;
+    __device__ __forceinline__ void issue(int slab, int slot, int, int) {
+        if (!COPY) return;
+        LDS_AS char* st = this->smem + slot * F::STAGE;
+        la.issue(slab, st, 0, decltype(la)::IPW);
+        lq.issue(slab, st + F::Y::A_BYTES, 0, decltype(lq)::IPW);
+        const int w = wave_id(), lane = lane_id(), u0 = unit_of(*p, s0 + slab);
+#pragma unroll
+        for (int u = 0; u < F::NU; ++u) {
+            LDS_AS char* to = st + F::Y::A_BYTES + F::Y::Q_BYTES + u * F::Y::UNIT + w * F::Y::REGION;
+            if (lane < F::Y::SL + 8)
+                la.template copy<0>(__builtin_amdgcn_make_buffer_rsrc((void*)p->sums, (short)0, -1, kBufferFlags),
+                                    unit_chunk<BM>(*p, tm, tn, u0 + u, w, lane), 0, to);
+        }
+    }
+    template <int N>
+    __device__ __forceinline__ void wait_slabs() { if (COPY) wait_vm<N * L>(); }
+    template <int BUF, int HAS, int PARTS>
+    __device__ __forceinline__ void math(int q) { this->template step<BUF>(q); }
+};
+
+// Bytes of a chunk moved down by `by`, zeros behind them (16 or more: all zeros).
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int by) {
+    if (by >= 16) return u32x4{0u, 0u, 0u, 0u};
+    return __builtin_bit_cast(u32x4, __builtin_bit_cast(unsigned __int128, v) >> (8 * by));
+}
+
+// Any pitch, alignment and size (K >= 64): 16-byte loads of any alignment into registers, one
+// slab ahead, written into the other slot in the last step but one.  A chunk past a row's end is read
+// as the row's last 16 bytes and shifted.  Rows past the end repeat the last.
+template <int T, int BM, int WM, bool S1>
+struct W4StagedOps : W4Compute<T, BM, WM, S1> {
+    typedef W4Compute<T, BM, WM, S1> F;
+    static constexpr int NT = 256 * WM, STEP = NT / 8, CA = BM / STEP;
+    static constexpr int UT = F::NU * kNC * (F::Y::SL + 8);   // threads with a chunk of the units
+    static_assert(STEP % 16 == 0 && CA * STEP == BM && UT <= NT && 2 * kBN <= NT, "chunks per thread");
+    const char* arow[CA];
+    const uint8_t* qrow;
+    uint32_t uchunk, ustep;
+    uint32_t dst;
+    u32x4 va[CA], vq, vu;
+    const W4Tile* p;
+    int k_bytes, q_bytes, s0, wslot = 0, slab_ = 0;
+    bool ask_write = false;
+    __device__ __forceinline__ void init_rows(const W4Tile& p_, int tm, int tn, int m0, int n0, int s0_) {
+        p = &p_;
+        s0 = s0_;
+        k_bytes = p->g.K * 2;
+        q_bytes = (p->g.K + 1) / 2;
+        const int t = threadIdx.x, row = t / 8, c = t % 8;
+#pragma unroll
+        for (int i = 0; i < CA; ++i) arow[i] = p->g.A + (int64_t)min(m0 + row + i * STEP, p->g.M - 1) * p->g.lda * 2;
+        dst = (uint32_t)(row * 128 + ((c ^ swz<8>(row)) << 4));
+        qrow = p->W + (int64_t)min(n0 + t / 2, p->g.N - 1) * p->ldw;
+        constexpr int PIECE = F::Y::SL + 8;
+        uchunk = unit_chunk<BM>(*p, tm, tn, t < UT ? t / (kNC * PIECE) : 0, t / PIECE % kNC, t % PIECE);
+        ustep = (uint32_t)(t % PIECE < F::Y::SL ? p->g.tiles_m * BM : p->g.tiles_n * kBN) * 4;
+    }
+    __device__ __forceinline__ void load(int slab) {
+        slab_ = s0 + slab;
+        const int ka = min(slab_ * 128 + (int)threadIdx.x % 8 * 16, k_bytes - 16);
+        const int kq = min(slab_ * 32 + (int)threadIdx.x % 2 * 16, q_bytes - 16);
+#pragma unroll
+        for (int i = 0; i < CA; ++i) va[i] = load16(arow[i] + ka);
+        if (NT == 2 * kBN || threadIdx.x < 2 * kBN) vq = load16(qrow + kq);
+        if ((int)threadIdx.x < UT) vu = load16(p->sums + (uchunk + (uint32_t)unit_of(*p, slab_) * ustep));
+        ask_write = true;
+    }
+    __device__ __forceinline__ void put() {
+        LDS_AS char* st = this->smem + wslot * F::STAGE;
+        const int t = threadIdx.x;
+        if ((slab_ + 1) * 128 > k_bytes) {   // the last slab, not filled
+            const int by = slab_ * 128 + t % 8 * 16 + 16 - k_bytes;
+#pragma unroll
+            for (int i = 0; i < CA; ++i) va[i] = by > 0 ? shift_down(va[i], by) : va[i];
+            const int byq = slab_ * 32 + t % 2 * 16 + 16 - q_bytes;
+            vq = byq > 0 ? shift_down(vq, byq) : vq;
+        }
+#pragma unroll
+        for (int i = 0; i < CA; ++i) *reinterpret_cast<LDS_AS u32x4*>(st + dst + i * STEP * 128) = va[i];
+        if (NT == 2 * kBN || t < 2 * kBN) *reinterpret_cast<LDS_AS u32x4*>(st + F::Y::A_BYTES + t * 16) = vq;
+        if (t < UT) *reinterpret_cast<LDS_AS u32x4*>(st + F::Y::A_BYTES + F::Y::Q_BYTES + t * 16) = vu;
+        ask_write = false;
+        wslot ^= 1;
+    }
+    __device__ __forceinline__ void write(int, int) {
+        if (ask_write) put();   // (only slab 0 has not been written by math())
+    }
+    template <int BUF, int HAS, int PARTS>
+    __device__ __forceinline__ void math(int q) {
+        this->template step<BUF>(q);
+        if (q == F::KS - 2 && ask_write) put();
+    }
+};
+
+// Splits of K (blockIdx.y) store plain sums, each into its own buffer.
+template <int T, int OUT, int BM, int WM, bool S1, bool DIRECT>
+__global__ __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(2)))
+void w4_tile_kernel(W4Tile p) {
+    typedef W4Compute<T, BM, WM, S1> F;
+    constexpr int S = DIRECT ? 3 : 2;
+    __shared__ __attribute__((aligned(1024))) char smem_raw[S * F::STAGE];
+    LDS_AS char* smem = (LDS_AS char*)smem_raw;
+    int tm, tn;
+    tile_coords(p.g, tm, tn);
+    const int m_keep = tm * BM, n_keep = tn * kBN;
+    const int m0 = max(0, min(m_keep, p.g.M - BM)), n0 = max(0, min(n_keep, p.g.N - kBN));
+    const int s0 = (int)blockIdx.y * p.per_split;
+    const int slabs = min((p.g.K + kSlabK - 1) / kSlabK - s0, p.per_split);
+    p.g.C += (int64_t)blockIdx.y * p.part;
+    if constexpr (DIRECT) {
+        auto run = [&](auto& ops) {
+            ops.init(smem, p, slabs);
+            ops.p = &p; ops.tm = tm; ops.tn = tn; ops.s0 = s0;
+            ops.la.init(p.g.A + ((int64_t)m0 * p.g.lda + (int64_t)s0 * kSlabK) * 2, p.g.lda * 2, kSlabK * 2);
+            ops.lq.init(reinterpret_cast<const char*>(p.W) + (int64_t)n0 * p.ldw + (int64_t)s0 * (kSlabK / 2), p.ldw, kSlabK / 2);
+            gemm_sched::ring_mainloop<S, F::KS, 1>(ops, slabs);
+            ops.template epilogue<OUT>(p.g, m0, n0, m_keep, n_keep);
+        };
+        if (WM == 1 || wave_id() < kNC) {
+            W4RingOps<T, BM, WM, S1, true> ops;
+            run(ops);
+        } else if constexpr (WM > 1) {
+            W4RingOps<T, BM, WM, S1, false> ops;
+            run(ops);
+        }
+    } else {
+        W4StagedOps<T, BM, WM, S1> ops;
+        ops.init(smem, p, slabs);
+        ops.init_rows(p, tm, tn, m0, n0, s0);
+        gemm_sched::staged_mainloop<S, F::KS>(ops, slabs);
+        ops.template epilogue<OUT>(p.g, m0, n0, m_keep, n_keep);
+    }
+}
+
+// Sums of A over units and the transposed scales.  Four lanes sum a unit of a row, 32 elements a turn; the
+// threads behind those move a scale each.
+struct W4Prepare {
+    const char* A;
+    const uint16_t* scales;
+    const uint16_t* zeros;
+    float* sums;
+    uint32_t* sz;
+    int64_t lda, lds;
+    int M, N, K, group, unit, units, tiles_m, tiles_n, bm, tm;   // tm: blocks of 16 rows of a wave's tile
+    int64_t sum_blocks;
+};
+template <int T>
+__global__ __launch_bounds__(256) void w4_prepare_kernel(const W4Prepare p) {
+    if ((int64_t)blockIdx.x < p.sum_blocks) {
+        const int64_t id = (int64_t)blockIdx.x * 64 + threadIdx.x / 4;   // (row of a tile, unit), the unit first
+        const int64_t rows = (int64_t)p.tiles_m * p.bm;
+        if (id >= rows * p.units) return;
+        const int64_t row = id / p.units;
+        const int u = (int)(id % p.units), tile = (int)(row / p.bm), local = (int)(row % p.bm);
+        const int m = min(max(0, min(tile * p.bm, p.M - p.bm)) + local, p.M - 1);
+        const char* a = p.A + (int64_t)m * p.lda * 2;
+        float sum = 0.0f;
+        const int end = (int)min((int64_t)(u + 1) * p.unit, (int64_t)p.K);
+        for (int k = u * p.unit + (int)threadIdx.x % 4 * 8; k < end; k += 32) {
+            const u32x4 v = load_a(a, k, p.K);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum += to_f32<T>((uint16_t)v[e]) + to_f32<T>((uint16_t)(v[e] >> 16));
+        }
+        sum += __shfl_xor(sum, 1, 64);
+        sum += __shfl_xor(sum, 2, 64);
+        const int wt = p.tm * 16;   // rows of a wave's tile: its lanes have tm sums each, side by side
+        if (threadIdx.x % 4 == 0)
+            p.sums[(int64_t)u * rows + (int64_t)tile * p.bm + local / wt * wt + local % 16 * p.tm + local % wt / 16] = sum;
+        return;
+    }
+    const int64_t id = ((int64_t)blockIdx.x - p.sum_blocks) * 256 + threadIdx.x, cols = (int64_t)p.tiles_n * kBN;
+    if (id >= cols * p.units) return;
+    const int u = (int)(id / cols), at = (int)(id % cols);
+    const int n = min(max(0, min(at / kBN * kBN, p.N - kBN)) + at % kBN, p.N - 1);
+    uint32_t v = 0;   // a unit past the end: A is zero there
+    if ((int64_t)u * p.unit < p.K) {
+        const int64_t i = n * p.lds + (int64_t)u * p.unit / p.group;
+        const uint16_t eight = T == DT_BF16 ? 0x4100 : 0x4800;
+        v = p.scales[i] | (uint32_t)(p.zeros ? p.zeros[i] : eight) << 16;
+    }
+    p.sz[id] = v;
+}
+
+// C = alpha * (sum of the splits, in order) + beta * C
+template <int OUT>
+__global__ __launch_bounds__(256) void w4_join_kernel(const GemmParams p, const char* part, int64_t each, int ldp, int splits) {
+    const int64_t quads = ldp / 4, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (id >= quads * p.M) return;
+    const int64_t m = id / quads;
+    const int n = (int)(id % quads) * 4;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = 0; i < splits; ++i) s += *reinterpret_cast<const f32x4*>(part + i * each + (m * ldp + n) * 4);
+    store4<OUT>(p, m, n, s);
+}
+
+struct W4Plan {
+    int bm, splits, unit, units, per_split;
+    int64_t slabs, tiles_m, tiles_n;
+    size_t sums, sz, parts;   // bytes of the workspace's pieces
+};
+size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
+int64_t ldp_of(int64_t N) { return (N + 3) / 4 * 4; }
+
+// 64 rows a tile where that holds all of A, 256 where such tiles fill the card, else 128.
+W4Plan w4_plan(int64_t M, int64_t N, int64_t K, int64_t group, size_t room) {
+    W4Plan q;
+    const int64_t cu = num_compute_units();
+    q.bm = M <= 64 ? 64 : M <= 128 || ceil_div(M, 256) * ceil_div(N, kBN) < cu ? 128 : 256;
+    q.tiles_m = ceil_div(M, q.bm);
+    q.tiles_n = ceil_div(N, kBN);
+    q.slabs = ceil_div(K, kSlabK);
+    q.unit = group % kSlabK == 0 ? (int)group : 32;
+    q.units = (int)(q.unit == 32 ? 2 * q.slabs : ceil_div(K, group));
+    q.sums = round256((size_t)q.units * q.tiles_m * q.bm * 4);
+    q.sz = round256((size_t)q.units * q.tiles_n * kBN * 4);
+    // splits end with a unit, keep at least eight slabs and fill two workgroups a compute unit at most
+    const int64_t per_unit = q.unit == 32 ? 1 : group / kSlabK, tiles = q.tiles_m * q.tiles_n, each = M * ldp_of(N) * 4;
+    int64_t s = tiles * 2 <= cu ? (q.bm == 256 ? 1 : 2) * cu / tiles : 1;
+    s = s < q.slabs / 8 ? s : q.slabs / 8;
+    s = s < 16 ? s : 16;
+    while (s > 1 && q.sums + q.sz + (size_t)(s * each) > room) --s;
+    if (s < 1) s = 1;
+    q.per_split = (int)(ceil_div(ceil_div(q.slabs, s), per_unit) * per_unit);
+    q.splits = (int)ceil_div(q.slabs, q.per_split);
+    q.parts = q.splits > 1 ? (size_t)(q.splits * each) : 0;
+    return q;
+}
+
+template <int T, int OUT, int BM, int WM>
+hipError_t tile_of(const W4Tile& t, bool short_units, bool direct, int splits, hipStream_t st) {
+    const dim3 grid((unsigned)(t.g.tiles_m * t.g.tiles_n), (unsigned)splits), block(256 * WM);
+    if (short_units) {
+        if (direct) hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, WM, true, true>), grid, block, 0, st, t);
+        else hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, WM, true, false>), grid, block, 0, st, t);
+    } else {
+        if (direct) hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, WM, false, true>), grid, block, 0, st, t);
+        else hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, WM, false, false>), grid, block, 0, st, t);
+    }
+    return hipGetLastError();
+}
+template <int T, int OUT>
+hipError_t out_of(const W4Plan& q, const W4Tile& t, bool direct, hipStream_t st) {
+    const bool s1 = q.unit == 32;
+    if (q.bm == 256) return tile_of<T, OUT, 256, 2>(t, s1, direct, q.splits, st);
+    if (q.bm == 128) return tile_of<T, OUT, 128, 1>(t, s1, direct, q.splits, st);
+    return tile_of<T, OUT, 64, 1>(t, s1, direct, q.splits, st);
+}
+
+template <int T>
+hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, hipStream_t st) {
+    W4Prepare a = {};
+    a.A = f.A;
+    a.scales = reinterpret_cast<const uint16_t*>(f.scales);
+    a.zeros = reinterpret_cast<const uint16_t*>(f.zeros);
+    a.sums = reinterpret_cast<float*>(ws);
+    a.sz = reinterpret_cast<uint32_t*>(ws + q.sums);
+    a.lda = f.lda; a.lds = f.lds;
+    a.M = f.M; a.N = f.N; a.K = f.K; a.group = f.group;
+    a.unit = q.unit; a.units = q.units;
+    a.tiles_m = (int)q.tiles_m; a.tiles_n = (int)q.tiles_n;
+    a.bm = q.bm; a.tm = q.bm == 64 ? 4 : 8;
+    a.sum_blocks = ceil_div(q.tiles_m * q.bm * q.units, 64);
+    hipLaunchKernelGGL(w4_prepare_kernel<T>, dim3((unsigned)(a.sum_blocks + ceil_div(q.tiles_n * kBN * q.units, 256))), dim3(256), 0, st, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    W4Tile t = {};
+    GemmParams& p = t.g;
+    p.A = f.A;
+    p.C = f.C;
+    p.lda = f.lda; p.ldc = f.ldc;
+    p.M = f.M; p.N = f.N; p.K = f.K;
+    p.alpha = 16.0f * f.alpha;   // the codes are sixteenths
+    p.beta = f.beta;
+    p.out_type = f.out_type;
+    p.tiles_m = (int)q.tiles_m; p.tiles_n = (int)q.tiles_n;
+    p.group_m = 8;
+    p.xcd_remap = 1;
+    t.W = f.W;
+    t.ldw = f.ldw;
+    t.sums = ws;
+    t.sz_at = (uint32_t)q.sums;
+    t.per_unit = q.unit == 32 ? 0 : q.unit / kSlabK;
+    t.per_split = q.per_split;
+    const bool direct = f.M >= q.bm && f.N >= kBN && f.K % kSlabK == 0 && f.lda % 8 == 0 && f.ldw % 16 == 0 &&
+                        ((uintptr_t)f.A | (uintptr_t)f.W) % 16 == 0 && f.lda <= (1 << 21) && f.ldw <= (1 << 22);
+    if (q.splits > 1) {
+        const GemmParams whole = p;
+        const int64_t ldp = ldp_of(f.N);
+        char* parts = ws + q.sums + q.sz;
+        t.part = f.M * ldp * 4;
+        p.C = parts;
+        p.ldc = ldp;
+        p.alpha = 1.0f;
+        p.beta = 0.0f;
+        e = out_of<T, DT_F32>(q, t, direct, st);
+        if (e != hipSuccess) return e;
+        const dim3 grid((unsigned)ceil_div(f.M * ldp / 4, 256));
+        if (f.out_type == DT_F32) hipLaunchKernelGGL(w4_join_kernel<DT_F32>, grid, dim3(256), 0, st, whole, parts, t.part, (int)ldp, q.splits);
+        else hipLaunchKernelGGL(w4_join_kernel<T>, grid, dim3(256), 0, st, whole, parts, t.part, (int)ldp, q.splits);
+        return hipGetLastError();
+    }
+    return f.out_type == DT_F32 ? out_of<T, DT_F32>(q, t, direct, st) : out_of<T, T>(q, t, direct, st);
+}
+
+}  // namespace
+
+size_t w4_tile_workspace(int64_t M, int64_t N, int64_t K, int64_t group) {
+    const W4Plan q = w4_plan(M, N, K, group, ~size_t(0) >> 1);
+    return q.sums + q.sz + q.parts;
+}
+
+// K that the staged loads hold, grids and 32-bit offsets in range, and a workspace for the sums and scales.
+bool w4_tile_fits(const W4Params& f, size_t ws_bytes) {
+    if (f.K < kSlabK || f.K > (1 << 29)) return false;
+    const W4Plan q = w4_plan(f.M, f.N, f.K, f.group, ws_bytes);
+    return q.sums + q.sz + q.parts <= ws_bytes && q.tiles_m * q.tiles_n < (int64_t(1) << 22) &&
+           (q.sums + q.sz) / 4 < (size_t(1) << 30);
+}
+
+hipError_t launch_w4_tile(int in_type, const W4Params& f, void* ws, size_t ws_bytes, hipStream_t st) {
+    const W4Plan q = w4_plan(f.M, f.N, f.K, f.group, ws_bytes);
+    return in_type == DT_BF16 ? run_tiles<DT_BF16>(f, q, static_cast<char*>(ws), st) : run_tiles<DT_F16>(f, q, static_cast<char*>(ws), st);
+}
+
+}  // namespace gemm
