@@ -182,37 +182,68 @@ __device__ __forceinline__ u32x4 add_residual(const u32x4& x, const u32x4& r) {
     return Elem<T>::pack(f);
 }
 
-// WPR waves per row, RPG rows per workgroup of 64*WPR*RPG threads.
-template <int T, int WPR, int RPG, int V>
+// V vectors of weights from element c on, TPR vectors apart, as they lie in memory (WT: T or DT_F32); `c` of a vector
+// past the end is its row's last.
+template <int T, int WT>
+struct Weights {
+    static constexpr int VE = Elem<T>::VE, N = WT == T ? 1 : 2;   // 16-byte loads for VE weights
+    u32x4 raw[N];
+    __device__ __forceinline__ void load(const char* w, int c) {
+        if (!w) return;
+#pragma unroll
+        for (int q = 0; q < N; ++q) raw[q] = load16(w + (int64_t)c * (WT == DT_F32 ? 4 : 2) + 16 * q);
+    }
+    __device__ __forceinline__ float get(bool ones, int e) const {
+        return ones ? 1.0f : Elem<WT>::get(raw[e / Elem<WT>::VE], e % Elem<WT>::VE);
+    }
+};
+
+// WPR waves per row, RPG rows per workgroup of 64*WPR*RPG threads; rows of VE elements at least.
+//
+// No load stands behind a branch: a vector past the row's end, or across it, is the row's last VE elements,
+// and what other threads have of it is left out of the sums (and stored twice, as the same
+// value; every load of a row comes before its first store).  The weights stay in registers over the rows
+// of a workgroup; y is computed once for its largest magnitude and once more to be written, which
+// holds fewer registers than keeping it: 16 rather than 4 waves a compute unit for rows of 8192 (353 -> ... us).
+template <int T, bool F8, int WT, int WPR, int RPG, int V>
 __global__ __launch_bounds__(64 * WPR * RPG) void norm_kernel(const NormParams p) {
     constexpr int VE = Elem<T>::VE, SZ = Elem<T>::SIZE, TPR = 64 * WPR;
     static_assert(WPR == 1 || RPG == 1, "rows that share a workgroup have a wave each: no barrier in their loop");
     __shared__ float sums[2][WPR], wide[2][WPR];
     __shared__ uint32_t maxs[2][WPR];
     const int t = threadIdx.x % TPR;
+    auto own = [&](int i) { return (t + i * TPR) * VE; };                 // this thread's elements ...
+    auto from = [&](int i) { return min(own(i), p.cols - VE); };          // ... and where it reads them
+    auto whole = [&](int i) { return (i + 1) * TPR * VE <= p.cols; };     // every thread has all of its vector
+    const bool ones = p.w == nullptr;
+    Weights<T, WT> w[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[i].load(p.w, from(i));
     int turn = 0;   // the LDS words alternate, so a row's writes never meet the previous row's reads
     for (int64_t row = (int64_t)blockIdx.x * RPG + threadIdx.x / TPR; row < p.rows; row += (int64_t)gridDim.x * RPG) {
         u32x4 v[V];
         const char* xr = p.x + row * p.ldx * SZ;
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = load_vec<T>(xr, (t + i * TPR) * VE, p.cols);
+        for (int i = 0; i < V; ++i) v[i] = load16(xr + (int64_t)from(i) * SZ);
         if (p.r) {
             u32x4 r[V];
             const char* rr = p.r + row * p.ldr * SZ;
 #pragma unroll
-            for (int i = 0; i < V; ++i) r[i] = load_vec<T>(rr, (t + i * TPR) * VE, p.cols);
+            for (int i = 0; i < V; ++i) r[i] = load16(rr + (int64_t)from(i) * SZ);
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = add_residual<T>(v[i], r[i]);
         }
         auto squares = [&](float by) {
             float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int i = 0; i < V; ++i) {
+                const int first = whole(i) ? 0 : own(i) - from(i);   // elements before it are other threads'
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    const float f = by * Elem<T>::get(v[i], e);
+                    const float f = e >= first ? by * Elem<T>::get(v[i], e) : 0.0f;
                     sum = __builtin_fmaf(f, f, sum);
                 }
+            }
             return sum;
         };
         const float rstd = row_rstd(row_sum<WPR>(squares(1.0f), sums[turn]), p.cols, p.eps,
@@ -222,50 +253,33 @@ __global__ __launch_bounds__(64 * WPR * RPG) void norm_kernel(const NormParams p
             char* hr = p.h + row * p.ldh * SZ;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if ((t + i * TPR) * VE < p.cols) store_vec<T>(hr, (t + i * TPR) * VE, p.cols, v[i]);
+                if (own(i) < p.cols) store16(hr + (int64_t)from(i) * SZ, v[i]);
         }
-        char* yr = p.y + row * p.ldy * y_size(p.y_type);
-        if (p.y_type != DT_F8E4M3) {
+        auto y = [&](int i, int e) { return w[i].get(ones, e) * (Elem<T>::get(v[i], e) * rstd); };
+        float inv = 1.0f;
+        if constexpr (F8) {
+            uint32_t amax = 0;   // (what is read twice is in the row anyway)
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = (t + i * TPR) * VE;
-                if (c < p.cols) {
-                    float f[VE];
-                    load_weights<VE>(p.w, p.w_type, c, p.cols, f);
+            for (int i = 0; i < V; ++i)
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) f[e] *= Elem<T>::get(v[i], e) * rstd;
-                    store_y<VE>(yr, p.y_type, c, p.cols, f);
+                for (int e = 0; e < VE; ++e) {
+                    const uint32_t b = __float_as_uint(y(i, e)) & 0x7fffffffu;
+                    amax = b > amax ? b : amax;
                 }
-            }
-        } else {
-            float f[V][VE];
-            uint32_t amax = 0;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = (t + i * TPR) * VE;
-                if (c < p.cols) {
-                    load_weights<VE>(p.w, p.w_type, c, p.cols, f[i]);
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        f[i][e] *= Elem<T>::get(v[i], e) * rstd;
-                        const uint32_t b = __float_as_uint(f[i][e]) & 0x7fffffffu;
-                        if (c + e < p.cols) amax = b > amax ? b : amax;
-                    }
-                }
-            }
             const float s = row_scale(row_max<WPR>(amax, maxs[turn]));
-            const float inv = 1.0f / s;
+            inv = 1.0f / s;
             if (t == 0) p.scale[row] = s;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = (t + i * TPR) * VE;
-                if (c < p.cols) {
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) f[i][e] *= inv;
-                    store_y<VE>(yr, p.y_type, c, p.cols, f[i]);
-                }
-            }
         }
+        const int yt = F8 ? (int)DT_F8E4M3 : p.y_type;
+        char* yr = p.y + row * p.ldy * y_size(yt);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (own(i) < p.cols) {
+                float f[VE];
+#pragma unroll
+                for (int e = 0; e < VE; ++e) f[e] = F8 ? y(i, e) * inv : y(i, e);
+                store_y<VE>(yr, yt, from(i), p.cols, f);
+            }
         turn ^= 1;
     }
 }
@@ -340,36 +354,49 @@ __global__ __launch_bounds__(kLoopThreads) void norm_loop_kernel(const NormParam
 
 constexpr int64_t kMaxGrid = 1 << 20;   // workgroups of a launch; more rows loop
 
-template <int T, int WPR, int RPG, int V>
+// Workgroups that stay on the card with a row's worth of registers; each then takes every so many rows.
+constexpr int kResident = 8;
+template <int T, bool F8, int WT, int WPR, int RPG, int V>
 hipError_t go(const NormParams& p, hipStream_t st) {
     int64_t grid = (p.rows + RPG - 1) / RPG;
-    if (grid > kMaxGrid) grid = kMaxGrid;
-    hipLaunchKernelGGL((norm_kernel<T, WPR, RPG, V>), dim3((unsigned)grid), dim3(64 * WPR * RPG), 0, st, p);
+    const int64_t most = (int64_t)num_compute_units() * kResident;
+    if (grid > most) grid = most;
+    hipLaunchKernelGGL((norm_kernel<T, F8, WT, WPR, RPG, V>), dim3((unsigned)grid), dim3(64 * WPR * RPG), 0, st, p);
     return hipGetLastError();
 }
 
-template <int T>
+template <int T, bool F8, int WT>
 hipError_t norm_of(const NormParams& p, hipStream_t st) {
     const int64_t vecs = ((int64_t)p.cols + Elem<T>::VE - 1) / Elem<T>::VE;
-    if (vecs <= 64) return go<T, 1, 4, 1>(p, st);
-    if (vecs <= 128) return go<T, 1, 4, 2>(p, st);
-    if (vecs <= 256) return go<T, 4, 1, 1>(p, st);
-    if (vecs <= 512) return go<T, 4, 1, 2>(p, st);
-    if (vecs <= 1024) return go<T, 4, 1, 4>(p, st);
-    if (vecs <= 2048) return go<T, 8, 1, 4>(p, st);
-    if (vecs <= 4096) return go<T, 16, 1, 4>(p, st);
+    if (p.cols >= Elem<T>::VE) {
+        if (vecs <= 64) return go<T, F8, WT, 1, 4, 1>(p, st);
+        if (vecs <= 128) return go<T, F8, WT, 1, 4, 2>(p, st);
+        if (vecs <= 256) return go<T, F8, WT, 4, 1, 1>(p, st);
+        if (vecs <= 512) return go<T, F8, WT, 4, 1, 2>(p, st);
+        if (vecs <= 1024) return go<T, F8, WT, 4, 1, 4>(p, st);
+        if (vecs <= 2048) return go<T, F8, WT, 8, 1, 4>(p, st);
+        if (vecs <= 4096) return go<T, F8, WT, 16, 1, 4>(p, st);
+    }
     hipLaunchKernelGGL((norm_loop_kernel<T>), dim3((unsigned)(p.rows > kMaxGrid ? kMaxGrid : p.rows)),
                        dim3(kLoopThreads), 0, st, p);
     return hipGetLastError();
+}
+template <int T>
+hipError_t norm_in(const NormParams& p, hipStream_t st) {
+    const bool f8 = p.y_type == DT_F8E4M3;
+    if constexpr (T != DT_F32) {
+        if (p.w && p.w_type == DT_F32) return f8 ? norm_of<T, true, DT_F32>(p, st) : norm_of<T, false, DT_F32>(p, st);
+    }
+    return f8 ? norm_of<T, true, T>(p, st) : norm_of<T, false, T>(p, st);
 }
 
 }  // namespace
 
 hipError_t launch_norm(int in_type, const NormParams& p, hipStream_t st) {
     switch (in_type) {
-        case DT_F32: return norm_of<DT_F32>(p, st);
-        case DT_BF16: return norm_of<DT_BF16>(p, st);
-        case DT_F16: return norm_of<DT_F16>(p, st);
+        case DT_F32: return norm_in<DT_F32>(p, st);
+        case DT_BF16: return norm_in<DT_BF16>(p, st);
+        case DT_F16: return norm_in<DT_F16>(p, st);
     }
     return hipErrorInvalidValue;
 }
@@ -383,18 +410,23 @@ hipError_t launch_norm(int in_type, const NormParams& p, hipStream_t st) {
 // order, so the result is the same on every run.
 namespace {
 
-template <int T, int WPR, int RPG, int V>
+// Vectors past or across a row's end are read as in norm_kernel.
+template <int T, int WT, int WPR, int RPG, int V>
 __global__ __launch_bounds__(64 * WPR * RPG) void norm_bwd_kernel(const NormBwdParams p) {
     constexpr int VE = Elem<T>::VE, SZ = Elem<T>::SIZE, TPR = 64 * WPR;
     static_assert(WPR == 1 || RPG == 1, "rows that share a workgroup have a wave each: no barrier in their loop");
     __shared__ float sums[2][WPR];
     __shared__ float join[RPG > 1 ? (RPG - 1) * TPR * V * VE : 1];
     const int t = threadIdx.x % TPR;
+    auto own = [&](int i) { return (t + i * TPR) * VE; };
+    auto from = [&](int i) { return min(own(i), p.cols - VE); };
+    auto whole = [&](int i) { return (i + 1) * TPR * VE <= p.cols; };
+    const bool ones = p.w == nullptr;
     float acc[V][VE];
-    float w[V][VE];
+    Weights<T, WT> w[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        load_weights<VE>(p.w, p.w_type, (t + i * TPR) * VE, p.cols, w[i]);
+        w[i].load(p.w, from(i));
 #pragma unroll
         for (int e = 0; e < VE; ++e) acc[i][e] = 0.0f;
     }
@@ -404,41 +436,39 @@ __global__ __launch_bounds__(64 * WPR * RPG) void norm_bwd_kernel(const NormBwdP
         const char* yr = p.dy + row * p.lddy * SZ;
         const char* hr = p.h + row * p.ldh * SZ;
 #pragma unroll
-        for (int i = 0; i < V; ++i) dy[i] = load_vec<T>(yr, (t + i * TPR) * VE, p.cols);
+        for (int i = 0; i < V; ++i) dy[i] = load16(yr + (int64_t)from(i) * SZ);
 #pragma unroll
-        for (int i = 0; i < V; ++i) h[i] = load_vec<T>(hr, (t + i * TPR) * VE, p.cols);
+        for (int i = 0; i < V; ++i) h[i] = load16(hr + (int64_t)from(i) * SZ);
         if (p.dh) {
             const char* dr = p.dh + row * p.lddh * SZ;
 #pragma unroll
-            for (int i = 0; i < V; ++i) dh[i] = load_vec<T>(dr, (t + i * TPR) * VE, p.cols);
+            for (int i = 0; i < V; ++i) dh[i] = load16(dr + (int64_t)from(i) * SZ);
         }
         const float rstd = p.rstd[row];
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V; ++i) {
+            const int first = whole(i) ? 0 : own(i) - from(i);   // elements before it are other threads'
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                const float d = Elem<T>::get(dy[i], e), u = Elem<T>::get(h[i], e) * rstd;
-                const float du = d * u;
+                const float du = e >= first ? Elem<T>::get(dy[i], e) * (Elem<T>::get(h[i], e) * rstd) : 0.0f;
                 acc[i][e] += du;
-                sum = __builtin_fmaf(du, w[i][e], sum);
+                sum = __builtin_fmaf(du, w[i].get(ones, e), sum);
             }
+        }
         const float mean = row_sum<WPR>(sum, sums[turn]) / (float)p.cols;
         char* xr = p.dx + row * p.lddx * SZ;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (t + i * TPR) * VE;
-            if (c < p.cols) {
+        for (int i = 0; i < V; ++i)
+            if (own(i) < p.cols) {
                 float f[VE];
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    const float d = Elem<T>::get(dy[i], e), u = Elem<T>::get(h[i], e) * rstd;
-                    f[e] = rstd * (d * w[i][e] - u * mean);
+                    f[e] = rstd * (Elem<T>::get(dy[i], e) * w[i].get(ones, e) - Elem<T>::get(h[i], e) * rstd * mean);
                     if (p.dh) f[e] += Elem<T>::get(dh[i], e);
                 }
-                store_vec<T>(xr, c, p.cols, Elem<T>::pack(f));
+                store16(xr + (int64_t)from(i) * SZ, Elem<T>::pack(f));
             }
-        }
         turn ^= 1;
     }
     if (!p.dw) return;
@@ -463,8 +493,14 @@ __global__ __launch_bounds__(64 * WPR * RPG) void norm_bwd_kernel(const NormBwdP
     float* out = gridDim.x == 1 ? p.dw : p.part + (int64_t)blockIdx.x * p.cols;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = (t + i * TPR) * VE;
-        if (c < p.cols) store_y<VE>(reinterpret_cast<char*>(out), DT_F32, c, p.cols, acc[i]);
+        if (own(i) + VE <= p.cols) {
+            store_y<VE>(reinterpret_cast<char*>(out), DT_F32, own(i), p.cols, acc[i]);
+        } else {   // what this thread alone has of the row's last vector
+            const int first = own(i) - from(i);
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+                if (e >= first) out[from(i) + e] = acc[i][e];
+        }
     }
 }
 
@@ -545,10 +581,26 @@ __global__ __launch_bounds__(256) void zero_kernel(float* p, int n) {
     if (i < n) p[i] = 0.0f;
 }
 
-template <int T, int WPR, int RPG, int V>
+template <int T, int WT, int WPR, int RPG, int V>
 hipError_t go_bwd(const NormBwdParams& p, hipStream_t st) {
-    hipLaunchKernelGGL((norm_bwd_kernel<T, WPR, RPG, V>), dim3(p.parts), dim3(64 * WPR * RPG), 0, st, p);
+    hipLaunchKernelGGL((norm_bwd_kernel<T, WT, WPR, RPG, V>), dim3(p.parts), dim3(64 * WPR * RPG), 0, st, p);
     return hipGetLastError();
+}
+// Vectors of 16 bytes that the registers hold of a row (fp32 has half the sums of dw to keep).
+template <int T>
+constexpr int64_t kBwdVecs = T == DT_F32 ? 4096 : 2048;
+
+template <int T, int WT>
+hipError_t bwd_rows(const NormBwdParams& p, int64_t vecs, hipStream_t st) {
+    if (vecs <= 64) return go_bwd<T, WT, 1, 4, 1>(p, st);
+    if (vecs <= 128) return go_bwd<T, WT, 1, 4, 2>(p, st);
+    if (vecs <= 256) return go_bwd<T, WT, 4, 1, 1>(p, st);
+    if (vecs <= 512) return go_bwd<T, WT, 4, 1, 2>(p, st);
+    if (vecs <= 1024) return go_bwd<T, WT, 8, 1, 2>(p, st);
+    if constexpr (T == DT_F32) {
+        if (vecs > 2048) return go_bwd<T, WT, 16, 1, 4>(p, st);
+    }
+    return go_bwd<T, WT, 16, 1, 2>(p, st);
 }
 
 template <int T>
@@ -559,12 +611,10 @@ hipError_t bwd_of(const NormBwdParams& p, hipStream_t st) {
     }
     const int64_t vecs = ((int64_t)p.cols + Elem<T>::VE - 1) / Elem<T>::VE;
     hipError_t e;
-    if (vecs <= 64) e = go_bwd<T, 1, 4, 1>(p, st);
-    else if (vecs <= 128) e = go_bwd<T, 1, 4, 2>(p, st);
-    else if (vecs <= 256) e = go_bwd<T, 4, 1, 1>(p, st);
-    else if (vecs <= 512) e = go_bwd<T, 4, 1, 2>(p, st);
-    else if (vecs <= 1024) e = go_bwd<T, 8, 1, 2>(p, st);
-    else if (vecs <= 2048) e = go_bwd<T, 16, 1, 2>(p, st);
+    if (p.cols >= Elem<T>::VE && vecs <= kBwdVecs<T>) {
+        if (p.w && p.w_type == DT_F32) e = bwd_rows<T, DT_F32>(p, vecs, st);
+        else e = bwd_rows<T, T>(p, vecs, st);
+    }
     else {
         e = hipSuccess;
         if (p.dw) {
@@ -588,7 +638,8 @@ hipError_t bwd_of(const NormBwdParams& p, hipStream_t st) {
 int norm_bwd_parts(int in_type, int64_t rows, int cols) {
     const int ve = in_type == DT_F32 ? 4 : 8;
     const int64_t vecs = ((int64_t)cols + ve - 1) / ve;
-    if (vecs > 2048) return (int)(rows < 64 ? (rows < 1 ? 1 : rows) : 64);   // looping kernels: slices of the rows
+    if (cols < ve || vecs > (in_type == DT_F32 ? kBwdVecs<DT_F32> : kBwdVecs<DT_BF16>))   // looping kernels: slices of the rows
+        return (int)(rows < 64 ? (rows < 1 ? 1 : rows) : 64);
     const int per = vecs <= 128 ? 4 : 1;
     const int64_t groups = (rows + per - 1) / per;
     const int64_t most = 512;
