@@ -9,6 +9,8 @@
 // registers beside the 128 accumulators; so a slab is cut along M instead of K: step s multiplies AH
 // blocks of A's rows with all of the wave's B, only A's fragments are doubled, and B's are
 // read anew for the next slab in the last step, each right after its last use.
+#include <algorithm>
+
 #include "../mfma.hpp"
 #include "f8_common.hpp"
 
@@ -109,7 +111,7 @@ struct F8Compute : MfmaCompute<__bf16, BM, BN, 64, WM, WN, 16> {
 };
 
 // Direct global -> LDS copies by the first NC waves: 16-byte aligned rows, whole slabs and tiles.
-template <int BM, int BN, int WM, int WN, int KS, bool WIDE, int NC, bool COPY>
+template <int S, int BM, int BN, int WM, int WN, int KS, bool WIDE, int NC, bool COPY>
 struct F8RingOps : F8Compute<BM, BN, WM, WN, KS, WIDE> {
     typedef F8Compute<BM, BN, WM, WN, KS, WIDE> F;
     DirectLoader<BM, kSlabBytes, NC, true> la;
@@ -125,7 +127,7 @@ struct F8RingOps : F8Compute<BM, BN, WM, WN, KS, WIDE> {
     // the prologue's slabs go out at once, the others between the next math()'s products
     __device__ __forceinline__ void issue(int slab, int slot, int, int) {
         if (!COPY) return;
-        if (slab < 2) { copies(slab, slot, 0, L); return; }
+        if (slab < S) { copies(slab, slot, 0, L); return; }
         slab_ = slab; slot_ = slot; ask_copy = true;
     }
     template <int N>
@@ -140,7 +142,7 @@ struct F8RingOps : F8Compute<BM, BN, WM, WN, KS, WIDE> {
     }
 };
 
-// Any pitch, alignment and K >= 128: 16-byte loads of any alignment into registers, one slab ahead,
+// Any pitch, alignment and K >= 128: 16-byte loads of any alignment into registers, AHEAD slabs ahead,
 // written into the other slot in the last step but one.  A last slab that K does not fill is
 // the row's last 128 bytes, with zeros in A for what earlier slabs had.  Rows past the end
 // repeat the last (CLAMP), or there are none: the tile lies inside both operands.
@@ -155,9 +157,9 @@ struct F8StagedOps : F8Compute<BM, BN, WM, WN, KS, WIDE> {
     int64_t ld[2];
     uint32_t off[CLAMP ? CH : 2];
     uint32_t dst;
-    u32x4 v[CH], mask = {~0u, ~0u, ~0u, ~0u};
-    int K, wslot = 0;   // K: bytes of this workgroup's part of the rows
-    bool ask_write = false;
+    static constexpr int AHEAD = BM < 256 ? 2 : 1;   // slabs in registers (256 x 256: no room for two)
+    u32x4 v[AHEAD][CH], mask = {~0u, ~0u, ~0u, ~0u};
+    int K;              // bytes of this workgroup's part of the rows
     __device__ __forceinline__ void init_rows(const uint8_t* A, int64_t lda, int m0, int M, const uint8_t* B, int64_t ldb,
                                               int n0, int N) {
         const int row = (int)threadIdx.x / 8, c = (int)threadIdx.x % 8;
@@ -176,6 +178,7 @@ struct F8StagedOps : F8Compute<BM, BN, WM, WN, KS, WIDE> {
         }
         dst = (uint32_t)(row * kSlabBytes + ((c ^ swz<8>(row)) << 4));
     }
+    template <int V>
     __device__ __forceinline__ void load(int slab) {
         int k = slab * kSlabBytes;
         if (k + kSlabBytes > K) {
@@ -189,33 +192,67 @@ struct F8StagedOps : F8Compute<BM, BN, WM, WN, KS, WIDE> {
         }
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            if constexpr (CLAMP) v[i] = load16(base[i >= CA] + k + off[i]);
-            else v[i] = load16(base[i >= CA] + (k + (i >= CA ? i - CA : i) * STEP * ld[i >= CA]) + off[i >= CA]);
+            if constexpr (CLAMP) v[V][i] = load16(base[i >= CA] + k + off[i]);
+            else v[V][i] = load16(base[i >= CA] + (k + (i >= CA ? i - CA : i) * STEP * ld[i >= CA]) + off[i >= CA]);
         }
-        ask_write = true;
     }
-    __device__ __forceinline__ void put(int i) {
-        *reinterpret_cast<LDS_AS u32x4*>(this->smem + wslot * F::C::STAGE + dst + i * STEP * kSlabBytes) = i < CA ? v[i] & mask : v[i];
+    template <int V>
+    __device__ __forceinline__ void put(int i, int slot, bool last) {   // (the mask is the last slab's)
+        u32x4 x = v[V][i];
+        if (i < CA && last) x &= mask;
+        *reinterpret_cast<LDS_AS u32x4*>(this->smem + slot * F::C::STAGE + dst + i * STEP * kSlabBytes) = x;
     }
-    __device__ __forceinline__ void write(int, int) {
-        if (!ask_write) return;   // (only slab 0 has not been written by math())
+    // Multiplies slab kt out of its slot, kt mod 2.  Slab kt + AHEAD is loaded into registers V; slab kt + 1 goes from
+    // registers W to the other slot, which the barrier before this slab freed.
+    template <int V, int W, bool LAST>
+    __device__ __forceinline__ void slab(int kt, int slabs) {
+        const int slot = kt & 1;
+        if (!LAST) load<V>(min(kt + AHEAD, slabs - 1));
+        const bool last = kt + 2 == slabs;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) put(i);
-        ask_write = false;
-        wslot ^= 1;
-    }
-    template <int BUF, int HAS, int PARTS>
-    __device__ __forceinline__ void math(int ks) {
-        constexpr int TN = F::C::TN;
-        const bool now = ks == KS - 2 && ask_write;
-        this->template step<BUF>(ks, [&](int j) {
-            if (now) {
+        for (int ks = 0; ks < KS; ++ks) {
+            if (ks < KS - 1) {
+                if (ks % 2 == 0) this->template frag<1>(kt, slot, ks + 1);
+                else this->template frag<0>(kt, slot, ks + 1);
+            } else if (!LAST) {
+                this->wait_lds();
+                this->barrier();
+                this->template frag<0>(kt + 1, slot ^ 1, 0);
+            }
+            auto between = [&](int j) {
+                if (LAST || ks != KS - 2) return;
 #pragma unroll
                 for (int i = 0; i < CH; ++i)
-                    if (i * TN / CH == j) put(i);
+                    if (i * F::C::TN / CH == j) put<W>(i, slot ^ 1, last);
+            };
+            if (ks % 2 == 0) this->template step<0>(ks, between);
+            else this->template step<1>(ks, between);
+        }
+    }
+    __device__ __forceinline__ void run(int slabs) {
+        load<0>(0);
+        if constexpr (AHEAD == 2) load<1>(min(1, slabs - 1));
+#pragma unroll
+        for (int i = 0; i < CH; ++i) put<0>(i, 0, slabs == 1);
+        this->wait_lds();
+        this->barrier();
+        this->template frag<0>(0, 0, 0);
+        int kt = 0;
+        if constexpr (AHEAD == 1) {
+            for (; kt + 1 < slabs; ++kt) slab<0, 0, false>(kt, slabs);
+            slab<0, 0, true>(kt, slabs);
+        } else {
+            for (; kt + 2 < slabs; kt += 2) {
+                slab<0, 1, false>(kt, slabs);
+                slab<1, 0, false>(kt + 1, slabs);
             }
-        });
-        if (now) { ask_write = false; wslot ^= 1; }
+            if (kt + 2 == slabs) {
+                slab<0, 1, false>(kt, slabs);
+                slab<1, 0, true>(kt + 1, slabs);
+            } else {
+                slab<0, 1, true>(kt, slabs);
+            }
+        }
     }
 };
 
@@ -226,12 +263,13 @@ struct F8Extra {
     int64_t part;      // bytes between the splits' results
 };
 
-// OUT: type of what is stored.  Splits of K (blockIdx.y) store plain sums, each into its own buffer.
-template <int OUT, int BM, int BN, int WM, int WN, int KS, bool WIDE, bool DIRECT>
+// OUT: type of what is stored; S: slots of the ring (0: staged loads).  Splits of K (blockIdx.y) store plain sums,
+// each into its own buffer.
+template <int OUT, int BM, int BN, int WM, int WN, int KS, bool WIDE, int S>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)))
 void f8_tile_kernel(GemmParams p, const F8Extra x) {
     constexpr int NW = WM * WN, NC = NW < 4 ? NW : 4;
-    constexpr int RING = 2 * (BM + BN) * kSlabBytes, EPI = (OUT != DT_F32 && BN == 256) ? BM * BN * 2 : 0;
+    constexpr int RING = (S > 0 ? S : 2) * (BM + BN) * kSlabBytes, EPI = (OUT != DT_F32 && BN == 256) ? BM * BN * 2 : 0;
     __shared__ __attribute__((aligned(1024))) char smem_raw[RING > EPI ? RING : EPI];
     LDS_AS char* smem = (LDS_AS char*)smem_raw;
     int tm, tn;
@@ -255,18 +293,18 @@ void f8_tile_kernel(GemmParams p, const F8Extra x) {
         }
         ops.template epilogue<OUT>(p, m0, n0, m_keep, n_keep);
     };
-    if constexpr (DIRECT) {
+    if constexpr (S > 0) {
         if (NC == NW || wave_id() < NC) {
-            F8RingOps<BM, BN, WM, WN, KS, WIDE, NC, true> ops;
+            F8RingOps<S, BM, BN, WM, WN, KS, WIDE, NC, true> ops;
             ops.init(smem);
             ops.la.init(reinterpret_cast<const char*>(A) + (int64_t)m0 * p.lda, p.lda, kSlabBytes);
             ops.lb.init(reinterpret_cast<const char*>(B) + (int64_t)n0 * p.ldb, p.ldb, kSlabBytes);
-            gemm_sched::ring_mainloop<2, KS, 1>(ops, slabs);
+            gemm_sched::ring_mainloop<S, KS, 1>(ops, slabs);
             finish(ops);
         } else if constexpr (NC < NW) {
-            F8RingOps<BM, BN, WM, WN, KS, WIDE, NC, false> ops;
+            F8RingOps<S, BM, BN, WM, WN, KS, WIDE, NC, false> ops;
             ops.init(smem);
-            gemm_sched::ring_mainloop<2, KS, 1>(ops, slabs);
+            gemm_sched::ring_mainloop<S, KS, 1>(ops, slabs);
             finish(ops);
         }
     } else {
@@ -274,7 +312,7 @@ void f8_tile_kernel(GemmParams p, const F8Extra x) {
         ops.init(smem);
         ops.init_rows(A, p.lda, m0, p.M, B, p.ldb, n0, p.N);
         ops.K = K;
-        gemm_sched::staged_mainloop<2, KS>(ops, slabs);
+        ops.run(slabs);
         finish(ops);
     }
 }
@@ -287,6 +325,7 @@ __global__ __launch_bounds__(256) void f8_join_kernel(const GemmParams p, const 
     const int64_t m = id / quads;
     const int n = (int)(id % quads) * 4;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int i = 0; i < splits; ++i)
         s += *reinterpret_cast<const f32x4*>(part + i * x.part + (m * ldp + n) * 4);
     const float a = scale_or_one(x.sa, m);
@@ -299,43 +338,58 @@ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct F8Plan {
     int big;       // 256 x 256 tiles (else 128 x 128)
-    int direct;
     int splits;
 };
 
-// The tile with the least time on the fullest compute unit, a 256 x 256 tile costing four
-// units and a 128 x 128 one kSmallCost; two of the latter share a compute unit.
-constexpr double kSmallCost = 1.35;
+// The tile with the least time on the fullest compute unit: a 256 x 256 tile costs four units and a 128 x 128 one
+// kSmallCost (both measured on 4096 x 4096 x 4096 and 8192^3).  Few small tiles are split along K where that pays: a slab
+// takes kSlabUs on a compute unit that has nothing else to hide its loads with, a split writes and reads
+// its fp32 sums once (at the rate of a copy) and needs one more launch.
+constexpr double kSmallCost = 1.35, kSlabUs = 0.45, kJoinUs = 4.0, kBytesPerUs = 4.5e6;
+constexpr double kStagedUs = 0.5;   // what a slab takes longer through registers from rows of any alignment
 int64_t f8_ldp(int64_t N) { return (N + 3) / 4 * 4; }
 F8Plan f8_plan(int64_t M, int64_t N, int64_t K, bool wide) {
-    F8Plan q;
+    F8Plan q = {0, 1};
     const int64_t cu = num_compute_units();
     const int64_t t256 = ceil_div(M, 256) * ceil_div(N, 256), t128 = ceil_div(M, 128) * ceil_div(N, 128);
     q.big = !wide && M >= 256 && N >= 256 && ceil_div(t256, cu) * 4.0 <= ceil_div(t128, cu) * kSmallCost;
-    q.direct = 0;
-    q.splits = 1;
-    const int64_t tiles = q.big ? t256 : t128, slabs = ceil_div(K, kSlabBytes);
-    if (tiles * 2 <= cu) {   // a split keeps at least four slabs
-        int64_t s = (q.big ? 1 : 2) * cu / tiles;
-        s = s < slabs / 4 ? s : slabs / 4;
-        s = s < 16 ? s : 16;
-        if (s > 1) q.splits = (int)s;
+    if (q.big || t128 > cu) return q;
+    const int64_t slabs = ceil_div(K, kSlabBytes);
+    double best = 0.0;
+    for (int64_t s = 1; s <= 16 && s * 4 <= slabs + 3; ++s) {
+        const double us = ceil_div(t128 * s, cu) * ceil_div(slabs, s) * kSlabUs +
+                          (s > 1 ? kJoinUs + s * (double)M * f8_ldp(N) * 8.0 / kBytesPerUs : 0.0);
+        if (s == 1 || us < best) {
+            best = us;
+            q.splits = (int)s;
+        }
     }
     return q;
 }
 
-template <int OUT, int BM, int WM, int WN, bool WIDE, bool DIRECT>
+// Whether the launch that copies (`bytes` of copies) costs less than the staged loads' slower slabs.
+bool f8_copy_pays(const F8Plan& q, const F8Params& f, int64_t slabs, size_t bytes) {
+    const int64_t bt = q.big ? 256 : 128, rounds = ceil_div(ceil_div(f.M, bt) * ceil_div(f.N, bt) * q.splits, num_compute_units());
+    const double staged_us = rounds * ceil_div(slabs, q.splits) * (q.big ? 2.0 : 1.0) * kStagedUs;
+    return kJoinUs + 2.0 * bytes / kBytesPerUs < staged_us;
+}
+
+template <int OUT, int BM, int WM, int WN, bool WIDE, int S>
 hipError_t go(const GemmParams& p, const F8Extra& x, int splits, hipStream_t st) {
-    hipLaunchKernelGGL((f8_tile_kernel<OUT, BM, BM, WM, WN, 4, WIDE, DIRECT>), dim3((unsigned)(p.tiles_m * p.tiles_n), (unsigned)splits),
+    hipLaunchKernelGGL((f8_tile_kernel<OUT, BM, BM, WM, WN, 4, WIDE, S>), dim3((unsigned)(p.tiles_m * p.tiles_n), (unsigned)splits),
                        dim3(64 * WM * WN), 0, st, p, x);
     return hipGetLastError();
 }
+// Four slots for small tiles that have a compute unit to themselves, so that three slabs are on their way: else
+// a second workgroup, which two slots leave room for, does as much.
 template <int OUT, bool WIDE>
-hipError_t tile_of(const F8Plan& q, const GemmParams& p, const F8Extra& x, hipStream_t st) {
+hipError_t tile_of(const F8Plan& q, bool direct, const GemmParams& p, const F8Extra& x, hipStream_t st) {
     if constexpr (!WIDE) {
-        if (q.big) return q.direct ? go<OUT, 256, 2, 4, WIDE, true>(p, x, q.splits, st) : go<OUT, 256, 2, 4, WIDE, false>(p, x, q.splits, st);
+        if (q.big) return direct ? go<OUT, 256, 2, 4, WIDE, 2>(p, x, q.splits, st) : go<OUT, 256, 2, 4, WIDE, 0>(p, x, q.splits, st);
     }
-    return q.direct ? go<OUT, 128, 2, 2, WIDE, true>(p, x, q.splits, st) : go<OUT, 128, 2, 2, WIDE, false>(p, x, q.splits, st);
+    const bool alone = (int64_t)p.tiles_m * p.tiles_n * q.splits <= num_compute_units();
+    if (!direct) return alone ? go<OUT, 128, 2, 4, WIDE, 0>(p, x, q.splits, st) : go<OUT, 128, 2, 2, WIDE, 0>(p, x, q.splits, st);
+    return alone ? go<OUT, 128, 2, 4, WIDE, 4>(p, x, q.splits, st) : go<OUT, 128, 2, 2, WIDE, 2>(p, x, q.splits, st);
 }
 template <int OUT>
 hipError_t join_of(const GemmParams& p, const F8Extra& x, const void* part, int64_t ldp, int splits, hipStream_t st) {
@@ -346,9 +400,15 @@ hipError_t join_of(const GemmParams& p, const F8Extra& x, const void* part, int6
 
 }  // namespace
 
+// Bytes for the splits and, for rows that whole slabs do not fill, the copies of both operands.
 size_t f8_tile_workspace(int64_t M, int64_t N, int64_t K, bool wide) {
     const F8Plan q = f8_plan(M, N, K, wide);
-    return q.splits > 1 ? (size_t)q.splits * M * f8_ldp(N) * sizeof(float) : 0;
+    const int64_t bt = q.big ? 256 : 128, kp = ceil_div(K, kSlabBytes) * kSlabBytes;
+    size_t bytes = q.splits > 1 ? (size_t)q.splits * M * f8_ldp(N) * sizeof(float) : 0;
+    bytes = (bytes + 255) & ~size_t(255);
+    if (K % kSlabBytes || M < bt) bytes += (size_t)(std::max(M, bt) * kp);
+    if (K % kSlabBytes || N < bt) bytes += (size_t)(std::max(N, bt) * kp);
+    return bytes;
 }
 
 // K >= 128 and strides that the tiles' 32-bit offsets hold (256 rows below 2^31 bytes).
@@ -367,13 +427,34 @@ hipError_t launch_f8_tile(const F8Params& f, void* ws, size_t ws_bytes, hipStrea
     if (q.splits < 2) q.splits = 1;
     F8Extra x = {f.sa, f.sb, (int)ceil_div(slabs, q.splits), each};
     q.splits = (int)ceil_div(slabs, x.per_split);
-    q.direct = f.M >= bt && f.N >= bt && f.K % kSlabBytes == 0 && ((uintptr_t)f.A | (uintptr_t)f.B | f.lda | f.ldb) % 16 == 0;
+    // operands that the direct copies cannot take, copied behind the splits' sums where there is room
+    const int64_t kp = slabs * kSlabBytes;
+    auto copy_of = [&](const uint8_t* src, int64_t ld, int64_t rows) {
+        RowsJob j = {src, nullptr, ld, rows, f.K, std::max(rows, (int64_t)bt), kp};
+        if (rows >= bt && f.K == kp && ((uintptr_t)src | ld) % 16 == 0) j.src = nullptr;
+        return j;
+    };
+    RowsJob ja = copy_of(f.A, f.lda, f.M), jb = copy_of(f.B, f.ldb, f.N);
+    const size_t used = q.splits > 1 ? ((size_t)(q.splits * each) + 255) & ~size_t(255) : 0;
+    const size_t wants = used + (ja.src ? ja.bytes() : 0) + (jb.src ? jb.bytes() : 0);
+    const bool copies = (ja.src || jb.src) && wants <= ws_bytes && f8_copy_pays(q, f, slabs, wants - used);
+    const bool direct = copies || (!ja.src && !jb.src);
+    F8Params o = f;
+    if (copies) {
+        ja.dst = static_cast<uint8_t*>(ws) + used;
+        jb.dst = ja.dst + (ja.src ? ja.bytes() : 0);
+        const hipError_t e = launch_rows_pack(ja, jb, st);
+        if (e != hipSuccess) return e;
+        if (ja.src) { o.A = ja.dst; o.lda = kp; }
+        if (jb.src) { o.B = jb.dst; o.ldb = kp; }
+        o.K = (int)kp;
+    }
     GemmParams p = {};
-    p.A = reinterpret_cast<const char*>(f.A);
-    p.B = reinterpret_cast<const char*>(f.B);
+    p.A = reinterpret_cast<const char*>(o.A);
+    p.B = reinterpret_cast<const char*>(o.B);
     p.C = f.C;
-    p.lda = f.lda; p.ldb = f.ldb; p.ldc = f.ldc;
-    p.M = f.M; p.N = f.N; p.K = f.K;
+    p.lda = o.lda; p.ldb = o.ldb; p.ldc = f.ldc;
+    p.M = f.M; p.N = f.N; p.K = o.K;
     p.alpha = f.alpha; p.beta = f.beta;
     p.out_type = f.out_type;
     p.tiles_m = (int)ceil_div(f.M, bt);
@@ -388,13 +469,13 @@ hipError_t launch_f8_tile(const F8Params& f, void* ws, size_t ws_bytes, hipStrea
         s.ldc = ldp;
         s.alpha = 1.0f;
         s.beta = 0.0f;
-        const hipError_t e = wide ? tile_of<DT_F32, true>(q, s, y, st) : tile_of<DT_F32, false>(q, s, y, st);
+        const hipError_t e = wide ? tile_of<DT_F32, true>(q, direct, s, y, st) : tile_of<DT_F32, false>(q, direct, s, y, st);
         if (e != hipSuccess) return e;
         if (wide) return join_of<DT_F32>(p, x, ws, ldp, q.splits, st);
         return f.out_type == DT_BF16 ? join_of<DT_BF16>(p, x, ws, ldp, q.splits, st) : join_of<DT_F16>(p, x, ws, ldp, q.splits, st);
     }
-    if (wide) return tile_of<DT_F32, true>(q, p, x, st);
-    return f.out_type == DT_BF16 ? tile_of<DT_BF16, false>(q, p, x, st) : tile_of<DT_F16, false>(q, p, x, st);
+    if (wide) return tile_of<DT_F32, true>(q, direct, p, x, st);
+    return f.out_type == DT_BF16 ? tile_of<DT_BF16, false>(q, direct, p, x, st) : tile_of<DT_F16, false>(q, direct, p, x, st);
 }
 
 }  // namespace gemm

@@ -53,6 +53,17 @@ struct NormBwdParams {
 int norm_bwd_parts(int in_type, int64_t rows, int cols);
 hipError_t launch_norm_bwd(int in_type, const NormBwdParams& p, hipStream_t st);
 
+// ---------------------------------------------------------------- rows into a workspace
+// dst: rows_pad rows of len_pad bytes (a multiple of 16), the source's rows of len bytes (ld apart) with zeros behind
+// and below; fewer than 2^32 chunks of 16 bytes.  src == NULL: no job.
+struct RowsJob {
+    const uint8_t* src;
+    uint8_t* dst;
+    int64_t ld, rows, len, rows_pad, len_pad;
+    int64_t bytes() const { return rows_pad * len_pad; }
+};
+hipError_t launch_rows_pack(const RowsJob& a, const RowsJob& b, hipStream_t st);
+
 // ---------------------------------------------------------------- 8-bit product
 struct F8Params {
     const uint8_t* A;    // M x K, K contiguous

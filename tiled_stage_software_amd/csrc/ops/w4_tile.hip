@@ -11,6 +11,8 @@
 // A launch before prepares what the group's end needs, so that the ring brings it along with the slabs: the sum of A over
 // each unit (a group; 32 k for short groups), which the zero points multiply, in the order of the
 // accumulators; and scales with zero points, transposed to rows of columns.
+#include <algorithm>
+
 #include "../mfma.hpp"
 #include "w4_common.hpp"
 
@@ -411,8 +413,17 @@ hipError_t out_of(const W4Plan& q, const W4Tile& t, bool direct, hipStream_t st)
     return tile_of<T, OUT, 64, 1>(t, s1, direct, q.splits, st);
 }
 
+// Copies of A and the codes that make their rows fit the direct copies (src NULL: they do).
+void copies_of(const W4Params& f, const W4Plan& q, RowsJob& a, RowsJob& w) {
+    const int64_t kp = q.slabs * kSlabK;
+    a = {reinterpret_cast<const uint8_t*>(f.A), nullptr, f.lda * 2, f.M, (int64_t)f.K * 2, std::max((int64_t)f.M, (int64_t)q.bm), kp * 2};
+    w = {f.W, nullptr, f.ldw, f.N, ((int64_t)f.K + 1) / 2, std::max((int64_t)f.N, (int64_t)kBN), kp / 2};
+    if (f.K == kp && f.M >= q.bm && ((uintptr_t)a.src | a.ld) % 16 == 0 && f.lda <= (1 << 21)) a.src = nullptr;
+    if (f.K == kp && f.N >= kBN && ((uintptr_t)w.src | w.ld) % 16 == 0 && f.ldw <= (1 << 22)) w.src = nullptr;
+}
+
 template <int T>
-hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, hipStream_t st) {
+hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, size_t ws_bytes, hipStream_t st) {
     W4Prepare a = {};
     a.A = f.A;
     a.scales = reinterpret_cast<const uint16_t*>(f.scales);
@@ -440,14 +451,32 @@ hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, hipStream_t s
     p.tiles_m = (int)q.tiles_m; p.tiles_n = (int)q.tiles_n;
     p.group_m = 8;
     p.xcd_remap = 1;
+    // operands that the direct copies cannot take, copied behind the rest where there is room
+    RowsJob ja, jw;
+    copies_of(f, q, ja, jw);
+    const size_t used = q.sums + q.sz + round256(q.parts), wants = used + (ja.src ? ja.bytes() : 0) + (jw.src ? jw.bytes() : 0);
+    const bool copies = (ja.src || jw.src) && wants <= ws_bytes;
+    const bool direct = copies || (!ja.src && !jw.src);
     t.W = f.W;
     t.ldw = f.ldw;
+    if (copies) {
+        ja.dst = reinterpret_cast<uint8_t*>(ws) + used;
+        jw.dst = ja.dst + (ja.src ? ja.bytes() : 0);
+        e = launch_rows_pack(ja, jw, st);
+        if (e != hipSuccess) return e;
+        if (ja.src) {
+            p.A = reinterpret_cast<const char*>(ja.dst);
+            p.lda = ja.len_pad / 2;
+        }
+        if (jw.src) {
+            t.W = jw.dst;
+            t.ldw = jw.len_pad;
+        }
+    }
     t.sums = ws;
     t.sz_at = (uint32_t)q.sums;
     t.per_unit = q.unit == 32 ? 0 : q.unit / kSlabK;
     t.per_split = q.per_split;
-    const bool direct = f.M >= q.bm && f.N >= kBN && f.K % kSlabK == 0 && f.lda % 8 == 0 && f.ldw % 16 == 0 &&
-                        ((uintptr_t)f.A | (uintptr_t)f.W) % 16 == 0 && f.lda <= (1 << 21) && f.ldw <= (1 << 22);
     if (q.splits > 1) {
         const GemmParams whole = p;
         const int64_t ldp = ldp_of(f.N);
@@ -469,9 +498,13 @@ hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, hipStream_t s
 
 }  // namespace
 
+// Bytes for the sums, the scales, the splits and, for rows that whole slabs do not fill, the copies.
 size_t w4_tile_workspace(int64_t M, int64_t N, int64_t K, int64_t group) {
     const W4Plan q = w4_plan(M, N, K, group, ~size_t(0) >> 1);
-    return q.sums + q.sz + q.parts;
+    size_t bytes = q.sums + q.sz + round256(q.parts);
+    if (K % kSlabK || M < q.bm) bytes += (size_t)(std::max(M, (int64_t)q.bm) * q.slabs * kSlabK * 2);
+    if (K % kSlabK || N < kBN) bytes += (size_t)(std::max(N, (int64_t)kBN) * q.slabs * kSlabK / 2);
+    return bytes;
 }
 
 // K that the staged loads hold, grids and 32-bit offsets in range, and a workspace for the sums and scales.
@@ -484,7 +517,8 @@ bool w4_tile_fits(const W4Params& f, size_t ws_bytes) {
 
 hipError_t launch_w4_tile(int in_type, const W4Params& f, void* ws, size_t ws_bytes, hipStream_t st) {
     const W4Plan q = w4_plan(f.M, f.N, f.K, f.group, ws_bytes);
-    return in_type == DT_BF16 ? run_tiles<DT_BF16>(f, q, static_cast<char*>(ws), st) : run_tiles<DT_F16>(f, q, static_cast<char*>(ws), st);
+    return in_type == DT_BF16 ? run_tiles<DT_BF16>(f, q, static_cast<char*>(ws), ws_bytes, st)
+                              : run_tiles<DT_F16>(f, q, static_cast<char*>(ws), ws_bytes, st);
 }
 
 }  // namespace gemm
