@@ -1,11 +1,11 @@
-// w4_tile.hip -- the product with 4-bit weights on large tiles: BM x 128 of C per workgroup, waves
-// of WTM x 32, slabs of 64 k in an LDS ring, v_mfma_f32_16x16x32 on 16 x 16 blocks.
+// w4_tile.hip -- the product with 4-bit weights on large tiles: BM x 128 of C per workgroup, four waves
+// of BM x 32, slabs of 64 k in an LDS ring, v_mfma_f32_16x16x32 on 16 x 16 blocks.
 //
 // No weight is rounded, so a group's scale multiplies an fp32 sum: each accumulator has a second one
 // for the running group, and one pass of two FMAs for each joins them at the group's end.  That and
 // turning codes into operands is vector work beside the matrix cores' (per wave, 128 x 32 tile and
 // 128 k: 1024 cycles of matrix instructions; 4 x 2 x 10 operations for the codes, 2 x 64 for a group's end,
-// four cycles each).  Wide blocks of A's rows keep it below theirs: one turned code serves WTM / 16
+// four cycles each).  Wide blocks of A's rows keep it below theirs: one turned code serves BM / 16
 // instructions.  Groups shorter than 64 end with every 32 k, which makes the vector work the bound.
 //
 // A launch before prepares what the group's end needs, so that the ring brings it along with the slabs: the sum of A over
@@ -19,7 +19,7 @@
 namespace gemm {
 namespace {
 
-constexpr int kSlabK = 64, kBN = 128, kNC = 4;   // kNC: waves that copy
+constexpr int kSlabK = 64, kBN = 128, kNC = 4;   // kNC: waves, side by side along N
 
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -42,9 +42,9 @@ struct W4Layout {
 };
 
 // S1: units are 32 k, two to a slab.
-template <int T, int BM, int WM, bool S1>
-struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, WM, 4, 16> {
-    typedef MfmaCompute<typename Half<T>::type, BM, kBN, 64, WM, 4, 16> C;
+template <int T, int BM, bool S1>
+struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> {
+    typedef MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> C;
     typedef W4Layout<BM> Y;
     static constexpr int TM = C::TM, TN = C::TN, AH = TM / 2, NU = S1 ? 2 : 1;
     static constexpr int STAGE = Y::A_BYTES + Y::Q_BYTES + NU * Y::UNIT;
@@ -61,10 +61,10 @@ struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, WM, 4, 16> {
 
     __device__ __forceinline__ void init(LDS_AS char* smem_, const W4Tile& p, int slabs) {
         C::init(smem_);
-        const int w = wave_id(), wm = w / 4, wn = w % 4, lane = lane_id(), r = lane % 16, g = lane / 16;
+        const int wn = wave_id(), lane = lane_id(), r = lane % 16, g = lane / 16;
         const int kc = (g & 1) * 2 + (g >> 1);   // the k-chunk of lane group g, as in A's fragments
         qo = (uint32_t)(Y::A_BYTES + (wn * 32 + r) * 32 + kc * 4);
-        const int at = wm * C::WTM + r * TM;     // this lane's sums, TM of them
+        const int at = r * TM;                   // this lane's sums, TM of them
         so = (uint32_t)(Y::A_BYTES + Y::Q_BYTES + at / (BM / kNC) * Y::REGION + at % (BM / kNC) * 4);
         zo = (uint32_t)(Y::A_BYTES + Y::Q_BYTES + wn * Y::REGION + Y::SL * 16 + g * 16);
         per_unit = p.per_unit;
@@ -155,17 +155,16 @@ __device__ __forceinline__ uint32_t unit_chunk(const W4Tile& p, int tm, int tn, 
 // First unit of slab s of the whole K.
 __device__ __forceinline__ int unit_of(const W4Tile& p, int s) { return p.per_unit ? s / p.per_unit : 2 * s; }
 
-// Direct global -> LDS copies by the first four waves: 16-byte aligned rows, whole slabs and tiles.
-template <int T, int BM, int WM, bool S1, bool COPY>
-struct W4RingOps : W4Compute<T, BM, WM, S1> {
-    typedef W4Compute<T, BM, WM, S1> F;
+// Direct global -> LDS copies: 16-byte aligned rows, whole slabs and tiles.
+template <int T, int BM, bool S1>
+struct W4RingOps : W4Compute<T, BM, S1> {
+    typedef W4Compute<T, BM, S1> F;
     DirectLoader<BM, 128, kNC, true> la;
     DirectLoader<kBN, 32, kNC, false> lq;
     static constexpr int L = decltype(la)::IPW + decltype(lq)::IPW + F::NU;
     const W4Tile* p;
     int tm, tn, s0;
     __device__ __forceinline__ void issue(int slab, int slot, int, int) {
-        if (!COPY) return;
         LDS_AS char* st = this->smem + slot * F::STAGE;
         la.issue(slab, st, 0, decltype(la)::IPW);
         lq.issue(slab, st + F::Y::A_BYTES, 0, decltype(lq)::IPW);
@@ -179,7 +178,7 @@ struct W4RingOps : W4Compute<T, BM, WM, S1> {
         }
     }
     template <int N>
-    __device__ __forceinline__ void wait_slabs() { if (COPY) wait_vm<N * L>(); }
+    __device__ __forceinline__ void wait_slabs() { wait_vm<N * L>(); }
     template <int BUF, int HAS, int PARTS>
     __device__ __forceinline__ void math(int q) { this->template step<BUF>(q); }
 };
@@ -193,12 +192,12 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 v, int by) {
 // Any pitch, alignment and size (K >= 64): 16-byte loads of any alignment into registers, one
 // slab ahead, written into the other slot in the last step but one.  A chunk past a row's end is read
 // as the row's last 16 bytes and shifted.  Rows past the end repeat the last.
-template <int T, int BM, int WM, bool S1>
-struct W4StagedOps : W4Compute<T, BM, WM, S1> {
-    typedef W4Compute<T, BM, WM, S1> F;
-    static constexpr int NT = 256 * WM, STEP = NT / 8, CA = BM / STEP;
+template <int T, int BM, bool S1>
+struct W4StagedOps : W4Compute<T, BM, S1> {
+    typedef W4Compute<T, BM, S1> F;
+    static constexpr int NT = 64 * kNC, STEP = NT / 8, CA = BM / STEP;
     static constexpr int UT = F::NU * kNC * (F::Y::SL + 8);   // threads with a chunk of the units
-    static_assert(STEP % 16 == 0 && CA * STEP == BM && UT <= NT && 2 * kBN <= NT, "chunks per thread");
+    static_assert(STEP % 16 == 0 && CA * STEP == BM && UT <= NT && 2 * kBN == NT, "chunks per thread");
     const char* arow[CA];
     const uint8_t* qrow;
     uint32_t uchunk, ustep;
@@ -227,7 +226,7 @@ struct W4StagedOps : W4Compute<T, BM, WM, S1> {
         const int kq = min(slab_ * 32 + (int)threadIdx.x % 2 * 16, q_bytes - 16);
 #pragma unroll
         for (int i = 0; i < CA; ++i) va[i] = load16(arow[i] + ka);
-        if (NT == 2 * kBN || threadIdx.x < 2 * kBN) vq = load16(qrow + kq);
+        vq = load16(qrow + kq);
         if ((int)threadIdx.x < UT) vu = load16(p->sums + (uchunk + (uint32_t)unit_of(*p, slab_) * ustep));
         ask_write = true;
     }
@@ -243,7 +242,7 @@ struct W4StagedOps : W4Compute<T, BM, WM, S1> {
         }
 #pragma unroll
         for (int i = 0; i < CA; ++i) *reinterpret_cast<LDS_AS u32x4*>(st + dst + i * STEP * 128) = va[i];
-        if (NT == 2 * kBN || t < 2 * kBN) *reinterpret_cast<LDS_AS u32x4*>(st + F::Y::A_BYTES + t * 16) = vq;
+        *reinterpret_cast<LDS_AS u32x4*>(st + F::Y::A_BYTES + t * 16) = vq;
         if (t < UT) *reinterpret_cast<LDS_AS u32x4*>(st + F::Y::A_BYTES + F::Y::Q_BYTES + t * 16) = vu;
         ask_write = false;
         wslot ^= 1;
@@ -259,10 +258,10 @@ struct W4StagedOps : W4Compute<T, BM, WM, S1> {
 };
 
 // Splits of K (blockIdx.y) store plain sums, each into its own buffer.
-template <int T, int OUT, int BM, int WM, bool S1, bool DIRECT>
-__global__ __launch_bounds__(256 * WM) __attribute__((amdgpu_waves_per_eu(2)))
+template <int T, int OUT, int BM, bool S1, bool DIRECT>
+__global__ __launch_bounds__(64 * kNC) __attribute__((amdgpu_waves_per_eu(2)))
 void w4_tile_kernel(W4Tile p) {
-    typedef W4Compute<T, BM, WM, S1> F;
+    typedef W4Compute<T, BM, S1> F;
     constexpr int S = DIRECT ? 3 : 2;
     __shared__ __attribute__((aligned(1024))) char smem_raw[S * F::STAGE];
     LDS_AS char* smem = (LDS_AS char*)smem_raw;
@@ -274,23 +273,15 @@ void w4_tile_kernel(W4Tile p) {
     const int slabs = min((p.g.K + kSlabK - 1) / kSlabK - s0, p.per_split);
     p.g.C += (int64_t)blockIdx.y * p.part;
     if constexpr (DIRECT) {
-        auto run = [&](auto& ops) {
-            ops.init(smem, p, slabs);
-            ops.p = &p; ops.tm = tm; ops.tn = tn; ops.s0 = s0;
-            ops.la.init(p.g.A + ((int64_t)m0 * p.g.lda + (int64_t)s0 * kSlabK) * 2, p.g.lda * 2, kSlabK * 2);
-            ops.lq.init(reinterpret_cast<const char*>(p.W) + (int64_t)n0 * p.ldw + (int64_t)s0 * (kSlabK / 2), p.ldw, kSlabK / 2);
-            gemm_sched::ring_mainloop<S, F::KS, 1>(ops, slabs);
-            ops.template epilogue<OUT>(p.g, m0, n0, m_keep, n_keep);
-        };
-        if (WM == 1 || wave_id() < kNC) {
-            W4RingOps<T, BM, WM, S1, true> ops;
-            run(ops);
-        } else if constexpr (WM > 1) {
-            W4RingOps<T, BM, WM, S1, false> ops;
-            run(ops);
-        }
+        W4RingOps<T, BM, S1> ops;
+        ops.init(smem, p, slabs);
+        ops.p = &p; ops.tm = tm; ops.tn = tn; ops.s0 = s0;
+        ops.la.init(p.g.A + ((int64_t)m0 * p.g.lda + (int64_t)s0 * kSlabK) * 2, p.g.lda * 2, kSlabK * 2);
+        ops.lq.init(reinterpret_cast<const char*>(p.W) + (int64_t)n0 * p.ldw + (int64_t)s0 * (kSlabK / 2), p.ldw, kSlabK / 2);
+        gemm_sched::ring_mainloop<S, F::KS, 1>(ops, slabs);
+        ops.template epilogue<OUT>(p.g, m0, n0, m_keep, n_keep);
     } else {
-        W4StagedOps<T, BM, WM, S1> ops;
+        W4StagedOps<T, BM, S1> ops;
         ops.init(smem, p, slabs);
         ops.init_rows(p, tm, tn, m0, n0, s0);
         gemm_sched::staged_mainloop<S, F::KS>(ops, slabs);
@@ -307,7 +298,7 @@ struct W4Prepare {
     float* sums;
     uint32_t* sz;
     int64_t lda, lds;
-    int M, N, K, group, unit, units, tiles_m, tiles_n, bm, tm;   // tm: blocks of 16 rows of a wave's tile
+    int M, N, K, group, unit, units, tiles_m, tiles_n, bm, tm;   // tm: blocks of 16 rows of a tile
     int64_t sum_blocks;
 };
 template <int T>
@@ -329,9 +320,8 @@ __global__ __launch_bounds__(256) void w4_prepare_kernel(const W4Prepare p) {
         }
         sum += __shfl_xor(sum, 1, 64);
         sum += __shfl_xor(sum, 2, 64);
-        const int wt = p.tm * 16;   // rows of a wave's tile: its lanes have tm sums each, side by side
-        if (threadIdx.x % 4 == 0)
-            p.sums[(int64_t)u * rows + (int64_t)tile * p.bm + local / wt * wt + local % 16 * p.tm + local % wt / 16] = sum;
+            if (threadIdx.x % 4 == 0)
+            p.sums[(int64_t)u * rows + (int64_t)tile * p.bm + local % 16 * p.tm + local / 16] = sum;   // a lane's tm sums side by side
         return;
     }
     const int64_t id = ((int64_t)blockIdx.x - p.sum_blocks) * 256 + threadIdx.x, cols = (int64_t)p.tiles_n * kBN;
@@ -368,11 +358,13 @@ struct W4Plan {
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 int64_t ldp_of(int64_t N) { return (N + 3) / 4 * 4; }
 
-// 64 rows a tile where that holds all of A, 256 where such tiles fill the card, else 128.
+// 64 rows a tile where that holds all of A, else 128: two workgroups of four waves then share a compute unit, and
+// one's group ends, barriers and stores run under the other's instructions (2048 x 14336 x 4096: 294 us; with one workgroup of
+// eight waves on 256 rows 313).
 W4Plan w4_plan(int64_t M, int64_t N, int64_t K, int64_t group, size_t room) {
     W4Plan q;
     const int64_t cu = num_compute_units();
-    q.bm = M <= 64 ? 64 : M <= 128 || ceil_div(M, 256) * ceil_div(N, kBN) < cu ? 128 : 256;
+    q.bm = M <= 64 ? 64 : 128;
     q.tiles_m = ceil_div(M, q.bm);
     q.tiles_n = ceil_div(N, kBN);
     q.slabs = ceil_div(K, kSlabK);
@@ -382,7 +374,7 @@ W4Plan w4_plan(int64_t M, int64_t N, int64_t K, int64_t group, size_t room) {
     q.sz = round256((size_t)q.units * q.tiles_n * kBN * 4);
     // splits end with a unit, keep at least eight slabs and fill two workgroups a compute unit at most
     const int64_t per_unit = q.unit == 32 ? 1 : group / kSlabK, tiles = q.tiles_m * q.tiles_n, each = M * ldp_of(N) * 4;
-    int64_t s = tiles * 2 <= cu ? (q.bm == 256 ? 1 : 2) * cu / tiles : 1;
+    int64_t s = tiles * 2 <= cu ? 2 * cu / tiles : 1;
     s = s < q.slabs / 8 ? s : q.slabs / 8;
     s = s < 16 ? s : 16;
     while (s > 1 && q.sums + q.sz + (size_t)(s * each) > room) --s;
@@ -393,24 +385,23 @@ W4Plan w4_plan(int64_t M, int64_t N, int64_t K, int64_t group, size_t room) {
     return q;
 }
 
-template <int T, int OUT, int BM, int WM>
+template <int T, int OUT, int BM>
 hipError_t tile_of(const W4Tile& t, bool short_units, bool direct, int splits, hipStream_t st) {
-    const dim3 grid((unsigned)(t.g.tiles_m * t.g.tiles_n), (unsigned)splits), block(256 * WM);
+    const dim3 grid((unsigned)(t.g.tiles_m * t.g.tiles_n), (unsigned)splits), block(256);
     if (short_units) {
-        if (direct) hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, WM, true, true>), grid, block, 0, st, t);
-        else hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, WM, true, false>), grid, block, 0, st, t);
+        if (direct) hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, true, true>), grid, block, 0, st, t);
+        else hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, true, false>), grid, block, 0, st, t);
     } else {
-        if (direct) hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, WM, false, true>), grid, block, 0, st, t);
-        else hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, WM, false, false>), grid, block, 0, st, t);
+        if (direct) hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, false, true>), grid, block, 0, st, t);
+        else hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, false, false>), grid, block, 0, st, t);
     }
     return hipGetLastError();
 }
 template <int T, int OUT>
 hipError_t out_of(const W4Plan& q, const W4Tile& t, bool direct, hipStream_t st) {
     const bool s1 = q.unit == 32;
-    if (q.bm == 256) return tile_of<T, OUT, 256, 2>(t, s1, direct, q.splits, st);
-    if (q.bm == 128) return tile_of<T, OUT, 128, 1>(t, s1, direct, q.splits, st);
-    return tile_of<T, OUT, 64, 1>(t, s1, direct, q.splits, st);
+    if (q.bm == 128) return tile_of<T, OUT, 128>(t, s1, direct, q.splits, st);
+    return tile_of<T, OUT, 64>(t, s1, direct, q.splits, st);
 }
 
 // Copies of A and the codes that make their rows fit the direct copies (src NULL: they do).
@@ -434,7 +425,7 @@ hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, size_t ws_byt
     a.M = f.M; a.N = f.N; a.K = f.K; a.group = f.group;
     a.unit = q.unit; a.units = q.units;
     a.tiles_m = (int)q.tiles_m; a.tiles_n = (int)q.tiles_n;
-    a.bm = q.bm; a.tm = q.bm == 64 ? 4 : 8;
+    a.bm = q.bm; a.tm = q.bm / 16;
     a.sum_blocks = ceil_div(q.tiles_m * q.bm * q.units, 64);
     hipLaunchKernelGGL(w4_prepare_kernel<T>, dim3((unsigned)(a.sum_blocks + ceil_div(q.tiles_n * kBN * q.units, 256))), dim3(256), 0, st, a);
     hipError_t e = hipGetLastError();
