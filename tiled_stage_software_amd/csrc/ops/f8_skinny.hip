@@ -42,14 +42,14 @@ __global__ __launch_bounds__(64 * WAVES) void f8_skinny_kernel(const F8Params p)
     for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     u32x4 b[DEPTH][2], a[DEPTH][AL];
 
-    const int count = (p.K + kStep - 1) / kStep;           // steps; a step past the last loads the last one
+    const int count = (p.K + kStep - 1) / kStep;           // steps; one past the last loads one line for all lanes
     auto first_byte = [&](int s) { return min((int64_t)s * kStep, (int64_t)p.K - kStep); };
     auto load = [&](int d, int s) {
         const int64_t k = first_byte(s);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) b[d][h] = load16(bsrc[h] + k);
+        for (int h = 0; h < 2; ++h) b[d][h] = load16(s < count ? bsrc[h] + k : p.B);
 #pragma unroll
-        for (int h = 0; h < AL; ++h) a[d][h] = load16(asrc[h] + k);
+        for (int h = 0; h < AL; ++h) a[d][h] = load16(s < count ? asrc[h] + k : p.A);
     };
     auto at = [&](int row, int c) { return reinterpret_cast<LDS_AS u32x4*>(slot + row * kStep + ((c ^ swz<8>(row)) << 4)); };
     auto multiply = [&](int d, int s) {

@@ -231,7 +231,7 @@ gemm_status_t gemm_w4(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, int
     p.out_type = c_type;
     if (!workspace) workspace_bytes = 0;
     if (M <= kW4VectorRows) return launched(launch_w4_vector(in_type, p, stream));
-    if (M > kW4SkinnyRows && w4_tile_fits(p, workspace_bytes))
+    if (w4_tile_fits(p, workspace_bytes) && w4_tile_us(p, workspace_bytes) < w4_skinny_us(p))
         return launched(launch_w4_tile(in_type, p, workspace, workspace_bytes, stream));
     return launched(launch_w4_skinny(in_type, p, stream));
 }
@@ -245,7 +245,11 @@ gemm_status_t gemm_w4_workspace_size(gemm_dtype_t in_type, int64_t M, int64_t N,
     TRY(check_size("N", N));
     TRY(check_size("K", K));
     REQUIRE(group >= 32 && group % 32 == 0 && group <= kMaxSize, "group=%lld: a multiple of 32", (long long)group);
-    if (M > kW4SkinnyRows && N > 0 && K > 0) *bytes = w4_tile_workspace(M, N, K, group);
+    if (M > kW4VectorRows && N > 0 && K > 0) {
+        W4Params p = {};
+        p.M = (int)M; p.N = (int)N; p.K = (int)K; p.group = (int)group;   // (of aligned operands)
+        if (w4_tile_us(p, SIZE_MAX / 2) < w4_skinny_us(p)) *bytes = w4_tile_workspace(M, N, K, group);
+    }
     return GEMM_OK;
 }
 

@@ -97,7 +97,8 @@ struct W4Params {
 };
 constexpr int kW4VectorRows = 4;    // rows of A that launch_w4_vector takes
 hipError_t launch_w4_vector(int in_type, const W4Params& p, hipStream_t st);
-constexpr int kW4SkinnyRows = 32;   // rows up to which launch_w4_skinny is chosen where the tiles have their workspace
+double w4_skinny_us(const W4Params& p);                // what either is expected to take
+double w4_tile_us(const W4Params& p, size_t ws_bytes);
 bool w4_tile_fits(const W4Params& p, size_t ws_bytes);
 size_t w4_tile_workspace(int64_t M, int64_t N, int64_t K, int64_t group);
 hipError_t launch_w4_tile(int in_type, const W4Params& p, void* ws, size_t ws_bytes, hipStream_t st);

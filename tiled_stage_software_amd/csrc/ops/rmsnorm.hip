@@ -12,6 +12,8 @@
 // vectors of 16 bytes of it, and rows of any pitch use unaligned vectors with only a row's
 // last, partial vector element by element.  Rows longer than the registers hold are read
 // once per pass by the looping kernel.
+#include <algorithm>
+
 #include "ops_common.hpp"
 
 namespace gemm {
@@ -642,9 +644,9 @@ int norm_bwd_parts(int in_type, int64_t rows, int cols) {
         return (int)(rows < 64 ? (rows < 1 ? 1 : rows) : 64);
     const int per = vecs <= 128 ? 4 : 1;
     const int64_t groups = (rows + per - 1) / per;
-    // two rows each at least: a partial row of dw costs as much as half a row of the pass (513 x 3001 fp32: 256
-    // parts 9.8 us, 512 parts 11.4), and three rows in turn cost less than the launch that joins
-    const int64_t most = 512, parts = groups <= 3 ? 1 : groups / 2;
+    // Three rows in turn cost less than the launch that joins; many rows are shared by two at least, as a partial row of dw
+    // costs half a row of the pass (513 x 3001 fp32: 256 parts 9.8 us, 512 parts 11.4).
+    const int64_t most = 512, parts = groups <= 3 ? 1 : groups <= 256 ? groups : std::max<int64_t>(256, groups / 2);
     return (int)(parts < most ? parts : most);
 }
 

@@ -68,25 +68,46 @@ template <int T>
 __device__ __forceinline__ float zero16(uint16_t z) { return 1.0f + to_f32<T>(z) * 0.0625f; }
 constexpr float kZero16 = 1.5f;   // of z = 8
 
-// Eight elements of a row of K from k, zeros past its end.
+// Bytes of a chunk moved down by `by`, zeros behind them (16 or more: all zeros).
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int by) {
+    if (by >= 16) return u32x4{0u, 0u, 0u, 0u};
+    return __builtin_bit_cast(u32x4, __builtin_bit_cast(unsigned __int128, v) >> (8 * by));
+}
+// Eight elements of a row of K from k, zeros past its end.  Those across or past it are read as the row's last eight and moved
+// down: one load whatever k is, none behind a branch.
 __device__ __forceinline__ u32x4 load_a(const char* row, int k, int K) {
-    if (k + 8 <= K) return load16(row + (int64_t)k * 2);
+    if (K >= 8) {
+        const int at = min(k, K - 8);
+        const u32x4 v = load16(row + (int64_t)at * 2);
+        return k == at ? v : shift_down(v, 2 * (k - at));
+    }
     u32x4 v = {0u, 0u, 0u, 0u};
     for (int i = 0; i < 8; ++i)
         if (k + i < K) v[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[k + i] << ((i & 1) * 16);
     return v;
 }
-// Eight codes (four bytes) from k; what lies past the row's bytes is not read.  (Codes past
-// K meet zeros of A.)
+// Eight codes (four bytes) from k, zeros past the row's bytes, in the same way.  (Codes past K meet zeros of A.)
 __device__ __forceinline__ uint32_t load_q(const uint8_t* row, int k, int K) {
+    const int bytes = (K + 1) >> 1;
     uint32_t v = 0;
-    if (k + 8 <= K) {
-        __builtin_memcpy(&v, row + (k >> 1), 4);
-        return v;
+    if (bytes >= 4) {
+        const int at = min(k >> 1, bytes - 4), by = (k >> 1) - at;
+        __builtin_memcpy(&v, row + at, 4);
+        return by >= 4 ? 0u : v >> (8 * by);
     }
     for (int i = 0; i < 4; ++i)
         if (k + 2 * i < K) v |= (uint32_t)row[(k >> 1) + i] << (8 * i);
     return v;
+}
+
+// The same for 32 codes (16 bytes).
+__device__ __forceinline__ u32x4 load_q16(const uint8_t* row, int k, int K) {
+    const int bytes = (K + 1) >> 1;
+    if (bytes >= 16) {
+        const int at = min(k >> 1, bytes - 16);
+        return shift_down(load16(row + at), (k >> 1) - at);
+    }
+    return u32x4{load_q(row, k, K), load_q(row, k + 8, K), load_q(row, k + 16, K), load_q(row, k + 24, K)};
 }
 
 }  // namespace gemm

@@ -83,7 +83,7 @@ void w4_skinny_kernel(const W4Params p) {
             }
         }
     };
-    auto step = [&](int d, int at, int in) {
+    auto step = [&](int d, int at, int in, int left) {
         wave_fence();
         const int row = lane / 4;
         *reinterpret_cast<LDS_AS u32x4*>(slot + row * 64 + (((lane % 4) ^ swz<4>(row)) << 4)) = q[d];
@@ -93,7 +93,7 @@ void w4_skinny_kernel(const W4Params p) {
         uint32_t word[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) word[t] = *reinterpret_cast<LDS_AS uint32_t*>(slot + r * 64 + ((t ^ swz<4>(r)) << 4) + 4 * g);
-        multiply(at, in, kStep, word, [&](int i, int t) -> u32x4 {
+        multiply(at, in, left, word, [&](int i, int t) -> u32x4 {
             return *a_at(16 * i + r, 4 * t + g);
         });
         __builtin_amdgcn_sched_barrier(0);   // steps mixed by the scheduler would not fit the registers
@@ -120,21 +120,18 @@ void w4_skinny_kernel(const W4Params p) {
         for (int s = s0 + w; s < s1; s += DEPTH * WAVES)
 #pragma unroll
             for (int d = 0; d < DEPTH; ++d) {
-                if (s + d * WAVES < s1) step(d, at, in);
+                if (s + d * WAVES < s1) step(d, at, in, kStep);
                 load(d, min(s + (d + DEPTH) * WAVES, s1 - 1));
                 at += WAVES * kStep / p.group;
                 in += WAVES * kStep % p.group;
                 if (in >= p.group) { in -= p.group; ++at; }
             }
-        if (k0 + span >= p.K && full * kStep < p.K && full % WAVES == w) {   // the last, partial step, as its instructions want it
-            const uint8_t* qrow = p.W + min(n0 + r, (int64_t)p.N - 1) * p.ldw;
-            uint32_t word[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) word[t] = load_q(qrow, full * kStep + 32 * t + 8 * g, p.K);
+        if (k0 + span >= p.K && full * kStep < p.K && full % WAVES == w) {   // the last, partial step
             const int k = full * kStep, at = k / p.group;
-            multiply(at - g0, k - at * p.group, p.K - k, word, [&](int i, int t) -> u32x4 {
-                return load_a(p.A + (int64_t)min(m0 + 16 * i + r, p.M - 1) * p.lda * 2, full * kStep + 32 * t + 8 * g, p.K);
-            });
+            q[0] = load_q16(p.W + min(n0 + lane / 4, (int64_t)p.N - 1) * p.ldw, k + 32 * (lane % 4), p.K);
+#pragma unroll
+            for (int h = 0; h < AL; ++h) a[0][h] = load_a(p.A + (int64_t)min(m0 + g + 4 * h, p.M - 1) * p.lda * 2, k + 8 * r, p.K);
+            step(0, at - g0, k - at * p.group, p.K - k);
         }
     }
     lds_barrier();   // the slots are free
@@ -165,12 +162,16 @@ hipError_t go(const W4Params& p, hipStream_t st) {
 }
 
 // Waves for 16 on each compute unit (a wave's start costs as much as some steps, so no more share K).
+int w4_waves(const W4Params& p, int mt) {
+    const int64_t blocks = ((int64_t)p.N + 15) / 16 * ((p.M + 16 * mt - 1) / (16 * mt)), cu = num_compute_units();
+    if (blocks >= 3 * cu || p.K < 1024) return 4;
+    return mt > 1 || blocks >= 3 * cu / 2 || p.K < 4096 ? 8 : 16;
+}
 template <int T, int MT>
 hipError_t rows_of(const W4Params& p, hipStream_t st) {
-    const int64_t blocks = ((int64_t)p.N + 15) / 16 * ((p.M + 16 * MT - 1) / (16 * MT)), cu = num_compute_units();
-    if (blocks >= 3 * cu || p.K < 1024) return go<T, MT, 4>(p, st);
-    if (MT > 1 || blocks >= 3 * cu / 2 || p.K < 4096) return go<T, MT, 8>(p, st);
-    return go<T, 1, 16>(p, st);
+    const int waves = w4_waves(p, MT);
+    if (waves == 4) return go<T, MT, 4>(p, st);
+    return waves == 8 ? go<T, MT, 8>(p, st) : go<T, 1, 16>(p, st);
 }
 template <int T>
 hipError_t skinny_of(const W4Params& p, hipStream_t st) {
@@ -178,6 +179,15 @@ hipError_t skinny_of(const W4Params& p, hipStream_t st) {
 }
 
 }  // namespace
+
+// Expected microseconds: rounds of workgroups, each a start and its waves' steps in turn (measured from 1 to 32 steps
+// and 1 to 112 rounds).
+double w4_skinny_us(const W4Params& p) {
+    const int64_t mt = p.M <= 16 ? 1 : 2, blocks = ((int64_t)p.N + 15) / 16 * ((p.M + 16 * mt - 1) / (16 * mt));
+    const int64_t waves = w4_waves(p, (int)mt), at_once = num_compute_units() * (mt == 1 ? 16 : 8) / waves;
+    const double steps = (double)(((int64_t)p.K + kStep * waves - 1) / (kStep * waves));
+    return 3.0 + (double)((blocks + at_once - 1) / at_once) * (2.7 + 0.95 * steps);
+}
 
 hipError_t launch_w4_skinny(int in_type, const W4Params& p, hipStream_t st) {
     return in_type == DT_BF16 ? skinny_of<DT_BF16>(p, st) : skinny_of<DT_F16>(p, st);

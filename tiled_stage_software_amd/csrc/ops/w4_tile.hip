@@ -183,12 +183,6 @@ struct W4RingOps : W4Compute<T, BM, S1> {
     __device__ __forceinline__ void math(int q) { this->template step<BUF>(q); }
 };
 
-// Bytes of a chunk moved down by `by`, zeros behind them (16 or more: all zeros).
-__device__ __forceinline__ u32x4 shift_down(u32x4 v, int by) {
-    if (by >= 16) return u32x4{0u, 0u, 0u, 0u};
-    return __builtin_bit_cast(u32x4, __builtin_bit_cast(unsigned __int128, v) >> (8 * by));
-}
-
 // Any pitch, alignment and size (K >= 64): 16-byte loads of any alignment into registers, one
 // slab ahead, written into the other slot in the last step but one.  A chunk past a row's end is read
 // as the row's last 16 bytes and shifted.  Rows past the end repeat the last.
@@ -354,7 +348,11 @@ struct W4Plan {
     int bm, splits, unit, units, per_split;
     int64_t slabs, tiles_m, tiles_n;
     size_t sums, sz, parts;   // bytes of the workspace's pieces
+    double us;                // what it is expected to take
 };
+// Measured times of the pieces, in microseconds: the launch that prepares, a workgroup's first loads and stores, a slab on a
+// compute unit with two workgroups (units of 64 k and more, short units), the launch that joins; a copy's bytes.
+constexpr double kPrepareUs = 5.0, kFillUs = 4.0, kSlabUs = 0.9, kShortSlabUs = 1.3, kJoinUs = 5.0, kBytesPerUs = 4.5e6;
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 int64_t ldp_of(int64_t N) { return (N + 3) / 4 * 4; }
 
@@ -372,13 +370,20 @@ W4Plan w4_plan(int64_t M, int64_t N, int64_t K, int64_t group, size_t room) {
     q.units = (int)(q.unit == 32 ? 2 * q.slabs : ceil_div(K, group));
     q.sums = round256((size_t)q.units * q.tiles_m * q.bm * 4);
     q.sz = round256((size_t)q.units * q.tiles_n * kBN * 4);
-    // splits end with a unit, keep at least eight slabs and fill two workgroups a compute unit at most
+    // Splits of K, which end with a unit, as many as make the whole fastest: a round of slabs on the fullest compute unit (two
+    // workgroups each), then the sums written and read once at a copy's rate and one more launch.
     const int64_t per_unit = q.unit == 32 ? 1 : group / kSlabK, tiles = q.tiles_m * q.tiles_n, each = M * ldp_of(N) * 4;
-    int64_t s = tiles * 2 <= cu ? 2 * cu / tiles : 1;
-    s = s < q.slabs / 8 ? s : q.slabs / 8;
-    s = s < 16 ? s : 16;
-    while (s > 1 && q.sums + q.sz + (size_t)(s * each) > room) --s;
-    if (s < 1) s = 1;
+    const double slab_us = q.unit == 32 ? kShortSlabUs : kSlabUs;
+    int64_t s = 1;
+    for (int64_t t = 1; t <= 64 && t * 4 <= q.slabs + 3; ++t) {
+        if (t > 1 && q.sums + q.sz + (size_t)(t * each) > room) break;
+        const double us = kPrepareUs + ceil_div(tiles * t, 2 * cu) * (kFillUs + ceil_div(q.slabs, t) * slab_us) +
+                          (t > 1 ? kJoinUs + t * each * 2.0 / kBytesPerUs : 0.0);
+        if (t == 1 || us < q.us) {
+            q.us = us;
+            s = t;
+        }
+    }
     q.per_split = (int)(ceil_div(ceil_div(q.slabs, s), per_unit) * per_unit);
     q.splits = (int)ceil_div(q.slabs, q.per_split);
     q.parts = q.splits > 1 ? (size_t)(q.splits * each) : 0;
@@ -496,6 +501,15 @@ size_t w4_tile_workspace(int64_t M, int64_t N, int64_t K, int64_t group) {
     if (K % kSlabK || M < q.bm) bytes += (size_t)(std::max(M, (int64_t)q.bm) * q.slabs * kSlabK * 2);
     if (K % kSlabK || N < kBN) bytes += (size_t)(std::max(N, (int64_t)kBN) * q.slabs * kSlabK / 2);
     return bytes;
+}
+
+// Expected microseconds.
+double w4_tile_us(const W4Params& f, size_t ws_bytes) {
+    const W4Plan q = w4_plan(f.M, f.N, f.K, f.group, ws_bytes);
+    RowsJob a, w;
+    copies_of(f, q, a, w);
+    const double bytes = (a.src ? (double)a.bytes() : 0.0) + (w.src ? (double)w.bytes() : 0.0);
+    return q.us + (bytes > 0.0 ? kJoinUs + 2.0 * bytes / kBytesPerUs : 0.0);
 }
 
 // K that the staged loads hold, grids and 32-bit offsets in range, and a workspace for the sums and scales.
