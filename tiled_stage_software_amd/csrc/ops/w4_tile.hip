@@ -284,7 +284,7 @@ void w4_tile_kernel(W4Tile p) {
 }
 
 // Sums of A over units and the transposed scales.  Four lanes sum a unit of a row, 32 elements a turn; the
-// threads behind those move a scale each.
+// workgroups behind those turn the scales.
 struct W4Prepare {
     const char* A;
     const uint16_t* scales;
@@ -295,6 +295,7 @@ struct W4Prepare {
     int M, N, K, group, unit, units, tiles_m, tiles_n, bm, tm;   // tm: blocks of 16 rows of a tile
     int64_t sum_blocks;
 };
+constexpr int kTurnCols = 64, kTurnUnits = 32;
 template <int T>
 __global__ __launch_bounds__(256) void w4_prepare_kernel(const W4Prepare p) {
     if ((int64_t)blockIdx.x < p.sum_blocks) {
@@ -318,17 +319,27 @@ __global__ __launch_bounds__(256) void w4_prepare_kernel(const W4Prepare p) {
             p.sums[(int64_t)u * rows + (int64_t)tile * p.bm + local % 16 * p.tm + local / 16] = sum;   // a lane's tm sums side by side
         return;
     }
-    const int64_t id = ((int64_t)blockIdx.x - p.sum_blocks) * 256 + threadIdx.x, cols = (int64_t)p.tiles_n * kBN;
-    if (id >= cols * p.units) return;
-    const int u = (int)(id / cols), at = (int)(id % cols);
-    const int n = min(max(0, min(at / kBN * kBN, p.N - kBN)) + at % kBN, p.N - 1);
-    uint32_t v = 0;   // a unit past the end: A is zero there
-    if ((int64_t)u * p.unit < p.K) {
-        const int64_t i = n * p.lds + (int64_t)u * p.unit / p.group;
-        const uint16_t eight = T == DT_BF16 ? 0x4100 : 0x4800;
-        v = p.scales[i] | (uint32_t)(p.zeros ? p.zeros[i] : eight) << 16;
+    // 64 columns by 32 units: read along the units of a column, written along the columns of a unit
+    __shared__ uint32_t turn[kTurnUnits][kTurnCols + 1];
+    const int64_t cols = (int64_t)p.tiles_n * kBN, id = (int64_t)blockIdx.x - p.sum_blocks;
+    const int at0 = (int)(id % (cols / kTurnCols)) * kTurnCols, u0 = (int)(id / (cols / kTurnCols)) * kTurnUnits;
+    const int ul = threadIdx.x % kTurnUnits;
+#pragma unroll
+    for (int c = threadIdx.x / kTurnUnits; c < kTurnCols; c += 256 / kTurnUnits) {
+        const int at = at0 + c, n = min(max(0, min(at / kBN * kBN, p.N - kBN)) + at % kBN, p.N - 1);
+        const int64_t k = (int64_t)(u0 + ul) * p.unit;
+        uint32_t v = 0;   // a unit past the end: A is zero there
+        if (k < p.K) {
+            const int64_t i = n * p.lds + k / p.group;
+            const uint16_t eight = T == DT_BF16 ? 0x4100 : 0x4800;
+            v = p.scales[i] | (uint32_t)(p.zeros ? p.zeros[i] : eight) << 16;
+        }
+        turn[ul][c] = v;
     }
-    p.sz[id] = v;
+    __syncthreads();
+#pragma unroll
+    for (int u = threadIdx.x / kTurnCols; u < kTurnUnits; u += 256 / kTurnCols)
+        if (u0 + u < p.units) p.sz[(u0 + u) * cols + at0 + threadIdx.x % kTurnCols] = turn[u][threadIdx.x % kTurnCols];
 }
 
 // C = alpha * (sum of the splits, in order) + beta * C
@@ -350,40 +361,49 @@ struct W4Plan {
     size_t sums, sz, parts;   // bytes of the workspace's pieces
     double us;                // what it is expected to take
 };
-// Measured times of the pieces, in microseconds: the launch that prepares, a workgroup's first loads and stores, a slab on a
-// compute unit with two workgroups (units of 64 k and more, short units), the launch that joins; a copy's bytes.
-constexpr double kPrepareUs = 5.0, kFillUs = 4.0, kSlabUs = 0.9, kShortSlabUs = 1.3, kJoinUs = 5.0, kBytesPerUs = 4.5e6;
+// Measured times of the pieces, in microseconds: the launch that prepares, a workgroup's first loads and its stores, the
+// launch that joins, a copy's bytes; and a slab, alone on its compute unit or with a second workgroup there, for
+// units of 64 k or more and for short ones (tiles of 64 and 128 rows, 256 and 512 of them, K 1024 and 4096).
+constexpr double kPrepareUs = 4.0, kFillUs = 3.0, kJoinUs = 5.0, kBytesPerUs = 4.5e6;
+double slab_us(int bm, bool alone, bool short_units) {
+    if (bm == 64) return alone ? (short_units ? 0.9 : 0.69) : (short_units ? 1.21 : 0.9);
+    return alone ? (short_units ? 1.45 : 1.07) : (short_units ? 1.83 : 1.28);
+}
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 int64_t ldp_of(int64_t N) { return (N + 3) / 4 * 4; }
 
-// 64 rows a tile where that holds all of A, else 128: two workgroups of four waves then share a compute unit, and
-// one's group ends, barriers and stores run under the other's instructions (2048 x 14336 x 4096: 294 us; with one workgroup of
-// eight waves on 256 rows 313).
+// Tiles of 128 rows fill a compute unit with two workgroups of four waves (one of eight waves on 256 rows: 2048 x 14336 x 4096
+// 313 us instead of 294: its group ends, barriers and stores have nothing to run under); tiles of 64 rows are for
+// small problems.  Splits of K end with a unit; their sums are written and read once and take one more launch.
+// Of both heights and all splits the one that should be fastest.
 W4Plan w4_plan(int64_t M, int64_t N, int64_t K, int64_t group, size_t room) {
-    W4Plan q;
+    W4Plan q = {};
     const int64_t cu = num_compute_units();
-    q.bm = M <= 64 ? 64 : 128;
-    q.tiles_m = ceil_div(M, q.bm);
     q.tiles_n = ceil_div(N, kBN);
     q.slabs = ceil_div(K, kSlabK);
     q.unit = group % kSlabK == 0 ? (int)group : 32;
     q.units = (int)(q.unit == 32 ? 2 * q.slabs : ceil_div(K, group));
-    q.sums = round256((size_t)q.units * q.tiles_m * q.bm * 4);
     q.sz = round256((size_t)q.units * q.tiles_n * kBN * 4);
-    // Splits of K, which end with a unit, as many as make the whole fastest: a round of slabs on the fullest compute unit (two
-    // workgroups each), then the sums written and read once at a copy's rate and one more launch.
-    const int64_t per_unit = q.unit == 32 ? 1 : group / kSlabK, tiles = q.tiles_m * q.tiles_n, each = M * ldp_of(N) * 4;
-    const double slab_us = q.unit == 32 ? kShortSlabUs : kSlabUs;
+    const int64_t per_unit = q.unit == 32 ? 1 : group / kSlabK, each = M * ldp_of(N) * 4;
     int64_t s = 1;
-    for (int64_t t = 1; t <= 64 && t * 4 <= q.slabs + 3; ++t) {
-        if (t > 1 && q.sums + q.sz + (size_t)(t * each) > room) break;
-        const double us = kPrepareUs + ceil_div(tiles * t, 2 * cu) * (kFillUs + ceil_div(q.slabs, t) * slab_us) +
-                          (t > 1 ? kJoinUs + t * each * 2.0 / kBytesPerUs : 0.0);
-        if (t == 1 || us < q.us) {
-            q.us = us;
-            s = t;
+    for (int bm = 64; bm <= 128; bm += 64) {
+        const int64_t tiles = ceil_div(M, bm) * q.tiles_n;
+        const size_t sums = round256((size_t)q.units * ceil_div(M, bm) * bm * 4);
+        for (int64_t t = 1; t <= 64 && t * 4 <= q.slabs + 3; ++t) {
+            if (t > 1 && sums + q.sz + (size_t)(t * each) > room) break;
+            const int64_t slabs = ceil_div(q.slabs, t), full = tiles * t / (2 * cu), rest = tiles * t % (2 * cu);
+            double us = kPrepareUs + full * (kFillUs + slabs * slab_us(bm, false, q.unit == 32));
+            if (rest) us += kFillUs + slabs * slab_us(bm, rest <= cu, q.unit == 32);
+            if (t > 1) us += kJoinUs + t * each * 2.0 / kBytesPerUs;
+            if (q.us == 0.0 || us < q.us) {
+                q.us = us;
+                q.bm = bm;
+                q.sums = sums;
+                s = t;
+            }
         }
     }
+    q.tiles_m = ceil_div(M, q.bm);
     q.per_split = (int)(ceil_div(ceil_div(q.slabs, s), per_unit) * per_unit);
     q.splits = (int)ceil_div(q.slabs, q.per_split);
     q.parts = q.splits > 1 ? (size_t)(q.splits * each) : 0;
@@ -432,7 +452,7 @@ hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, size_t ws_byt
     a.tiles_m = (int)q.tiles_m; a.tiles_n = (int)q.tiles_n;
     a.bm = q.bm; a.tm = q.bm / 16;
     a.sum_blocks = ceil_div(q.tiles_m * q.bm * q.units, 64);
-    hipLaunchKernelGGL(w4_prepare_kernel<T>, dim3((unsigned)(a.sum_blocks + ceil_div(q.tiles_n * kBN * q.units, 256))), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(w4_prepare_kernel<T>, dim3((unsigned)(a.sum_blocks + q.tiles_n * (kBN / kTurnCols) * ceil_div(q.units, kTurnUnits))), dim3(256), 0, st, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     W4Tile t = {};
