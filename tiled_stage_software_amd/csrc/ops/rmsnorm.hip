@@ -206,7 +206,8 @@ struct Weights {
 // and what other threads have of it is left out of the sums (and stored twice, as the same
 // value; every load of a row comes before its first store).  The weights stay in registers over the rows
 // of a workgroup; y is computed once for its largest magnitude and once more to be written, which
-// holds fewer registers than keeping it: 16 rather than 4 waves a compute unit for rows of 8192 (353 -> 178 us).
+// holds fewer registers than keeping it (16384 x 8192 bf16 with residual to 8 bits: 353 -> 176 us, 5.3 TB/s; 2049 x 4001
+// f16 8.6 us, 3.8 TB/s: rows that start anywhere).
 template <int T, bool F8, int WT, int WPR, int RPG, int V>
 __global__ __launch_bounds__(64 * WPR * RPG) void norm_kernel(const NormParams p) {
     constexpr int VE = Elem<T>::VE, SZ = Elem<T>::SIZE, TPR = 64 * WPR;
@@ -221,20 +222,29 @@ __global__ __launch_bounds__(64 * WPR * RPG) void norm_kernel(const NormParams p
     Weights<T, WT> w[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) w[i].load(p.w, from(i));
-    int turn = 0;   // the LDS words alternate, so a row's writes never meet the previous row's reads
-    for (int64_t row = (int64_t)blockIdx.x * RPG + threadIdx.x / TPR; row < p.rows; row += (int64_t)gridDim.x * RPG) {
-        u32x4 v[V];
+    // the next row is on its way while this one is summed and written (but for sixteen waves a row, which fill the registers)
+    constexpr bool AHEAD = WPR < 16;
+    u32x4 nx[V], nr[V];
+    auto load = [&](int64_t row) {
         const char* xr = p.x + row * p.ldx * SZ;
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = load16(xr + (int64_t)from(i) * SZ);
+        for (int i = 0; i < V; ++i) nx[i] = load16(xr + (int64_t)from(i) * SZ);
         if (p.r) {
-            u32x4 r[V];
             const char* rr = p.r + row * p.ldr * SZ;
 #pragma unroll
-            for (int i = 0; i < V; ++i) r[i] = load16(rr + (int64_t)from(i) * SZ);
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = add_residual<T>(v[i], r[i]);
+            for (int i = 0; i < V; ++i) nr[i] = load16(rr + (int64_t)from(i) * SZ);
         }
+    };
+    int turn = 0;   // the LDS words alternate, so a row's writes never meet the previous row's reads
+    int64_t row = (int64_t)blockIdx.x * RPG + threadIdx.x / TPR;
+    const int64_t stride = (int64_t)gridDim.x * RPG;
+    if (AHEAD && row < p.rows) load(row);
+    for (; row < p.rows; row += stride) {
+        if (!AHEAD) load(row);
+        u32x4 v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = p.r ? add_residual<T>(nx[i], nr[i]) : nx[i];
+        if (AHEAD && row + stride < p.rows) load(row + stride);
         auto squares = [&](float by) {
             float sum = 0.0f;
 #pragma unroll
@@ -356,12 +366,11 @@ __global__ __launch_bounds__(kLoopThreads) void norm_loop_kernel(const NormParam
 
 constexpr int64_t kMaxGrid = 1 << 20;   // workgroups of a launch; more rows loop
 
-// Workgroups that stay on the card with a row's worth of registers; each then takes every so many rows.
-constexpr int kResident = 8;
+// As many workgroups as the registers let stay on the card; each takes every so many rows.
 template <int T, bool F8, int WT, int WPR, int RPG, int V>
 hipError_t go(const NormParams& p, hipStream_t st) {
     int64_t grid = (p.rows + RPG - 1) / RPG;
-    const int64_t most = (int64_t)num_compute_units() * kResident;
+    const int64_t most = (int64_t)num_compute_units() * (V == 1 ? 8 : 4);
     if (grid > most) grid = most;
     hipLaunchKernelGGL((norm_kernel<T, F8, WT, WPR, RPG, V>), dim3((unsigned)grid), dim3(64 * WPR * RPG), 0, st, p);
     return hipGetLastError();
