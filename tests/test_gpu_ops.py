@@ -392,7 +392,10 @@ def test_w4(M, N, K, group, t):
 
 @pytest.mark.parametrize("M,N,K,group,pad", [(2048, 2304, 1024, 128, 0), (2049, 2307, 1090, 64, 0), (1000, 1536, 640, 32, 3),
                                              (64, 1024, 8192, 128, 0), (100, 515, 8197, 64, 1), (300, 130, 16000, 32, 0),
-                                             (257, 8200, 450, 192, 5), (33, 128, 64, 32, 0), (47, 200, 65, 64, 0)])
+                                             (257, 8200, 450, 192, 5), (33, 128, 64, 32, 0), (47, 200, 65, 64, 0),
+                                             (4, 155, 14848, 128, 3), (3, 40, 5000, 96, 0), (2, 300, 20001, 64, 0),
+                                             (1, 33, 40000, 32, 1), (1, 12400, 999, 128, 0), (4, 6300, 4097, 64, 0),
+                                             (16, 155, 33000, 128, 0), (7, 4100, 9000, 32, 0), (20, 96, 20000, 64, 2)])
 @pytest.mark.parametrize("t", ["bf16", "f16"])
 def test_w4_exact_integers_large(M, N, K, group, pad, t):
     """Small whole numbers: every sum is exact in fp32, so every bit has to be right, on the large tiles

@@ -157,7 +157,7 @@ struct F8StagedOps : F8Compute<BM, BN, WM, WN, KS, WIDE> {
     int64_t ld[2];
     uint32_t off[CLAMP ? CH : 2];
     uint32_t dst;
-    static constexpr int AHEAD = BM < 256 ? 2 : 1;   // slabs in registers (256 x 256: no room for two)
+    static constexpr int AHEAD = BM < 256 && !(WIDE && NT == 256) ? 2 : 1;   // slabs in registers (where two fit)
     u32x4 v[AHEAD][CH], mask = {~0u, ~0u, ~0u, ~0u};
     int K;              // bytes of this workgroup's part of the rows
     __device__ __forceinline__ void init_rows(const uint8_t* A, int64_t lda, int m0, int M, const uint8_t* B, int64_t ldb,
@@ -197,9 +197,9 @@ struct F8StagedOps : F8Compute<BM, BN, WM, WN, KS, WIDE> {
         }
     }
     template <int V>
-    __device__ __forceinline__ void put(int i, int slot, bool last) {   // (the mask is the last slab's)
+    __device__ __forceinline__ void put(int i, int slot, bool last) {   // (the mask is the last slab's; one slab ahead, whole until then)
         u32x4 x = v[V][i];
-        if (i < CA && last) x &= mask;
+        if (i < CA && (AHEAD == 1 || last)) x &= mask;
         *reinterpret_cast<LDS_AS u32x4*>(this->smem + slot * F::C::STAGE + dst + i * STEP * kSlabBytes) = x;
     }
     // Multiplies slab kt out of its slot, kt mod 2.  Slab kt + AHEAD is loaded into registers V; slab kt + 1 goes from
@@ -207,7 +207,7 @@ struct F8StagedOps : F8Compute<BM, BN, WM, WN, KS, WIDE> {
     template <int V, int W, bool LAST>
     __device__ __forceinline__ void slab(int kt, int slabs) {
         const int slot = kt & 1;
-        if (!LAST) load<V>(min(kt + AHEAD, slabs - 1));
+        if (!LAST) load<V>(AHEAD == 1 ? kt + 1 : min(kt + 2, slabs - 1));
         const bool last = kt + 2 == slabs;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -343,9 +343,9 @@ struct F8Plan {
 
 // The tile with the least time on the fullest compute unit: a 256 x 256 tile costs four units and a 128 x 128 one
 // kSmallCost (both measured on 4096 x 4096 x 4096 and 8192^3).  Few small tiles are split along K where that pays: a slab
-// takes kSlabUs on a compute unit that has nothing else to hide its loads with, a split writes and reads
+// takes kSlabUs (fp32 results: kWideSlabUs) on a compute unit that has nothing else to hide its loads with, a split writes and reads
 // its fp32 sums once (at the rate of a copy) and needs one more launch.
-constexpr double kSmallCost = 1.35, kSlabUs = 0.45, kJoinUs = 4.0, kBytesPerUs = 4.5e6;
+constexpr double kSmallCost = 1.35, kSlabUs = 0.45, kWideSlabUs = 1.0, kJoinUs = 4.0, kBytesPerUs = 4.5e6;
 constexpr double kStagedUs = 0.5;   // what a slab takes longer through registers from rows of any alignment
 int64_t f8_ldp(int64_t N) { return (N + 3) / 4 * 4; }
 F8Plan f8_plan(int64_t M, int64_t N, int64_t K, bool wide) {
@@ -357,7 +357,7 @@ F8Plan f8_plan(int64_t M, int64_t N, int64_t K, bool wide) {
     const int64_t slabs = ceil_div(K, kSlabBytes);
     double best = 0.0;
     for (int64_t s = 1; s <= 16 && s * 4 <= slabs + 3; ++s) {
-        const double us = ceil_div(t128 * s, cu) * ceil_div(slabs, s) * kSlabUs +
+        const double us = ceil_div(t128 * s, cu) * ceil_div(slabs, s) * (wide ? kWideSlabUs : kSlabUs) +
                           (s > 1 ? kJoinUs + s * (double)M * f8_ldp(N) * 8.0 / kBytesPerUs : 0.0);
         if (s == 1 || us < best) {
             best = us;

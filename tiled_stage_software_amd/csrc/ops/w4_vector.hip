@@ -89,7 +89,7 @@ void w4_vector_kernel(const W4Params p, const Walk walk) {
         const int last = p.K - k0 < SPAN ? (int)((p.K - k0 + kStep - 1) / kStep) * kStep : SPAN;   // codes of this round, in steps
         auto piece = [&](int i) { return load_a(p.A + min(i / (SPAN / 8), p.M - 1) * p.lda * 2, (int)k0 + i % (SPAN / 8) * 8, p.K); };
         if (k0 > 0) { gi = ((int)k0 + w * kStep) / p.group; in = ((int)k0 + w * kStep) % p.group; }
-        const u32x4 first = (int)threadIdx.x * 8 < last ? piece(threadIdx.x) : u32x4{0u, 0u, 0u, 0u};
+        const u32x4 first = (int)threadIdx.x % (SPAN / 8) * 8 < last ? piece(threadIdx.x) : u32x4{0u, 0u, 0u, 0u};
         if (s1 > s0)
 #pragma unroll
             for (int d = 0; d < DEPTH; ++d) load(d, min(s0 + w + d * WAVES, s1 - 1));
