@@ -432,8 +432,10 @@ gemm_status_t gemm_rmsnorm_bwd_workspace_size(gemm_dtype_t in_type, int64_t rows
  * largest before they are added in fp32: on random operands 1.5e-5 of the result, far below
  * C's own rounding.  K == 0 or alpha == 0: C = beta * C.
  * workspace: lets the call split a long K over more workgroups where M x N alone gives too
- * few; gemm_f8_workspace_size gives the bytes it would use.  With less (or NULL) the call
- * does not split.
+ * few, and copy operands whose rows are not 16-byte aligned or not whole slabs of 128 into such
+ * rows where that pays.  gemm_f8_workspace_size gives the bytes for the splits and for the copies that K and M ask
+ * for; rows that are unaligned though K is a multiple of 128 can use (M + N) * K more.  With
+ * less (or NULL) the call does without, with the same result up to the order of sums.
  * Errors: as gemm_bf16, plus GEMM_ERR_INVALID_ARG for a workspace not 256-byte aligned. */
 gemm_status_t gemm_f8(int64_t M, int64_t N, int64_t K, float alpha, const void* A, int64_t lda, const float* scale_a,
                       const void* B, int64_t ldb, const float* scale_b, float beta, void* C, gemm_dtype_t c_type,
@@ -448,8 +450,12 @@ gemm_status_t gemm_f8_workspace_size(int64_t M, int64_t N, int64_t K, size_t* by
  * may be NULL (8 everywhere).  group: a multiple of 32, the last group may be short.  C:
  * row-major, in_type or GEMM_F32.
  * No weight is rounded: for each group s * (sum of a * code - z * sum of a), in fp32.  A
- * row of A with an infinity therefore gives NaN where the exact sum may be infinite.
- * K == 0 or alpha == 0: C = beta * C.  workspace: as in gemm_f8.
+ * row of A with an infinity therefore gives NaN where the exact sum may be infinite.  A code enters as
+ * 1 + code/16, so the sums that cancel are up to 16 times the weights: an fp32 result is good to a few
+ * 2^-22 of its terms.
+ * K == 0 or alpha == 0: C = beta * C.  workspace: more rows than a few run on large tiles, which keep the sums of
+ * A and the transposed scales there, beside what gemm_f8 uses one for; gemm_w4_workspace_size gives
+ * the bytes.  Without them (or with NULL) every size still runs, many rows several times slower.
  * Errors: as gemm_bf16, plus GEMM_ERR_INVALID_ARG for a group that is not a positive multiple of 32, a
  * pitch too small, NULL codes or scales, a workspace not 256-byte aligned. */
 gemm_status_t gemm_w4(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, int64_t group, float alpha, const void* A,

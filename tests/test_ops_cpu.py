@@ -1,11 +1,16 @@
 """The operators around the products, on the CPU: refusals before anything is launched, quick
 returns, workspace sizes, and the quantisers."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 from tiled_stage_software_amd import libgemm as lg, ops
 from ops_util import unpack4
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P = 0x10000  # a fake device address: nothing here launches
 F32, BF16, F16, F8 = lg.GEMM_F32, lg.GEMM_BF16, lg.GEMM_F16, lg.GEMM_F8E4M3
 BAD = lg.GEMM_ERR_INVALID_ARG
@@ -109,6 +114,24 @@ def test_product_workspaces():
     assert lg.gemm_f8_workspace_size(-1, 1, 1)[0] == BAD
     assert lg.gemm_w4_workspace_size(F32, 1, 1, 1, 32)[0] == BAD
     assert lg.gemm_w4_workspace_size(BF16, 1, 1, 1, 33)[0] == BAD
+
+
+@pytest.mark.skipif(torch.cuda.device_count() > 0, reason="the calls pass fake device addresses that a launch would dereference")
+def test_debugging_names_the_kernel():
+    """GEMM_DEBUG=1: each call's sizes and kernel on stderr, before the launch (which the runtime refuses: no GPU)."""
+    code = ("from tiled_stage_software_amd import libgemm as lg\n"
+            "P = 0x10000\n"
+            "lg.gemm_f8(1, 64, 256, 1.0, P, 256, P, P, 256, P, 0.0, P, 1, 64)\n"
+            "lg.gemm_f8(300, 640, 256, 1.0, P, 256, P, P, 256, P, 0.0, P, 1, 640)\n"
+            "lg.gemm_w4(1, 1, 64, 256, 128, 1.0, P, 256, P, 128, P, 0, 2, 0.0, P, 1, 64)\n"
+            "lg.gemm_rmsnorm(1, 1, 3, 2, 64, 1e-6, P, 64, 0, 0, P, 0, 0, P, 64, P, P)\n")
+    env = dict(os.environ, GEMM_DEBUG="1")
+    err = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, cwd=ROOT).stderr
+    for text in ("f8 -> type 1 M=1 N=64 K=256: few rows", "M=300 N=640 K=256: tiles", "128 x 128 tiles, 1 splits",
+                 "w4 type 1 -> 1 M=1 N=64 K=256 group=128: dot products", "rmsnorm type 1 -> 3 rows=2 cols=64"):
+        assert text in err, (text, err)
+    env.pop("GEMM_DEBUG")
+    assert "libgemm:" not in subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, cwd=ROOT).stderr
 
 
 def test_wrappers_refuse_other_shapes_and_types():

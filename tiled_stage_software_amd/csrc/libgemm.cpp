@@ -637,7 +637,15 @@ gemm_status_t op_fail(gemm_status_t s, const char* fmt, ...) {
     return fail(s, "%s", text);
 }
 void op_clear_error() { g_err[0] = 0; }
-bool op_debug_on() { return debug_on(); }
+void op_note(const char* fmt, ...) {
+    if (!debug_on()) return;
+    char text[256];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(text, sizeof(text), fmt, ap);
+    va_end(ap);
+    fprintf(stderr, "libgemm: %s\n", text);
+}
 
 }  // namespace gemm
 

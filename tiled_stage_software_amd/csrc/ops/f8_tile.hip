@@ -401,6 +401,8 @@ hipError_t join_of(const GemmParams& p, const F8Extra& x, const void* part, int6
 }  // namespace
 
 // Bytes for the splits and, for rows that whole slabs do not fill, the copies of both operands.
+constexpr size_t kMostCopied = size_t(1) << 34;   // rows_pack counts chunks in 32 bits
+
 size_t f8_tile_workspace(int64_t M, int64_t N, int64_t K, bool wide) {
     const F8Plan q = f8_plan(M, N, K, wide);
     const int64_t bt = q.big ? 256 : 128, kp = ceil_div(K, kSlabBytes) * kSlabBytes;
@@ -437,8 +439,9 @@ hipError_t launch_f8_tile(const F8Params& f, void* ws, size_t ws_bytes, hipStrea
     RowsJob ja = copy_of(f.A, f.lda, f.M), jb = copy_of(f.B, f.ldb, f.N);
     const size_t used = q.splits > 1 ? ((size_t)(q.splits * each) + 255) & ~size_t(255) : 0;
     const size_t wants = used + (ja.src ? ja.bytes() : 0) + (jb.src ? jb.bytes() : 0);
-    const bool copies = (ja.src || jb.src) && wants <= ws_bytes && f8_copy_pays(q, f, slabs, wants - used);
+    const bool copies = (ja.src || jb.src) && wants <= ws_bytes && wants < kMostCopied && f8_copy_pays(q, f, slabs, wants - used);
     const bool direct = copies || (!ja.src && !jb.src);
+    op_note("  %d x %d tiles, %d splits of K, %s loads%s", bt, bt, q.splits, direct ? "direct" : "staged", copies ? " of copied rows" : "");
     F8Params o = f;
     if (copies) {
         ja.dst = static_cast<uint8_t*>(ws) + used;

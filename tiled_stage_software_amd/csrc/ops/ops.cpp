@@ -110,6 +110,8 @@ gemm_status_t gemm_rmsnorm(gemm_dtype_t in_type, gemm_dtype_t w_type, gemm_dtype
     p.w_type = w_type;
     p.y_type = y_type;
     p.eps = eps;
+    op_note("rmsnorm type %d -> %d rows=%lld cols=%lld residual=%d weights=%d", (int)in_type, (int)y_type, (long long)rows,
+            (long long)cols, r != nullptr, w ? (int)w_type : -1);
     return launched(launch_norm(in_type, p, stream));
 }
 
@@ -149,6 +151,7 @@ gemm_status_t gemm_rmsnorm_bwd(gemm_dtype_t in_type, gemm_dtype_t w_type, int64_
     p.w_type = w_type;
     // (without dw there are no partial sums to keep)
     p.parts = dw ? parts_for(in_type, rows, cols, workspace ? workspace_bytes : 0) : norm_bwd_parts(in_type, rows, (int)cols);
+    op_note("rmsnorm_bwd type %d rows=%lld cols=%lld in %d parts", (int)in_type, (long long)rows, (long long)cols, p.parts);
     return launched(launch_norm_bwd(in_type, p, stream));
 }
 
@@ -185,8 +188,11 @@ gemm_status_t gemm_f8(int64_t M, int64_t N, int64_t K, float alpha, const void* 
     p.M = (int)M; p.N = (int)N; p.K = (int)K;
     p.alpha = alpha; p.beta = beta;
     p.out_type = c_type;
-    if (M <= kF8SkinnyRows) return launched(launch_f8_skinny(p, stream));
-    return launched(f8_tile_fits(p) ? launch_f8_tile(p, workspace, workspace_bytes, stream) : launch_f8_staged(p, stream));
+    const bool few = M <= kF8SkinnyRows, tiles = !few && f8_tile_fits(p);
+    op_note("f8 -> type %d M=%lld N=%lld K=%lld: %s", (int)c_type, (long long)M, (long long)N, (long long)K,
+            few ? "few rows" : tiles ? "tiles" : "64 x 64 tiles");
+    if (few) return launched(launch_f8_skinny(p, stream));
+    return launched(tiles ? launch_f8_tile(p, workspace, workspace_bytes, stream) : launch_f8_staged(p, stream));
 }
 
 gemm_status_t gemm_f8_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
@@ -230,9 +236,12 @@ gemm_status_t gemm_w4(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, int
     p.alpha = alpha; p.beta = beta;
     p.out_type = c_type;
     if (!workspace) workspace_bytes = 0;
-    if (M <= kW4VectorRows) return launched(launch_w4_vector(in_type, p, stream));
-    if (w4_tile_fits(p, workspace_bytes) && w4_tile_us(p, workspace_bytes) < w4_skinny_us(p))
-        return launched(launch_w4_tile(in_type, p, workspace, workspace_bytes, stream));
+    const bool vector = M <= kW4VectorRows;
+    const bool tiles = !vector && w4_tile_fits(p, workspace_bytes) && w4_tile_us(p, workspace_bytes) < w4_skinny_us(p);
+    op_note("w4 type %d -> %d M=%lld N=%lld K=%lld group=%lld: %s", (int)in_type, (int)c_type, (long long)M, (long long)N,
+            (long long)K, (long long)group, vector ? "dot products" : tiles ? "tiles" : "few rows");
+    if (vector) return launched(launch_w4_vector(in_type, p, stream));
+    if (tiles) return launched(launch_w4_tile(in_type, p, workspace, workspace_bytes, stream));
     return launched(launch_w4_skinny(in_type, p, stream));
 }
 

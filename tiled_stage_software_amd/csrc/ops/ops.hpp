@@ -14,7 +14,7 @@ enum : int { DT_F8E4M3 = 3 };   // continues common.hpp's DT_*: OCP 8-bit floats
 // Records a status and its text for gemm_last_error() and returns it (libgemm.cpp).
 gemm_status_t op_fail(gemm_status_t s, const char* fmt, ...);
 void op_clear_error();
-bool op_debug_on();
+void op_note(const char* fmt, ...);   // a line on stderr with GEMM_DEBUG set
 
 // ---------------------------------------------------------------- norm
 struct NormParams {

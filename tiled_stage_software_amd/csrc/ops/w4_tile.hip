@@ -471,8 +471,10 @@ hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, size_t ws_byt
     RowsJob ja, jw;
     copies_of(f, q, ja, jw);
     const size_t used = q.sums + q.sz + round256(q.parts), wants = used + (ja.src ? ja.bytes() : 0) + (jw.src ? jw.bytes() : 0);
-    const bool copies = (ja.src || jw.src) && wants <= ws_bytes;
+    const bool copies = (ja.src || jw.src) && wants <= ws_bytes && wants < (size_t(1) << 34);   // (rows_pack counts chunks in 32 bits)
     const bool direct = copies || (!ja.src && !jw.src);
+    op_note("  %d x %d tiles, units of %d, %d splits of K, %s loads%s", q.bm, kBN, q.unit, q.splits, direct ? "direct" : "staged",
+            copies ? " of copied rows" : "");
     t.W = f.W;
     t.ldw = f.ldw;
     if (copies) {
