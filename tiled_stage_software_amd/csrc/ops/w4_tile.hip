@@ -34,6 +34,10 @@ struct W4Tile {
     int64_t part;          // bytes between the splits' results
 };
 
+// A row's two chunks of codes change places in every other eight rows, so that the 16 rows a read takes lie on
+// different banks.
+__device__ __forceinline__ int codes_swz(int row) { return (row >> 3) & 1; }
+
 template <int BM>
 struct W4Layout {
     static constexpr int A_BYTES = BM * 128, Q_BYTES = kBN * 32;
@@ -63,7 +67,7 @@ struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> 
         C::init(smem_);
         const int wn = wave_id(), lane = lane_id(), r = lane % 16, g = lane / 16;
         const int kc = (g & 1) * 2 + (g >> 1);   // the k-chunk of lane group g, as in A's fragments
-        qo = (uint32_t)(Y::A_BYTES + (wn * 32 + r) * 32 + kc * 4);
+        qo = (uint32_t)(Y::A_BYTES + (wn * 32 + r) * 32 + codes_swz(r) * 16 + kc * 4);
         const int at = r * TM;                   // this lane's sums, TM of them
         so = (uint32_t)(Y::A_BYTES + Y::Q_BYTES + at / (BM / kNC) * Y::REGION + at % (BM / kNC) * 4);
         zo = (uint32_t)(Y::A_BYTES + Y::Q_BYTES + wn * Y::REGION + Y::SL * 16 + g * 16);
@@ -79,7 +83,7 @@ struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> 
             fa[BUF][i] = *reinterpret_cast<LDS_AS const u32x4*>(st + this->a_off[q / 2] + (q % 2 * AH + i) * 16 * 128);
         if (q % 2 == 0) {
 #pragma unroll
-            for (int j = 0; j < TN; ++j) word[j] = *reinterpret_cast<LDS_AS const uint32_t*>(st + qo + j * 16 * 32 + q / 2 * 16);
+            for (int j = 0; j < TN; ++j) word[j] = *reinterpret_cast<LDS_AS const uint32_t*>(st + (qo ^ (q / 2 * 16)) + j * 16 * 32);
         }
         if (q == 1) {   // (before the barrier that frees the slot)
 #pragma unroll
@@ -236,7 +240,7 @@ struct W4StagedOps : W4Compute<T, BM, S1> {
         }
 #pragma unroll
         for (int i = 0; i < CA; ++i) *reinterpret_cast<LDS_AS u32x4*>(st + dst + i * STEP * 128) = va[i];
-        *reinterpret_cast<LDS_AS u32x4*>(st + F::Y::A_BYTES + t * 16) = vq;
+        *reinterpret_cast<LDS_AS u32x4*>(st + F::Y::A_BYTES + (t ^ codes_swz(t / 2)) * 16) = vq;
         if (t < UT) *reinterpret_cast<LDS_AS u32x4*>(st + F::Y::A_BYTES + F::Y::Q_BYTES + t * 16) = vu;
         ask_write = false;
         wslot ^= 1;
@@ -272,6 +276,8 @@ void w4_tile_kernel(W4Tile p) {
         ops.p = &p; ops.tm = tm; ops.tn = tn; ops.s0 = s0;
         ops.la.init(p.g.A + ((int64_t)m0 * p.g.lda + (int64_t)s0 * kSlabK) * 2, p.g.lda * 2, kSlabK * 2);
         ops.lq.init(reinterpret_cast<const char*>(p.W) + (int64_t)n0 * p.ldw + (int64_t)s0 * (kSlabK / 2), p.ldw, kSlabK / 2);
+        const int lane = lane_id();
+        ops.lq.vpat[0] = (uint32_t)(lane / 2 * (int)p.ldw + ((lane % 2) ^ codes_swz(lane / 2)) * 16);
         gemm_sched::ring_mainloop<S, F::KS, 1>(ops, slabs);
         ops.template epilogue<OUT>(p.g, m0, n0, m_keep, n_keep);
     } else {
