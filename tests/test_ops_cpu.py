@@ -127,7 +127,7 @@ def test_debugging_names_the_kernel():
             "lg.gemm_rmsnorm(1, 1, 3, 2, 64, 1e-6, P, 64, 0, 0, P, 0, 0, P, 64, P, P)\n")
     env = dict(os.environ, GEMM_DEBUG="1")
     err = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, cwd=ROOT).stderr
-    for text in ("f8 -> type 1 M=1 N=64 K=256: few rows", "M=300 N=640 K=256: tiles", "128 x 128 tiles, 1 splits",
+    for text in ("f8 -> type 1 M=1 N=64 K=256: few rows", "M=300 N=640 K=256: tiles", " x 128 tiles, 1 splits of K",
                  "w4 type 1 -> 1 M=1 N=64 K=256 group=128: dot products", "rmsnorm type 1 -> 3 rows=2 cols=64"):
         assert text in err, (text, err)
     env.pop("GEMM_DEBUG")

@@ -1,4 +1,4 @@
-// f8_tile.hip -- the 8-bit product on large tiles: BM x BN of C per workgroup, slabs of 128
+// f8_tile.hip -- the 8-bit product on tiles: BM x BN of C per workgroup, slabs of 128
 // bytes of K in a two-slot LDS ring, v_mfma_f32_16x16x128_f8f6f4 (or its bf16 form for fp32
 // results) on 16 x 16 blocks.
 //
@@ -337,31 +337,41 @@ __global__ __launch_bounds__(256) void f8_join_kernel(const GemmParams p, const 
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct F8Plan {
-    int big;       // 256 x 256 tiles (else 128 x 128)
+    int bm, bn;    // rows and columns of a tile: 256 x 256, 128 x 128 or 64 x 128
     int splits;
 };
 
 // The tile with the least time on the fullest compute unit: a 256 x 256 tile costs four units and a 128 x 128 one
-// kSmallCost (both measured on 4096 x 4096 x 4096 and 8192^3).  Few small tiles are split along K where that pays: a slab
-// takes kSlabUs (fp32 results: kWideSlabUs) on a compute unit that has nothing else to hide its loads with, a split writes and reads
-// its fp32 sums once (at the rate of a copy) and needs one more launch.
-constexpr double kSmallCost = 1.35, kSlabUs = 0.45, kWideSlabUs = 1.0, kJoinUs = 4.0, kBytesPerUs = 4.5e6;
-constexpr double kStagedUs = 0.5;   // what a slab takes longer through registers from rows of any alignment
+// kSmallCost (both measured on 4096 x 4096 x 4096 and 8192^3).  Where small tiles do not fill the card: the height
+// and the splits of K that should be fastest.  A slab takes slab_us() on a compute unit that has nothing else to hide its
+// loads with; more workgroups than units share them at kShared; a split writes and reads its fp32
+// sums once (at the rate of a copy) and needs one more launch.
+constexpr double kSmallCost = 1.35, kShared = 0.75, kJoinUs = 4.0, kBytesPerUs = 4.5e6;
+double slab_us(int bm, bool wide) { return bm == 64 ? (wide ? 0.6 : 0.35) : (wide ? 1.05 : 0.5); }   // 112 to 256 workgroups, 16 to 32 slabs
+double staged_us(int bm) { return bm == 256 ? 1.0 : bm == 128 ? 0.5 : 0.4; }   // longer from rows of any alignment
+double rounds_of(int64_t workgroups) {
+    const int64_t cu = num_compute_units();
+    return workgroups <= cu ? 1.0 : kShared * ceil_div(workgroups, cu);
+}
 int64_t f8_ldp(int64_t N) { return (N + 3) / 4 * 4; }
 F8Plan f8_plan(int64_t M, int64_t N, int64_t K, bool wide) {
-    F8Plan q = {0, 1};
+    F8Plan q = {128, 128, 1};
     const int64_t cu = num_compute_units();
     const int64_t t256 = ceil_div(M, 256) * ceil_div(N, 256), t128 = ceil_div(M, 128) * ceil_div(N, 128);
-    q.big = !wide && M >= 256 && N >= 256 && ceil_div(t256, cu) * 4.0 <= ceil_div(t128, cu) * kSmallCost;
-    if (q.big || t128 > cu) return q;
+    if (!wide && M >= 256 && N >= 256 && ceil_div(t256, cu) * 4.0 <= ceil_div(t128, cu) * kSmallCost) return F8Plan{256, 256, 1};
+    if (t128 > cu) return q;
     const int64_t slabs = ceil_div(K, kSlabBytes);
     double best = 0.0;
-    for (int64_t s = 1; s <= 16 && s * 4 <= slabs + 3; ++s) {
-        const double us = ceil_div(t128 * s, cu) * ceil_div(slabs, s) * (wide ? kWideSlabUs : kSlabUs) +
-                          (s > 1 ? kJoinUs + s * (double)M * f8_ldp(N) * 8.0 / kBytesPerUs : 0.0);
-        if (s == 1 || us < best) {
-            best = us;
-            q.splits = (int)s;
+    for (int bm = 128; bm >= 64; bm -= 64) {
+        const int64_t tiles = ceil_div(M, bm) * ceil_div(N, 128);
+        for (int64_t s = 1; s <= 16 && s * 4 <= slabs + 3; ++s) {
+            const double us = rounds_of(tiles * s) * ceil_div(slabs, s) * slab_us(bm, wide) +
+                              (s > 1 ? kJoinUs + s * (double)M * f8_ldp(N) * 8.0 / kBytesPerUs : 0.0);
+            if (best == 0.0 || us < best) {
+                best = us;
+                q.bm = bm;
+                q.splits = (int)s;
+            }
         }
     }
     return q;
@@ -369,27 +379,30 @@ F8Plan f8_plan(int64_t M, int64_t N, int64_t K, bool wide) {
 
 // Whether the launch that copies (`bytes` of copies) costs less than the staged loads' slower slabs.
 bool f8_copy_pays(const F8Plan& q, const F8Params& f, int64_t slabs, size_t bytes) {
-    const int64_t bt = q.big ? 256 : 128, rounds = ceil_div(ceil_div(f.M, bt) * ceil_div(f.N, bt) * q.splits, num_compute_units());
-    const double staged_us = rounds * ceil_div(slabs, q.splits) * (q.big ? 2.0 : 1.0) * kStagedUs;
-    return kJoinUs + 2.0 * bytes / kBytesPerUs < staged_us;
+    const double rounds = rounds_of(ceil_div(f.M, q.bm) * ceil_div(f.N, q.bn) * q.splits);
+    return kJoinUs + 2.0 * bytes / kBytesPerUs < rounds * ceil_div(slabs, q.splits) * staged_us(q.bm);
 }
 
-template <int OUT, int BM, int WM, int WN, bool WIDE, int S>
+template <int OUT, int BM, int BN, int WM, int WN, bool WIDE, int S>
 hipError_t go(const GemmParams& p, const F8Extra& x, int splits, hipStream_t st) {
-    hipLaunchKernelGGL((f8_tile_kernel<OUT, BM, BM, WM, WN, 4, WIDE, S>), dim3((unsigned)(p.tiles_m * p.tiles_n), (unsigned)splits),
+    hipLaunchKernelGGL((f8_tile_kernel<OUT, BM, BN, WM, WN, 4, WIDE, S>), dim3((unsigned)(p.tiles_m * p.tiles_n), (unsigned)splits),
                        dim3(64 * WM * WN), 0, st, p, x);
     return hipGetLastError();
 }
-// Four slots for small tiles that have a compute unit to themselves, so that three slabs are on their way: else
-// a second workgroup, which two slots leave room for, does as much.
+// Small tiles that have a compute unit to themselves: eight waves, so that two on a SIMD take turns, and four slots, so that
+// three slabs are on their way.  Else a second workgroup, which two slots leave room for, does both.
 template <int OUT, bool WIDE>
 hipError_t tile_of(const F8Plan& q, bool direct, const GemmParams& p, const F8Extra& x, hipStream_t st) {
     if constexpr (!WIDE) {
-        if (q.big) return direct ? go<OUT, 256, 2, 4, WIDE, 2>(p, x, q.splits, st) : go<OUT, 256, 2, 4, WIDE, 0>(p, x, q.splits, st);
+        if (q.bm == 256) return direct ? go<OUT, 256, 256, 2, 4, WIDE, 2>(p, x, q.splits, st) : go<OUT, 256, 256, 2, 4, WIDE, 0>(p, x, q.splits, st);
     }
     const bool alone = (int64_t)p.tiles_m * p.tiles_n * q.splits <= num_compute_units();
-    if (!direct) return alone ? go<OUT, 128, 2, 4, WIDE, 0>(p, x, q.splits, st) : go<OUT, 128, 2, 2, WIDE, 0>(p, x, q.splits, st);
-    return alone ? go<OUT, 128, 2, 4, WIDE, 4>(p, x, q.splits, st) : go<OUT, 128, 2, 2, WIDE, 2>(p, x, q.splits, st);
+    if (q.bm == 64) {
+        if (!direct) return go<OUT, 64, 128, 1, 8, WIDE, 0>(p, x, q.splits, st);
+        return alone ? go<OUT, 64, 128, 1, 8, WIDE, 4>(p, x, q.splits, st) : go<OUT, 64, 128, 1, 8, WIDE, 2>(p, x, q.splits, st);
+    }
+    if (!direct) return alone ? go<OUT, 128, 128, 2, 4, WIDE, 0>(p, x, q.splits, st) : go<OUT, 128, 128, 2, 2, WIDE, 0>(p, x, q.splits, st);
+    return alone ? go<OUT, 128, 128, 2, 4, WIDE, 4>(p, x, q.splits, st) : go<OUT, 128, 128, 2, 2, WIDE, 2>(p, x, q.splits, st);
 }
 template <int OUT>
 hipError_t join_of(const GemmParams& p, const F8Extra& x, const void* part, int64_t ldp, int splits, hipStream_t st) {
@@ -405,11 +418,11 @@ constexpr size_t kMostCopied = size_t(1) << 34;   // rows_pack counts chunks in 
 
 size_t f8_tile_workspace(int64_t M, int64_t N, int64_t K, bool wide) {
     const F8Plan q = f8_plan(M, N, K, wide);
-    const int64_t bt = q.big ? 256 : 128, kp = ceil_div(K, kSlabBytes) * kSlabBytes;
+    const int64_t kp = ceil_div(K, kSlabBytes) * kSlabBytes;
     size_t bytes = q.splits > 1 ? (size_t)q.splits * M * f8_ldp(N) * sizeof(float) : 0;
     bytes = (bytes + 255) & ~size_t(255);
-    if (K % kSlabBytes || M < bt) bytes += (size_t)(std::max(M, bt) * kp);
-    if (K % kSlabBytes || N < bt) bytes += (size_t)(std::max(N, bt) * kp);
+    if (K % kSlabBytes || M < q.bm) bytes += (size_t)(std::max(M, (int64_t)q.bm) * kp);
+    if (K % kSlabBytes || N < q.bn) bytes += (size_t)(std::max(N, (int64_t)q.bn) * kp);
     return bytes;
 }
 
@@ -422,7 +435,6 @@ bool f8_tile_fits(const F8Params& f) {
 hipError_t launch_f8_tile(const F8Params& f, void* ws, size_t ws_bytes, hipStream_t st) {
     const bool wide = f.out_type == DT_F32;
     F8Plan q = f8_plan(f.M, f.N, f.K, wide);
-    const int bt = q.big ? 256 : 128;
     const int64_t slabs = ceil_div(f.K, kSlabBytes), ldp = f8_ldp(f.N), each = (int64_t)f.M * ldp * sizeof(float);
     if (!ws) ws_bytes = 0;
     if (q.splits > 1 && ws_bytes < (size_t)(q.splits * each)) q.splits = (int)(ws_bytes / each);
@@ -431,17 +443,17 @@ hipError_t launch_f8_tile(const F8Params& f, void* ws, size_t ws_bytes, hipStrea
     q.splits = (int)ceil_div(slabs, x.per_split);
     // operands that the direct copies cannot take, copied behind the splits' sums where there is room
     const int64_t kp = slabs * kSlabBytes;
-    auto copy_of = [&](const uint8_t* src, int64_t ld, int64_t rows) {
-        RowsJob j = {src, nullptr, ld, rows, f.K, std::max(rows, (int64_t)bt), kp};
-        if (rows >= bt && f.K == kp && ((uintptr_t)src | ld) % 16 == 0) j.src = nullptr;
+    auto copy_of = [&](const uint8_t* src, int64_t ld, int64_t rows, int64_t least) {
+        RowsJob j = {src, nullptr, ld, rows, f.K, std::max(rows, least), kp};
+        if (rows >= least && f.K == kp && ((uintptr_t)src | ld) % 16 == 0) j.src = nullptr;
         return j;
     };
-    RowsJob ja = copy_of(f.A, f.lda, f.M), jb = copy_of(f.B, f.ldb, f.N);
+    RowsJob ja = copy_of(f.A, f.lda, f.M, q.bm), jb = copy_of(f.B, f.ldb, f.N, q.bn);
     const size_t used = q.splits > 1 ? ((size_t)(q.splits * each) + 255) & ~size_t(255) : 0;
     const size_t wants = used + (ja.src ? ja.bytes() : 0) + (jb.src ? jb.bytes() : 0);
     const bool copies = (ja.src || jb.src) && wants <= ws_bytes && wants < kMostCopied && f8_copy_pays(q, f, slabs, wants - used);
     const bool direct = copies || (!ja.src && !jb.src);
-    op_note("  %d x %d tiles, %d splits of K, %s loads%s", bt, bt, q.splits, direct ? "direct" : "staged", copies ? " of copied rows" : "");
+    op_note("  %d x %d tiles, %d splits of K, %s loads%s", q.bm, q.bn, q.splits, direct ? "direct" : "staged", copies ? " of copied rows" : "");
     F8Params o = f;
     if (copies) {
         ja.dst = static_cast<uint8_t*>(ws) + used;
@@ -460,8 +472,8 @@ hipError_t launch_f8_tile(const F8Params& f, void* ws, size_t ws_bytes, hipStrea
     p.M = f.M; p.N = f.N; p.K = o.K;
     p.alpha = f.alpha; p.beta = f.beta;
     p.out_type = f.out_type;
-    p.tiles_m = (int)ceil_div(f.M, bt);
-    p.tiles_n = (int)ceil_div(f.N, bt);
+    p.tiles_m = (int)ceil_div(f.M, q.bm);
+    p.tiles_n = (int)ceil_div(f.N, q.bn);
     p.group_m = 8;
     p.xcd_remap = 1;
     if (q.splits > 1) {
