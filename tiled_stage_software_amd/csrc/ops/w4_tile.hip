@@ -27,8 +27,9 @@ struct W4Tile {
     GemmParams g;          // A, C, sizes, tiles; B unused
     const uint8_t* W;
     int64_t ldw;
-    const char* sums;      // [unit][tile of M][BM] floats
-    uint32_t sz_at;        // from there: [unit][tile of N][128], scale in the low half, zero point in the high one
+    const char* scales;    // [unit][tile of N][128] floats
+    const char* zeros;     // the same: -s * (1 + z/16)
+    const char* sums;      // [unit][tile of M][BM] floats, a lane's together
     int per_unit;          // slabs of a unit (0: two units to a slab)
     int per_split;         // slabs of a split of K
     int64_t part;          // bytes between the splits' results
@@ -38,28 +39,21 @@ struct W4Tile {
 // different banks.
 __device__ __forceinline__ int codes_swz(int row) { return (row >> 3) & 1; }
 
-template <int BM>
-struct W4Layout {
-    static constexpr int A_BYTES = BM * 128, Q_BYTES = kBN * 32;
-    static constexpr int SL = BM / 16, REGION = (SL + 8) * 16;   // a copying wave's piece of a unit: SL chunks of sums, 8 of scales
-    static constexpr int UNIT = kNC * REGION;
-};
-
 // S1: units are 32 k, two to a slab.
 template <int T, int BM, bool S1>
 struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> {
     typedef MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> C;
-    typedef W4Layout<BM> Y;
     static constexpr int TM = C::TM, TN = C::TN, AH = TM / 2, NU = S1 ? 2 : 1;
-    static constexpr int STAGE = Y::A_BYTES + Y::Q_BYTES + NU * Y::UNIT;
+    static constexpr int A_BYTES = BM * 128, Q_BYTES = kBN * 32, S_AT = A_BYTES + Q_BYTES;
+    static constexpr int SL = 8 * NU;   // chunks of a wave's scales: [wave][unit][8]
+    static constexpr int STAGE = S_AT + kNC * SL * 16;
     static constexpr int KS = 4;   // steps of a slab: two k-steps by two halves of A's blocks
     static_assert(TN == 2 && TM % 2 == 0, "waves of 32 columns");
     f32x4 dot[TM][TN];
     u32x4 fa[2][AH], b[TN];
     uint32_t word[TN];
-    u32x4 fsz[NU][TN];
-    f32x4 fsum[NU][TM / 4];
-    uint32_t qo, zo, so;   // LDS offsets of codes, scales and sums within a slot
+    f32x4 scale[NU][TN];
+    uint32_t qo, so;   // LDS offsets of codes and scales within a slot
     Spread<T> spread;
     int pos = 0, per_unit, left;   // slab within its unit; slabs left
 
@@ -67,10 +61,8 @@ struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> 
         C::init(smem_);
         const int wn = wave_id(), lane = lane_id(), r = lane % 16, g = lane / 16;
         const int kc = (g & 1) * 2 + (g >> 1);   // the k-chunk of lane group g, as in A's fragments
-        qo = (uint32_t)(Y::A_BYTES + (wn * 32 + r) * 32 + codes_swz(r) * 16 + kc * 4);
-        const int at = r * TM;                   // this lane's sums, TM of them
-        so = (uint32_t)(Y::A_BYTES + Y::Q_BYTES + at / (BM / kNC) * Y::REGION + at % (BM / kNC) * 4);
-        zo = (uint32_t)(Y::A_BYTES + Y::Q_BYTES + wn * Y::REGION + Y::SL * 16 + g * 16);
+        qo = (uint32_t)(A_BYTES + (wn * 32 + r) * 32 + codes_swz(r) * 16 + kc * 4);
+        so = (uint32_t)(S_AT + wn * SL * 16 + g * 16);
         per_unit = p.per_unit;
         left = slabs;
     }
@@ -87,12 +79,9 @@ struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> 
         }
         if (q == 1) {   // (before the barrier that frees the slot)
 #pragma unroll
-            for (int u = 0; u < NU; ++u) {
+            for (int u = 0; u < NU; ++u)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) fsz[u][j] = *reinterpret_cast<LDS_AS const u32x4*>(st + zo + u * Y::UNIT + j * 64);
-#pragma unroll
-                for (int i = 0; i < TM / 4; ++i) fsum[u][i] = *reinterpret_cast<LDS_AS const f32x4*>(st + so + u * Y::UNIT + i * 16);
-            }
+                for (int j = 0; j < TN; ++j) scale[u][j] = *reinterpret_cast<LDS_AS const f32x4*>(st + so + u * 128 + j * 64);
         }
     }
     template <int BUF, bool FIRST>
@@ -106,21 +95,56 @@ struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> 
                 d = Half<T>::mfma(b[j], fa[BUF][i], FIRST ? zero : d);
             }
     }
-    // acc += s * (dot - (1 + z/16) * sum)
     __device__ __forceinline__ void finish_unit(int u) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            float s[4], z[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[e] = to_f32<T>((uint16_t)fsz[u][j][e]);
-                z[e] = -zero16<T>((uint16_t)(fsz[u][j][e] >> 16));
-            }
+        for (int j = 0; j < TN; ++j)
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    this->acc[i][j][e] = __builtin_fmaf(s[e], __builtin_fmaf(z[e], fsum[u][i / 4][i % 4], dot[i][j][e]), this->acc[i][j][e]);
+                for (int e = 0; e < 4; ++e) this->acc[i][j][e] = __builtin_fmaf(scale[u][j][e], dot[i][j][e], this->acc[i][j][e]);
+    }
+    // acc += zeros * sums over units u0 .. end - 1, four of them a step, each eight k of the instruction: a float is cut into
+    // three bf16 parts h, m, l that hold all its bits, and of the nine products all but l * l are taken.
+    static __device__ __forceinline__ void cut(float v, uint32_t& h, uint32_t& m, uint32_t& l) {
+        h = __builtin_bit_cast(uint32_t, v) & 0xFFFF0000u;
+        v -= __builtin_bit_cast(float, h);
+        m = __builtin_bit_cast(uint32_t, v) & 0xFFFF0000u;
+        l = __builtin_bit_cast(uint32_t, v - __builtin_bit_cast(float, m));
+    }
+    static __device__ __forceinline__ uint32_t tops(uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); }
+    __device__ __forceinline__ void zero_points(const W4Tile& p, int tm, int tn, int u0, int end) {
+        const int lane = lane_id(), r = lane % 16, g = lane / 16;
+        const char* sums = p.sums + ((int64_t)tm * BM + r * TM) * 4;
+        const char* zeros = p.zeros + ((int64_t)tn * kBN + wave_id() * 32 + r) * 4;
+        const int64_t sum_step = (int64_t)p.g.tiles_m * BM * 4, zero_step = (int64_t)p.g.tiles_n * kBN * 4;
+        f32x4 sum[TM / 4];
+        float zero[TN];
+        auto load = [&](int u) {   // (past the end: the last one's)
+            const int at = min(u + g, end - 1);
+#pragma unroll
+            for (int i = 0; i < TM / 4; ++i) sum[i] = *reinterpret_cast<const f32x4*>(sums + at * sum_step + i * 16);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) zero[j] = *reinterpret_cast<const float*>(zeros + at * zero_step + j * 64);
+        };
+        load(u0);
+        for (int u = u0; u < end; u += 4) {
+            uint32_t h, m, l;
+            u32x4 zb[TN], sb[TM];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                cut(u + g < end ? zero[j] : 0.0f, h, m, l);
+                zb[j] = u32x4{tops(h, m), tops(h, l), tops(m, h), tops(m, l)};
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                cut(u + g < end ? sum[i / 4][i % 4] : 0.0f, h, m, l);
+                sb[i] = u32x4{tops(h, h), tops(m, h), tops(m, l), tops(l, m)};
+            }
+            load(u + 4);
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int i = 0; i < TM; ++i) this->acc[i][j] = Half<DT_BF16>::mfma(zb[j], sb[i], this->acc[i][j]);
         }
     }
     template <int BUF>
@@ -149,12 +173,9 @@ struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> 
     __device__ __forceinline__ void barrier() { gemm::barrier(); }
 };
 
-// Where chunk l of a unit's piece that copying wave w brings lies, in bytes from the sums on.
-template <int BM>
-__device__ __forceinline__ uint32_t unit_chunk(const W4Tile& p, int tm, int tn, int unit, int w, int l) {
-    constexpr int SL = W4Layout<BM>::SL;
-    if (l < SL) return (((uint32_t)unit * p.g.tiles_m + tm) * BM + w * (BM / kNC)) * 4 + l * 16;
-    return p.sz_at + (((uint32_t)unit * p.g.tiles_n + tn) * kBN + w * (kBN / kNC)) * 4 + (l - SL) * 16;
+// Where chunk l (of SL) of wave w's scales lies, from unit `unit` on.
+__device__ __forceinline__ uint32_t scale_chunk(const W4Tile& p, int tn, int unit, int w, int l) {
+    return (((uint32_t)(unit + l / 8) * p.g.tiles_n + tn) * kBN + w * (kBN / kNC)) * 4 + l % 8 * 16;
 }
 // First unit of slab s of the whole K.
 __device__ __forceinline__ int unit_of(const W4Tile& p, int s) { return p.per_unit ? s / p.per_unit : 2 * s; }
@@ -165,21 +186,17 @@ struct W4RingOps : W4Compute<T, BM, S1> {
     typedef W4Compute<T, BM, S1> F;
     DirectLoader<BM, 128, kNC, true> la;
     DirectLoader<kBN, 32, kNC, false> lq;
-    static constexpr int L = decltype(la)::IPW + decltype(lq)::IPW + F::NU;
+    static constexpr int L = decltype(la)::IPW + decltype(lq)::IPW + 1;
     const W4Tile* p;
-    int tm, tn, s0;
+    int tn, s0;
     __device__ __forceinline__ void issue(int slab, int slot, int, int) {
         LDS_AS char* st = this->smem + slot * F::STAGE;
         la.issue(slab, st, 0, decltype(la)::IPW);
-        lq.issue(slab, st + F::Y::A_BYTES, 0, decltype(lq)::IPW);
-        const int w = wave_id(), lane = lane_id(), u0 = unit_of(*p, s0 + slab);
-#pragma unroll
-        for (int u = 0; u < F::NU; ++u) {
-            LDS_AS char* to = st + F::Y::A_BYTES + F::Y::Q_BYTES + u * F::Y::UNIT + w * F::Y::REGION;
-            if (lane < F::Y::SL + 8)
-                la.template copy<0>(__builtin_amdgcn_make_buffer_rsrc((void*)p->sums, (short)0, -1, kBufferFlags),
-                                    unit_chunk<BM>(*p, tm, tn, u0 + u, w, lane), 0, to);
-        }
+        lq.issue(slab, st + F::A_BYTES, 0, decltype(lq)::IPW);
+        const int w = wave_id(), lane = lane_id();
+        if (lane < F::SL)
+            la.template copy<0>(__builtin_amdgcn_make_buffer_rsrc((void*)p->scales, (short)0, -1, kBufferFlags),
+                                scale_chunk(*p, tn, unit_of(*p, s0 + slab), w, lane), 0, st + F::S_AT + w * F::SL * 16);
     }
     template <int N>
     __device__ __forceinline__ void wait_slabs() { wait_vm<N * L>(); }
@@ -194,7 +211,7 @@ template <int T, int BM, bool S1>
 struct W4StagedOps : W4Compute<T, BM, S1> {
     typedef W4Compute<T, BM, S1> F;
     static constexpr int NT = 64 * kNC, STEP = NT / 8, CA = BM / STEP;
-    static constexpr int UT = F::NU * kNC * (F::Y::SL + 8);   // threads with a chunk of the units
+    static constexpr int UT = kNC * F::SL;   // threads with a chunk of the scales
     static_assert(STEP % 16 == 0 && CA * STEP == BM && UT <= NT && 2 * kBN == NT, "chunks per thread");
     const char* arow[CA];
     const uint8_t* qrow;
@@ -204,7 +221,7 @@ struct W4StagedOps : W4Compute<T, BM, S1> {
     const W4Tile* p;
     int k_bytes, q_bytes, s0, wslot = 0, slab_ = 0;
     bool ask_write = false;
-    __device__ __forceinline__ void init_rows(const W4Tile& p_, int tm, int tn, int m0, int n0, int s0_) {
+    __device__ __forceinline__ void init_rows(const W4Tile& p_, int tn, int m0, int n0, int s0_) {
         p = &p_;
         s0 = s0_;
         k_bytes = p->g.K * 2;
@@ -214,9 +231,8 @@ struct W4StagedOps : W4Compute<T, BM, S1> {
         for (int i = 0; i < CA; ++i) arow[i] = p->g.A + (int64_t)min(m0 + row + i * STEP, p->g.M - 1) * p->g.lda * 2;
         dst = (uint32_t)(row * 128 + ((c ^ swz<8>(row)) << 4));
         qrow = p->W + (int64_t)min(n0 + t / 2, p->g.N - 1) * p->ldw;
-        constexpr int PIECE = F::Y::SL + 8;
-        uchunk = unit_chunk<BM>(*p, tm, tn, t < UT ? t / (kNC * PIECE) : 0, t / PIECE % kNC, t % PIECE);
-        ustep = (uint32_t)(t % PIECE < F::Y::SL ? p->g.tiles_m * BM : p->g.tiles_n * kBN) * 4;
+        uchunk = scale_chunk(*p, tn, 0, t / F::SL % kNC, t % F::SL);
+        ustep = (uint32_t)(p->g.tiles_n * kBN) * 4;
     }
     __device__ __forceinline__ void load(int slab) {
         slab_ = s0 + slab;
@@ -225,7 +241,7 @@ struct W4StagedOps : W4Compute<T, BM, S1> {
 #pragma unroll
         for (int i = 0; i < CA; ++i) va[i] = load16(arow[i] + ka);
         vq = load16(qrow + kq);
-        if ((int)threadIdx.x < UT) vu = load16(p->sums + (uchunk + (uint32_t)unit_of(*p, slab_) * ustep));
+        if ((int)threadIdx.x < UT) vu = load16(p->scales + (uchunk + (uint32_t)unit_of(*p, slab_) * ustep));
         ask_write = true;
     }
     __device__ __forceinline__ void put() {
@@ -240,8 +256,8 @@ struct W4StagedOps : W4Compute<T, BM, S1> {
         }
 #pragma unroll
         for (int i = 0; i < CA; ++i) *reinterpret_cast<LDS_AS u32x4*>(st + dst + i * STEP * 128) = va[i];
-        *reinterpret_cast<LDS_AS u32x4*>(st + F::Y::A_BYTES + (t ^ codes_swz(t / 2)) * 16) = vq;
-        if (t < UT) *reinterpret_cast<LDS_AS u32x4*>(st + F::Y::A_BYTES + F::Y::Q_BYTES + t * 16) = vu;
+        *reinterpret_cast<LDS_AS u32x4*>(st + F::A_BYTES + (t ^ codes_swz(t / 2)) * 16) = vq;
+        if (t < UT) *reinterpret_cast<LDS_AS u32x4*>(st + F::S_AT + t * 16) = vu;
         ask_write = false;
         wslot ^= 1;
     }
@@ -269,22 +285,25 @@ void w4_tile_kernel(W4Tile p) {
     const int m0 = max(0, min(m_keep, p.g.M - BM)), n0 = max(0, min(n_keep, p.g.N - kBN));
     const int s0 = (int)blockIdx.y * p.per_split;
     const int slabs = min((p.g.K + kSlabK - 1) / kSlabK - s0, p.per_split);
+    const int u0 = unit_of(p, s0), u1 = S1 ? u0 + 2 * slabs : u0 + (slabs + p.per_unit - 1) / p.per_unit;
     p.g.C += (int64_t)blockIdx.y * p.part;
     if constexpr (DIRECT) {
         W4RingOps<T, BM, S1> ops;
         ops.init(smem, p, slabs);
-        ops.p = &p; ops.tm = tm; ops.tn = tn; ops.s0 = s0;
+        ops.p = &p; ops.tn = tn; ops.s0 = s0;
         ops.la.init(p.g.A + ((int64_t)m0 * p.g.lda + (int64_t)s0 * kSlabK) * 2, p.g.lda * 2, kSlabK * 2);
         ops.lq.init(reinterpret_cast<const char*>(p.W) + (int64_t)n0 * p.ldw + (int64_t)s0 * (kSlabK / 2), p.ldw, kSlabK / 2);
         const int lane = lane_id();
         ops.lq.vpat[0] = (uint32_t)(lane / 2 * (int)p.ldw + ((lane % 2) ^ codes_swz(lane / 2)) * 16);
         gemm_sched::ring_mainloop<S, F::KS, 1>(ops, slabs);
+        ops.zero_points(p, tm, tn, u0, u1);
         ops.template epilogue<OUT>(p.g, m0, n0, m_keep, n_keep);
     } else {
         W4StagedOps<T, BM, S1> ops;
         ops.init(smem, p, slabs);
-        ops.init_rows(p, tm, tn, m0, n0, s0);
+        ops.init_rows(p, tn, m0, n0, s0);
         gemm_sched::staged_mainloop<S, F::KS>(ops, slabs);
+        ops.zero_points(p, tm, tn, u0, u1);
         ops.template epilogue<OUT>(p.g, m0, n0, m_keep, n_keep);
     }
 }
@@ -296,7 +315,8 @@ struct W4Prepare {
     const uint16_t* scales;
     const uint16_t* zeros;
     float* sums;
-    uint32_t* sz;
+    float* s;
+    float* z;
     int64_t lda, lds;
     int M, N, K, group, unit, units, tiles_m, tiles_n, bm, tm;   // tm: blocks of 16 rows of a tile
     int64_t sum_blocks;
@@ -321,7 +341,7 @@ __global__ __launch_bounds__(256) void w4_prepare_kernel(const W4Prepare p) {
         }
         sum += __shfl_xor(sum, 1, 64);
         sum += __shfl_xor(sum, 2, 64);
-            if (threadIdx.x % 4 == 0)
+        if (threadIdx.x % 4 == 0)
             p.sums[(int64_t)u * rows + (int64_t)tile * p.bm + local % 16 * p.tm + local / 16] = sum;   // a lane's tm sums side by side
         return;
     }
@@ -345,7 +365,13 @@ __global__ __launch_bounds__(256) void w4_prepare_kernel(const W4Prepare p) {
     __syncthreads();
 #pragma unroll
     for (int u = threadIdx.x / kTurnCols; u < kTurnUnits; u += 256 / kTurnCols)
-        if (u0 + u < p.units) p.sz[(u0 + u) * cols + at0 + threadIdx.x % kTurnCols] = turn[u][threadIdx.x % kTurnCols];
+        if (u0 + u < p.units) {
+            const int64_t i = (u0 + u) * cols + at0 + threadIdx.x % kTurnCols;
+            const uint32_t v = turn[u][threadIdx.x % kTurnCols];
+            const float s = to_f32<T>((uint16_t)v);
+            p.s[i] = s;
+            p.z[i] = -s * zero16<T>((uint16_t)(v >> 16));
+        }
 }
 
 // C = alpha * (sum of the splits, in order) + beta * C
@@ -389,7 +415,7 @@ W4Plan w4_plan(int64_t M, int64_t N, int64_t K, int64_t group, size_t room) {
     q.slabs = ceil_div(K, kSlabK);
     q.unit = group % kSlabK == 0 ? (int)group : 32;
     q.units = (int)(q.unit == 32 ? 2 * q.slabs : ceil_div(K, group));
-    q.sz = round256((size_t)q.units * q.tiles_n * kBN * 4);
+    q.sz = (size_t)q.units * q.tiles_n * kBN * 8;
     const int64_t per_unit = q.unit == 32 ? 1 : group / kSlabK, each = M * ldp_of(N) * 4;
     int64_t s = 1;
     for (int bm = 64; bm <= 128; bm += 64) {
@@ -451,7 +477,8 @@ hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, size_t ws_byt
     a.scales = reinterpret_cast<const uint16_t*>(f.scales);
     a.zeros = reinterpret_cast<const uint16_t*>(f.zeros);
     a.sums = reinterpret_cast<float*>(ws);
-    a.sz = reinterpret_cast<uint32_t*>(ws + q.sums);
+    a.s = reinterpret_cast<float*>(ws + q.sums);
+    a.z = reinterpret_cast<float*>(ws + q.sums + q.sz / 2);
     a.lda = f.lda; a.lds = f.lds;
     a.M = f.M; a.N = f.N; a.K = f.K; a.group = f.group;
     a.unit = q.unit; a.units = q.units;
@@ -498,7 +525,8 @@ hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, size_t ws_byt
         }
     }
     t.sums = ws;
-    t.sz_at = (uint32_t)q.sums;
+    t.scales = ws + q.sums;
+    t.zeros = ws + q.sums + q.sz / 2;
     t.per_unit = q.unit == 32 ? 0 : q.unit / kSlabK;
     t.per_split = q.per_split;
     if (q.splits > 1) {
