@@ -35,19 +35,20 @@ template <> struct Half<DT_F16> {
 template <int T>
 struct Spread {
     static constexpr int TOP = Half<T>::TOP;
-    uint32_t mask, ones;
-    __device__ __forceinline__ Spread() : mask(0x000F000Fu << TOP), ones(Half<T>::ONES) {
+    uint32_t mask, ones, twice;
+    __device__ __forceinline__ Spread() : mask(0x000F000Fu << TOP), ones(Half<T>::ONES), twice(0x1001u << TOP) {
         asm("" : "+s"(mask));
         asm("" : "+v"(ones));
+        asm("" : "+v"(twice));
     }
     __device__ __forceinline__ uint32_t place(uint32_t v) const { return (v & mask) | ones; }
     // Eight codes (code i in bits 4 i .. 4 i + 3) in their order.  Two rotations put every even and every odd
     // code at bit TOP of some byte; a byte permute then pairs codes 2 i and 2 i + 1: ten operations.
     __device__ __forceinline__ u32x4 in_order(uint32_t w) const {
-        const uint32_t even = __builtin_amdgcn_alignbit(w, w, 32 - TOP);          // left by TOP
-        const uint32_t odd = __builtin_amdgcn_alignbit(w, w, (36 - TOP) & 31);    // left by TOP - 4
-        return u32x4{place(__builtin_amdgcn_perm(odd, even, 0x05040100u)), place(__builtin_amdgcn_perm(odd, even, 0x06050201u)),
-                     place(__builtin_amdgcn_perm(odd, even, 0x07060302u)), place(__builtin_amdgcn_perm(odd, even, 0x04070003u))};
+        u32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = place(__umul24((w >> 8 * i) & 0xFF, twice));
+        return v;
     }
     // The same as pairs (0, 4), (1, 5), (2, 6), (3, 7), for an A whose eight elements lie so: eight operations.
     __device__ __forceinline__ u32x4 in_pairs(uint32_t w) const {
