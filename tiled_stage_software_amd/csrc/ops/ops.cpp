@@ -256,7 +256,8 @@ gemm_status_t gemm_w4_workspace_size(gemm_dtype_t in_type, int64_t M, int64_t N,
     REQUIRE(group >= 32 && group % 32 == 0 && group <= kMaxSize, "group=%lld: a multiple of 32", (long long)group);
     if (M > kW4VectorRows && N > 0 && K > 0) {
         W4Params p = {};
-        p.M = (int)M; p.N = (int)N; p.K = (int)K; p.group = (int)group;   // (of aligned operands)
+        p.M = (int)M; p.N = (int)N; p.K = (int)K; p.group = (int)group;
+        p.lda = K; p.ldw = (K + 1) / 2;   // (of contiguous operands)
         if (w4_tile_us(p, SIZE_MAX / 2) < w4_skinny_us(p)) *bytes = w4_tile_workspace(M, N, K, group);
     }
     return GEMM_OK;

@@ -181,12 +181,15 @@ hipError_t skinny_of(const W4Params& p, hipStream_t st) {
 }  // namespace
 
 // Expected microseconds: rounds of workgroups, each a start and its waves' steps in turn (measured from 1 to 32 steps
-// and 1 to 112 rounds).
+// and 1 to 112 rounds).  Groups below 128 end more often; rows that are not 16-byte aligned take two lines a load
+// (128 x 3001 x 9001, groups of 64: 70 us, on tiles with copied rows 39).
 double w4_skinny_us(const W4Params& p) {
     const int64_t mt = p.M <= 16 ? 1 : 2, blocks = ((int64_t)p.N + 15) / 16 * ((p.M + 16 * mt - 1) / (16 * mt));
     const int64_t waves = w4_waves(p, (int)mt), at_once = num_compute_units() * (mt == 1 ? 16 : 8) / waves;
     const double steps = (double)(((int64_t)p.K + kStep * waves - 1) / (kStep * waves));
-    return 3.0 + (double)((blocks + at_once - 1) / at_once) * (2.7 + 0.95 * steps);
+    const bool aligned = ((uintptr_t)p.A | (uintptr_t)p.W | (uint64_t)p.lda * 2 | (uint64_t)p.ldw) % 16 == 0;
+    const double step_us = 0.95 * (p.group < 128 ? 1.2 : 1.0) * (aligned ? 1.0 : 2.0);
+    return 3.0 + (double)((blocks + at_once - 1) / at_once) * (2.7 + step_us * steps);
 }
 
 hipError_t launch_w4_skinny(int in_type, const W4Params& p, hipStream_t st) {
