@@ -11,8 +11,8 @@
 // read anew for the next slab in the last step, each right after its last use.
 #include <algorithm>
 
-#include "../mfma.hpp"
 #include "f8_common.hpp"
+#include "short_loader.hpp"
 
 namespace gemm {
 namespace {
@@ -114,7 +114,7 @@ struct F8Compute : MfmaCompute<__bf16, BM, BN, 64, WM, WN, 16> {
 template <int S, int BM, int BN, int WM, int WN, int KS, bool WIDE, int NC, bool COPY>
 struct F8RingOps : F8Compute<BM, BN, WM, WN, KS, WIDE> {
     typedef F8Compute<BM, BN, WM, WN, KS, WIDE> F;
-    DirectLoader<BM, kSlabBytes, NC, true> la;
+    ALoader<BM, kSlabBytes, NC> la;
     DirectLoader<BN, kSlabBytes, NC, true> lb;
     static constexpr int LA = decltype(la)::IPW, L = LA + decltype(lb)::IPW;
     int slab_ = 0, slot_ = 0;
@@ -297,7 +297,7 @@ void f8_tile_kernel(GemmParams p, const F8Extra x) {
         if (NC == NW || wave_id() < NC) {
             F8RingOps<S, BM, BN, WM, WN, KS, WIDE, NC, true> ops;
             ops.init(smem);
-            ops.la.init(reinterpret_cast<const char*>(A) + (int64_t)m0 * p.lda, p.lda, kSlabBytes);
+            init_a<BM, kSlabBytes, NC>(ops.la, reinterpret_cast<const char*>(A) + (int64_t)m0 * p.lda, p.lda, kSlabBytes, p.M - m0);
             ops.lb.init(reinterpret_cast<const char*>(B) + (int64_t)n0 * p.ldb, p.ldb, kSlabBytes);
             gemm_sched::ring_mainloop<S, KS, 1>(ops, slabs);
             finish(ops);
@@ -413,15 +413,15 @@ hipError_t join_of(const GemmParams& p, const F8Extra& x, const void* part, int6
 
 }  // namespace
 
-// Bytes for the splits and, for rows that whole slabs do not fill, the copies of both operands.
 constexpr size_t kMostCopied = size_t(1) << 34;   // rows_pack counts chunks in 32 bits
 
+// Bytes for the splits and, for rows that whole slabs do not fill, the copies of both operands.
 size_t f8_tile_workspace(int64_t M, int64_t N, int64_t K, bool wide) {
     const F8Plan q = f8_plan(M, N, K, wide);
     const int64_t kp = ceil_div(K, kSlabBytes) * kSlabBytes;
     size_t bytes = q.splits > 1 ? (size_t)q.splits * M * f8_ldp(N) * sizeof(float) : 0;
     bytes = (bytes + 255) & ~size_t(255);
-    if (K % kSlabBytes || M < q.bm) bytes += (size_t)(std::max(M, (int64_t)q.bm) * kp);
+    if (K % kSlabBytes || M < least_rows(q.bm)) bytes += (size_t)(std::max(M, least_rows(q.bm)) * kp);
     if (K % kSlabBytes || N < q.bn) bytes += (size_t)(std::max(N, (int64_t)q.bn) * kp);
     return bytes;
 }
@@ -448,7 +448,7 @@ hipError_t launch_f8_tile(const F8Params& f, void* ws, size_t ws_bytes, hipStrea
         if (rows >= least && f.K == kp && ((uintptr_t)src | ld) % 16 == 0) j.src = nullptr;
         return j;
     };
-    RowsJob ja = copy_of(f.A, f.lda, f.M, q.bm), jb = copy_of(f.B, f.ldb, f.N, q.bn);
+    RowsJob ja = copy_of(f.A, f.lda, f.M, least_rows(q.bm)), jb = copy_of(f.B, f.ldb, f.N, q.bn);
     const size_t used = q.splits > 1 ? ((size_t)(q.splits * each) + 255) & ~size_t(255) : 0;
     const size_t wants = used + (ja.src ? ja.bytes() : 0) + (jb.src ? jb.bytes() : 0);
     const bool copies = (ja.src || jb.src) && wants <= ws_bytes && wants < kMostCopied && f8_copy_pays(q, f, slabs, wants - used);

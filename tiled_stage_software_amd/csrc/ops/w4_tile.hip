@@ -13,7 +13,7 @@
 // accumulators; and scales with zero points, transposed to rows of columns.
 #include <algorithm>
 
-#include "../mfma.hpp"
+#include "short_loader.hpp"
 #include "w4_common.hpp"
 
 namespace gemm {
@@ -184,7 +184,7 @@ __device__ __forceinline__ int unit_of(const W4Tile& p, int s) { return p.per_un
 template <int T, int BM, bool S1>
 struct W4RingOps : W4Compute<T, BM, S1> {
     typedef W4Compute<T, BM, S1> F;
-    DirectLoader<BM, 128, kNC, true> la;
+    ALoader<BM, 128, kNC> la;
     DirectLoader<kBN, 32, kNC, false> lq;
     static constexpr int L = decltype(la)::IPW + decltype(lq)::IPW + 1;
     const W4Tile* p;
@@ -291,7 +291,7 @@ void w4_tile_kernel(W4Tile p) {
         W4RingOps<T, BM, S1> ops;
         ops.init(smem, p, slabs);
         ops.p = &p; ops.tn = tn; ops.s0 = s0;
-        ops.la.init(p.g.A + ((int64_t)m0 * p.g.lda + (int64_t)s0 * kSlabK) * 2, p.g.lda * 2, kSlabK * 2);
+        init_a<BM, 128, kNC>(ops.la, p.g.A + ((int64_t)m0 * p.g.lda + (int64_t)s0 * kSlabK) * 2, p.g.lda * 2, kSlabK * 2, p.g.M - m0);
         ops.lq.init(reinterpret_cast<const char*>(p.W) + (int64_t)n0 * p.ldw + (int64_t)s0 * (kSlabK / 2), p.ldw, kSlabK / 2);
         const int lane = lane_id();
         ops.lq.vpat[0] = (uint32_t)(lane / 2 * (int)p.ldw + ((lane % 2) ^ codes_swz(lane / 2)) * 16);
@@ -464,9 +464,9 @@ hipError_t out_of(const W4Plan& q, const W4Tile& t, bool direct, hipStream_t st)
 // Copies of A and the codes that make their rows fit the direct copies (src NULL: they do).
 void copies_of(const W4Params& f, const W4Plan& q, RowsJob& a, RowsJob& w) {
     const int64_t kp = q.slabs * kSlabK;
-    a = {reinterpret_cast<const uint8_t*>(f.A), nullptr, f.lda * 2, f.M, (int64_t)f.K * 2, std::max((int64_t)f.M, (int64_t)q.bm), kp * 2};
+    a = {reinterpret_cast<const uint8_t*>(f.A), nullptr, f.lda * 2, f.M, (int64_t)f.K * 2, std::max((int64_t)f.M, least_rows(q.bm)), kp * 2};
     w = {f.W, nullptr, f.ldw, f.N, ((int64_t)f.K + 1) / 2, std::max((int64_t)f.N, (int64_t)kBN), kp / 2};
-    if (f.K == kp && f.M >= q.bm && ((uintptr_t)a.src | a.ld) % 16 == 0 && f.lda <= (1 << 21)) a.src = nullptr;
+    if (f.K == kp && f.M >= least_rows(q.bm) && ((uintptr_t)a.src | a.ld) % 16 == 0 && f.lda <= (1 << 21)) a.src = nullptr;
     if (f.K == kp && f.N >= kBN && ((uintptr_t)w.src | w.ld) % 16 == 0 && f.ldw <= (1 << 22)) w.src = nullptr;
 }
 
@@ -554,7 +554,7 @@ hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, size_t ws_byt
 size_t w4_tile_workspace(int64_t M, int64_t N, int64_t K, int64_t group) {
     const W4Plan q = w4_plan(M, N, K, group, ~size_t(0) >> 1);
     size_t bytes = q.sums + q.sz + round256(q.parts);
-    if (K % kSlabK || M < q.bm) bytes += (size_t)(std::max(M, (int64_t)q.bm) * q.slabs * kSlabK * 2);
+    if (K % kSlabK || M < least_rows(q.bm)) bytes += (size_t)(std::max(M, least_rows(q.bm)) * q.slabs * kSlabK * 2);
     if (K % kSlabK || N < kBN) bytes += (size_t)(std::max(N, (int64_t)kBN) * q.slabs * kSlabK / 2);
     return bytes;
 }
