@@ -535,3 +535,76 @@ def test_example_block():
     assert off < 0.15
     for t in (out, dx, dw):
         assert bool(torch.isfinite(t).all())
+
+
+@pytest.mark.parametrize("M,N,K,pad", [(1, 20000, 512, 0), (5, 14000, 384, 16), (17, 6001, 640, 0), (29, 15003, 1040, 48),
+                                       (32, 33000, 256, 0), (20, 9000, 1029, 3), (33, 700, 1024, 0), (47, 515, 4096, 16),
+                                       (63, 9001, 256, 0)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_f8_few_rows_on_tiles(M, N, K, pad, out):
+    """Fewer rows than a tile has, read without a copy of A: exact on small whole numbers, nothing written beside C."""
+    g = torch.Generator(DEV).manual_seed(M + N + K)
+    draw = lambda rows: torch.randint(-3, 4, (rows, K), generator=g, device=DEV).float()  # noqa: E731
+    a, b = draw(M), draw(N)
+    A = padded(a.to(torch.float8_e4m3fn), pad, DEV)[0]
+    B = padded(b.to(torch.float8_e4m3fn), pad, DEV)[0]
+    sa = 2.0 ** torch.randint(-1, 2, (M,), generator=g, device=DEV).float()
+    sb = 2.0 ** torch.randint(-1, 2, (N,), generator=g, device=DEV).float()
+    want = (a @ b.t()) * sa[:, None] * sb              # whole numbers by powers of two, below 2^24: exact in fp32
+    C, whole = padded(torch.full((M, N), float("nan"), device=DEV).to(DT[out]), pad, DEV)
+    for ws in ("auto", None):
+        ops.matmul_f8(A, B, sa, sb, C=C, workspace=ws)
+        assert untouched(C, whole)
+        assert torch.equal(C, want.to(DT[out]))
+
+
+@pytest.mark.parametrize("M,N,K,group,pad", [(33, 16384, 512, 128, 0), (40, 16500, 576, 64, 8), (63, 16384, 512, 32, 16),
+                                             (48, 4096, 8192, 64, 0), (57, 4100, 9001, 64, 1)])
+def test_w4_few_rows_on_tiles(M, N, K, group, pad):
+    g = torch.Generator(DEV).manual_seed(M + N + K)
+    groups = -(-K // group)
+    a = torch.randint(-2, 3, (M, K), generator=g, device=DEV).float()
+    codes = torch.randint(0, 256, (N, (K + 1) // 2), generator=g, device=DEV, dtype=torch.uint8)
+    s = 2.0 ** torch.randint(-1, 2, (N, groups), generator=g, device=DEV).float()
+    z = torch.randint(0, 16, (N, groups), generator=g, device=DEV).float()
+    q = torch.stack([codes & 15, codes >> 4], 2).flatten(1)[:, :K].float()
+    each = lambda v: v.repeat_interleave(group, 1)[:, :K]  # noqa: E731
+    A, Q = padded(a.bfloat16(), pad, DEV)[0], padded(codes, pad, DEV)[0]
+    want = a @ (each(s) * (q - each(z))).t()
+    C, whole = padded(torch.full((M, N), float("nan"), device=DEV), pad, DEV)
+    ops.matmul_w4(A, Q, s.bfloat16(), z.bfloat16(), group, C=C)
+    assert untouched(C, whole)
+    assert torch.equal(C, want)
+
+
+@pytest.mark.parametrize("group,t,zeros", [(32, "bf16", True), (64, "f16", True), (128, "bf16", True), (128, "f16", False)])
+def test_w4_tiles_with_a_mean(group, t, zeros):
+    """Rows of A with a large mean: what the zero points take off is many times what is left.  Zero points that are no
+    whole numbers, scales of zero and of very different size."""
+    M, N, K = 300, 4096, 2048
+    a, codes, s, z = w4_operands(M, N, K, group, t, zeros, 77)
+    a = (a.float() + 3.0).to(a.dtype)
+    s[5] = 0.0
+    s[9, ::2] = 2.0 ** -14
+    if zeros:
+        z = (z.float() + 0.37).to(z.dtype)
+    C = ops.matmul_w4(a.to(DEV), codes.to(DEV), s.to(DEV), z.to(DEV) if zeros else None, group, out_dtype=torch.float32).cpu()
+    p64, size = w4_64(a, codes, s, z, group)
+    assert torch.equal(C[:, 5], torch.zeros(M))
+    e = close(C, None, p64, size, group + s.shape[1] + 16, 1.0, 0.0)
+    assert e <= 1, e
+
+
+def test_w4_tiles_nan_stays_in_its_row_and_column():
+    M, N, K, group = 300, 4096, 1000, 64
+    a, codes, s, z = w4_operands(M, N, K, group, "bf16", True, 78)
+    want = ops.matmul_w4(a.to(DEV), codes.to(DEV), s.to(DEV), z.to(DEV), group, out_dtype=torch.float32).cpu()
+    a[17, K - 1], a[255, 3] = float("nan"), float("inf")
+    s[4095, 0], z[40, s.shape[1] - 1] = float("nan"), float("inf")
+    C = ops.matmul_w4(a.to(DEV), codes.to(DEV), s.to(DEV), z.to(DEV), group, out_dtype=torch.float32).cpu()
+    rows = torch.ones(M, dtype=torch.bool)
+    rows[[17, 255]] = False
+    cols = torch.ones(N, dtype=torch.bool)
+    cols[[40, 4095]] = False
+    assert torch.equal(C[rows][:, cols], want[rows][:, cols])
+    assert not C[~rows].isfinite().any() and not C[:, ~cols].isfinite().any()

@@ -122,6 +122,16 @@ hipError_t go(const F8Params& p, hipStream_t st) {
 
 }  // namespace
 
+// Expected microseconds: rounds of workgroups (the second one whole, later ones as waves come free), each a start and K's bytes;
+// less on a half empty card (16 and 32 rows, N from 1000 to 128000, K from 512 to 14336; rows that are not 16-byte
+// aligned on K = 2049 and 4097).
+double f8_skinny_us(const F8Params& p) {
+    const bool two = p.M > 16, aligned = ((uintptr_t)p.A | (uintptr_t)p.B | (uint64_t)p.lda | (uint64_t)p.ldb) % 16 == 0;
+    const double all = (double)(((int64_t)p.N + 15) / 16) / num_compute_units(), rounds = all <= 0.5 ? 0.6 : all <= 1.0 ? 1.0 : all <= 2.0 ? 2.0 : all;
+    const double round_us = two ? 2.0 + 0.85e-3 * p.K : 1.0 + 0.75e-3 * p.K;
+    return 2.5 + rounds * round_us * (aligned ? 1.0 : two ? 1.7 : 1.5);
+}
+
 // Sixteen waves where eight would leave most of the card's wave slots empty and each still has steps to take.
 hipError_t launch_f8_skinny(const F8Params& p, hipStream_t st) {
     const bool deep = ((int64_t)p.N + 15) / 16 <= 2 * num_compute_units() && p.K >= 2048;

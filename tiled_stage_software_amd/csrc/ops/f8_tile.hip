@@ -359,7 +359,7 @@ F8Plan f8_plan(int64_t M, int64_t N, int64_t K, bool wide) {
     const int64_t cu = num_compute_units();
     const int64_t t256 = ceil_div(M, 256) * ceil_div(N, 256), t128 = ceil_div(M, 128) * ceil_div(N, 128);
     if (!wide && M >= 256 && N >= 256 && ceil_div(t256, cu) * 4.0 <= ceil_div(t128, cu) * kSmallCost) return F8Plan{256, 256, 1};
-    if (t128 > cu) return q;
+    if (t128 > cu && M > kShortRows) return q;
     const int64_t slabs = ceil_div(K, kSlabBytes);
     double best = 0.0;
     for (int bm = 128; bm >= 64; bm -= 64) {
@@ -432,31 +432,67 @@ bool f8_tile_fits(const F8Params& f) {
     return f.K >= kSlabBytes && f.lda <= most && f.ldb <= most && ceil_div(f.M, 128) * ceil_div(f.N, 128) < (int64_t(1) << 22);
 }
 
-hipError_t launch_f8_tile(const F8Params& f, void* ws, size_t ws_bytes, hipStream_t st) {
-    const bool wide = f.out_type == DT_F32;
-    F8Plan q = f8_plan(f.M, f.N, f.K, wide);
-    const int64_t slabs = ceil_div(f.K, kSlabBytes), ldp = f8_ldp(f.N), each = (int64_t)f.M * ldp * sizeof(float);
-    if (!ws) ws_bytes = 0;
-    if (q.splits > 1 && ws_bytes < (size_t)(q.splits * each)) q.splits = (int)(ws_bytes / each);
+namespace {
+
+// What a call does with the workspace it has.
+struct F8Launch {
+    F8Plan q;
+    int per_split;       // slabs of a split
+    int64_t each, kp;    // bytes of a split's sums; K in whole slabs
+    RowsJob ja, jb;      // operands that the direct copies cannot take (src NULL: they can), copied behind the splits' sums
+    size_t used, wants;
+    bool copies, direct;
+};
+F8Launch f8_launch_of(const F8Params& f, size_t ws_bytes) {
+    F8Launch l;
+    F8Plan& q = l.q;
+    q = f8_plan(f.M, f.N, f.K, f.out_type == DT_F32);
+    const int64_t slabs = ceil_div(f.K, kSlabBytes);
+    l.each = (int64_t)f.M * f8_ldp(f.N) * sizeof(float);
+    if (q.splits > 1 && ws_bytes < (size_t)(q.splits * l.each)) q.splits = (int)(ws_bytes / l.each);
     if (q.splits < 2) q.splits = 1;
-    F8Extra x = {f.sa, f.sb, (int)ceil_div(slabs, q.splits), each};
-    q.splits = (int)ceil_div(slabs, x.per_split);
-    // operands that the direct copies cannot take, copied behind the splits' sums where there is room
-    const int64_t kp = slabs * kSlabBytes;
+    l.per_split = (int)ceil_div(slabs, q.splits);
+    q.splits = (int)ceil_div(slabs, l.per_split);
+    l.kp = slabs * kSlabBytes;
     auto copy_of = [&](const uint8_t* src, int64_t ld, int64_t rows, int64_t least) {
-        RowsJob j = {src, nullptr, ld, rows, f.K, std::max(rows, least), kp};
-        if (rows >= least && f.K == kp && ((uintptr_t)src | ld) % 16 == 0) j.src = nullptr;
+        RowsJob j = {src, nullptr, ld, rows, f.K, std::max(rows, least), l.kp};
+        if (rows >= least && f.K == l.kp && ((uintptr_t)src | ld) % 16 == 0) j.src = nullptr;
         return j;
     };
-    RowsJob ja = copy_of(f.A, f.lda, f.M, least_rows(q.bm)), jb = copy_of(f.B, f.ldb, f.N, q.bn);
-    const size_t used = q.splits > 1 ? ((size_t)(q.splits * each) + 255) & ~size_t(255) : 0;
-    const size_t wants = used + (ja.src ? ja.bytes() : 0) + (jb.src ? jb.bytes() : 0);
-    const bool copies = (ja.src || jb.src) && wants <= ws_bytes && wants < kMostCopied && f8_copy_pays(q, f, slabs, wants - used);
-    const bool direct = copies || (!ja.src && !jb.src);
+    l.ja = copy_of(f.A, f.lda, f.M, least_rows(q.bm));
+    l.jb = copy_of(f.B, f.ldb, f.N, q.bn);
+    l.used = q.splits > 1 ? ((size_t)(q.splits * l.each) + 255) & ~size_t(255) : 0;
+    l.wants = l.used + (l.ja.src ? l.ja.bytes() : 0) + (l.jb.src ? l.jb.bytes() : 0);
+    l.copies = (l.ja.src || l.jb.src) && l.wants <= ws_bytes && l.wants < kMostCopied && f8_copy_pays(q, f, slabs, l.wants - l.used);
+    l.direct = l.copies || (!l.ja.src && !l.jb.src);
+    return l;
+}
+
+}  // namespace
+
+// Expected microseconds of few rows: rounds of slabs and the launches beside them, or reading B (5 TB/s).
+double f8_tile_us(const F8Params& f, size_t ws_bytes) {
+    const F8Launch l = f8_launch_of(f, ws_bytes);
+    const double slab = slab_us(l.q.bm, f.out_type == DT_F32) + (l.direct ? 0.0 : staged_us(l.q.bm));
+    double us = rounds_of(ceil_div(f.M, l.q.bm) * ceil_div(f.N, l.q.bn) * l.q.splits) * l.per_split * slab;
+    if (l.q.splits > 1) us += kJoinUs + 2.0 * l.used / kBytesPerUs;
+    if (l.copies) us += kJoinUs + 2.0 * (l.wants - l.used) / kBytesPerUs;
+    return 2.7 + std::max(us, (double)f.N * f.K / 5.0e6);
+}
+
+hipError_t launch_f8_tile(const F8Params& f, void* ws, size_t ws_bytes, hipStream_t st) {
+    const bool wide = f.out_type == DT_F32;
+    if (!ws) ws_bytes = 0;
+    F8Launch l = f8_launch_of(f, ws_bytes);
+    const F8Plan& q = l.q;
+    RowsJob &ja = l.ja, &jb = l.jb;
+    const bool copies = l.copies, direct = l.direct;
+    const int64_t ldp = f8_ldp(f.N), kp = l.kp;
+    const F8Extra x = {f.sa, f.sb, l.per_split, l.each};
     op_note("  %d x %d tiles, %d splits of K, %s loads%s", q.bm, q.bn, q.splits, direct ? "direct" : "staged", copies ? " of copied rows" : "");
     F8Params o = f;
     if (copies) {
-        ja.dst = static_cast<uint8_t*>(ws) + used;
+        ja.dst = static_cast<uint8_t*>(ws) + l.used;
         jb.dst = ja.dst + (ja.src ? ja.bytes() : 0);
         const hipError_t e = launch_rows_pack(ja, jb, st);
         if (e != hipSuccess) return e;

@@ -77,6 +77,8 @@ struct F8Params {
     int out_type;
 };
 constexpr int kF8SkinnyRows = 32;   // rows of A that launch_f8_skinny takes
+double f8_skinny_us(const F8Params& p);              // what either is expected to take with so few rows
+double f8_tile_us(const F8Params& p, size_t ws_bytes);
 hipError_t launch_f8_skinny(const F8Params& p, hipStream_t st);
 bool f8_tile_fits(const F8Params& p);
 size_t f8_tile_workspace(int64_t M, int64_t N, int64_t K, bool wide);
