@@ -13,6 +13,7 @@
 // accumulators; and scales with zero points, transposed to rows of columns.
 #include <algorithm>
 
+#include "rows_pack.hpp"
 #include "short_loader.hpp"
 #include "w4_common.hpp"
 
@@ -309,7 +310,7 @@ void w4_tile_kernel(W4Tile p) {
 }
 
 // Sums of A over units and the transposed scales.  Four lanes sum a unit of a row, 32 elements a turn; the
-// workgroups behind those turn the scales.
+// workgroups behind those turn the scales; the first ones make the copies that the direct loads need, if any.
 struct W4Prepare {
     const char* A;
     const uint16_t* scales;
@@ -320,12 +321,19 @@ struct W4Prepare {
     int64_t lda, lds;
     int M, N, K, group, unit, units, tiles_m, tiles_n, bm, tm;   // tm: blocks of 16 rows of a tile
     int64_t sum_blocks;
+    RowsJob pack_a, pack_w;
+    uint32_t a_blocks, pack_blocks;
 };
 constexpr int kTurnCols = 64, kTurnUnits = 32;
 template <int T>
 __global__ __launch_bounds__(256) void w4_prepare_kernel(const W4Prepare p) {
-    if ((int64_t)blockIdx.x < p.sum_blocks) {
-        const int64_t id = (int64_t)blockIdx.x * 64 + threadIdx.x / 4;   // (row of a tile, unit), the unit first
+    if (blockIdx.x < p.pack_blocks) {
+        rows_pack(p.pack_a, p.pack_w, p.a_blocks, blockIdx.x);
+        return;
+    }
+    const int64_t block = blockIdx.x - p.pack_blocks;
+    if (block < p.sum_blocks) {
+        const int64_t id = block * 64 + threadIdx.x / 4;   // (row of a tile, unit), the unit first
         const int64_t rows = (int64_t)p.tiles_m * p.bm;
         if (id >= rows * p.units) return;
         const int64_t row = id / p.units;
@@ -347,7 +355,7 @@ __global__ __launch_bounds__(256) void w4_prepare_kernel(const W4Prepare p) {
     }
     // 64 columns by 32 units: read along the units of a column, written along the columns of a unit
     __shared__ uint32_t turn[kTurnUnits][kTurnCols + 1];
-    const int64_t cols = (int64_t)p.tiles_n * kBN, id = (int64_t)blockIdx.x - p.sum_blocks;
+    const int64_t cols = (int64_t)p.tiles_n * kBN, id = block - p.sum_blocks;
     const int at0 = (int)(id % (cols / kTurnCols)) * kTurnCols, u0 = (int)(id / (cols / kTurnCols)) * kTurnUnits;
     const int ul = threadIdx.x % kTurnUnits;
 #pragma unroll
@@ -485,9 +493,6 @@ hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, size_t ws_byt
     a.tiles_m = (int)q.tiles_m; a.tiles_n = (int)q.tiles_n;
     a.bm = q.bm; a.tm = q.bm / 16;
     a.sum_blocks = ceil_div(q.tiles_m * q.bm * q.units, 64);
-    hipLaunchKernelGGL(w4_prepare_kernel<T>, dim3((unsigned)(a.sum_blocks + q.tiles_n * (kBN / kTurnCols) * ceil_div(q.units, kTurnUnits))), dim3(256), 0, st, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
     W4Tile t = {};
     GemmParams& p = t.g;
     p.A = f.A;
@@ -513,8 +518,10 @@ hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, size_t ws_byt
     if (copies) {
         ja.dst = reinterpret_cast<uint8_t*>(ws) + used;
         jw.dst = ja.dst + (ja.src ? ja.bytes() : 0);
-        e = launch_rows_pack(ja, jw, st);
-        if (e != hipSuccess) return e;
+        a.pack_a = ja;
+        a.pack_w = jw;
+        a.a_blocks = rows_pack_blocks(ja);
+        a.pack_blocks = a.a_blocks + rows_pack_blocks(jw);
         if (ja.src) {
             p.A = reinterpret_cast<const char*>(ja.dst);
             p.lda = ja.len_pad / 2;
@@ -524,6 +531,9 @@ hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, size_t ws_byt
             t.ldw = jw.len_pad;
         }
     }
+    hipLaunchKernelGGL(w4_prepare_kernel<T>, dim3((unsigned)(a.pack_blocks + a.sum_blocks + q.tiles_n * (kBN / kTurnCols) * ceil_div(q.units, kTurnUnits))), dim3(256), 0, st, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     t.sums = ws;
     t.scales = ws + q.sums;
     t.zeros = ws + q.sums + q.sz / 2;
@@ -565,7 +575,7 @@ double w4_tile_us(const W4Params& f, size_t ws_bytes) {
     RowsJob a, w;
     copies_of(f, q, a, w);
     const double bytes = (a.src ? (double)a.bytes() : 0.0) + (w.src ? (double)w.bytes() : 0.0);
-    return q.us + (bytes > 0.0 ? kJoinUs + 2.0 * bytes / kBytesPerUs : 0.0);
+    return q.us + (bytes > 0.0 ? 1.0 + 2.0 * bytes / kBytesPerUs : 0.0);
 }
 
 // K that the staged loads hold, grids and 32-bit offsets in range, and a workspace for the sums and scales.
