@@ -42,8 +42,8 @@ struct Spread {
         asm("" : "+v"(twice));
     }
     __device__ __forceinline__ uint32_t place(uint32_t v) const { return (v & mask) | ones; }
-    // Eight codes (code i in bits 4 i .. 4 i + 3) in their order.  Two rotations put every even and every odd
-    // code at bit TOP of some byte; a byte permute then pairs codes 2 i and 2 i + 1: ten operations.
+    // Eight codes (code i in bits 4 i .. 4 i + 3) in their order: byte i times 2^TOP + 2^(12 + TOP) has code 2 i at bit TOP and
+    // code 2 i + 1 at bit 16 + TOP, and the mask drops the rest.  Eight operations, the byte chosen by the product's operand.
     __device__ __forceinline__ u32x4 in_order(uint32_t w) const {
         u32x4 v;
 #pragma unroll

@@ -2,15 +2,20 @@
 // of BM x 32, slabs of 64 k in an LDS ring, v_mfma_f32_16x16x32 on 16 x 16 blocks.
 //
 // No weight is rounded, so a group's scale multiplies an fp32 sum: each accumulator has a second one
-// for the running group, and one pass of two FMAs for each joins them at the group's end.  That and
+// for the running group, and an FMA for each joins them at the group's end.  That and
 // turning codes into operands is vector work beside the matrix cores' (per wave, 128 x 32 tile and
-// 128 k: 1024 cycles of matrix instructions; 4 x 2 x 10 operations for the codes, 2 x 64 for a group's end,
+// 128 k: 1024 cycles of matrix instructions; 4 x 2 x 8 operations for the codes, 64 for a group's end,
 // four cycles each).  Wide blocks of A's rows keep it below theirs: one turned code serves BM / 16
-// instructions.  Groups shorter than 64 end with every 32 k, which makes the vector work the bound.
+// instructions (waves of 64 x 64, with half the fragment reads: 308 us instead of 300 for
+// 2048 x 14336 x 4096; 96 rows and three workgroups a compute unit: 308; measured back to back, in turn with
+// other work 261).  Groups shorter than 64 end with every 32 k (390 us).
 //
-// A launch before prepares what the group's end needs, so that the ring brings it along with the slabs: the sum of A over
-// each unit (a group; 32 k for short groups), which the zero points multiply, in the order of the
-// accumulators; and scales with zero points, transposed to rows of columns.
+// The zero points' part of all groups, sum over units of (s * (1 + z/16)) * (sum of A over the unit), is a product of its
+// own with one k for a unit (a group; 32 k for short groups).  It runs behind the loop on matrix instructions, which took a
+// second FMA a group off the loop (320 us before, 434 for groups of 32).
+//
+// A launch before prepares the sums of A, in the order of the accumulators; the scales, transposed to rows of columns, which
+// the ring brings along with the slabs; and their products with the zero points.
 #include <algorithm>
 
 #include "rows_pack.hpp"
