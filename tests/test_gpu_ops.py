@@ -608,3 +608,33 @@ def test_w4_tiles_nan_stays_in_its_row_and_column():
     cols[[40, 4095]] = False
     assert torch.equal(C[rows][:, cols], want[rows][:, cols])
     assert not C[~rows].isfinite().any() and not C[:, ~cols].isfinite().any()
+
+
+@pytest.mark.parametrize("rows", [4, 5, 13, 16, 17, 40, 127, 128, 129])
+@pytest.mark.parametrize("cols,t", [(4, "f32"), (37, "f32"), (250, "bf16"), (1000, "f16"), (3001, "f32"), (4097, "bf16"), (16000, "f16")])
+def test_norm_backward_few_rows(rows, cols, t):
+    """dw in the launch of dx: against the formula, every column once, and the bits of the two launches that a dx on dy takes."""
+    g = gen(rows * 31 + cols)
+    dy, h = (torch.randn(rows, cols, generator=g).to(DT[t]) for _ in range(2))
+    w = torch.randn(cols, generator=g).to(DT[t])
+    rstd = torch.rand(rows, generator=g) + 0.5
+    DY, H = padded(dy, 3, DEV)[0], padded(h, 5, DEV)[0]
+    W, R = w.to(DEV), rstd.to(DEV)
+    ws = torch.empty(rows * cols * 4 + 256, dtype=torch.uint8, device=DEV)
+
+    def run(a, dx):
+        dw = torch.full((cols + 8,), float("nan"), device=DEV)
+        lg.check(lg.gemm_rmsnorm_bwd(code(a), code(W), rows, cols, a.data_ptr(), a.stride(0), H.data_ptr(), H.stride(0),
+                                     W.data_ptr(), R.data_ptr(), 0, 0, dx.data_ptr(), dx.stride(0), dw.data_ptr(),
+                                     ws.data_ptr(), ws.numel(), stream()))
+        torch.cuda.synchronize()
+        assert bool(dw[cols:].isnan().all())
+        return dx, dw[:cols]
+
+    dx, dw = run(DY, torch.empty_like(DY))
+    dx64, dw64, dx_size, dw_size = norm_bwd64(dy, h, w, rstd, None)
+    assert off(dx, dx64, rounding(dx64, DT[t]) + (norm_steps(cols) + 12) * U32 * dx_size) <= 1
+    assert off(dw, dw64, (rows + 8) * U32 * dw_size + 2.0 ** -149) <= 1
+    mine = padded(dy, 3, DEV)[0]
+    dx2, dw2 = run(mine, mine)
+    assert torch.equal(dx2, dx) and torch.equal(dw2, dw)

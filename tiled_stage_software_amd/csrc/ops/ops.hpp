@@ -47,6 +47,7 @@ struct NormBwdParams {
     int cols;
     int w_type;
     int parts;           // workgroups, each a fixed set of rows and one partial row of dw
+    int strip_blocks;    // (the launch's: workgroups that sum dw by columns, before the others)
 };
 // Rows that one workgroup of the backward kernel works on at a time, and the number of
 // workgroups it would like for this problem (its partial sums need parts * cols floats).
