@@ -638,3 +638,22 @@ def test_norm_backward_few_rows(rows, cols, t):
     mine = padded(dy, 3, DEV)[0]
     dx2, dw2 = run(mine, mine)
     assert torch.equal(dx2, dx) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("M,lda", [(130, 4194368), (64, 4194368), (130, 8388608)])
+def test_w4_rows_of_a_long_pitch(M, lda):
+    """Rows of A that lie 8 MiB and more apart, below and past what the direct loads' offsets hold (128 rows of 2^24
+    bytes): exact on small whole numbers."""
+    N, K, group = 4096, 512, 64
+    g = torch.Generator(DEV).manual_seed(lda + M)
+    a = torch.randint(-2, 3, (M, K), generator=g, device=DEV).float()
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device=DEV, dtype=torch.uint8)
+    s = 2.0 ** torch.randint(-1, 2, (N, K // group), generator=g, device=DEV).float()
+    z = torch.randint(0, 16, (N, K // group), generator=g, device=DEV).float()
+    q = torch.stack([codes & 15, codes >> 4], 2).flatten(1).float()
+    each = lambda v: v.repeat_interleave(group, 1)  # noqa: E731
+    A = torch.empty(M * lda, dtype=torch.bfloat16, device=DEV).view(M, lda)[:, :K]
+    A.copy_(a)
+    want = a @ (each(s) * (q - each(z))).t()
+    C = ops.matmul_w4(A, codes, s.bfloat16(), z.bfloat16(), group, out_dtype=torch.float32)
+    assert torch.equal(C, want)

@@ -184,3 +184,32 @@ def test_quantize_f8():
     assert s[0] == ops.TINY and s[1] == 1.0
     assert torch.equal(q[:2].float(), t[:2])
     assert bool(((q.float() * s[:, None] - t).abs() <= 2.0 ** -4 * t.abs()).all())
+
+
+no_gpu = pytest.mark.skipif(torch.cuda.device_count() > 0, reason="the calls pass fake device addresses that a launch would dereference")
+
+
+def notes(calls):
+    """What GEMM_DEBUG prints for these calls of lg.* at fake addresses (P), before the launch that the runtime refuses."""
+    code = f"from tiled_stage_software_amd import libgemm as lg\nP = {P}\n" + "\n".join(calls)
+    r = subprocess.run([sys.executable, "-c", code], env=dict(os.environ, GEMM_DEBUG="1"), capture_output=True, text=True, cwd=ROOT)
+    assert r.returncode == 0, r.stderr
+    return r.stderr
+
+
+@no_gpu
+@pytest.mark.parametrize("M,N,K,loads", [
+    (256, 512, 8388481, "direct loads of copied rows"),   # 128 rows of 2 * 8388544 bytes: just below 2^31
+    (256, 512, 8388609, "staged loads"), (256, 512, 17000001, "staged loads"), (256, 512, 17000064, "staged loads"),
+    (64, 128, 16777089, "direct loads of copied rows"), (64, 128, 35000001, "staged loads"),
+    (256, 512, 8388544, "direct loads\n"), (256, 512, 8388608, "staged loads"),
+])
+def test_w4_rows_whose_copies_pass_32_bits_are_not_copied(M, N, K, loads):
+    """The direct loads hold a row's offset in its tile in 32 bits, also in a copy; longer rows take the staged loads,
+    and no workspace is asked for a copy of them."""
+    groups = -(-K // 128)
+    s, nbytes = lg.gemm_w4_workspace_size(BF16, M, N, K, 128)
+    err = notes([f"lg.gemm_w4(1, {M}, {N}, {K}, 128, 1.0, P, {K}, P, {(K + 1) // 2}, P, P, {groups}, 0.0, P, 1, {N}, P, {nbytes})"])
+    assert s == lg.GEMM_OK and f"K={K} group=128: tiles" in err and loads in err, err
+    copies = M * -(-K // 64) * 128 + N * -(-K // 64) * 32
+    assert (nbytes >= copies) == ("copied" in loads)

@@ -474,13 +474,25 @@ hipError_t out_of(const W4Plan& q, const W4Tile& t, bool direct, hipStream_t st)
     return tile_of<T, OUT, 64>(t, s1, direct, q.splits, st);
 }
 
-// Copies of A and the codes that make their rows fit the direct copies (src NULL: they do).
-void copies_of(const W4Params& f, const W4Plan& q, RowsJob& a, RowsJob& w) {
+// What the direct loads need of A and the codes.  They hold a row's offset in its tile in 32 bits, as it lies in memory and
+// as a copy lays it out: longer rows go through the staged loads, whose addresses are whole ones.
+struct W4Copies {
+    RowsJob a, w;
+    bool copy_a, copy_w;   // whose rows they cannot read in place
+    bool held;             // whether they can read the copies
+    size_t bytes() const { return (copy_a ? a.bytes() : 0) + (copy_w ? w.bytes() : 0); }
+};
+W4Copies copies_of(const W4Params& f, const W4Plan& q) {
     const int64_t kp = q.slabs * kSlabK;
-    a = {reinterpret_cast<const uint8_t*>(f.A), nullptr, f.lda * 2, f.M, (int64_t)f.K * 2, std::max((int64_t)f.M, least_rows(q.bm)), kp * 2};
-    w = {f.W, nullptr, f.ldw, f.N, ((int64_t)f.K + 1) / 2, std::max((int64_t)f.N, (int64_t)kBN), kp / 2};
-    if (f.K == kp && f.M >= least_rows(q.bm) && ((uintptr_t)a.src | a.ld) % 16 == 0 && f.lda <= (1 << 21)) a.src = nullptr;
-    if (f.K == kp && f.N >= kBN && ((uintptr_t)w.src | w.ld) % 16 == 0 && f.ldw <= (1 << 22)) w.src = nullptr;
+    auto held = [](int64_t rows, int64_t pitch) { return rows * pitch < (int64_t(1) << 31); };
+    W4Copies c;
+    c.a = {reinterpret_cast<const uint8_t*>(f.A), nullptr, f.lda * 2, f.M, (int64_t)f.K * 2, std::max((int64_t)f.M, least_rows(q.bm)), kp * 2};
+    c.w = {f.W, nullptr, f.ldw, f.N, ((int64_t)f.K + 1) / 2, std::max((int64_t)f.N, (int64_t)kBN), kp / 2};
+    c.copy_a = f.K != kp || f.M < least_rows(q.bm) || ((uintptr_t)f.A | c.a.ld) % 16 || !held(q.bm, c.a.ld);
+    c.copy_w = f.K != kp || f.N < kBN || ((uintptr_t)f.W | c.w.ld) % 16 || !held(kBN, c.w.ld);
+    c.held = (!c.copy_a || held(q.bm, c.a.len_pad)) && (!c.copy_w || held(kBN, c.w.len_pad)) &&
+             c.bytes() < (size_t(1) << 34);   // (rows_pack counts chunks in 32 bits)
+    return c;
 }
 
 template <int T>
@@ -511,29 +523,30 @@ hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, size_t ws_byt
     p.group_m = 8;
     p.xcd_remap = 1;
     // operands that the direct copies cannot take, copied behind the rest where there is room
-    RowsJob ja, jw;
-    copies_of(f, q, ja, jw);
-    const size_t used = q.sums + q.sz + round256(q.parts), wants = used + (ja.src ? ja.bytes() : 0) + (jw.src ? jw.bytes() : 0);
-    const bool copies = (ja.src || jw.src) && wants <= ws_bytes && wants < (size_t(1) << 34);   // (rows_pack counts chunks in 32 bits)
-    const bool direct = copies || (!ja.src && !jw.src);
+    W4Copies c = copies_of(f, q);
+    const size_t used = q.sums + q.sz + round256(q.parts);
+    const bool copies = (c.copy_a || c.copy_w) && c.held && used + c.bytes() <= ws_bytes;
+    const bool direct = copies || (!c.copy_a && !c.copy_w);
     op_note("  %d x %d tiles, units of %d, %d splits of K, %s loads%s", q.bm, kBN, q.unit, q.splits, direct ? "direct" : "staged",
             copies ? " of copied rows" : "");
     t.W = f.W;
     t.ldw = f.ldw;
     if (copies) {
-        ja.dst = reinterpret_cast<uint8_t*>(ws) + used;
-        jw.dst = ja.dst + (ja.src ? ja.bytes() : 0);
-        a.pack_a = ja;
-        a.pack_w = jw;
-        a.a_blocks = rows_pack_blocks(ja);
-        a.pack_blocks = a.a_blocks + rows_pack_blocks(jw);
-        if (ja.src) {
-            p.A = reinterpret_cast<const char*>(ja.dst);
-            p.lda = ja.len_pad / 2;
+        uint8_t* at = reinterpret_cast<uint8_t*>(ws) + used;
+        if (c.copy_a) {
+            c.a.dst = at;
+            at += c.a.bytes();
+            a.pack_a = c.a;
+            a.a_blocks = a.pack_blocks = rows_pack_blocks(c.a);
+            p.A = reinterpret_cast<const char*>(c.a.dst);
+            p.lda = c.a.len_pad / 2;
         }
-        if (jw.src) {
-            t.W = jw.dst;
-            t.ldw = jw.len_pad;
+        if (c.copy_w) {
+            c.w.dst = at;
+            a.pack_w = c.w;
+            a.pack_blocks += rows_pack_blocks(c.w);
+            t.W = c.w.dst;
+            t.ldw = c.w.len_pad;
         }
     }
     hipLaunchKernelGGL(w4_prepare_kernel<T>, dim3((unsigned)(a.pack_blocks + a.sum_blocks + q.tiles_n * (kBN / kTurnCols) * ceil_div(q.units, kTurnUnits))), dim3(256), 0, st, a);
@@ -568,18 +581,18 @@ hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, size_t ws_byt
 // Bytes for the sums, the scales, the splits and, for rows that whole slabs do not fill, the copies.
 size_t w4_tile_workspace(int64_t M, int64_t N, int64_t K, int64_t group) {
     const W4Plan q = w4_plan(M, N, K, group, ~size_t(0) >> 1);
-    size_t bytes = q.sums + q.sz + round256(q.parts);
-    if (K % kSlabK || M < least_rows(q.bm)) bytes += (size_t)(std::max(M, least_rows(q.bm)) * q.slabs * kSlabK * 2);
-    if (K % kSlabK || N < kBN) bytes += (size_t)(std::max(N, (int64_t)kBN) * q.slabs * kSlabK / 2);
-    return bytes;
+    W4Params f = {};
+    f.M = (int)M; f.N = (int)N; f.K = (int)K;
+    f.lda = K; f.ldw = (K + 1) / 2;   // (of contiguous operands)
+    const W4Copies c = copies_of(f, q);
+    return q.sums + q.sz + round256(q.parts) + (c.held ? c.bytes() : 0);
 }
 
 // Expected microseconds.
 double w4_tile_us(const W4Params& f, size_t ws_bytes) {
     const W4Plan q = w4_plan(f.M, f.N, f.K, f.group, ws_bytes);
-    RowsJob a, w;
-    copies_of(f, q, a, w);
-    const double bytes = (a.src ? (double)a.bytes() : 0.0) + (w.src ? (double)w.bytes() : 0.0);
+    const W4Copies c = copies_of(f, q);
+    const double bytes = c.held ? (double)c.bytes() : 0.0;
     return q.us + (bytes > 0.0 ? 1.0 + 2.0 * bytes / kBytesPerUs : 0.0);
 }
 
