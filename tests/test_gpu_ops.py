@@ -657,3 +657,23 @@ def test_w4_rows_of_a_long_pitch(M, lda):
     want = a @ (each(s) * (q - each(z))).t()
     C = ops.matmul_w4(A, codes, s.bfloat16(), z.bfloat16(), group, out_dtype=torch.float32)
     assert torch.equal(C, want)
+
+
+@pytest.mark.parametrize("cols,t", [(2049, "bf16"), (2055, "bf16"), (4099, "bf16"), (1025, "f32"), (2051, "f16"), (9003, "bf16"), (4101, "f32")])
+@pytest.mark.parametrize("rows", [3, 200])
+def test_norm_backward_in_place_of_odd_widths(cols, t, rows):
+    """dx on dy, on h and on dh where a row's last vector reaches into another wave's elements."""
+    g = gen(cols)
+    h, dy, dh = (torch.randn(rows, cols, generator=g).to(DT[t]).to(DEV) for _ in range(3))
+    w = torch.randn(cols, generator=g).to(DT[t]).to(DEV)
+    rstd = torch.rand(rows, generator=g).to(DEV) + 0.5
+    want = ops.rmsnorm_backward(dy, h, w, rstd, dh)
+    ws = torch.empty(rows * cols * 4 + 256, dtype=torch.uint8, device=DEV)
+    for place in (0, 1, 2):
+        a = [dy.clone(), h.clone(), dh.clone()]
+        dw = torch.empty(cols, device=DEV)
+        lg.check(lg.gemm_rmsnorm_bwd(code(h), code(h), rows, cols, a[0].data_ptr(), cols, a[1].data_ptr(), cols, w.data_ptr(),
+                                     rstd.data_ptr(), a[2].data_ptr(), cols, a[place].data_ptr(), cols, dw.data_ptr(),
+                                     ws.data_ptr(), ws.numel(), stream()))
+        torch.cuda.synchronize()
+        assert torch.equal(a[place], want[0]) and torch.equal(dw, want[1])

@@ -518,6 +518,12 @@ __global__ __launch_bounds__(64 * WPR * RPG) void norm_bwd_kernel(const NormBwdP
                 sum = __builtin_fmaf(du, w[i].get(ones, e), sum);
             }
         }
+        // dx may lie on dh, and a row's last elements may be another wave's to store as well: dh is here before the barrier in
+        // row_sum(), as dy and h are, which the sum has used
+        if (p.dh) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) asm volatile("" : "+v"(dh[i]));
+        }
         const float mean = row_sum<WPR>(sum, sums[turn]) / (float)p.cols;
         char* xr = p.dx + row * p.lddx * SZ;
 #pragma unroll
