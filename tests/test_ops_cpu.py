@@ -213,3 +213,24 @@ def test_w4_rows_whose_copies_pass_32_bits_are_not_copied(M, N, K, loads):
     assert s == lg.GEMM_OK and f"K={K} group=128: tiles" in err and loads in err, err
     copies = M * -(-K // 64) * 128 + N * -(-K // 64) * 32
     assert (nbytes >= copies) == ("copied" in loads)
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("k", [64, 75])
+def test_quantize_w4_of_groups_far_from_zero(t, k):
+    """Zero points are whole numbers from 0 to 15, whatever the group: one value, values far from zero, zeros.  A value is
+    off by half a step for its code and, at the end of the codes, half a step for the rounding of the zero point, plus
+    what the scale's own rounding moves fifteen steps by."""
+    g = torch.Generator().manual_seed(k)
+    noise = 2 * torch.rand(12, k, generator=g) - 1
+    mid = torch.tensor([5.0, -5.0, 4096.0, 6.0, 1.0, 1.0, -1.0, 0.0, 0.0, 3.0, 0.25, -0.5])
+    wide = torch.tensor([0.0, 0.0, 0.0, 1e-4, 1e-3, 1e-2, 0.1, 0.0, 1.0, 3.0, 0.3, 2.0])
+    w = mid[:, None] + wide[:, None] * noise
+    codes, s, z = ops.quantize_w4(w, 32, t, True)
+    assert bool((z == z.round()).all()) and bool(((z >= 0) & (z <= 15)).all())
+    each = lambda v: v.float().repeat_interleave(32, 1)[:, :k]  # noqa: E731
+    back = each(s) * (unpack4(codes, k).float() - each(z))
+    steps = 0.5 + 15 * torch.finfo(t).eps / 2 + 1e-3
+    assert float(((back - w).abs() / each(s)).max()) <= steps
+    reach = torch.maximum(w.amax(1), torch.zeros(12)) - torch.minimum(w.amin(1), torch.zeros(12))
+    assert bool((s.float() <= (reach / 15).clamp_min(torch.finfo(t).tiny)[:, None] * (1 + torch.finfo(t).eps)).all())

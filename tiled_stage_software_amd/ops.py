@@ -201,7 +201,8 @@ def quantize_f8(t):
 def quantize_w4(w, group: int = 128, dtype=None, zeros: bool = False):
     """(codes, scales, zeros or None) of an N x K weight for ``matmul_w4``; scales in `dtype`
     (w's by default).  Without zeros the codes are centred on 8, with them they run from a group's
-    least value to its largest."""
+    least value, or zero, to its largest, or zero: a zero point is then a whole number from 0 to
+    15, which any type holds."""
     import torch
     if group < 32 or group % 32:
         raise ValueError(f"group {group}: a multiple of 32")
@@ -213,9 +214,9 @@ def quantize_w4(w, group: int = 128, dtype=None, zeros: bool = False):
     v = v.view(N, groups, group)
     least = torch.finfo(dtype).tiny
     if zeros:
-        low, high = v.amin(2), v.amax(2)
+        low, high = v.amin(2).clamp_max(0), v.amax(2).clamp_min(0)
         scales = ((high - low) / 15).clamp_min(least).to(dtype)
-        zero = (-low / scales.float()).round().to(dtype)
+        zero = (-low / scales.float()).round().clamp(0, 15).to(dtype)
     else:
         scales = (v.abs().amax(2) / 7.5).clamp_min(least).to(dtype)
         zero = torch.full_like(scales, 8.0)
