@@ -677,3 +677,72 @@ def test_norm_backward_in_place_of_odd_widths(cols, t, rows):
                                      ws.data_ptr(), ws.numel(), stream()))
         torch.cuda.synchronize()
         assert torch.equal(a[place], want[0]) and torch.equal(dw, want[1])
+
+
+# ------------------------------------------------------------------ streams given by their handles
+
+def each_call(rows=512):
+    """(name, call(stream), the result that is kept) of every torch form that allocates."""
+    x, r, w, b, sb, codes, s, dy = chain_inputs(rows, 11)
+    n = ops.rmsnorm(x, w, r, out_dtype=torch.float8_e4m3fn)
+    B = torch.randn(512, 640, generator=gen(4)).bfloat16().to(DEV)
+    return [("rmsnorm", lambda st: ops.rmsnorm(x, w, r, stream=st)[0]),
+            ("rmsnorm to 8 bits", lambda st: ops.rmsnorm(x, w, r, out_dtype=torch.float8_e4m3fn, stream=st)[0].view(torch.uint8)),
+            ("backward", lambda st: ops.rmsnorm_backward(dy, n.h, w, n.rstd, stream=st)[0]),
+            ("f8", lambda st: ops.matmul_f8(n.y, b, n.scale, sb, stream=st)),
+            ("w4", lambda st: ops.matmul_w4(torch.cat([x, r[:, :128]], 1), codes, s, group=64, stream=st)),
+            ("bf16", lambda st: lg.matmul(x, B, stream=st, workspace="auto"))]
+
+
+SPIN = 100_000_000   # of the device's clock: tens of milliseconds and more
+
+
+@pytest.mark.parametrize("i", range(6))
+def test_results_dropped_while_another_stream_writes_them(i):
+    """What a call on a busy stream wrote and the caller dropped is not handed out before that stream is done."""
+    name, call = each_call()[i]
+    want = call(None).clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    sizes = [512 * 4, 512 * 4, 512 * 1024, 512 * 1280, 512 * 512, 640 * 4]   # rstd, scale, h or y, C, 8 bits, dw
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(SPIN)
+    call(side.cuda_stream)
+    kept = call(side.cuda_stream)
+    fresh = [torch.full((n,), 7, dtype=torch.uint8, device=DEV) for n in sizes * 3]
+    side.synchronize()
+    torch.cuda.synchronize()
+    for t in fresh:
+        assert bool((t == 7).all()), name
+    assert torch.equal(kept, want), name
+
+
+@pytest.mark.parametrize("i", range(6))
+def test_results_in_memory_that_the_current_stream_still_writes(i):
+    """A call on another stream gets no block that was freed with work of the current stream still to come."""
+    name, call = each_call()[i]
+    want = call(None).clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    old = [torch.empty(want.numel() * want.element_size(), dtype=torch.uint8, device=DEV) for _ in range(4)]
+    torch.cuda._sleep(SPIN)
+    for t in old:
+        t.fill_(7)
+    del old, t
+    got = call(side.cuda_stream)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want), name
+
+
+def test_the_default_stream_by_its_handle():
+    x, r, w, b, sb, codes, s, dy = chain_inputs(33, 12)
+    want = ops.rmsnorm(x, w, r)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = ops.rmsnorm(x, w, r, stream=torch.cuda.default_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(got.y, want.y) and torch.equal(got.h, want.h)

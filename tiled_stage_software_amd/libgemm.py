@@ -330,6 +330,43 @@ def check(status: int):
 
 # ------------------------------------------------------------------ torch convenience
 
+class Running:
+    """The stream that a call's kernels run on (a handle; None: the current one), as torch's
+    current stream while the call lasts: what the call allocates comes from that stream's
+    memory, not from blocks that earlier work of the caller's stream may still use.  The
+    tensors that the call is given are marked for that stream, and by ``keep`` its results for
+    the caller's: either may be dropped at once."""
+
+    def __init__(self, stream, device, *given):
+        import torch
+        if device.type != "cuda":
+            raise ValueError(f"tensors on {device}: the kernels run on the GPU")
+        self.caller = torch.cuda.current_stream(device)
+        self.handle = self.caller.cuda_stream if stream is None else stream
+        self.other = None
+        if self.handle != self.caller.cuda_stream:
+            runs = torch.cuda.ExternalStream(self.handle, device=device)
+            self.other = torch.cuda.stream(runs)
+            for t in given:
+                if isinstance(t, torch.Tensor) and t.is_cuda:
+                    t.record_stream(runs)
+
+    def __enter__(self):
+        if self.other is not None:
+            self.other.__enter__()
+        return self
+
+    def __exit__(self, *error):
+        if self.other is not None:
+            self.other.__exit__(*error)
+
+    def keep(self, *tensors):
+        if self.other is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.caller)
+
+
 def _layout_of(t, rows, cols):
     """(layout, ld) of a 2-D tensor view, or None if it is neither row- nor column-major."""
     s0, s1 = t.stride()
@@ -362,49 +399,45 @@ def matmul(A, B, C=None, alpha: float = 1.0, beta: float = 0.0, out_dtype=None, 
     if C is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs C")
-        if out_dtype is None:
-            out_dtype = A.dtype
-        C = torch.empty((M, N), dtype=out_dtype, device=A.device)
-    if C.dim() != 2 or tuple(C.shape) != (M, N) or (N > 1 and C.stride(1) != 1):
+    elif C.dim() != 2 or tuple(C.shape) != (M, N) or (N > 1 and C.stride(1) != 1):
         raise ValueError("C must be an M x N row-major view")
-    if M > 1 and C.stride(0) < N:
+    elif M > 1 and C.stride(0) < N:
         # an expanded or row-overlapping view: the kernels would write past its storage
         raise ValueError(f"C rows overlap (stride {C.stride(0)} < N = {N})")
-    ldc = C.stride(0) if M > 1 else max(N, 1)
-    st = stream if stream is not None else torch.cuda.current_stream(A.device).cuda_stream
-    o = _opts(nstage, kernel, tile, flags)
-    if A.dtype == torch.float32:
-        if C.dtype != torch.float32:
-            raise ValueError("fp32 inputs give fp32 C")
-        s = gemm_f32_ex(la[0], lb[0], M, N, K, alpha, A.data_ptr(), la[1], B.data_ptr(), lb[1],
-                        beta, C.data_ptr(), ldc, st, o)
-    elif A.dtype in (torch.bfloat16, torch.float16):
-        ct = {torch.float32: GEMM_F32, torch.bfloat16: GEMM_BF16, torch.float16: GEMM_F16}[C.dtype]
-        if workspace is None:
-            fn = gemm_bf16_ex if A.dtype == torch.bfloat16 else gemm_f16_ex
-            s = fn(la[0], lb[0], M, N, K, alpha, A.data_ptr(), la[1], B.data_ptr(), lb[1],
-                   beta, C.data_ptr(), ct, ldc, st, o)
+    with Running(stream, A.device, A, B, C, workspace) as on:
+        if C is None:
+            C = torch.empty((M, N), dtype=A.dtype if out_dtype is None else out_dtype, device=A.device)
+            on.keep(C)
+        ldc = C.stride(0) if M > 1 else max(N, 1)
+        st = on.handle
+        o = _opts(nstage, kernel, tile, flags)
+        if A.dtype == torch.float32:
+            if C.dtype != torch.float32:
+                raise ValueError("fp32 inputs give fp32 C")
+            s = gemm_f32_ex(la[0], lb[0], M, N, K, alpha, A.data_ptr(), la[1], B.data_ptr(), lb[1],
+                            beta, C.data_ptr(), ldc, st, o)
+        elif A.dtype in (torch.bfloat16, torch.float16):
+            ct = {torch.float32: GEMM_F32, torch.bfloat16: GEMM_BF16, torch.float16: GEMM_F16}[C.dtype]
+            if workspace is None:
+                fn = gemm_bf16_ex if A.dtype == torch.bfloat16 else gemm_f16_ex
+                s = fn(la[0], lb[0], M, N, K, alpha, A.data_ptr(), la[1], B.data_ptr(), lb[1],
+                       beta, C.data_ptr(), ct, ldc, st, o)
+            else:
+                if isinstance(workspace, str):
+                    if workspace != "auto":
+                        raise ValueError("workspace: a device tensor or 'auto'")
+                    it = GEMM_BF16 if A.dtype == torch.bfloat16 else GEMM_F16
+                    s, nbytes, _ = gemm_workspace_size(it, ct, la[0], lb[0], M, N, K, alpha, A.data_ptr(), la[1],
+                                                       B.data_ptr(), lb[1], beta, C.data_ptr(), ldc, o)
+                    check(s)
+                    workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=A.device)
+                fn = gemm_bf16_ws if A.dtype == torch.bfloat16 else gemm_f16_ws
+                s = fn(la[0], lb[0], M, N, K, alpha, A.data_ptr(), la[1], B.data_ptr(), lb[1],
+                       beta, C.data_ptr(), ct, ldc, st, o, workspace.data_ptr(),
+                       workspace.numel() * workspace.element_size())
         else:
-            if isinstance(workspace, str):
-                if workspace != "auto":
-                    raise ValueError("workspace: a device tensor or 'auto'")
-                it = GEMM_BF16 if A.dtype == torch.bfloat16 else GEMM_F16
-                s, nbytes, _ = gemm_workspace_size(it, ct, la[0], lb[0], M, N, K, alpha, A.data_ptr(), la[1],
-                                                   B.data_ptr(), lb[1], beta, C.data_ptr(), ldc, o)
-                check(s)
-                workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=A.device)
-                if st != torch.cuda.current_stream(A.device).cuda_stream:
-                    # the caching allocator orders reuse against the allocating stream only:
-                    # tie the block to the stream the pack and the multiply run on, so that
-                    # it is not handed out again before they have finished
-                    workspace.record_stream(torch.cuda.ExternalStream(st, device=A.device))
-            fn = gemm_bf16_ws if A.dtype == torch.bfloat16 else gemm_f16_ws
-            s = fn(la[0], lb[0], M, N, K, alpha, A.data_ptr(), la[1], B.data_ptr(), lb[1],
-                   beta, C.data_ptr(), ct, ldc, st, o, workspace.data_ptr(),
-                   workspace.numel() * workspace.element_size())
-    else:
-        raise ValueError(f"unsupported dtype {A.dtype}")
-    check(s)
+            raise ValueError(f"unsupported dtype {A.dtype}")
+        check(s)
     return C
 
 

@@ -61,16 +61,7 @@ def _vector(t, name: str, n: int, dtype, device) -> int:
     return t.data_ptr()
 
 
-def _stream(stream, device) -> int:
-    if device.type != "cuda":
-        raise ValueError(f"tensors on {device}: the kernels run on the GPU")
-    if stream is not None:
-        return stream
-    import torch
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _workspace(workspace, size, device, stream):
+def _workspace(workspace, size, device):
     """(tensor, pointer, bytes) of a workspace: None, a device tensor, or "auto" (allocated here)."""
     import torch
     if workspace is None:
@@ -83,9 +74,6 @@ def _workspace(workspace, size, device, stream):
         if not nbytes:
             return None, 0, 0
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        if stream != torch.cuda.current_stream(device).cuda_stream:
-            # the allocator orders reuse against the allocating stream only
-            workspace.record_stream(torch.cuda.ExternalStream(stream, device=device))
     if workspace.device != device:
         raise ValueError(f"workspace is on {workspace.device}, not {device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -100,18 +88,18 @@ def rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None, st
     out_dtype = out_dtype or x.dtype
     w = _vector(weight, "weight", cols, (x.dtype, torch.float32), x.device)
     y_code = _code(out_dtype)
-    h, ldr, ldh = x, 0, 0
-    if residual is not None:
-        ldr = _rows(residual, "residual", x.shape, x.dtype, x.device)
-        h = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-        ldh = max(cols, 1)
-    y = torch.empty((rows, cols), dtype=out_dtype, device=x.device)
-    scale = torch.empty(rows, device=x.device) if y_code == lg.GEMM_F8E4M3 else None
-    rstd = torch.empty(rows, device=x.device)
-    lg.check(lg.gemm_rmsnorm(_code(x.dtype), _code(weight.dtype) if w else 0, y_code, rows, cols, eps, x.data_ptr(), ldx,
-                             residual.data_ptr() if ldr else 0, ldr, w, h.data_ptr() if ldh else 0, ldh, y.data_ptr(),
-                             max(cols, 1), scale.data_ptr() if scale is not None else 0, rstd.data_ptr(),
-                             _stream(stream, x.device)))
+    ldr = _rows(residual, "residual", x.shape, x.dtype, x.device) if residual is not None else 0
+    with lg.Running(stream, x.device, x, weight, residual) as on:
+        h, ldh = x, 0
+        if ldr:
+            h, ldh = torch.empty((rows, cols), dtype=x.dtype, device=x.device), max(cols, 1)
+        y = torch.empty((rows, cols), dtype=out_dtype, device=x.device)
+        scale = torch.empty(rows, device=x.device) if y_code == lg.GEMM_F8E4M3 else None
+        rstd = torch.empty(rows, device=x.device)
+        on.keep(h if ldr else None, y, scale, rstd)
+        lg.check(lg.gemm_rmsnorm(_code(x.dtype), _code(weight.dtype) if w else 0, y_code, rows, cols, eps, x.data_ptr(), ldx,
+                                 residual.data_ptr() if ldr else 0, ldr, w, h.data_ptr() if ldh else 0, ldh, y.data_ptr(),
+                                 max(cols, 1), scale.data_ptr() if scale is not None else 0, rstd.data_ptr(), on.handle))
     return RmsNorm(y, scale, h, rstd)
 
 
@@ -125,24 +113,26 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, need_dw: bool = True, workspa
     lddh = _rows(dh, "dh", h.shape, h.dtype, h.device) if dh is not None else 0
     w = _vector(weight, "weight", cols, (h.dtype, torch.float32), h.device)
     r = _vector(rstd, "rstd", rows, torch.float32, h.device)
-    dx = torch.empty((rows, cols), dtype=h.dtype, device=h.device)
-    dw = torch.empty(cols, device=h.device) if need_dw else None
-    st = _stream(stream, h.device)
-    keep, ws, nbytes = _workspace(workspace if need_dw else None,
-                                  lambda: lg.gemm_rmsnorm_bwd_workspace_size(_code(h.dtype), rows, cols), h.device, st)
-    lg.check(lg.gemm_rmsnorm_bwd(_code(h.dtype), _code(weight.dtype) if w else 0, rows, cols, dy.data_ptr(), lddy,
-                                 h.data_ptr(), ldh, w, r, dh.data_ptr() if lddh else 0, lddh, dx.data_ptr(),
-                                 max(cols, 1), dw.data_ptr() if need_dw else 0, ws, nbytes, st))
+    with lg.Running(stream, h.device, dy, h, weight, rstd, dh, workspace) as on:
+        dx = torch.empty((rows, cols), dtype=h.dtype, device=h.device)
+        dw = torch.empty(cols, device=h.device) if need_dw else None
+        on.keep(dx, dw)
+        held, ws, nbytes = _workspace(workspace if need_dw else None,
+                                      lambda: lg.gemm_rmsnorm_bwd_workspace_size(_code(h.dtype), rows, cols), h.device)
+        lg.check(lg.gemm_rmsnorm_bwd(_code(h.dtype), _code(weight.dtype) if w else 0, rows, cols, dy.data_ptr(), lddy,
+                                     h.data_ptr(), ldh, w, r, dh.data_ptr() if lddh else 0, lddh, dx.data_ptr(),
+                                     max(cols, 1), dw.data_ptr() if need_dw else 0, ws, nbytes, on.handle))
     return dx, dw
 
 
-def _result(C, M, N, beta, out_dtype, device):
+def _result(on, C, M, N, beta, out_dtype, device):
     """(C, its leading dimension) of a product."""
     import torch
     if C is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs C")
         C = torch.empty((M, N), dtype=out_dtype, device=device)
+        on.keep(C)
     return C, _rows(C, "C", (M, N), None, device)
 
 
@@ -158,11 +148,11 @@ def matmul_f8(a, b, scale_a=None, scale_b=None, C=None, alpha: float = 1.0, beta
         raise ValueError(f"shapes {tuple(a.shape)} and {tuple(b.shape)}: rows of different lengths")
     sa = _vector(scale_a, "scale_a", M, torch.float32, a.device)
     sb = _vector(scale_b, "scale_b", N, torch.float32, a.device)
-    C, ldc = _result(C, M, N, beta, out_dtype or torch.bfloat16, a.device)
-    st = _stream(stream, a.device)
-    keep, ws, nbytes = _workspace(workspace, lambda: lg.gemm_f8_workspace_size(M, N, K), a.device, st)
-    lg.check(lg.gemm_f8(M, N, K, alpha, a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb, beta, C.data_ptr(), _code(C.dtype),
-                        ldc, ws, nbytes, st))
+    with lg.Running(stream, a.device, a, b, scale_a, scale_b, C, workspace) as on:
+        C, ldc = _result(on, C, M, N, beta, out_dtype or torch.bfloat16, a.device)
+        held, ws, nbytes = _workspace(workspace, lambda: lg.gemm_f8_workspace_size(M, N, K), a.device)
+        lg.check(lg.gemm_f8(M, N, K, alpha, a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb, beta, C.data_ptr(), _code(C.dtype),
+                            ldc, ws, nbytes, on.handle))
     return C
 
 
@@ -180,13 +170,13 @@ def matmul_w4(a, codes, scales, zeros=None, group: int = 128, C=None, alpha: flo
     lds = _rows(scales, "scales", (N, groups), a.dtype, a.device)
     if zeros is not None and _rows(zeros, "zeros", (N, groups), a.dtype, a.device) != lds:
         raise ValueError("zeros: the row stride of scales")
-    C, ldc = _result(C, M, N, beta, out_dtype or a.dtype, a.device)
-    st = _stream(stream, a.device)
     code = _code(a.dtype)
-    keep, ws, nbytes = _workspace(workspace, lambda: lg.gemm_w4_workspace_size(code, M, N, K, group), a.device, st)
-    lg.check(lg.gemm_w4(code, M, N, K, group, alpha, a.data_ptr(), lda, codes.data_ptr(), ldw, scales.data_ptr(),
-                        zeros.data_ptr() if zeros is not None else 0, lds, beta, C.data_ptr(), _code(C.dtype), ldc, ws,
-                        nbytes, st))
+    with lg.Running(stream, a.device, a, codes, scales, zeros, C, workspace) as on:
+        C, ldc = _result(on, C, M, N, beta, out_dtype or a.dtype, a.device)
+        held, ws, nbytes = _workspace(workspace, lambda: lg.gemm_w4_workspace_size(code, M, N, K, group), a.device)
+        lg.check(lg.gemm_w4(code, M, N, K, group, alpha, a.data_ptr(), lda, codes.data_ptr(), ldw, scales.data_ptr(),
+                            zeros.data_ptr() if zeros is not None else 0, lds, beta, C.data_ptr(), _code(C.dtype), ldc, ws,
+                            nbytes, on.handle))
     return C
 
 
