@@ -234,3 +234,35 @@ def test_quantize_w4_of_groups_far_from_zero(t, k):
     assert float(((back - w).abs() / each(s)).max()) <= steps
     reach = torch.maximum(w.amax(1), torch.zeros(12)) - torch.minimum(w.amin(1), torch.zeros(12))
     assert bool((s.float() <= (reach / 15).clamp_min(torch.finfo(t).tiny)[:, None] * (1 + torch.finfo(t).eps)).all())
+
+
+def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
+    """A stream's handle does not name a device (0 is each one's default stream): the call makes its tensors' device the
+    current one, and the caller's again."""
+    at = [0]
+
+    class Device:
+        def __init__(self, d):
+            self.index = d.index
+
+        def __enter__(self):
+            self.before, at[0] = at[0], self.index
+
+        def __exit__(self, *error):
+            at[0] = self.before
+
+    class Stream:
+        cuda_stream = 0
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: at[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    for stream in (None, 0):
+        for index in (0, 1):
+            with lg.Running(stream, torch.device("cuda", index)) as on:
+                assert at[0] == index and on.handle == 0
+            assert at[0] == 0
+    with pytest.raises(KeyError):
+        with lg.Running(None, torch.device("cuda", 1)):
+            raise KeyError
+    assert at[0] == 0

@@ -331,11 +331,12 @@ def check(status: int):
 # ------------------------------------------------------------------ torch convenience
 
 class Running:
-    """The stream that a call's kernels run on (a handle; None: the current one), as torch's
-    current stream while the call lasts: what the call allocates comes from that stream's
-    memory, not from blocks that earlier work of the caller's stream may still use.  The
-    tensors that the call is given are marked for that stream, and by ``keep`` its results for
-    the caller's: either may be dropped at once."""
+    """The device and the stream that a call's kernels run on (a handle; None: the current one),
+    as torch's current ones while the call lasts.  Handle 0 is every device's default stream, so a
+    launch would else run on whichever device is current.  What the call allocates comes from that
+    stream's memory, not from blocks that earlier work of the caller's stream may still use.  The
+    tensors that the call is given are marked for that stream, and by ``keep`` its results for the
+    caller's: either may be dropped at once."""
 
     def __init__(self, stream, device, *given):
         import torch
@@ -343,6 +344,7 @@ class Running:
             raise ValueError(f"tensors on {device}: the kernels run on the GPU")
         self.caller = torch.cuda.current_stream(device)
         self.handle = self.caller.cuda_stream if stream is None else stream
+        self.device = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
         self.other = None
         if self.handle != self.caller.cuda_stream:
             runs = torch.cuda.ExternalStream(self.handle, device=device)
@@ -352,6 +354,8 @@ class Running:
                     t.record_stream(runs)
 
     def __enter__(self):
+        if self.device is not None:
+            self.device.__enter__()
         if self.other is not None:
             self.other.__enter__()
         return self
@@ -359,6 +363,8 @@ class Running:
     def __exit__(self, *error):
         if self.other is not None:
             self.other.__exit__(*error)
+        if self.device is not None:
+            self.device.__exit__(*error)
 
     def keep(self, *tensors):
         if self.other is not None:
