@@ -266,3 +266,14 @@ def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
         with lg.Running(None, torch.device("cuda", 1)):
             raise KeyError
     assert at[0] == 0
+
+
+def test_workspaces_have_to_be_whole_memory():
+    """A call uses all bytes from a workspace's first to as many as it has elements: in a strided view those are others'."""
+    big = torch.zeros(64, 64, dtype=torch.uint8)
+    assert ops._workspace(big[3:5], None, big.device)[1:] == (big.data_ptr() + 192, 128)
+    for view in (big[:, :8], big[::2], big.t()[:5], big[:1].expand(4, 64)):
+        with pytest.raises(ValueError, match="contiguous"):
+            ops._workspace(view, None, big.device)
+    with pytest.raises(ValueError, match="contiguous"):
+        lg.workspace_of(big[:, :8], big.device)

@@ -373,6 +373,16 @@ class Running:
                     t.record_stream(self.caller)
 
 
+def workspace_of(t, device):
+    """(pointer, bytes) of a tensor that serves as workspace: whole memory, as the call uses every
+    byte from its first on."""
+    if t.device != device:
+        raise ValueError(f"workspace is on {t.device}, not {device}")
+    if not t.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _layout_of(t, rows, cols):
     """(layout, ld) of a 2-D tensor view, or None if it is neither row- nor column-major."""
     s0, s1 = t.stride()
@@ -439,8 +449,7 @@ def matmul(A, B, C=None, alpha: float = 1.0, beta: float = 0.0, out_dtype=None, 
                     workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=A.device)
                 fn = gemm_bf16_ws if A.dtype == torch.bfloat16 else gemm_f16_ws
                 s = fn(la[0], lb[0], M, N, K, alpha, A.data_ptr(), la[1], B.data_ptr(), lb[1],
-                       beta, C.data_ptr(), ct, ldc, st, o, workspace.data_ptr(),
-                       workspace.numel() * workspace.element_size())
+                       beta, C.data_ptr(), ct, ldc, st, o, *workspace_of(workspace, A.device))
         else:
             raise ValueError(f"unsupported dtype {A.dtype}")
         check(s)

@@ -74,9 +74,7 @@ def _workspace(workspace, size, device):
         if not nbytes:
             return None, 0, 0
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if workspace.device != device:
-        raise ValueError(f"workspace is on {workspace.device}, not {device}")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace, *lg.workspace_of(workspace, device)
 
 
 def rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None, stream=None) -> RmsNorm:
