@@ -425,8 +425,8 @@ gemm_status_t gemm_rmsnorm_bwd_workspace_size(gemm_dtype_t in_type, int64_t rows
 
 /* C = alpha * diag(scale_a) * (A * B^T) * diag(scale_b) + beta * C for operands in 8 bits:
  * A is M x K, B is N x K, both e4m3 with K contiguous (lda, ldb >= K, in elements: any
- * pitch); scale_a: M floats, scale_b: N floats, either may be NULL (ones).  The scales
- * multiply the sum; C is row-major, GEMM_F32, GEMM_BF16 or GEMM_F16, rounded once.  A
+ * pitch); scale_a: M floats, scale_b: N floats, either may be NULL (ones).  The sum is
+ * multiplied by its scale_a, then by its scale_b, in fp32; C is row-major, GEMM_F32, GEMM_BF16 or GEMM_F16, rounded once.  A
  * GEMM_F32 C is summed wholly in fp32.  For a 16-bit C the 8-bit matrix instructions may
  * be used (twice as fast), which cut the products of each eight consecutive k at 2^-13 of the
  * largest before they are added in fp32: on random operands 1.5e-5 of the result, far below

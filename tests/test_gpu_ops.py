@@ -746,3 +746,28 @@ def test_the_default_stream_by_its_handle():
         got = ops.rmsnorm(x, w, r, stream=torch.cuda.default_stream().cuda_stream)
     torch.cuda.synchronize()
     assert torch.equal(got.y, want.y) and torch.equal(got.h, want.h)
+
+
+@pytest.mark.parametrize("M,N,K,ws", [(1, 70, 640, WS), (20, 300, 200, WS), (40, 33, 90, 0), (64, 200, 512, WS), (200, 260, 384, 0),
+                                      (129, 260, 8200, WS), (300, 520, 1000, WS), (512, 768, 640, WS)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_f8_scales_whose_product_leaves_the_range(M, N, K, ws, out):
+    """Scales far from one whose results are ordinary floats: the product of two scales alone would be rounded to few bits,
+    to 0 or to infinity.  A row of zeros with the largest scales stays one."""
+    a, sa, b, sb = f8_operands(M, N, K, M + N + K)
+    if M > 1:
+        a[M // 2] = 0
+    A, B = a.to(DEV), b.to(DEV)
+    W = torch.empty(max(ws, 256), dtype=torch.uint8, device=DEV)
+    for ea, eb in ((-66, -60), (-46, -80), (-100, -26), (110, -90), (-120, 60), (0, 0)):
+        ta, tb = sa * 2.0 ** ea, sb * 2.0 ** eb
+        tb[N // 3] = 2.0 ** 100
+        if M > 1:
+            ta[M // 2] = 2.0 ** 126
+        C = ops.matmul_f8(A, B, ta.to(DEV), tb.to(DEV), out_dtype=DT[out], workspace=W if ws else None).cpu()
+        p64, size = f8_64(a, b, ta, tb)
+        cut = 0.0 if out == "f32" else f8_cut(a, b, ta.double(), tb.double())
+        fine = p64.abs() < 2.0 ** 127
+        e = off(torch.where(fine, C.double(), p64), p64, rounding(p64, DT[out]) + cut + U32 * ((K + 6) * size + 4 * p64.abs()))
+        assert e <= 1, (ea, eb, e)
+        assert int(fine.sum()) >= M * (N - 1) and (M == 1 or bool((C[M // 2] == 0).all()))

@@ -62,6 +62,7 @@ __device__ __forceinline__ u32x4 load_chunk(const uint8_t* row, int k, int K) {
     return v;
 }
 
+// A result is (sum * scale_a) * scale_b: the product of the scales alone may leave fp32's range where the result does not.
 __device__ __forceinline__ float scale_or_one(const float* s, int64_t i) { return s ? s[i] : 1.0f; }
 
 }  // namespace gemm

@@ -108,7 +108,7 @@ __global__ __launch_bounds__(64 * WAVES) void f8_skinny_kernel(const F8Params p)
         float v = 0.0f;
 #pragma unroll
         for (int q = 0; q < WAVES; ++q) v += reinterpret_cast<LDS_AS float*>(part(q, m / 16, n / 4 * 16 + m % 16))[n % 4];
-        store_c1(p.C, p.out_type, m * p.ldc + n0 + n, v * (scale_or_one(p.sa, m) * scale_or_one(p.sb, n0 + n)), p.alpha, p.beta);
+        store_c1(p.C, p.out_type, m * p.ldc + n0 + n, v * scale_or_one(p.sa, m) * scale_or_one(p.sb, n0 + n), p.alpha, p.beta);
     }
 }
 

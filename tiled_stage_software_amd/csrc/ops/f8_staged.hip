@@ -87,7 +87,7 @@ __global__ __launch_bounds__(kStagedThreads) void f8_staged_kernel(const F8Param
             for (int e = 0; e < 4; ++e) {
                 const int n = n0 + wn + 16 * j + 4 * g + e;
                 if (n < p.N)
-                    store_c1(p.C, p.out_type, (int64_t)m * p.ldc + n, acc[i][j][e] * (sa * scale_or_one(p.sb, n)),
+                    store_c1(p.C, p.out_type, (int64_t)m * p.ldc + n, acc[i][j][e] * sa * scale_or_one(p.sb, n),
                              p.alpha, p.beta);
             }
     }

@@ -105,7 +105,7 @@ struct F8Compute : MfmaCompute<__bf16, BM, BN, 64, WM, WN, 16> {
 #pragma unroll
             for (int j = 0; j < C::TN; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) this->acc[i][j][e] *= f * fb[j][e];
+                for (int e = 0; e < 4; ++e) this->acc[i][j][e] = this->acc[i][j][e] * f * fb[j][e];
         }
     }
 };
@@ -330,7 +330,7 @@ __global__ __launch_bounds__(256) void f8_join_kernel(const GemmParams p, const 
         s += *reinterpret_cast<const f32x4*>(part + i * x.part + (m * ldp + n) * 4);
     const float a = scale_or_one(x.sa, m);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] *= a * scale_or_one(x.sb, min(n + e, p.N - 1));
+    for (int e = 0; e < 4; ++e) s[e] = s[e] * a * scale_or_one(x.sb, min(n + e, p.N - 1));
     store4<OUT>(p, m, n, s);
 }
 
