@@ -452,7 +452,10 @@ gemm_status_t gemm_f8_workspace_size(int64_t M, int64_t N, int64_t K, size_t* by
  * No weight is rounded: for each group s * (sum of a * code - z * sum of a), in fp32.  A
  * row of A with an infinity therefore gives NaN where the exact sum may be infinite.  A code enters as
  * 1 + code/16, so the sums that cancel are up to 16 times the weights: an fp32 result is good to a few
- * 2^-22 of its terms.  s * (1 + z/16) is formed in fp32 and has to stay in its range.
+ * 2^-22 of its terms.  A GEMM_F32 C takes z * sum of a off group by group.  For a 16-bit C large
+ * products may take it off once behind all of K: with a mean in A of three times its deviation that is
+ * 5e-5 of the result at K = 14336, below C's own rounding.  s * (1 + z/16) is then formed in fp32 and has to
+ * stay in its range.
  * K == 0 or alpha == 0: C = beta * C.  workspace: more rows than a few run on large tiles, which keep the sums of
  * A and the transposed scales there, beside what gemm_f8 uses one for; gemm_w4_workspace_size gives
  * the bytes.  Without them (or with NULL) every size still runs, many rows several times slower.

@@ -771,3 +771,29 @@ def test_f8_scales_whose_product_leaves_the_range(M, N, K, ws, out):
         e = off(torch.where(fine, C.double(), p64), p64, rounding(p64, DT[out]) + cut + U32 * ((K + 6) * size + 4 * p64.abs()))
         assert e <= 1, (ea, eb, e)
         assert int(fine.sum()) >= M * (N - 1) and (M == 1 or bool((C[M // 2] == 0).all()))
+
+
+@pytest.mark.parametrize("M,N,K,group,ws", [(300, 4096, 4096, 128, "auto"), (300, 4096, 4096, 32, "auto"), (40, 16384, 4096, 64, "auto"),
+                                            (200, 520, 8192, 192, "auto"), (256, 512, 8192, 32, "auto"), (300, 4096, 4095, 64, 8 << 20),
+                                            (300, 4100, 4097, 32, 8 << 20), (300, 4096, 4095, 128, "auto"), (3, 200, 8192, 64, None),
+                                            (16, 200, 8192, 128, None), (30, 200, 8191, 32, None)])
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_w4_zero_points_come_off_group_by_group(M, N, K, group, ws, t):
+    """Rows of A that are all positive: a * (1 + q/16) and a * (1 + z/16) add up to far more than 2^24 of their smallest parts
+    over K, but in each group, and once the zero points are off, to less.  So an fp32 C that takes them off group by
+    group is exact."""
+    g = torch.Generator(DEV).manual_seed(M + N + K + group)
+    groups = -(-K // group)
+    a = torch.randint(200, 257, (M, K), generator=g, device=DEV)
+    codes = torch.randint(0, 256, (N, (K + 1) // 2), generator=g, device=DEV, dtype=torch.uint8)
+    s = 8.0 ** torch.randint(0, 2, (N, groups), generator=g, device=DEV).float()
+    z = torch.randint(7, 10, (N, groups), generator=g, device=DEV).float()
+    q = torch.stack([codes & 15, codes >> 4], 2).flatten(1)[:, :K]
+    each = lambda v: v.repeat_interleave(group, 1)[:, :K]  # noqa: E731
+    w = (each(s) * (q.float() - each(z))).double()
+    want = a.double() @ w.t()
+    assert float(want.abs().max()) < 2 ** 24 and float((a.double()[:1] @ (each(s) * (16 + q.float())).double().t()).mean()) > 2 ** 26
+    if isinstance(ws, int):
+        ws = torch.empty(ws, dtype=torch.uint8, device=DEV)
+    C = ops.matmul_w4(a.to(DT[t]), codes, s.to(DT[t]), z.to(DT[t]), group, out_dtype=torch.float32, workspace=ws)
+    assert torch.equal(C.double(), want)

@@ -8,14 +8,18 @@
 // four cycles each).  Wide blocks of A's rows keep it below theirs: one turned code serves BM / 16
 // instructions (waves of 64 x 64, with half the fragment reads: 308 us instead of 300 for
 // 2048 x 14336 x 4096; 96 rows and three workgroups a compute unit: 308; measured back to back, in turn with
-// other work 261).  Groups shorter than 64 end with every 32 k (390 us).
+// other work 261).  Groups shorter than 64 end with every 32 k (347 us).
 //
-// The zero points' part of all groups, sum over units of (s * (1 + z/16)) * (sum of A over the unit), is a product of its
-// own with one k for a unit (a group; 32 k for short groups).  It runs behind the loop on matrix instructions, which took a
-// second FMA a group off the loop (320 us before, 434 for groups of 32).
+// What the zero points take off a group is (1 + z/16) * (sum of A over it).  EACH: it comes off the group's dot product before
+// the scale, a second FMA, so that the running sum over K never holds more than the result and one group.  For an fp32 C.
+// Otherwise the part of all groups, sum over units of (s * (1 + z/16)) * (sum of A over the unit), is a product of its own
+// with one k for a unit (a group; 32 k for short groups), and runs behind the loop on matrix instructions: 260 us instead of
+// 275 (groups of 32: 347 and 371).  The running sum then holds what does not cancel until the end: on 300 x 4096 x 4096 and
+// 14336 in f16, with a mean of three deviations in A, fp32 sums are off by 2.4e-5 and 5.0e-5 of the result instead of 3.1e-6
+// (without a mean 9e-7 and 4e-7).  A 16-bit C's rounding hides that: 2.09e-4 and 2.13e-4 off in f16, of which the rounding is 2.08e-4.
 //
-// A launch before prepares the sums of A, in the order of the accumulators; the scales, transposed to rows of columns, which
-// the ring brings along with the slabs; and their products with the zero points.
+// A launch before prepares the sums of A, in the order of the accumulators, and the scales and zero points, transposed to rows
+// of columns; the ring brings along with the slabs what their ends need.
 #include <algorithm>
 
 #include "rows_pack.hpp"
@@ -33,9 +37,9 @@ struct W4Tile {
     GemmParams g;          // A, C, sizes, tiles; B unused
     const uint8_t* W;
     int64_t ldw;
-    const char* scales;    // [unit][tile of N][128] floats
-    const char* zeros;     // the same: -s * (1 + z/16)
     const char* sums;      // [unit][tile of M][BM] floats, a lane's together
+    const char* scales;    // [unit][tile of N][128] floats, behind the sums
+    const char* zeros;     // the same, behind the scales: -(1 + z/16) with EACH, -s * (1 + z/16) without
     int per_unit;          // slabs of a unit (0: two units to a slab)
     int per_split;         // slabs of a split of K
     int64_t part;          // bytes between the splits' results
@@ -45,21 +49,22 @@ struct W4Tile {
 // different banks.
 __device__ __forceinline__ int codes_swz(int row) { return (row >> 3) & 1; }
 
-// S1: units are 32 k, two to a slab.
-template <int T, int BM, bool S1>
+// S1: units are 32 k, two to a slab.  EACH: the zero points come off at each unit's end (the other form: zero_points()).
+template <int T, int BM, bool S1, bool EACH>
 struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> {
     typedef MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> C;
     static constexpr int TM = C::TM, TN = C::TN, AH = TM / 2, NU = S1 ? 2 : 1;
     static constexpr int A_BYTES = BM * 128, Q_BYTES = kBN * 32, S_AT = A_BYTES + Q_BYTES;
-    static constexpr int SL = 8 * NU;   // chunks of a wave's scales: [wave][unit][8]
-    static constexpr int STAGE = S_AT + kNC * SL * 16;
+    static constexpr int SL = 8 * NU, RL = BM / 16;   // chunks of a wave's scales, [unit][8]; of a unit's sums that a wave copies
+    static constexpr int UL = EACH ? 2 * SL + NU * RL : SL;   // of a wave: scales, then zero points, then its part of the sums
+    static constexpr int STAGE = S_AT + kNC * UL * 16;
     static constexpr int KS = 4;   // steps of a slab: two k-steps by two halves of A's blocks
     static_assert(TN == 2 && TM % 2 == 0, "waves of 32 columns");
     f32x4 dot[TM][TN];
     u32x4 fa[2][AH], b[TN];
     uint32_t word[TN];
-    f32x4 scale[NU][TN];
-    uint32_t qo, so;   // LDS offsets of codes and scales within a slot
+    f32x4 scale[TN], point[TN], a_sum[TM / 4];   // of the unit that ends next: scales, zero points, sums of A
+    uint32_t qo, so, mo;   // LDS offsets of codes, scales and sums within a slot
     Spread<T> spread;
     int pos = 0, per_unit, left;   // slab within its unit; slabs left
 
@@ -68,7 +73,9 @@ struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> 
         const int wn = wave_id(), lane = lane_id(), r = lane % 16, g = lane / 16;
         const int kc = (g & 1) * 2 + (g >> 1);   // the k-chunk of lane group g, as in A's fragments
         qo = (uint32_t)(A_BYTES + (wn * 32 + r) * 32 + codes_swz(r) * 16 + kc * 4);
-        so = (uint32_t)(S_AT + wn * SL * 16 + g * 16);
+        so = (uint32_t)(S_AT + wn * UL * 16 + g * 16);
+        const int at = r * TM / 4;   // this lane's sums, TM of them
+        mo = (uint32_t)(S_AT + (at / RL * UL + 2 * SL + at % RL) * 16);
         per_unit = p.per_unit;
         left = slabs;
     }
@@ -83,11 +90,17 @@ struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> 
 #pragma unroll
             for (int j = 0; j < TN; ++j) word[j] = *reinterpret_cast<LDS_AS const uint32_t*>(st + (qo ^ (q / 2 * 16)) + j * 16 * 32);
         }
-        if (q == 1) {   // (before the barrier that frees the slot)
+        if (S1 ? q % 2 == 1 : q == 1) {   // (before the barrier that frees the slot)
+            const int u = S1 ? q / 2 : 0;
 #pragma unroll
-            for (int u = 0; u < NU; ++u)
+            for (int j = 0; j < TN; ++j) {
+                scale[j] = *reinterpret_cast<LDS_AS const f32x4*>(st + so + u * 128 + j * 64);
+                if constexpr (EACH) point[j] = *reinterpret_cast<LDS_AS const f32x4*>(st + so + SL * 16 + u * 128 + j * 64);
+            }
+            if constexpr (EACH) {
 #pragma unroll
-                for (int j = 0; j < TN; ++j) scale[u][j] = *reinterpret_cast<LDS_AS const f32x4*>(st + so + u * 128 + j * 64);
+                for (int i = 0; i < TM / 4; ++i) a_sum[i] = *reinterpret_cast<LDS_AS const f32x4*>(st + mo + (u * RL + i) * 16);
+            }
         }
     }
     template <int BUF, bool FIRST>
@@ -101,13 +114,22 @@ struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> 
                 d = Half<T>::mfma(b[j], fa[BUF][i], FIRST ? zero : d);
             }
     }
-    __device__ __forceinline__ void finish_unit(int u) {
+    __device__ __forceinline__ void finish_unit() {
 #pragma unroll
         for (int j = 0; j < TN; ++j)
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) this->acc[i][j][e] = __builtin_fmaf(scale[u][j][e], dot[i][j][e], this->acc[i][j][e]);
+                for (int e = 0; e < 4; ++e) {
+                    float d = dot[i][j][e];
+                    if constexpr (EACH) d = __builtin_fmaf(point[j][e], a_sum[i / 4][i % 4], d);
+                    this->acc[i][j][e] = __builtin_fmaf(scale[j][e], d, this->acc[i][j][e]);
+                }
+        // (here: moved down to the slab's end, as they would be, a unit's products would take registers until then)
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) asm volatile("" : "+v"(this->acc[i][j]));
     }
     // acc += zeros * sums over units u0 .. end - 1, four of them a step, each eight k of the instruction: a float is cut into
     // three bf16 parts h, m, l that hold all its bits, and of the nine products all but l * l are taken.
@@ -161,14 +183,14 @@ struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> 
         }
         if (S1) {
             products<BUF, true>(q % 2);
-            if (q % 2 == 1) finish_unit(q / 2);
+            if (q % 2 == 1) finish_unit();
         } else {
             if (q < 2 && pos == 0) products<BUF, true>(q % 2);
             else products<BUF, false>(q % 2);
             if (q == KS - 1) {
                 --left;
                 if (++pos == per_unit || left == 0) {
-                    finish_unit(0);
+                    finish_unit();
                     pos = 0;
                 }
             }
@@ -179,30 +201,49 @@ struct W4Compute : MfmaCompute<typename Half<T>::type, BM, kBN, 64, 1, kNC, 16> 
     __device__ __forceinline__ void barrier() { gemm::barrier(); }
 };
 
-// Where chunk l (of SL) of wave w's scales lies, from unit `unit` on.
-__device__ __forceinline__ uint32_t scale_chunk(const W4Tile& p, int tn, int unit, int w, int l) {
-    return (((uint32_t)(unit + l / 8) * p.g.tiles_n + tn) * kBN + w * (kBN / kNC)) * 4 + l % 8 * 16;
+// Where chunk l (of UL) of what wave w copies lies for unit 0, in bytes from the sums, and the bytes from one unit to the next.
+template <class F>
+__device__ __forceinline__ uint32_t unit_chunk(const W4Tile& p, int tm, int tn, int w, int l) {
+    if (l < 2 * F::SL)
+        return (uint32_t)((l < F::SL ? p.scales : p.zeros) - p.sums) +
+               (((uint32_t)(l % F::SL / 8) * p.g.tiles_n + tn) * kBN + w * (kBN / kNC)) * 4 + l % 8 * 16;
+    l -= 2 * F::SL;
+    return (((uint32_t)(l / F::RL) * p.g.tiles_m + tm) * (F::RL * 16) + (w * F::RL + l % F::RL) * 4) * 4;
+}
+template <class F>
+__device__ __forceinline__ uint32_t unit_step(const W4Tile& p, int l) {
+    return (uint32_t)(l < 2 * F::SL ? p.g.tiles_n * kBN : p.g.tiles_m * (F::RL * 16)) * 4;
 }
 // First unit of slab s of the whole K.
 __device__ __forceinline__ int unit_of(const W4Tile& p, int s) { return p.per_unit ? s / p.per_unit : 2 * s; }
 
 // Direct global -> LDS copies: 16-byte aligned rows, whole slabs and tiles.
-template <int T, int BM, bool S1>
-struct W4RingOps : W4Compute<T, BM, S1> {
-    typedef W4Compute<T, BM, S1> F;
+template <int T, int BM, bool S1, bool EACH>
+struct W4RingOps : W4Compute<T, BM, S1, EACH> {
+    typedef W4Compute<T, BM, S1, EACH> F;
     ALoader<BM, 128, kNC> la;
     DirectLoader<kBN, 32, kNC, false> lq;
-    static constexpr int L = decltype(la)::IPW + decltype(lq)::IPW + 1;
+    static constexpr int ZL = EACH ? 2 * F::SL : F::SL;   // chunks of the scales, and of the zero points: one copy; the sums another
+    static constexpr int L = decltype(la)::IPW + decltype(lq)::IPW + (EACH ? 2 : 1);
     const W4Tile* p;
-    int tn, s0;
+    uint32_t at_scales, at_sums;
+    int s0;
+    __device__ __forceinline__ void init_units(const W4Tile& p_, int tm, int tn, int s0_) {
+        p = &p_;
+        s0 = s0_;
+        at_scales = unit_chunk<F>(p_, tm, tn, wave_id(), lane_id());
+        at_sums = EACH ? unit_chunk<F>(p_, tm, tn, wave_id(), ZL + lane_id()) : 0;
+    }
     __device__ __forceinline__ void issue(int slab, int slot, int, int) {
         LDS_AS char* st = this->smem + slot * F::STAGE;
         la.issue(slab, st, 0, decltype(la)::IPW);
         lq.issue(slab, st + F::A_BYTES, 0, decltype(lq)::IPW);
-        const int w = wave_id(), lane = lane_id();
-        if (lane < F::SL)
-            la.template copy<0>(__builtin_amdgcn_make_buffer_rsrc((void*)p->scales, (short)0, -1, kBufferFlags),
-                                scale_chunk(*p, tn, unit_of(*p, s0 + slab), w, lane), 0, st + F::S_AT + w * F::SL * 16);
+        const int w = wave_id(), lane = lane_id(), u = unit_of(*p, s0 + slab);
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)p->sums, (short)0, -1, kBufferFlags);
+        if (lane < ZL) la.template copy<0>(rs, at_scales, u * unit_step<F>(*p, 0), st + F::S_AT + w * F::UL * 16);
+        if constexpr (EACH) {
+            if (lane < F::UL - ZL) la.template copy<0>(rs, at_sums, u * unit_step<F>(*p, ZL), st + F::S_AT + (w * F::UL + ZL) * 16);
+        }
     }
     template <int N>
     __device__ __forceinline__ void wait_slabs() { wait_vm<N * L>(); }
@@ -213,11 +254,11 @@ struct W4RingOps : W4Compute<T, BM, S1> {
 // Any pitch, alignment and size (K >= 64): 16-byte loads of any alignment into registers, one
 // slab ahead, written into the other slot in the last step but one.  A chunk past a row's end is read
 // as the row's last 16 bytes and shifted.  Rows past the end repeat the last.
-template <int T, int BM, bool S1>
-struct W4StagedOps : W4Compute<T, BM, S1> {
-    typedef W4Compute<T, BM, S1> F;
+template <int T, int BM, bool S1, bool EACH>
+struct W4StagedOps : W4Compute<T, BM, S1, EACH> {
+    typedef W4Compute<T, BM, S1, EACH> F;
     static constexpr int NT = 64 * kNC, STEP = NT / 8, CA = BM / STEP;
-    static constexpr int UT = kNC * F::SL;   // threads with a chunk of the scales
+    static constexpr int UT = kNC * F::UL;   // threads with a chunk of the units
     static_assert(STEP % 16 == 0 && CA * STEP == BM && UT <= NT && 2 * kBN == NT, "chunks per thread");
     const char* arow[CA];
     const uint8_t* qrow;
@@ -227,7 +268,7 @@ struct W4StagedOps : W4Compute<T, BM, S1> {
     const W4Tile* p;
     int k_bytes, q_bytes, s0, wslot = 0, slab_ = 0;
     bool ask_write = false;
-    __device__ __forceinline__ void init_rows(const W4Tile& p_, int tn, int m0, int n0, int s0_) {
+    __device__ __forceinline__ void init_rows(const W4Tile& p_, int tm, int tn, int m0, int n0, int s0_) {
         p = &p_;
         s0 = s0_;
         k_bytes = p->g.K * 2;
@@ -237,8 +278,8 @@ struct W4StagedOps : W4Compute<T, BM, S1> {
         for (int i = 0; i < CA; ++i) arow[i] = p->g.A + (int64_t)min(m0 + row + i * STEP, p->g.M - 1) * p->g.lda * 2;
         dst = (uint32_t)(row * 128 + ((c ^ swz<8>(row)) << 4));
         qrow = p->W + (int64_t)min(n0 + t / 2, p->g.N - 1) * p->ldw;
-        uchunk = scale_chunk(*p, tn, 0, t / F::SL % kNC, t % F::SL);
-        ustep = (uint32_t)(p->g.tiles_n * kBN) * 4;
+        uchunk = unit_chunk<F>(*p, tm, tn, t / F::UL % kNC, t % F::UL);
+        ustep = unit_step<F>(*p, t % F::UL);
     }
     __device__ __forceinline__ void load(int slab) {
         slab_ = s0 + slab;
@@ -247,7 +288,7 @@ struct W4StagedOps : W4Compute<T, BM, S1> {
 #pragma unroll
         for (int i = 0; i < CA; ++i) va[i] = load16(arow[i] + ka);
         vq = load16(qrow + kq);
-        if ((int)threadIdx.x < UT) vu = load16(p->scales + (uchunk + (uint32_t)unit_of(*p, slab_) * ustep));
+        if ((int)threadIdx.x < UT) vu = load16(p->sums + (uchunk + (uint32_t)unit_of(*p, slab_) * ustep));
         ask_write = true;
     }
     __device__ __forceinline__ void put() {
@@ -278,10 +319,10 @@ struct W4StagedOps : W4Compute<T, BM, S1> {
 };
 
 // Splits of K (blockIdx.y) store plain sums, each into its own buffer.
-template <int T, int OUT, int BM, bool S1, bool DIRECT>
+template <int T, int OUT, int BM, bool S1, bool EACH, bool DIRECT>
 __global__ __launch_bounds__(64 * kNC) __attribute__((amdgpu_waves_per_eu(2)))
 void w4_tile_kernel(W4Tile p) {
-    typedef W4Compute<T, BM, S1> F;
+    typedef W4Compute<T, BM, S1, EACH> F;
     constexpr int S = DIRECT ? 3 : 2;
     __shared__ __attribute__((aligned(1024))) char smem_raw[S * F::STAGE];
     LDS_AS char* smem = (LDS_AS char*)smem_raw;
@@ -294,22 +335,22 @@ void w4_tile_kernel(W4Tile p) {
     const int u0 = unit_of(p, s0), u1 = S1 ? u0 + 2 * slabs : u0 + (slabs + p.per_unit - 1) / p.per_unit;
     p.g.C += (int64_t)blockIdx.y * p.part;
     if constexpr (DIRECT) {
-        W4RingOps<T, BM, S1> ops;
+        W4RingOps<T, BM, S1, EACH> ops;
         ops.init(smem, p, slabs);
-        ops.p = &p; ops.tn = tn; ops.s0 = s0;
+        ops.init_units(p, tm, tn, s0);
         init_a<BM, 128, kNC>(ops.la, p.g.A + ((int64_t)m0 * p.g.lda + (int64_t)s0 * kSlabK) * 2, p.g.lda * 2, kSlabK * 2, p.g.M - m0);
         ops.lq.init(reinterpret_cast<const char*>(p.W) + (int64_t)n0 * p.ldw + (int64_t)s0 * (kSlabK / 2), p.ldw, kSlabK / 2);
         const int lane = lane_id();
         ops.lq.vpat[0] = (uint32_t)(lane / 2 * (int)p.ldw + ((lane % 2) ^ codes_swz(lane / 2)) * 16);
         gemm_sched::ring_mainloop<S, F::KS, 1>(ops, slabs);
-        ops.zero_points(p, tm, tn, u0, u1);
+        if constexpr (!EACH) ops.zero_points(p, tm, tn, u0, u1);
         ops.template epilogue<OUT>(p.g, m0, n0, m_keep, n_keep);
     } else {
-        W4StagedOps<T, BM, S1> ops;
+        W4StagedOps<T, BM, S1, EACH> ops;
         ops.init(smem, p, slabs);
-        ops.init_rows(p, tn, m0, n0, s0);
+        ops.init_rows(p, tm, tn, m0, n0, s0);
         gemm_sched::staged_mainloop<S, F::KS>(ops, slabs);
-        ops.zero_points(p, tm, tn, u0, u1);
+        if constexpr (!EACH) ops.zero_points(p, tm, tn, u0, u1);
         ops.template epilogue<OUT>(p.g, m0, n0, m_keep, n_keep);
     }
 }
@@ -325,6 +366,7 @@ struct W4Prepare {
     float* z;
     int64_t lda, lds;
     int M, N, K, group, unit, units, tiles_m, tiles_n, bm, tm;   // tm: blocks of 16 rows of a tile
+    bool each;             // zero points by themselves, not times their scales
     int64_t sum_blocks;
     RowsJob pack_a, pack_w;
     uint32_t a_blocks, pack_blocks;
@@ -383,7 +425,7 @@ __global__ __launch_bounds__(256) void w4_prepare_kernel(const W4Prepare p) {
             const uint32_t v = turn[u][threadIdx.x % kTurnCols];
             const float s = to_f32<T>((uint16_t)v);
             p.s[i] = s;
-            p.z[i] = -s * zero16<T>((uint16_t)(v >> 16));
+            p.z[i] = (p.each ? -1.0f : -s) * zero16<T>((uint16_t)(v >> 16));
         }
 }
 
@@ -455,23 +497,23 @@ W4Plan w4_plan(int64_t M, int64_t N, int64_t K, int64_t group, size_t room) {
     return q;
 }
 
-template <int T, int OUT, int BM>
+template <int T, int OUT, int BM, bool EACH>
 hipError_t tile_of(const W4Tile& t, bool short_units, bool direct, int splits, hipStream_t st) {
     const dim3 grid((unsigned)(t.g.tiles_m * t.g.tiles_n), (unsigned)splits), block(256);
     if (short_units) {
-        if (direct) hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, true, true>), grid, block, 0, st, t);
-        else hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, true, false>), grid, block, 0, st, t);
+        if (direct) hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, true, EACH, true>), grid, block, 0, st, t);
+        else hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, true, EACH, false>), grid, block, 0, st, t);
     } else {
-        if (direct) hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, false, true>), grid, block, 0, st, t);
-        else hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, false, false>), grid, block, 0, st, t);
+        if (direct) hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, false, EACH, true>), grid, block, 0, st, t);
+        else hipLaunchKernelGGL((w4_tile_kernel<T, OUT, BM, false, EACH, false>), grid, block, 0, st, t);
     }
     return hipGetLastError();
 }
-template <int T, int OUT>
+template <int T, int OUT, bool EACH>
 hipError_t out_of(const W4Plan& q, const W4Tile& t, bool direct, hipStream_t st) {
     const bool s1 = q.unit == 32;
-    if (q.bm == 128) return tile_of<T, OUT, 128>(t, s1, direct, q.splits, st);
-    return tile_of<T, OUT, 64>(t, s1, direct, q.splits, st);
+    if (q.bm == 128) return tile_of<T, OUT, 128, EACH>(t, s1, direct, q.splits, st);
+    return tile_of<T, OUT, 64, EACH>(t, s1, direct, q.splits, st);
 }
 
 // What the direct loads need of A and the codes.  They hold a row's offset in its tile in 32 bits, as it lies in memory and
@@ -509,6 +551,8 @@ hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, size_t ws_byt
     a.unit = q.unit; a.units = q.units;
     a.tiles_m = (int)q.tiles_m; a.tiles_n = (int)q.tiles_n;
     a.bm = q.bm; a.tm = q.bm / 16;
+    const bool each = f.out_type == DT_F32;   // (see above: what a 16-bit C hides)
+    a.each = each;
     a.sum_blocks = ceil_div(q.tiles_m * q.bm * q.units, 64);
     W4Tile t = {};
     GemmParams& p = t.g;
@@ -566,14 +610,14 @@ hipError_t run_tiles(const W4Params& f, const W4Plan& q, char* ws, size_t ws_byt
         p.ldc = ldp;
         p.alpha = 1.0f;
         p.beta = 0.0f;
-        e = out_of<T, DT_F32>(q, t, direct, st);
+        e = each ? out_of<T, DT_F32, true>(q, t, direct, st) : out_of<T, DT_F32, false>(q, t, direct, st);
         if (e != hipSuccess) return e;
         const dim3 grid((unsigned)ceil_div(f.M * ldp / 4, 256));
         if (f.out_type == DT_F32) hipLaunchKernelGGL(w4_join_kernel<DT_F32>, grid, dim3(256), 0, st, whole, parts, t.part, (int)ldp, q.splits);
         else hipLaunchKernelGGL(w4_join_kernel<T>, grid, dim3(256), 0, st, whole, parts, t.part, (int)ldp, q.splits);
         return hipGetLastError();
     }
-    return f.out_type == DT_F32 ? out_of<T, DT_F32>(q, t, direct, st) : out_of<T, T>(q, t, direct, st);
+    return each ? out_of<T, DT_F32, true>(q, t, direct, st) : out_of<T, T, false>(q, t, direct, st);
 }
 
 }  // namespace
