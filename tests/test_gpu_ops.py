@@ -797,3 +797,27 @@ def test_w4_zero_points_come_off_group_by_group(M, N, K, group, ws, t):
         ws = torch.empty(ws, dtype=torch.uint8, device=DEV)
     C = ops.matmul_w4(a.to(DT[t]), codes, s.to(DT[t]), z.to(DT[t]), group, out_dtype=torch.float32, workspace=ws)
     assert torch.equal(C.double(), want)
+
+
+@pytest.mark.parametrize("M,N,K,op", [(2097120 + 2097152 + 17, 19, 32, "w4"), (5, (1 << 28) + 35, 1, "w4"), (2, (1 << 28) + 35, 1, "w4"),
+                                      ((1 << 29) + 70, 1, 1, "f8"), (70, (1 << 24) + 35, 1, "f8"), (1, (1 << 28) + 35, 1, "f8")])
+def test_sizes_beyond_one_launch(M, N, K, op):
+    """More workgroups than a grid counts, without a workspace: exact on small whole numbers, the last rows and columns too."""
+    g = torch.Generator(DEV).manual_seed(5)
+    a = torch.randint(-2, 3, (M, K), generator=g, device=DEV, dtype=torch.int8)
+    if op == "w4":
+        codes = torch.randint(0, 16, (N, (K + 1) // 2), generator=g, device=DEV, dtype=torch.uint8) * 17   # both halves alike
+        s = torch.ones(N, 1, dtype=torch.bfloat16, device=DEV)
+        C = ops.matmul_w4(a.bfloat16(), codes, s, group=32, workspace=None)
+        b = (codes & 15).to(torch.int8) - 8
+        b = b.repeat_interleave(2, 1)[:, :K]
+    else:
+        b = torch.randint(-2, 3, (N, K), generator=g, device=DEV, dtype=torch.int8)
+        sa = torch.full((M,), 2.0, device=DEV)
+        sb = torch.ones(N, device=DEV)
+        C = ops.matmul_f8(a.to(torch.float8_e4m3fn), b.to(torch.float8_e4m3fn), sa, sb, workspace=None)
+        a = a * 2
+    for m in range(0, M, 1 << 24):
+        for n in range(0, N, 1 << 24):
+            want = a[m:m + (1 << 24)].float() @ b[n:n + (1 << 24)].float().t()
+            assert torch.equal(C[m:m + (1 << 24), n:n + (1 << 24)], want.bfloat16())

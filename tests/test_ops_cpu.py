@@ -277,3 +277,19 @@ def test_workspaces_have_to_be_whole_memory():
             ops._workspace(view, None, big.device)
     with pytest.raises(ValueError, match="contiguous"):
         lg.workspace_of(big[:, :8], big.device)
+
+
+@no_gpu
+@pytest.mark.parametrize("call", [
+    "lg.gemm_w4(1, 1 << 30, 64, 32, 32, 1.0, P, 32, P, 16, P, 0, 1, 0.0, P, 1, 64)",
+    "lg.gemm_w4(1, 5, 1 << 30, 32, 32, 1.0, P, 32, P, 16, P, 0, 1, 0.0, P, 1, 1 << 30)",
+    "lg.gemm_w4(1, 1, 1 << 30, 32, 32, 1.0, P, 32, P, 16, P, 0, 1, 0.0, P, 1, 1 << 30)",
+    "lg.gemm_f8(1 << 30, 1 << 30, 16, 1.0, P, 16, 0, P, 16, 0, 0.0, P, 1, 1 << 30)",
+    "lg.gemm_f8(5, 1 << 30, 16, 1.0, P, 16, 0, P, 16, 0, 0.0, P, 1, 1 << 30)",
+    "lg.gemm_f8(1 << 30, 1 << 30, 1 << 20, 1.0, P, 1 << 20, 0, P, 1 << 20, 0, 0.0, P, 1, 1 << 30)",
+])
+def test_every_size_is_launched(call):
+    """The largest sizes pass the limits of one grid: they go out in several launches, and nothing but the missing device is
+    in their way."""
+    err = notes([call])
+    assert "no ROCm-capable device" in err and "invalid" not in err, err

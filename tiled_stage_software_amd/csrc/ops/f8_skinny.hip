@@ -133,12 +133,14 @@ double f8_skinny_us(const F8Params& p) {
 }
 
 // Sixteen waves where eight would leave most of the card's wave slots empty and each still has steps to take.
-hipError_t launch_f8_skinny(const F8Params& p, hipStream_t st) {
-    const bool deep = ((int64_t)p.N + 15) / 16 <= 2 * num_compute_units() && p.K >= 2048;
-    if (p.M <= kFewRows) return deep ? go<1, 16, true>(p, st) : go<1, 8, true>(p, st);
-    if (p.M <= 16) return deep ? go<1, 16, false>(p, st) : go<1, 8, false>(p, st);
-    if (p.M > kF8SkinnyRows) return hipErrorInvalidValue;
-    return deep ? go<2, 16, false>(p, st) : go<2, 8, false>(p, st);
+hipError_t launch_f8_skinny(const F8Params& f, hipStream_t st) {
+    if (f.M > kF8SkinnyRows) return hipErrorInvalidValue;
+    return in_pieces(f, kF8SkinnyRows, kMostCols, [&](const F8Params& p) {
+        const bool deep = ((int64_t)p.N + 15) / 16 <= 2 * num_compute_units() && p.K >= 2048;
+        if (p.M <= kFewRows) return deep ? go<1, 16, true>(p, st) : go<1, 8, true>(p, st);
+        if (p.M <= 16) return deep ? go<1, 16, false>(p, st) : go<1, 8, false>(p, st);
+        return deep ? go<2, 16, false>(p, st) : go<2, 8, false>(p, st);
+    });
 }
 
 }  // namespace gemm

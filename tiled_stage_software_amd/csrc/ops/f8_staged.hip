@@ -95,13 +95,15 @@ __global__ __launch_bounds__(kStagedThreads) void f8_staged_kernel(const F8Param
 
 }  // namespace
 
-hipError_t launch_f8_staged(const F8Params& p, hipStream_t st) {
-    const int64_t tm = ((int64_t)p.M + kTile - 1) / kTile, tn = ((int64_t)p.N + kTile - 1) / kTile;
-    if (tm * tn > INT32_MAX / kStagedThreads) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)(tm * tn)), block(kStagedThreads);
-    if (p.out_type == DT_F32) hipLaunchKernelGGL(f8_staged_kernel<true>, grid, block, 0, st, p, (int)tn);
-    else hipLaunchKernelGGL(f8_staged_kernel<false>, grid, block, 0, st, p, (int)tn);
-    return hipGetLastError();
+hipError_t launch_f8_staged(const F8Params& f, hipStream_t st) {
+    const int64_t cols = f.N < kMostCols ? f.N : kMostCols, most = INT32_MAX / kStagedThreads;   // tiles of a launch
+    return in_pieces(f, most / ((cols + kTile - 1) / kTile) * kTile, cols, [&](const F8Params& p) {
+        const int64_t tm = ((int64_t)p.M + kTile - 1) / kTile, tn = ((int64_t)p.N + kTile - 1) / kTile;
+        const dim3 grid((unsigned)(tm * tn)), block(kStagedThreads);
+        if (p.out_type == DT_F32) hipLaunchKernelGGL(f8_staged_kernel<true>, grid, block, 0, st, p, (int)tn);
+        else hipLaunchKernelGGL(f8_staged_kernel<false>, grid, block, 0, st, p, (int)tn);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace gemm

@@ -63,6 +63,36 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return v;
 }
 
+// Launches of a product's kernel for at most `rows` x `cols` of C each: grids are counted in 32 bits, workgroups times
+// threads, and have 65535 rows at most, which sizes up to 2^30 can pass.
+constexpr int64_t kMostCols = int64_t(1) << 24;
+inline void skip(F8Params& p, int64_t m, int64_t n) {
+    p.A += m * p.lda;
+    p.B += n * p.ldb;
+    if (p.sa) p.sa += m;
+    if (p.sb) p.sb += n;
+}
+inline void skip(W4Params& p, int64_t m, int64_t n) {
+    p.A += m * p.lda * 2;
+    p.W += n * p.ldw;
+    p.scales += n * p.lds * 2;
+    if (p.zeros) p.zeros += n * p.lds * 2;
+}
+template <class P, class Launch>
+hipError_t in_pieces(const P& p, int64_t rows, int64_t cols, Launch&& launch) {
+    for (int64_t m = 0; m < p.M; m += rows)
+        for (int64_t n = 0; n < p.N; n += cols) {
+            P q = p;
+            skip(q, m, n);
+            q.C += (m * p.ldc + n) * (p.out_type == DT_F32 ? 4 : 2);
+            q.M = (int)(p.M - m < rows ? p.M - m : rows);
+            q.N = (int)(p.N - n < cols ? p.N - n : cols);
+            const hipError_t e = launch(q);
+            if (e != hipSuccess) return e;
+        }
+    return hipSuccess;
+}
+
 // One element of C = alpha * acc + beta * C (beta == 0: C is not read).
 __device__ __forceinline__ void store_c1(char* C, int out_type, int64_t at, float acc, float alpha, float beta) {
     if (out_type == DT_F32) {

@@ -18,6 +18,7 @@ namespace gemm {
 namespace {
 
 constexpr int kStep = 128;
+constexpr int64_t kMostRows = int64_t(1) << 20;   // of a launch: blocks of 32 rows are its grid's second size
 
 // CHAIN: instructions of 32 codes that are sure to share a scale (groups are multiples of 32 * CHAIN).
 template <int T, int MT, int WAVES, int CHAIN>
@@ -153,7 +154,6 @@ void w4_skinny_kernel(const W4Params p) {
 template <int T, int MT, int WAVES>
 hipError_t go(const W4Params& p, hipStream_t st) {
     const int64_t tn = ((int64_t)p.N + 15) / 16, tm = ((int64_t)p.M + 16 * MT - 1) / (16 * MT);
-    if (tn > INT32_MAX / (64 * WAVES) || tm > 65535) return hipErrorInvalidValue;
     const dim3 grid((unsigned)tn, (unsigned)tm), block(64 * WAVES);
     if (p.group % 128 == 0) hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 4>), grid, block, 0, st, p);
     else if (p.group % 64 == 0) hipLaunchKernelGGL((w4_skinny_kernel<T, MT, WAVES, 2>), grid, block, 0, st, p);
@@ -193,7 +193,9 @@ double w4_skinny_us(const W4Params& p) {
 }
 
 hipError_t launch_w4_skinny(int in_type, const W4Params& p, hipStream_t st) {
-    return in_type == DT_BF16 ? skinny_of<DT_BF16>(p, st) : skinny_of<DT_F16>(p, st);
+    return in_pieces(p, kMostRows, kMostCols, [&](const W4Params& q) {
+        return in_type == DT_BF16 ? skinny_of<DT_BF16>(q, st) : skinny_of<DT_F16>(q, st);
+    });
 }
 
 }  // namespace gemm

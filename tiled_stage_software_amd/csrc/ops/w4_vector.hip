@@ -165,7 +165,9 @@ hipError_t vector_of(const W4Params& p, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_w4_vector(int in_type, const W4Params& p, hipStream_t st) {
-    return in_type == DT_BF16 ? vector_of<DT_BF16>(p, st) : vector_of<DT_F16>(p, st);
+    return in_pieces(p, kW4VectorRows, kMostCols, [&](const W4Params& q) {
+        return in_type == DT_BF16 ? vector_of<DT_BF16>(q, st) : vector_of<DT_F16>(q, st);
+    });
 }
 
 }  // namespace gemm
