@@ -414,7 +414,8 @@ gemm_status_t gemm_rmsnorm(gemm_dtype_t in_type, gemm_dtype_t w_type, gemm_dtype
  * may be NULL.  w as in the forward pass (NULL: ones).  dw: cols floats, or NULL (not
  * computed).  dx may be the same memory as dy, h or dh with the same leading dimension.
  * The sum over rows runs in fp32, in parts that meet in `workspace` in a fixed order:
- * gemm_rmsnorm_bwd_workspace_size gives the bytes for full speed; with less (or NULL) the
+ * gemm_rmsnorm_bwd_workspace_size gives the bytes for full speed, whatever dx lies on (up to 128
+ * rows are summed without touching it where dx lies on neither dy nor h); with less (or NULL) the
  * rows are cut into fewer parts.  rows == 0: dw = 0.  cols == 0: nothing is written.
  * Errors: as gemm_rmsnorm, plus GEMM_ERR_INVALID_ARG for a workspace not 256-byte aligned. */
 gemm_status_t gemm_rmsnorm_bwd(gemm_dtype_t in_type, gemm_dtype_t w_type, int64_t rows, int64_t cols, const void* dy,
@@ -433,8 +434,8 @@ gemm_status_t gemm_rmsnorm_bwd_workspace_size(gemm_dtype_t in_type, int64_t rows
  * C's own rounding.  K == 0 or alpha == 0: C = beta * C.
  * workspace: lets the call split a long K over more workgroups where M x N alone gives too
  * few, and copy operands whose rows are not 16-byte aligned or not whole slabs of 128 into such
- * rows where that pays.  gemm_f8_workspace_size gives the bytes for the splits and for the copies that K and M ask
- * for; rows that are unaligned though K is a multiple of 128 can use (M + N) * K more.  With
+ * rows where that pays.  gemm_f8_workspace_size gives the bytes that a product of contiguous aligned operands
+ * uses; rows that are unaligned though K is a multiple of 128 can use (M + N) * K more.  With
  * less (or NULL) the call does without, with the same result up to the order of sums.
  * Errors: as gemm_bf16, plus GEMM_ERR_INVALID_ARG for a workspace not 256-byte aligned. */
 gemm_status_t gemm_f8(int64_t M, int64_t N, int64_t K, float alpha, const void* A, int64_t lda, const float* scale_a,

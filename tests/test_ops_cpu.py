@@ -293,3 +293,40 @@ def test_every_size_is_launched(call):
     in their way."""
     err = notes([call])
     assert "no ROCm-capable device" in err and "invalid" not in err, err
+
+
+@no_gpu
+def test_workspaces_asked_for_are_used_and_enough():
+    """With the bytes of the query a call does what it would with any more; and where the query asks for some, a call of
+    one of the result types does something with them."""
+    g = torch.Generator().manual_seed(1)
+    draw = lambda low, high: int(round(low * (high / low) ** float(torch.rand(1, generator=g))))  # noqa: E731
+    shapes = [(256, 512, 17000001), (64, 100, 100), (40, 4096, 64), (333, 3001, 2049), (64, 128, 8388608), (1 << 30, 1 << 30, 1 << 30),
+              (33, 14336, 4096), (300, 520, 1000), (129, 260, 16000), (200, 300, 15000), (17, 14336, 4097), (300, 300, 40)]
+    shapes += [(draw(1, 4096), draw(16, 16384), draw(16, 16384)) for _ in range(60)]
+    calls, sizes = [], []
+    big = (1 << 62) - 1
+    for M, N, K in shapes:
+        s, f = lg.gemm_f8_workspace_size(M, N, K)
+        s4, w = lg.gemm_w4_workspace_size(BF16, M, N, K, 64)
+        assert s == s4 == lg.GEMM_OK
+        sizes.append((f, w))
+        for ws in (0, f, big):
+            for t in (1, 0):
+                calls.append(f"lg.gemm_f8({M}, {N}, {K}, 1.0, P, {K}, 0, P, {K}, 0, 0.0, P, {t}, {N}, P, {ws})")
+        for ws in (0, w, big):
+            calls.append(f"lg.gemm_w4(1, {M}, {N}, {K}, 64, 1.0, P, {K}, P, {(K + 1) // 2}, P, P, {-(-K // 64)}, 0.0, P, 1, {N}, P, {ws})")
+    said = []
+    for line in notes(calls).splitlines():
+        if " M=" in line:
+            said.append(line.split(": ", 2)[2])
+        elif "status" not in line:
+            said[-1] += line
+    assert len(said) == 9 * len(shapes)
+    for i, (f, w) in enumerate(sizes):
+        none, asked, more = said[9 * i:9 * i + 2], said[9 * i + 2:9 * i + 4], said[9 * i + 4:9 * i + 6]
+        assert asked == more, (shapes[i], asked, more)
+        assert (f > 0) == (asked != none), (shapes[i], f, none, asked)
+        none, asked, more = said[9 * i + 6:9 * i + 9]
+        assert asked == more, (shapes[i], asked, more)
+        assert (w > 0) == (asked != none), (shapes[i], w, none, asked)

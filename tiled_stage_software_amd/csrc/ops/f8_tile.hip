@@ -415,17 +415,6 @@ hipError_t join_of(const GemmParams& p, const F8Extra& x, const void* part, int6
 
 constexpr size_t kMostCopied = size_t(1) << 34;   // rows_pack counts chunks in 32 bits
 
-// Bytes for the splits and, for rows that whole slabs do not fill, the copies of both operands.
-size_t f8_tile_workspace(int64_t M, int64_t N, int64_t K, bool wide) {
-    const F8Plan q = f8_plan(M, N, K, wide);
-    const int64_t kp = ceil_div(K, kSlabBytes) * kSlabBytes;
-    size_t bytes = q.splits > 1 ? (size_t)q.splits * M * f8_ldp(N) * sizeof(float) : 0;
-    bytes = (bytes + 255) & ~size_t(255);
-    if (K % kSlabBytes || M < least_rows(q.bm)) bytes += (size_t)(std::max(M, least_rows(q.bm)) * kp);
-    if (K % kSlabBytes || N < q.bn) bytes += (size_t)(std::max(N, (int64_t)q.bn) * kp);
-    return bytes;
-}
-
 // K >= 128 and strides that the tiles' 32-bit offsets hold (256 rows below 2^31 bytes).
 bool f8_tile_fits(const F8Params& f) {
     const int64_t most = int64_t(1) << 22;
@@ -439,7 +428,8 @@ struct F8Launch {
     F8Plan q;
     int per_split;       // slabs of a split
     int64_t each, kp;    // bytes of a split's sums; K in whole slabs
-    RowsJob ja, jb;      // operands that the direct copies cannot take (src NULL: they can), copied behind the splits' sums
+    RowsJob ja, jb;      // copies of the operands, behind the splits' sums ...
+    bool copy_a, copy_b; // ... of those that the direct copies cannot take
     size_t used, wants;
     bool copies, direct;
 };
@@ -454,21 +444,25 @@ F8Launch f8_launch_of(const F8Params& f, size_t ws_bytes) {
     l.per_split = (int)ceil_div(slabs, q.splits);
     q.splits = (int)ceil_div(slabs, l.per_split);
     l.kp = slabs * kSlabBytes;
-    auto copy_of = [&](const uint8_t* src, int64_t ld, int64_t rows, int64_t least) {
-        RowsJob j = {src, nullptr, ld, rows, f.K, std::max(rows, least), l.kp};
-        if (rows >= least && f.K == l.kp && ((uintptr_t)src | ld) % 16 == 0) j.src = nullptr;
-        return j;
-    };
-    l.ja = copy_of(f.A, f.lda, f.M, least_rows(q.bm));
-    l.jb = copy_of(f.B, f.ldb, f.N, q.bn);
+    const int64_t least_a = least_rows(q.bm), least_b = q.bn;
+    l.ja = {f.A, nullptr, f.lda, f.M, f.K, std::max((int64_t)f.M, least_a), l.kp};
+    l.jb = {f.B, nullptr, f.ldb, f.N, f.K, std::max((int64_t)f.N, least_b), l.kp};
+    l.copy_a = f.M < least_a || f.K != l.kp || ((uintptr_t)f.A | f.lda) % 16;
+    l.copy_b = f.N < least_b || f.K != l.kp || ((uintptr_t)f.B | f.ldb) % 16;
     l.used = q.splits > 1 ? ((size_t)(q.splits * l.each) + 255) & ~size_t(255) : 0;
-    l.wants = l.used + (l.ja.src ? l.ja.bytes() : 0) + (l.jb.src ? l.jb.bytes() : 0);
-    l.copies = (l.ja.src || l.jb.src) && l.wants <= ws_bytes && l.wants < kMostCopied && f8_copy_pays(q, f, slabs, l.wants - l.used);
-    l.direct = l.copies || (!l.ja.src && !l.jb.src);
+    l.wants = l.used + (l.copy_a ? l.ja.bytes() : 0) + (l.copy_b ? l.jb.bytes() : 0);
+    l.copies = (l.copy_a || l.copy_b) && l.wants <= ws_bytes && l.wants < kMostCopied && f8_copy_pays(q, f, slabs, l.wants - l.used);
+    l.direct = l.copies || (!l.copy_a && !l.copy_b);
     return l;
 }
 
 }  // namespace
+
+// Bytes for the splits and for the copies of contiguous operands that the call would make.
+size_t f8_tile_workspace(const F8Params& f) {
+    const F8Launch l = f8_launch_of(f, SIZE_MAX / 2);
+    return l.copies ? l.wants : l.used;
+}
 
 // Expected microseconds of few rows: rounds of slabs and the launches beside them, or reading B (5 TB/s).
 double f8_tile_us(const F8Params& f, size_t ws_bytes) {
@@ -485,19 +479,27 @@ hipError_t launch_f8_tile(const F8Params& f, void* ws, size_t ws_bytes, hipStrea
     if (!ws) ws_bytes = 0;
     F8Launch l = f8_launch_of(f, ws_bytes);
     const F8Plan& q = l.q;
-    RowsJob &ja = l.ja, &jb = l.jb;
     const bool copies = l.copies, direct = l.direct;
     const int64_t ldp = f8_ldp(f.N), kp = l.kp;
     const F8Extra x = {f.sa, f.sb, l.per_split, l.each};
     op_note("  %d x %d tiles, %d splits of K, %s loads%s", q.bm, q.bn, q.splits, direct ? "direct" : "staged", copies ? " of copied rows" : "");
     F8Params o = f;
     if (copies) {
-        ja.dst = static_cast<uint8_t*>(ws) + l.used;
-        jb.dst = ja.dst + (ja.src ? ja.bytes() : 0);
+        uint8_t* at = static_cast<uint8_t*>(ws) + l.used;
+        RowsJob ja = {}, jb = {};
+        if (l.copy_a) {
+            ja = l.ja;
+            o.A = ja.dst = at;
+            o.lda = kp;
+            at += ja.bytes();
+        }
+        if (l.copy_b) {
+            jb = l.jb;
+            o.B = jb.dst = at;
+            o.ldb = kp;
+        }
         const hipError_t e = launch_rows_pack(ja, jb, st);
         if (e != hipSuccess) return e;
-        if (ja.src) { o.A = ja.dst; o.lda = kp; }
-        if (jb.src) { o.B = jb.dst; o.ldb = kp; }
         o.K = (int)kp;
     }
     GemmParams p = {};

@@ -4,6 +4,8 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "ops.hpp"
 
 namespace {
@@ -217,8 +219,8 @@ gemm_status_t gemm_f8_workspace_size(int64_t M, int64_t N, int64_t K, size_t* by
             p.M = (int)M; p.N = (int)N; p.K = (int)K;
             p.lda = p.ldb = K;   // (of contiguous operands)
             p.out_type = c_type;
-            const size_t need = f8_few(p, SIZE_MAX / 2) ? 0 : f8_tile_workspace(M, N, K, c_type == GEMM_F32);
-            if (need > *bytes) *bytes = need;
+            if (!f8_tile_fits(p) || f8_few(p, SIZE_MAX / 2)) continue;   // (the other kernels use none)
+            *bytes = std::max(*bytes, f8_tile_workspace(p));
         }
     return GEMM_OK;
 }
@@ -272,7 +274,7 @@ gemm_status_t gemm_w4_workspace_size(gemm_dtype_t in_type, int64_t M, int64_t N,
         W4Params p = {};
         p.M = (int)M; p.N = (int)N; p.K = (int)K; p.group = (int)group;
         p.lda = K; p.ldw = (K + 1) / 2;   // (of contiguous operands)
-        if (w4_tile_us(p, SIZE_MAX / 2) < w4_skinny_us(p)) *bytes = w4_tile_workspace(M, N, K, group);
+        if (w4_tile_fits(p, SIZE_MAX / 2) && w4_tile_us(p, SIZE_MAX / 2) < w4_skinny_us(p)) *bytes = w4_tile_workspace(M, N, K, group);
     }
     return GEMM_OK;
 }

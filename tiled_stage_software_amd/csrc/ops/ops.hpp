@@ -82,7 +82,7 @@ double f8_skinny_us(const F8Params& p);              // what either is expected 
 double f8_tile_us(const F8Params& p, size_t ws_bytes);
 hipError_t launch_f8_skinny(const F8Params& p, hipStream_t st);
 bool f8_tile_fits(const F8Params& p);
-size_t f8_tile_workspace(int64_t M, int64_t N, int64_t K, bool wide);
+size_t f8_tile_workspace(const F8Params& p);   // of a product that fits
 hipError_t launch_f8_tile(const F8Params& p, void* ws, size_t ws_bytes, hipStream_t st);
 hipError_t launch_f8_staged(const F8Params& p, hipStream_t st);
 
