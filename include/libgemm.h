@@ -392,7 +392,8 @@ gemm_status_t gemm_h2d_staged_async(void* dst, const void* src, int64_t bytes, v
  * matter whether h is stored.  y_type GEMM_F8E4M3: scale = max(max |y| / 448, 2^-126) per
  * row and y = y * (1 / scale) rounded to nearest even, so y * scale stands for the row; a
  * row with a NaN, or whose largest |y| is infinite, has a scale that is not finite and no finite
- * values.  A row of zeros gives zeros (with eps > 0) and the scale 2^-126.
+ * values.  A row of zeros gives zeros (with eps > 0) and the scale 2^-126.  eps may be 0 for rows whose rstd
+ * fp32 holds.
  * x, r, h: rows x cols of in_type (GEMM_F32, GEMM_BF16, GEMM_F16), leading dimensions in
  * elements; r may be NULL (no residual), h may be NULL (not stored).  w: cols weights of
  * w_type (in_type or GEMM_F32), NULL for ones.  y_type: GEMM_F32, GEMM_BF16, GEMM_F16 or

@@ -821,3 +821,17 @@ def test_sizes_beyond_one_launch(M, N, K, op):
         for n in range(0, N, 1 << 24):
             want = a[m:m + (1 << 24)].float() @ b[n:n + (1 << 24)].float().t()
             assert torch.equal(C[m:m + (1 << 24), n:n + (1 << 24)], want.bfloat16())
+
+
+@pytest.mark.parametrize("cols", [40, 1000, 4096, 40000])
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_norm_without_eps(cols, t):
+    """eps = 0, or nearly, and rows whose squares leave fp32's range at either end: the norm is of the row as it stands."""
+    g = gen(cols)
+    x = torch.randn(12, cols, generator=g)
+    x *= 2.0 ** torch.tensor([0, -40, -50, -62, -64, -75, -76, -100, -120, 62, 70, 110])[:, None]
+    x = x.to(DT[t])
+    w = (1 + 0.1 * torch.randn(cols, generator=g)).to(DT[t])
+    for eps in (0.0, 2.0 ** -140, 2.0 ** -100):
+        r = [check_norm(x, None, w, DT[out], eps=eps) for out in ("f32", "f8")]
+        say(f"[norm without eps] {t} {cols} {eps}: {max(r):.3f} of the tolerance")

@@ -164,15 +164,17 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits) {
 }
 
 // 1 / sqrt(sum / cols + eps) from the row's sum of squares.  Where that sum leaves fp32's range
-// though every element is finite (|h| above 2^64 / sqrt(cols)), `again` sums the squares of
-// h * 2^-80, which stay in range for any row.
+// though the row does not (|h| above 2^64 / sqrt(cols); |h| below 2^-45 with so small an eps), `again` sums
+// the squares of h * 2^-80 or h * 2^80, which stay in range for any such row.
 template <class F>
 __device__ __forceinline__ float row_rstd(float sum, int cols, float eps, F&& again) {
-    if (__builtin_isinf(sum)) {   // the same in every thread of the row
-        constexpr float kDown = 0x1p-80f;
-        return kDown / __builtin_sqrtf(again(kDown) / (float)cols + eps * kDown * kDown);
+    const float mean = sum / (float)cols + eps;
+    const bool high = __builtin_isinf(sum);
+    if (high || mean < 0x1p-90f) {   // the same in every thread of the row
+        const float by = high ? 0x1p-80f : 0x1p80f;
+        return by / __builtin_sqrtf(again(by) / (float)cols + eps * by * by);
     }
-    return 1.0f / __builtin_sqrtf(sum / (float)cols + eps);
+    return 1.0f / __builtin_sqrtf(mean);
 }
 
 // h = x + r in T; x alone where there is no residual.
