@@ -390,7 +390,7 @@ gemm_status_t gemm_h2d_staged_async(void* dst, const void* src, int64_t bytes, v
  *     y = h * rstd * w
  * in fp32; y is rounded once, to y_type.  The norm is of the rounded h, so it does not
  * matter whether h is stored.  y_type GEMM_F8E4M3: scale = max(max |y| / 448, 2^-126) per
- * row and y = y * (1 / scale) rounded to nearest even, so y * scale stands for the row; a
+ * row and y = y / scale rounded to nearest even, so y * scale stands for the row; a
  * row with a NaN, or whose largest |y| is infinite, has a scale that is not finite and no finite
  * values.  A row of zeros gives zeros (with eps > 0) and the scale 2^-126.  eps may be 0 for rows whose rstd
  * fp32 holds.

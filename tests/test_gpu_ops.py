@@ -835,3 +835,20 @@ def test_norm_without_eps(cols, t):
     for eps in (0.0, 2.0 ** -140, 2.0 ** -100):
         r = [check_norm(x, None, w, DT[out], eps=eps) for out in ("f32", "f8")]
         say(f"[norm without eps] {t} {cols} {eps}: {max(r):.3f} of the tolerance")
+
+
+@pytest.mark.parametrize("rows,cols", [(400, 8192), (800, 4096), (300, 1000), (40, 40000), (3000, 7)])
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_norm_codes_are_the_quotients(rows, cols, t):
+    """The 8-bit codes of a row are y / scale rounded once to fp32 and once to 8 bits, y as the call gives it in fp32.  Rows of
+    few different values, where quotients lie on the border of two codes."""
+    g = gen(rows + cols)
+    x = torch.randn(rows, cols, generator=g).bfloat16()
+    w = (1 + 0.1 * torch.randn(cols, generator=g)).bfloat16()
+    x[::2] = (torch.randint(-40, 41, (rows, cols), generator=g) * 0.25).bfloat16()[::2]
+    x, w = x.to(DT[t]).to(DEV), w.to(DT[t]).to(DEV)
+    y = ops.rmsnorm(x, w, out_dtype=torch.float32)
+    q = ops.rmsnorm(x, w, out_dtype=torch.float8_e4m3fn)
+    assert torch.equal(y.rstd, q.rstd)
+    want = (y.y.cpu() / q.scale.cpu()[:, None]).to(torch.float8_e4m3fn)
+    assert torch.equal(q.y.cpu().view(torch.uint8), want.view(torch.uint8))

@@ -162,6 +162,12 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits) {
     const float s = __uint_as_float(amax_bits) / kF8Max;
     return s < kTiny ? kTiny : s;   // (a NaN compares false and stays)
 }
+// y / s by s's reciprocal and what its product leaves, rounded as a division is: two operations more than the product
+// alone, which bytes hide.  (An infinite scale has no finite values in its row.)
+__device__ __forceinline__ float over_scale(float y, float s, float inv) {
+    const float q = y * inv;
+    return __builtin_fmaf(__builtin_fmaf(-q, s, y), inv, q);
+}
 
 // 1 / sqrt(sum / cols + eps) from the row's sum of squares.  Where that sum leaves fp32's range
 // though the row does not (|h| above 2^64 / sqrt(cols); |h| below 2^-45 with so small an eps), `again` sums
@@ -270,7 +276,7 @@ __global__ __launch_bounds__(64 * WPR * RPG) void norm_kernel(const NormParams p
                 if (own(i) < p.cols) store16(hr + (int64_t)from(i) * SZ, v[i]);
         }
         auto y = [&](int i, int e) { return w[i].get(ones, e) * (Elem<T>::get(v[i], e) * rstd); };
-        float inv = 1.0f;
+        float scale = 1.0f, inv = 1.0f;
         if constexpr (F8) {
             uint32_t amax = 0;   // (what is read twice is in the row anyway)
 #pragma unroll
@@ -280,9 +286,9 @@ __global__ __launch_bounds__(64 * WPR * RPG) void norm_kernel(const NormParams p
                     const uint32_t b = __float_as_uint(y(i, e)) & 0x7fffffffu;
                     amax = b > amax ? b : amax;
                 }
-            const float s = row_scale(row_max<WPR>(amax, maxs[turn]));
-            inv = 1.0f / s;
-            if (t == 0) p.scale[row] = s;
+            scale = row_scale(row_max<WPR>(amax, maxs[turn]));
+            inv = 1.0f / scale;
+            if (t == 0) p.scale[row] = scale;
         }
         const int yt = F8 ? (int)DT_F8E4M3 : p.y_type;
         char* yr = p.y + row * p.ldy * y_size(yt);
@@ -291,7 +297,7 @@ __global__ __launch_bounds__(64 * WPR * RPG) void norm_kernel(const NormParams p
             if (own(i) < p.cols) {
                 float f[VE];
 #pragma unroll
-                for (int e = 0; e < VE; ++e) f[e] = F8 ? y(i, e) * inv : y(i, e);
+                for (int e = 0; e < VE; ++e) f[e] = F8 ? over_scale(y(i, e), scale, inv) : y(i, e);
                 store_y<VE>(yr, yt, from(i), p.cols, f);
             }
         turn ^= 1;
@@ -331,7 +337,7 @@ __global__ __launch_bounds__(kLoopThreads) void norm_loop_kernel(const NormParam
         const float rstd = row_rstd(row_sum<W>(squares(1.0f), sums[turn]), p.cols, p.eps,
                                     [&](float by) { return row_sum<W>(squares(by), wide[turn]); });
         if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
-        float inv = 1.0f;
+        float scale = 1.0f, inv = 1.0f;
         if (p.y_type == DT_F8E4M3) {
             uint32_t amax = 0;
             for (int64_t c = (int64_t)threadIdx.x * VE; c < p.cols; c += kLoopThreads * VE) {
@@ -344,9 +350,9 @@ __global__ __launch_bounds__(kLoopThreads) void norm_loop_kernel(const NormParam
                     if (c + e < p.cols) amax = b > amax ? b : amax;
                 }
             }
-            const float s = row_scale(row_max<W>(amax, maxs[turn]));
-            inv = 1.0f / s;
-            if (threadIdx.x == 0) p.scale[row] = s;
+            scale = row_scale(row_max<W>(amax, maxs[turn]));
+            inv = 1.0f / scale;
+            if (threadIdx.x == 0) p.scale[row] = scale;
         }
         char* yr = p.y + row * p.ldy * y_size(p.y_type);
         for (int64_t c = (int64_t)threadIdx.x * VE; c < p.cols; c += kLoopThreads * VE) {
@@ -357,7 +363,7 @@ __global__ __launch_bounds__(kLoopThreads) void norm_loop_kernel(const NormParam
             for (int e = 0; e < VE; ++e) f[e] *= Elem<T>::get(v, e) * rstd;
             if (p.y_type == DT_F8E4M3) {
 #pragma unroll
-                for (int e = 0; e < VE; ++e) f[e] *= inv;
+                for (int e = 0; e < VE; ++e) f[e] = over_scale(f[e], scale, inv);
             }
             if (p.h) store_vec<T>(p.h + row * p.ldh * SZ, (int)c, p.cols, v);
             store_y<VE>(yr, p.y_type, (int)c, p.cols, f);
