@@ -852,3 +852,114 @@ def test_norm_codes_are_the_quotients(rows, cols, t):
     assert torch.equal(y.rstd, q.rstd)
     want = (y.y.cpu() / q.scale.cpu()[:, None]).to(torch.float8_e4m3fn)
     assert torch.equal(q.y.cpu().view(torch.uint8), want.view(torch.uint8))
+
+
+# ------------------------------------------------------------------ gradients through autograd
+
+@pytest.mark.parametrize("rows,cols", [(1, 40), (7, 513), (300, 1000), (33, 4096)])
+@pytest.mark.parametrize("t,wt,residual,used", [("f32", "f32", True, "both"), ("bf16", "bf16", True, "both"), ("f16", "f32", False, "both"),
+                                                ("bf16", None, True, "y"), ("f32", "f32", True, "h"), ("bf16", "f32", False, "y")])
+def test_norm_gradients_through_autograd(rows, cols, t, wt, residual, used):
+    """backward() of a loss of y and h reaches x, residual and weight with what rmsnorm_backward gives, which is the formula's."""
+    g = gen(rows + cols)
+    draw = lambda dt: torch.randn(rows, cols, generator=g).to(dt).to(DEV)  # noqa: E731
+    x, r = draw(DT[t]).requires_grad_(), draw(DT[t]).requires_grad_() if residual else None
+    w = (1 + 0.1 * torch.randn(cols, generator=g)).to(DT[wt]).to(DEV).requires_grad_() if wt else None
+    dy, dh = draw(DT[t]), draw(DT[t])
+    n = ops.rmsnorm(x, w, r)
+    with torch.no_grad():
+        plain = ops.rmsnorm(x.detach(), w, r)
+    assert torch.equal(n.y, plain.y) and torch.equal(n.h, plain.h) and torch.equal(n.rstd, plain.rstd)
+    assert n.y.requires_grad and n.h.requires_grad and not n.rstd.requires_grad and not plain.y.requires_grad
+    given = {"both": ([n.y, n.h], [dy, dh]), "y": ([n.y], [dy]), "h": ([n.h], [dh])}[used]
+    torch.autograd.backward(*given)
+    if used == "h":
+        assert torch.equal(x.grad, dh) and torch.equal(r.grad, dh) and w.grad is None
+        return
+    up = dh if used == "both" else None
+    dx, dw = ops.rmsnorm_backward(dy, plain.h, w.detach() if w is not None else None, plain.rstd,
+                                  up if residual else None)
+    if not residual and up is not None:
+        dx = dx + up           # h is x itself: its gradient joins x's
+    assert torch.equal(x.grad, dx)
+    assert not residual or torch.equal(r.grad, dx)
+    if w is not None:
+        assert w.grad.dtype == w.dtype and torch.equal(w.grad, dw.to(w.dtype))
+    dx64, dw64, dx_size, dw_size = norm_bwd64(dy.cpu(), plain.h.cpu(), w.detach().cpu() if w is not None else None,
+                                              plain.rstd.cpu(), up.cpu() if up is not None else None)
+    twice = 1 if residual else 2       # (roundings to x's type)
+    assert off(x.grad, dx64, twice * rounding(dx_size, DT[t]) + (norm_steps(cols) + 12) * U32 * dx_size) <= 1
+    if w is not None:
+        assert off(w.grad, dw64, rounding(dw64, w.dtype) + (rows + 8) * U32 * dw_size + 2.0 ** -149) <= 1
+
+
+def test_norm_gradients_of_another_output_type_and_of_strided_ones():
+    """y in another type than x: its gradient comes in that type and is not rounded to x's; a gradient of no stride."""
+    g = gen(3)
+    rows, cols = 40, 1000
+    x = torch.randn(rows, cols, generator=g).bfloat16().to(DEV).requires_grad_()
+    w = torch.randn(cols, generator=g).bfloat16().to(DEV).requires_grad_()
+    dy = torch.randn(rows, cols, generator=g).to(DEV)
+    n = ops.rmsnorm(x, w, out_dtype=torch.float32)
+    n.y.backward(dy)
+    dx64, dw64, dx_size, dw_size = norm_bwd64(dy.cpu(), x.detach().cpu(), w.detach().cpu(), n.rstd.cpu(), None)
+    assert off(x.grad, dx64, rounding(dx64, x.dtype) + (norm_steps(cols) + 12) * U32 * dx_size) <= 1
+    assert off(w.grad, dw64, rounding(dw64, w.dtype) + (rows + 8) * U32 * dw_size) <= 1
+    x.grad = None
+    ops.rmsnorm(x, w).y.sum().backward()
+    want, _ = ops.rmsnorm_backward(torch.ones_like(x), x.detach(), w.detach(), n.rstd)
+    assert torch.equal(x.grad, want)
+    x.grad = None
+    wide = torch.randn(rows, 2 * cols, generator=g).bfloat16().to(DEV)
+    (ops.rmsnorm(x, w).y.t() * wide[:, :cols].t()).sum().backward()
+    want, _ = ops.rmsnorm_backward(wide[:, :cols].contiguous(), x.detach(), w.detach(), n.rstd)
+    assert torch.equal(x.grad, want)
+
+
+def test_gradients_that_there_are_not():
+    """8-bit codes carry none, so a loss of them alone is refused; the products and second derivatives have none and say so."""
+    g = gen(4)
+    x = torch.randn(20, 64, generator=g).bfloat16().to(DEV).requires_grad_()
+    r = torch.randn(20, 64, generator=g).bfloat16().to(DEV)
+    n = ops.rmsnorm(x, None, r, out_dtype=torch.float8_e4m3fn)
+    assert not n.y.requires_grad and not n.scale.requires_grad and n.h.requires_grad
+    n.h.sum().backward()
+    assert torch.equal(x.grad, torch.ones_like(x))
+    codes, s, _ = ops.quantize_w4(torch.randn(48, 64, generator=g), 32, torch.bfloat16)
+    codes, s = codes.to(DEV), s.to(DEV)
+    want = ops.matmul_w4(x.detach(), codes, s, group=32)
+    C = torch.empty_like(want)
+    for out in (None, C):
+        got = ops.matmul_w4(x, codes, s, group=32, C=out)
+        assert torch.equal(got, want) and (out is None or got.data_ptr() == C.data_ptr())
+        with pytest.raises(RuntimeError, match="matmul_w4 has no backward pass"):
+            got.sum().backward()
+    q, sq = ops.quantize_f8(x.detach())
+    got = ops.matmul_f8(q, q, sq.requires_grad_(), sq)
+    with pytest.raises(RuntimeError, match="matmul_f8 has no backward pass"):
+        got.sum().backward()
+    with torch.no_grad():
+        assert not ops.matmul_w4(x, codes, s, group=32).requires_grad
+    dx, = torch.autograd.grad(ops.rmsnorm(x).y.float().square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.sum().backward()
+
+
+def test_norm_gradients_on_another_stream():
+    """The forward pass on a stream given by its handle, busy until later: the backward pass waits for it."""
+    g = gen(6)
+    x = torch.randn(300, 4096, generator=g).to(DEV).requires_grad_()
+    r, dy = (torch.randn(300, 4096, generator=g).to(DEV) for _ in range(2))
+    n = ops.rmsnorm(x, None, r)
+    n.y.backward(dy)
+    want, x.grad = x.grad, None
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(SPIN)
+    y = ops.rmsnorm(x, None, r, stream=side.cuda_stream).y
+    y.backward(dy)
+    del y
+    torch.cuda.synchronize()
+    assert torch.equal(x.grad, want)

@@ -1,5 +1,6 @@
 """Torch-tensor form of the operators around the products: the root-mean-square norm and its
-backward pass, the product of 8-bit operands and the product with 4-bit weights.
+backward pass (also through autograd), the product of 8-bit operands and the product with 4-bit
+weights (which have none).
 
 As ``libgemm.matmul``, these only read shapes, strides and pointers; every step on the
 GPU runs in the library's kernels, and there is no fallback.  ``quantize_f8`` and
@@ -7,6 +8,7 @@ GPU runs in the library's kernels, and there is no fallback.  ``quantize_f8`` an
 """
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple, Optional
 
 from . import libgemm as lg
@@ -77,9 +79,67 @@ def _workspace(workspace, size, device):
     return workspace, *lg.workspace_of(workspace, device)
 
 
+def _wants_gradient(*tensors) -> bool:
+    import torch
+    return torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in tensors)
+
+
+@functools.lru_cache(maxsize=None)
+def _functions():
+    """(the norm as autograd has it, the mark of a result that no gradient passes)."""
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class Norm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, residual, eps, out_dtype):
+            n = _rmsnorm(x, weight, residual, eps, out_dtype)
+            ctx.set_materialize_grads(False)
+            ctx.save_for_backward(n.h, weight, n.rstd)
+            ctx.mark_non_differentiable(*(t for t in (n.rstd, n.scale) if t is not None), *([n.y] if n.scale is not None else []))
+            return n.y, n.scale, n.h if residual is not None else None, n.rstd
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dy, _scale, dh, _rstd):
+            h, weight, rstd = ctx.saved_tensors
+            of_x, of_weight, of_residual = ctx.needs_input_grad[:3]
+            if dy is None:
+                return dh if of_x else None, None, dh if of_residual else None, None, None
+            rows = lambda t, dtype: t.to(dtype).contiguous() if t is not None else None  # noqa: E731
+            wide = h.dtype if dy.dtype == h.dtype else torch.float32   # (a y of another type: nothing is rounded on the way in)
+            w = weight if weight is None or weight.dtype == wide else weight.float()
+            dx, dw = rmsnorm_backward(rows(dy, wide), h if wide == h.dtype else h.float(), w, rstd, rows(dh, wide), of_weight)
+            dx = dx.to(h.dtype)
+            return (dx if of_x else None, dw.to(weight.dtype) if of_weight else None, dx if of_residual else None, None, None)
+
+    class NoBackward(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, name, result, *inputs):
+            ctx.name = name
+            ctx.mark_dirty(result)
+            return result
+
+        @staticmethod
+        def backward(ctx, _):
+            raise RuntimeError(f"{ctx.name} has no backward pass: detach its inputs")
+
+    return Norm, NoBackward
+
+
 def rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None, stream=None) -> RmsNorm:
     """h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight, row by row, in `out_dtype`
-    (x's by default; torch.float8_e4m3fn gives codes and a scale per row)."""
+    (x's by default; torch.float8_e4m3fn gives codes and a scale per row).  Gradients of y (not of
+    8-bit codes) and h reach x, weight and residual through ``rmsnorm_backward``."""
+    if not _wants_gradient(x, weight, residual):
+        return _rmsnorm(x, weight, residual, eps, out_dtype, stream)
+    with lg.Running(stream, x.device, x, weight, residual) as on:   # (its backward pass runs on the same stream)
+        y, scale, h, rstd = _functions()[0].apply(x, weight, residual, eps, out_dtype)
+        on.keep(y, scale, h, rstd)
+    return RmsNorm(y, scale, x if h is None else h, rstd)
+
+
+def _rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None, stream=None) -> RmsNorm:
     import torch
     ldx = _rows(x, "x")
     rows, cols = x.shape
@@ -123,6 +183,11 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, need_dw: bool = True, workspa
     return dx, dw
 
 
+def _no_gradient(name, C, *inputs):
+    """C; where an input (or the C that was added to) wants a gradient, one whose backward pass says that there is none."""
+    return _functions()[1].apply(name, C, *inputs) if _wants_gradient(C, *inputs) else C
+
+
 def _result(on, C, M, N, beta, out_dtype, device):
     """(C, its leading dimension) of a product."""
     import torch
@@ -151,7 +216,7 @@ def matmul_f8(a, b, scale_a=None, scale_b=None, C=None, alpha: float = 1.0, beta
         held, ws, nbytes = _workspace(workspace, lambda: lg.gemm_f8_workspace_size(M, N, K), a.device)
         lg.check(lg.gemm_f8(M, N, K, alpha, a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb, beta, C.data_ptr(), _code(C.dtype),
                             ldc, ws, nbytes, on.handle))
-    return C
+        return _no_gradient("matmul_f8", C, a, b, scale_a, scale_b)
 
 
 def matmul_w4(a, codes, scales, zeros=None, group: int = 128, C=None, alpha: float = 1.0, beta: float = 0.0,
@@ -175,7 +240,7 @@ def matmul_w4(a, codes, scales, zeros=None, group: int = 128, C=None, alpha: flo
         lg.check(lg.gemm_w4(code, M, N, K, group, alpha, a.data_ptr(), lda, codes.data_ptr(), ldw, scales.data_ptr(),
                             zeros.data_ptr() if zeros is not None else 0, lds, beta, C.data_ptr(), _code(C.dtype), ldc, ws,
                             nbytes, on.handle))
-    return C
+        return _no_gradient("matmul_w4", C, a, codes, scales, zeros)
 
 
 def quantize_f8(t):
