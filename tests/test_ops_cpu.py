@@ -330,3 +330,10 @@ def test_workspaces_asked_for_are_used_and_enough():
         none, asked, more = said[9 * i + 6:9 * i + 9]
         assert asked == more, (shapes[i], asked, more)
         assert (w > 0) == (asked != none), (shapes[i], w, none, asked)
+
+
+def test_the_package_has_the_operators():
+    import tiled_stage_software_amd as pkg
+    assert pkg.ops is ops and pkg.GEMM_F8E4M3 == lg.GEMM_F8E4M3
+    code = "import sys, tiled_stage_software_amd as p; p.ops, p.GEMM_F8E4M3; assert 'torch' not in sys.modules"
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT)
