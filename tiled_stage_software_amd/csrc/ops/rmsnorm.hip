@@ -527,11 +527,9 @@ __global__ __launch_bounds__(64 * WPR * RPG) void norm_bwd_kernel(const NormBwdP
             }
         }
         // dx may lie on dh, and a row's last elements may be another wave's to store as well: dh is here before the barrier in
-        // row_sum(), as dy and h are, which the sum has used
-        if (p.dh) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) asm volatile("" : "+v"(dh[i]));
-        }
+        // row_sum(), as dy and h are, which the sum has used.  (A wait, as uses of dh's registers here would make fp32 rows of
+        // 9000 and more spill: 2000 x 12000 116 us instead of 85.)
+        if (WPR > 1 && p.dh) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         const float mean = row_sum<WPR>(sum, sums[turn]) / (float)p.cols;
         char* xr = p.dx + row * p.lddx * SZ;
 #pragma unroll
