@@ -686,11 +686,12 @@ def each_call(rows=512):
     x, r, w, b, sb, codes, s, dy = chain_inputs(rows, 11)
     n = ops.rmsnorm(x, w, r, out_dtype=torch.float8_e4m3fn)
     B = torch.randn(512, 640, generator=gen(4)).bfloat16().to(DEV)
+    wide = torch.cat([x, r[:, :128]], 1)   # (here: what a call reads is there before its stream is chosen)
     return [("rmsnorm", lambda st: ops.rmsnorm(x, w, r, stream=st)[0]),
             ("rmsnorm to 8 bits", lambda st: ops.rmsnorm(x, w, r, out_dtype=torch.float8_e4m3fn, stream=st)[0].view(torch.uint8)),
             ("backward", lambda st: ops.rmsnorm_backward(dy, n.h, w, n.rstd, stream=st)[0]),
             ("f8", lambda st: ops.matmul_f8(n.y, b, n.scale, sb, stream=st)),
-            ("w4", lambda st: ops.matmul_w4(torch.cat([x, r[:, :128]], 1), codes, s, group=64, stream=st)),
+            ("w4", lambda st: ops.matmul_w4(wide, codes, s, group=64, stream=st)),
             ("bf16", lambda st: lg.matmul(x, B, stream=st, workspace="auto"))]
 
 
@@ -736,6 +737,23 @@ def test_results_in_memory_that_the_current_stream_still_writes(i):
     side.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(got, want), name
+
+
+def test_inputs_dropped_while_another_stream_reads_them():
+    x, r, w, b, sb, codes, s, dy = chain_inputs(512, 13)
+    want = ops.matmul_w4(torch.cat([x, r[:, :128]], 1), codes, s, group=64)
+    side = torch.cuda.Stream()
+    wide = torch.cat([x, r[:, :128]], 1)
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(SPIN)
+    size = wide.numel() * 2
+    got = ops.matmul_w4(wide, codes, s, group=64, stream=side.cuda_stream)
+    del wide
+    fresh = [torch.full((size,), 7, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and all(bool((t == 7).all()) for t in fresh)
 
 
 def test_the_default_stream_by_its_handle():
