@@ -469,6 +469,108 @@ gemm_status_t gemm_w4(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, int
                       hipStream_t stream);
 gemm_status_t gemm_w4_workspace_size(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, int64_t group, size_t* bytes);
 
+/* ------------------------------------------------------------------ dense parts of a transformer block
+ * The product with bias, activation and residual in its epilogue, and the norm of queries and keys for each head
+ * with the rotation by position, each with its backward pass.  The rules of the operators above hold for them. */
+
+typedef enum gemm_act {
+    GEMM_ACT_NONE = 0,
+    GEMM_ACT_RELU = 1,       /* max(z, 0) */
+    GEMM_ACT_GELU = 2,       /* z * Phi(z), Phi the normal distribution's */
+    GEMM_ACT_GELU_TANH = 3,  /* z / 2 * (1 + tanh(sqrt(2 / pi) * (z + 0.044715 z^3))) */
+    GEMM_ACT_SILU = 4        /* z / (1 + exp(-z)) */
+} gemm_act_t;
+
+/* C = act(Z) + R,  Z = A * W^T + bias
+ * A: M x K, W: N x K, both of in_type (GEMM_BF16 or GEMM_F16) with K contiguous, any pitch (lda, ldw >= K).  bias: N of
+ * bias_type (in_type or GEMM_F32), or NULL.  R: M x N of c_type, or NULL; it may be the same memory as C with the same
+ * leading dimension.  C: M x N of c_type (in_type or GEMM_F32).  Z: where it is stored (NULL: it is not), M x N of in_type:
+ * what gemm_linear_bwd reads.  No other overlap.
+ * Sums, bias, activation and residual are in fp32; C and Z are rounded once, each from the unrounded sums.  An activation is
+ * good to a few 2^-21 of its value for |z| up to 8, and to z^2 2^-23 beyond.  NaN stays NaN; infinite
+ * sums have the activations' limits.  K == 0: C = act(bias) + R.  M == 0 or N == 0: nothing is written.
+ * workspace: as gemm_f8 uses one, for splits of a long K and for copies of operands whose rows are not 16-byte aligned or not
+ * whole slabs of 64; gemm_linear_workspace_size gives the bytes for contiguous aligned operands.  With less (or NULL) the call
+ * does without, with the same result up to the order of sums.
+ * Errors: GEMM_ERR_INVALID_ARG for a negative or too large size, a leading dimension too small, a type or an activation not
+ * offered, NULL A, W or C, a workspace not 256-byte aligned. */
+gemm_status_t gemm_linear(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* W,
+                          int64_t ldw, const void* bias, gemm_dtype_t bias_type, gemm_act_t act, const void* R, int64_t ldr,
+                          void* Z, int64_t ldz, void* C, gemm_dtype_t c_type, int64_t ldc, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+gemm_status_t gemm_linear_workspace_size(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, size_t* bytes);
+
+/* Backward pass of gemm_linear (R's gradient is dC itself):
+ *     dZ = dC * act'(Z),  dA = dZ * W,  dW = dZ^T * A,  dbias = sum over the rows of dZ
+ * dC: M x N of dc_type (in_type or GEMM_F32).  Z: M x N of in_type, what gemm_linear stored; NULL allowed for GEMM_ACT_NONE (not read then).  dZ:
+ * M x N of in_type, written, and what both products read: it is rounded once; it may be the same memory as dC (of in_type) or
+ * Z with the same leading dimension.  With GEMM_ACT_NONE and a dC of in_type it may be NULL: dC is then read in its place.
+ * dA: M x K of in_type, or NULL (not computed; W is not read).  dW: N x K of dw_type (in_type or GEMM_F32), or NULL (A is not
+ * read).  dbias: N floats, summed in fp32 from unrounded values in a fixed order, or NULL.  M == 0: dW = 0, dbias = 0.
+ * The derivative of relu at 0 is 0.
+ * workspace: partial sums of dbias and rewritten operands of the two products, one after the other;
+ * gemm_linear_bwd_workspace_size gives the bytes for contiguous aligned operands.  With less (or NULL) the call does without.
+ * Errors: as gemm_linear, plus GEMM_ERR_INVALID_ARG for a NULL Z or dZ that is needed. */
+gemm_status_t gemm_linear_bwd(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, gemm_act_t act, const void* dC,
+                              gemm_dtype_t dc_type, int64_t lddc, const void* Z, int64_t ldz, const void* A, int64_t lda,
+                              const void* W, int64_t ldw, void* dZ, int64_t lddz, void* dA, int64_t ldda, void* dW,
+                              gemm_dtype_t dw_type, int64_t lddw, float* dbias, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+gemm_status_t gemm_linear_bwd_workspace_size(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, size_t* bytes);
+
+/* tokens x heads x head_dim elements: element e of a token's head at data[token * token_stride + head * head_stride + e]
+ * (strides in elements; queries and keys as they lie in a QKV product's rows, or each for itself, heads or tokens outermost). */
+typedef struct gemm_heads {
+    void* data;
+    int64_t token_stride;
+    int64_t head_stride;
+} gemm_heads_t;
+
+typedef enum gemm_rope_pairs {
+    GEMM_ROPE_HALVES = 0,      /* element i turns with element i + rot_dim / 2 */
+    GEMM_ROPE_NEIGHBOURS = 1   /* element 2 i turns with element 2 i + 1 */
+} gemm_rope_pairs_t;
+
+/* The rotation: token t turns pair i by the angle whose cosine and sine are cos[positions[t] * ld + i] and sin[...],
+ * i < rot_dim / 2.  cos, sin: `rows` rows, ld floats apart.  A position outside 0..rows-1 reads nothing and gives NaN. */
+typedef struct gemm_rope {
+    const int64_t* positions;   /* tokens of them, device memory */
+    const float* cos;
+    const float* sin;
+    int64_t ld;
+    int64_t rows;
+    int rot_dim;                /* even, 0..head_dim: the elements that turn, from a head's first on */
+    int pairs;                  /* gemm_rope_pairs_t */
+} gemm_rope_t;
+
+/* For each token and each head of q and k, in one launch:
+ *     v = x / sqrt(mean(x^2) + eps) * w,   y = v with its first rot_dim elements turned: (y_i, y_j) = (v_i c - v_j s, v_j c + v_i s)
+ * in fp32, rounded once.  q, k, out_q, out_k: in_type (GEMM_F32, GEMM_BF16, GEMM_F16), q_heads and k_heads (either may be 0) heads
+ * of head_dim (1..1024).  wq, wk: head_dim weights of w_type (in_type or GEMM_F32), NULL for ones.  rope: read by the call
+ * itself (the struct, not what it points to); NULL: no rotation.  out_q may be the same memory as q with the same strides, and
+ * out_k as k; no other overlap, and no two heads may overlap.
+ * Errors: GEMM_ERR_INVALID_ARG for a negative or too large size, head_dim outside 1..1024, strides with which heads overlap, eps
+ * negative or not finite, a type or pairing not offered, rot_dim odd or outside 0..head_dim, ld below rot_dim / 2, NULL where
+ * something is read or written. */
+gemm_status_t gemm_qk_norm_rope(gemm_dtype_t in_type, gemm_dtype_t w_type, int64_t tokens, int64_t q_heads, int64_t k_heads,
+                                int64_t head_dim, float eps, const gemm_heads_t* q, const gemm_heads_t* k, const void* wq,
+                                const void* wk, const gemm_rope_t* rope, const gemm_heads_t* out_q, const gemm_heads_t* out_k,
+                                hipStream_t stream);
+
+/* Backward pass of gemm_qk_norm_rope.  With u = x / sqrt(mean(x^2) + eps) and g = dy turned back:
+ *     dx = (g w - u * mean(g w u)) / sqrt(mean(x^2) + eps),   dw = sum over tokens and heads of g * u
+ * dq, dk: gradients of the outputs; q, k: the forward pass's inputs; dxq, dxk: written, may be the same memory as dq or q (dk or
+ * k) with the same strides.  dwq, dwk: head_dim floats, or NULL (not computed); zeros where there is nothing to sum.
+ * The sums run in fp32, in parts that meet in `workspace` in a fixed order: gemm_qk_norm_rope_bwd_workspace_size gives the bytes
+ * for full speed; with less (or NULL) there are fewer parts.  Errors: as gemm_qk_norm_rope, plus a workspace not 256-byte aligned. */
+gemm_status_t gemm_qk_norm_rope_bwd(gemm_dtype_t in_type, gemm_dtype_t w_type, int64_t tokens, int64_t q_heads, int64_t k_heads,
+                                    int64_t head_dim, float eps, const gemm_heads_t* dq, const gemm_heads_t* dk,
+                                    const gemm_heads_t* q, const gemm_heads_t* k, const void* wq, const void* wk,
+                                    const gemm_rope_t* rope, const gemm_heads_t* dxq, const gemm_heads_t* dxk, float* dwq,
+                                    float* dwk, void* workspace, size_t workspace_bytes, hipStream_t stream);
+gemm_status_t gemm_qk_norm_rope_bwd_workspace_size(gemm_dtype_t in_type, int64_t tokens, int64_t q_heads, int64_t k_heads,
+                                                   int64_t head_dim, size_t* bytes);
+
 const char* gemm_status_string(gemm_status_t status);
 
 /* Thread-local description of the last non-OK status on this thread ("" if none). */

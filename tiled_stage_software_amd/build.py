@@ -29,7 +29,7 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 def sources():
     ops = os.path.join(CSRC, "ops")
     return (sorted(glob.glob(os.path.join(CSRC, "*.hip"))) + [os.path.join(CSRC, "libgemm.cpp")] +
-            sorted(glob.glob(os.path.join(ops, "*.hip"))) + [os.path.join(ops, "ops.cpp")])
+            sorted(glob.glob(os.path.join(ops, "*.hip"))) + sorted(glob.glob(os.path.join(ops, "*.cpp"))))
 
 
 def _compile(src: str, extra) -> str:

@@ -1,0 +1,276 @@
+// block.cpp -- the C entry points of a transformer block's dense parts: the product with bias, activation and
+// residual, the norm and rotation of heads, and their backward passes.  Checks run before anything is enqueued.
+#include <math.h>
+
+#include <algorithm>
+
+#include "checks.hpp"
+
+namespace {
+
+using namespace gemm;
+
+bool half_type(int t) { return t == GEMM_BF16 || t == GEMM_F16; }
+int64_t round256(int64_t v) { return (v + 255) & ~int64_t(255); }
+
+gemm_status_t check_linear(int in_type, int act, int64_t M, int64_t N, int64_t K) {
+    REQUIRE(half_type(in_type), "in_type %d: bf16 or f16", in_type);
+    REQUIRE(act >= GEMM_ACT_NONE && act <= GEMM_ACT_SILU, "act %d", act);
+    TRY(check_size("M", M));
+    TRY(check_size("N", N));
+    TRY(check_size("K", K));
+    return GEMM_OK;
+}
+
+// One of the backward pass's products, through the library's own 16-bit entry points.
+gemm_status_t product(int in_type, gemm_layout_t la, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
+                      int64_t ldb, void* C, int c_type, int64_t ldc, void* ws, size_t bytes, hipStream_t st) {
+    return (in_type == GEMM_BF16 ? gemm_bf16_ws : gemm_f16_ws)(la, GEMM_ROW_MAJOR, M, N, K, 1.0f, A, lda, B, ldb, 0.0f, C,
+                                                               (gemm_dtype_t)c_type, ldc, st, nullptr, ws, ws ? bytes : 0);
+}
+
+gemm_status_t check_heads(const char* what, const gemm_heads_t* h, int64_t tokens, int64_t heads, int64_t dim, HeadsTensor* to) {
+    *to = HeadsTensor{nullptr, 0, 0};
+    if (tokens == 0 || heads == 0) return GEMM_OK;
+    REQUIRE(h && h->data, "%s is NULL", what);
+    const int64_t ld = h->token_stride, hs = h->head_stride, most = int64_t(1) << 40;
+    const bool one_token = tokens == 1, one_head = heads == 1;
+    // tokens outermost or heads outermost: nothing of one lies within another
+    const bool fine = (one_token || (ld > 0 && ld < most)) && (one_head || (hs > 0 && hs < most)) &&
+                      ((one_head || hs >= dim) && (one_token || ld >= (one_head ? dim : (heads - 1) * hs + dim)) ||
+                       (one_token || ld >= dim) && (one_head || hs >= (one_token ? dim : (tokens - 1) * ld + dim)));
+    REQUIRE(fine, "%s: heads overlap (token stride %lld, head stride %lld)", what, (long long)ld, (long long)hs);
+    *to = HeadsTensor{static_cast<const char*>(h->data), one_token ? 0 : ld, one_head ? 0 : hs};
+    return GEMM_OK;
+}
+
+// What both passes check, but for the tensors that they read and write.
+gemm_status_t check_qk(int in_type, int w_type, int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim, float eps,
+                       const void* wq, const void* wk, const gemm_rope_t* rope, HeadsParams* p) {
+    *p = HeadsParams{};
+    REQUIRE(float_type(in_type), "in_type %d", in_type);
+    REQUIRE((!wq && !wk) || w_type == in_type || w_type == GEMM_F32, "w_type %d not offered for in_type %d", w_type, in_type);
+    TRY(check_size("tokens", tokens));
+    REQUIRE(q_heads >= 0 && q_heads <= 65536, "q_heads=%lld: 0..65536", (long long)q_heads);
+    REQUIRE(k_heads >= 0 && k_heads <= 65536, "k_heads=%lld: 0..65536", (long long)k_heads);
+    REQUIRE(dim >= 1 && dim <= kMostHeadDim, "head_dim=%lld: 1..%d", (long long)dim, kMostHeadDim);
+    REQUIRE(eps >= 0.0f && isfinite(eps), "eps=%g", (double)eps);
+    if (rope && rope->rot_dim != 0) {
+        REQUIRE(rope->rot_dim > 0 && rope->rot_dim <= dim && rope->rot_dim % 2 == 0, "rot_dim=%d: even, 0..head_dim", rope->rot_dim);
+        REQUIRE(rope->pairs == GEMM_ROPE_HALVES || rope->pairs == GEMM_ROPE_NEIGHBOURS, "pairs %d", rope->pairs);
+        TRY(check_size("rows of the table", rope->rows));
+        TRY(check_ld("ld of the table", rope->ld, rope->rot_dim / 2));
+        if (tokens > 0 && q_heads + k_heads > 0) {
+            REQUIRE(rope->positions, "positions is NULL");
+            REQUIRE(rope->rows == 0 || (rope->cos && rope->sin), "cos or sin is NULL");
+        }
+        p->pos = rope->positions;
+        p->cos = rope->cos;
+        p->sin = rope->sin;
+        p->ldt = rope->ld;
+        p->table = rope->rows;
+        p->rot = rope->rot_dim;
+        p->neighbours = rope->pairs == GEMM_ROPE_NEIGHBOURS;
+    }
+    p->w[0] = static_cast<const char*>(wq);
+    p->w[1] = static_cast<const char*>(wk);
+    p->w_type = w_type;
+    p->tokens = tokens;
+    p->heads[0] = (int)q_heads;
+    p->heads[1] = (int)k_heads;
+    p->dim = (int)dim;
+    p->eps = eps;
+    return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_linear(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* W,
+                          int64_t ldw, const void* bias, gemm_dtype_t bias_type, gemm_act_t act, const void* R, int64_t ldr,
+                          void* Z, int64_t ldz, void* C, gemm_dtype_t c_type, int64_t ldc, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream) {
+    op_clear_error();
+    TRY(check_linear(in_type, act, M, N, K));
+    REQUIRE(c_type == GEMM_F32 || c_type == in_type, "c_type %d not offered for in_type %d", (int)c_type, (int)in_type);
+    REQUIRE(!bias || bias_type == GEMM_F32 || bias_type == in_type, "bias_type %d not offered for in_type %d", (int)bias_type, (int)in_type);
+    TRY(check_ld("lda", lda, K));
+    TRY(check_ld("ldw", ldw, K));
+    TRY(check_ld("ldc", ldc, N));
+    if (R) TRY(check_ld("ldr", ldr, N));
+    if (Z) TRY(check_ld("ldz", ldz, N));
+    TRY(check_ws(workspace));
+    if (M == 0 || N == 0) return GEMM_OK;
+    REQUIRE(C, "C is NULL");
+    REQUIRE(A || K == 0, "A is NULL");
+    REQUIRE(W || K == 0, "W is NULL");
+    LinearParams p;
+    p.A = static_cast<const char*>(A);
+    p.W = static_cast<const char*>(W);
+    p.bias = static_cast<const char*>(bias);
+    p.R = static_cast<const char*>(R);
+    p.Z = static_cast<char*>(Z);
+    p.C = static_cast<char*>(C);
+    p.lda = lda; p.ldw = ldw; p.ldr = R ? ldr : 0; p.ldz = Z ? ldz : 0; p.ldc = ldc;
+    p.M = (int)M; p.N = (int)N; p.K = (int)K;
+    p.act = act; p.bias_type = bias_type; p.out_type = c_type;
+    op_note("linear type %d -> %d M=%lld N=%lld K=%lld act=%d", (int)in_type, (int)c_type, (long long)M, (long long)N, (long long)K,
+            (int)act);
+    return launched(launch_linear_staged(in_type, p, stream));
+}
+
+gemm_status_t gemm_linear_workspace_size(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, size_t* bytes) {
+    op_clear_error();
+    REQUIRE(bytes, "bytes is NULL");
+    *bytes = 0;
+    TRY(check_linear(in_type, GEMM_ACT_NONE, M, N, K));
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_linear_bwd(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, gemm_act_t act, const void* dC,
+                              gemm_dtype_t dc_type, int64_t lddc, const void* Z, int64_t ldz, const void* A, int64_t lda,
+                              const void* W, int64_t ldw, void* dZ, int64_t lddz, void* dA, int64_t ldda, void* dW,
+                              gemm_dtype_t dw_type, int64_t lddw, float* dbias, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream) {
+    op_clear_error();
+    TRY(check_linear(in_type, act, M, N, K));
+    REQUIRE(dc_type == GEMM_F32 || dc_type == in_type, "dc_type %d not offered for in_type %d", (int)dc_type, (int)in_type);
+    REQUIRE(!dW || dw_type == GEMM_F32 || dw_type == in_type, "dw_type %d not offered for in_type %d", (int)dw_type, (int)in_type);
+    const bool some = M > 0 && N > 0, same = act == GEMM_ACT_NONE && dc_type == in_type;
+    TRY(check_ld("lddc", lddc, N));
+    if (act != GEMM_ACT_NONE) TRY(check_ld("ldz", ldz, N));
+    if (dZ) TRY(check_ld("lddz", lddz, N));
+    if (dA) {
+        TRY(check_ld("ldda", ldda, K));
+        TRY(check_ld("ldw", ldw, K));
+    }
+    if (dW) {
+        TRY(check_ld("lddw", lddw, K));
+        TRY(check_ld("lda", lda, K));
+    }
+    TRY(check_ws(workspace));
+    if (some) {
+        REQUIRE(dC, "dC is NULL");
+        REQUIRE(Z || act == GEMM_ACT_NONE, "Z is NULL");
+        REQUIRE(dZ || same || (!dA && !dW), "dZ is NULL");
+        REQUIRE(!dA || W || K == 0, "W is NULL");
+        REQUIRE(!dW || A || K == 0, "A is NULL");
+    }
+    if (!workspace) workspace_bytes = 0;
+    op_note("linear_bwd type %d M=%lld N=%lld K=%lld act=%d", (int)in_type, (long long)M, (long long)N, (long long)K, (int)act);
+    char* rest = static_cast<char*>(workspace);
+    size_t left = workspace_bytes;
+    if (N > 0 && (dbias || (some && dZ))) {
+        LinearBwdParams p;
+        p.dC = static_cast<const char*>(dC);
+        p.Z = static_cast<const char*>(Z);
+        p.dZ = some ? static_cast<char*>(dZ) : nullptr;
+        p.db = dbias;
+        p.lddc = lddc; p.ldz = ldz; p.lddz = lddz;
+        p.M = M;
+        p.N = (int)N;
+        p.act = act;
+        p.dc_type = dc_type;
+        p.part = reinterpret_cast<float*>(workspace);
+        p.parts = linear_bwd_parts(M, N);
+        if (dbias) {   // (partial sums are needed for db alone)
+            p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(p.parts, (int64_t)(left / ((size_t)N * sizeof(float)))));
+            if (p.parts > 1) {
+                const size_t used = std::min(left, (size_t)round256((int64_t)p.parts * N * (int64_t)sizeof(float)));
+                rest += used;
+                left -= used;
+            }
+        }
+        TRY(launched(launch_linear_bwd(in_type, p, stream)));
+    }
+    if (!dA && !dW) return GEMM_OK;
+    const void* dz = dZ ? dZ : dC;
+    const int64_t ld = dZ ? lddz : lddc;
+    if (!left) rest = nullptr;
+    if (dA) TRY(product(in_type, GEMM_ROW_MAJOR, M, K, N, dz, ld, W, ldw, dA, in_type, ldda, rest, left, stream));
+    if (dW) TRY(product(in_type, GEMM_COL_MAJOR, N, K, M, dz, ld, A, lda, dW, dw_type, lddw, rest, left, stream));
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_linear_bwd_workspace_size(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, size_t* bytes) {
+    op_clear_error();
+    REQUIRE(bytes, "bytes is NULL");
+    *bytes = 0;
+    TRY(check_linear(in_type, GEMM_ACT_NONE, M, N, K));
+    if (M == 0 || N == 0) return GEMM_OK;
+    const int parts = linear_bwd_parts(M, N);
+    const int64_t sums = parts > 1 ? round256((int64_t)parts * N * (int64_t)sizeof(float)) : 0;
+    size_t most = 0;
+    if (K > 0)
+        for (const gemm_dtype_t c_type : {in_type, GEMM_F32}) {
+            const void* at = reinterpret_cast<const void*>(uintptr_t(1) << 20);   // (contiguous aligned operands, wherever they are)
+            size_t b = 0;
+            TRY(gemm_workspace_size(in_type, c_type, GEMM_ROW_MAJOR, GEMM_ROW_MAJOR, M, K, N, 1.0f, at, N, at, K, 0.0f, at, K, nullptr, &b, nullptr));
+            most = std::max(most, b);
+            TRY(gemm_workspace_size(in_type, c_type, GEMM_COL_MAJOR, GEMM_ROW_MAJOR, N, K, M, 1.0f, at, N, at, K, 0.0f, at, K, nullptr, &b, nullptr));
+            most = std::max(most, b);
+        }
+    *bytes = (size_t)sums + most;
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_qk_norm_rope(gemm_dtype_t in_type, gemm_dtype_t w_type, int64_t tokens, int64_t q_heads, int64_t k_heads,
+                                int64_t head_dim, float eps, const gemm_heads_t* q, const gemm_heads_t* k, const void* wq,
+                                const void* wk, const gemm_rope_t* rope, const gemm_heads_t* out_q, const gemm_heads_t* out_k,
+                                hipStream_t stream) {
+    op_clear_error();
+    HeadsParams p;
+    TRY(check_qk(in_type, w_type, tokens, q_heads, k_heads, head_dim, eps, wq, wk, rope, &p));
+    TRY(check_heads("q", q, tokens, q_heads, head_dim, &p.x[0]));
+    TRY(check_heads("k", k, tokens, k_heads, head_dim, &p.x[1]));
+    TRY(check_heads("out_q", out_q, tokens, q_heads, head_dim, &p.y[0]));
+    TRY(check_heads("out_k", out_k, tokens, k_heads, head_dim, &p.y[1]));
+    if (tokens == 0 || q_heads + k_heads == 0) return GEMM_OK;
+    op_note("qk_norm_rope type %d tokens=%lld heads=%lld+%lld dim=%lld rot=%d", (int)in_type, (long long)tokens, (long long)q_heads,
+            (long long)k_heads, (long long)head_dim, p.rot);
+    return launched(launch_heads(in_type, p, stream));
+}
+
+gemm_status_t gemm_qk_norm_rope_bwd(gemm_dtype_t in_type, gemm_dtype_t w_type, int64_t tokens, int64_t q_heads, int64_t k_heads,
+                                    int64_t head_dim, float eps, const gemm_heads_t* dq, const gemm_heads_t* dk,
+                                    const gemm_heads_t* q, const gemm_heads_t* k, const void* wq, const void* wk,
+                                    const gemm_rope_t* rope, const gemm_heads_t* dxq, const gemm_heads_t* dxk, float* dwq,
+                                    float* dwk, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    op_clear_error();
+    HeadsParams p;
+    TRY(check_qk(in_type, w_type, tokens, q_heads, k_heads, head_dim, eps, wq, wk, rope, &p));
+    TRY(check_heads("dq", dq, tokens, q_heads, head_dim, &p.dy[0]));
+    TRY(check_heads("dk", dk, tokens, k_heads, head_dim, &p.dy[1]));
+    TRY(check_heads("q", q, tokens, q_heads, head_dim, &p.x[0]));
+    TRY(check_heads("k", k, tokens, k_heads, head_dim, &p.x[1]));
+    TRY(check_heads("dxq", dxq, tokens, q_heads, head_dim, &p.y[0]));
+    TRY(check_heads("dxk", dxk, tokens, k_heads, head_dim, &p.y[1]));
+    TRY(check_ws(workspace));
+    if ((tokens == 0 || q_heads + k_heads == 0) && !dwq && !dwk) return GEMM_OK;
+    p.dw[0] = dwq;
+    p.dw[1] = dwk;
+    p.part = static_cast<float*>(workspace);
+    p.parts = heads_bwd_parts(p);
+    if (dwq || dwk) {   // (partial sums are needed for dw alone)
+        const int64_t fit = workspace ? (int64_t)(workspace_bytes / (2 * (size_t)head_dim * sizeof(float))) : 0;
+        p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(p.parts, fit));
+    }
+    op_note("qk_norm_rope_bwd type %d tokens=%lld heads=%lld+%lld dim=%lld rot=%d in %d parts", (int)in_type, (long long)tokens,
+            (long long)q_heads, (long long)k_heads, (long long)head_dim, p.rot, p.parts);
+    return launched(launch_heads_bwd(in_type, p, stream));
+}
+
+gemm_status_t gemm_qk_norm_rope_bwd_workspace_size(gemm_dtype_t in_type, int64_t tokens, int64_t q_heads, int64_t k_heads,
+                                                   int64_t head_dim, size_t* bytes) {
+    op_clear_error();
+    REQUIRE(bytes, "bytes is NULL");
+    *bytes = 0;
+    HeadsParams p;
+    TRY(check_qk(in_type, in_type, tokens, q_heads, k_heads, head_dim, 0.0f, nullptr, nullptr, nullptr, &p));
+    const int parts = heads_bwd_parts(p);
+    if (parts > 1) *bytes = (size_t)parts * 2 * (size_t)head_dim * sizeof(float);
+    return GEMM_OK;
+}
+
+}  // extern "C"

@@ -107,4 +107,62 @@ size_t w4_tile_workspace(int64_t M, int64_t N, int64_t K, int64_t group);
 hipError_t launch_w4_tile(int in_type, const W4Params& p, void* ws, size_t ws_bytes, hipStream_t st);
 hipError_t launch_w4_skinny(int in_type, const W4Params& p, hipStream_t st);
 
+// ---------------------------------------------------------------- product with bias, activation and residual
+struct LinearParams {
+    const char* A;       // M x K, K contiguous, 16 bits
+    const char* W;       // N x K, the same
+    const char* bias;    // N, or NULL
+    const char* R;       // M x N of C's type, added behind the activation, or NULL
+    char* Z;             // M x N of A's type: the sums with their bias, or NULL
+    char* C;
+    int64_t lda, ldw, ldr, ldz, ldc;   // elements
+    int M, N, K;
+    int act, bias_type, out_type;
+};
+hipError_t launch_linear_staged(int in_type, const LinearParams& p, hipStream_t st);
+
+// dZ = dC * act'(Z) and its sums over the rows.
+struct LinearBwdParams {
+    const char* dC;      // M x N
+    const char* Z;       // M x N, or NULL (act 0)
+    char* dZ;            // M x N, or NULL (dC is it)
+    float* db;           // N, or NULL
+    float* part;         // parts x N partial sums of db (parts > 1)
+    int64_t lddc, ldz, lddz;
+    int64_t M;
+    int N;
+    int act, dc_type;
+    int parts;           // what the rows are cut into
+};
+int linear_bwd_parts(int64_t M, int64_t N);   // parts that the pass would like
+hipError_t launch_linear_bwd(int in_type, const LinearBwdParams& p, hipStream_t st);
+
+// ---------------------------------------------------------------- norm and rotation of heads
+struct HeadsTensor {
+    const char* p;
+    int64_t ld, hs;      // elements between tokens, between heads
+};
+struct HeadsParams {     // [0]: queries, [1]: keys
+    HeadsTensor x[2];
+    HeadsTensor dy[2];   // backward only
+    HeadsTensor y[2];    // what is written: y, or dx
+    const char* w[2];    // NULL: ones
+    float* dw[2];        // backward: NULL where not wanted
+    float* part;         // backward: parts x 2 x dim partial sums of dw (parts > 1)
+    const int64_t* pos;
+    const float* cos;
+    const float* sin;
+    int64_t ldt, table;  // the table's rows: floats apart, how many
+    int64_t tokens;
+    int heads[2];
+    int dim, rot, neighbours;
+    int w_type;
+    float eps;
+    int parts;
+};
+constexpr int kMostHeadDim = 1024;
+hipError_t launch_heads(int in_type, const HeadsParams& p, hipStream_t st);
+int heads_bwd_parts(const HeadsParams& p);
+hipError_t launch_heads_bwd(int in_type, const HeadsParams& p, hipStream_t st);
+
 }  // namespace gemm

@@ -34,6 +34,25 @@ __device__ __forceinline__ uint16_t from_f32(float v) {
     return T == DT_BF16 ? f32_to_bf16_bits(v) : f32_to_f16_bits(v);
 }
 
+template <int T>
+struct Elem {  // elements of a 16-byte vector
+    static constexpr int SIZE = T == DT_F32 ? 4 : 2;
+    static constexpr int VE = 16 / SIZE;
+    static __device__ __forceinline__ float get(const u32x4& v, int e) {
+        if constexpr (T == DT_F32) return __uint_as_float(v[e]);
+        else return to_f32<T>((uint16_t)(v[e >> 1] >> ((e & 1) * 16)));
+    }
+    static __device__ __forceinline__ u32x4 pack(const float* f) {
+        u32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (T == DT_F32) v[i] = __float_as_uint(f[i]);
+            else v[i] = (uint32_t)from_f32<T>(f[2 * i]) | ((uint32_t)from_f32<T>(f[2 * i + 1]) << 16);
+        }
+        return v;
+    }
+};
+
 // Element i of an array of 16- or 32-bit floats whose type is known at run time.
 __device__ __forceinline__ float load_elem(const char* p, int type, int64_t i) {
     if (type == DT_F32) return reinterpret_cast<const float*>(p)[i];
@@ -61,6 +80,20 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
         v = o > v ? o : v;
     }
     return v;
+}
+
+// 1 / sqrt(sum / cols + eps) from the row's sum of squares.  Where that sum leaves fp32's range
+// though the row does not (|h| above 2^64 / sqrt(cols); |h| below 2^-45 with so small an eps), `again` sums
+// the squares of h * 2^-80 or h * 2^80, which stay in range for any such row.
+template <class F>
+__device__ __forceinline__ float row_rstd(float sum, int cols, float eps, F&& again) {
+    const float mean = sum / (float)cols + eps;
+    const bool high = __builtin_isinf(sum);
+    if (high || mean < 0x1p-90f) {   // the same in every thread of the row
+        const float by = high ? 0x1p-80f : 0x1p80f;
+        return by / __builtin_sqrtf(again(by) / (float)cols + eps * by * by);
+    }
+    return 1.0f / __builtin_sqrtf(mean);
 }
 
 // Launches of a product's kernel for at most `rows` x `cols` of C each: grids are counted in 32 bits, workgroups times

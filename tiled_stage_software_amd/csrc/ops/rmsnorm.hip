@@ -22,25 +22,6 @@ namespace {
 constexpr float kF8Max = 448.0f;
 constexpr float kTiny = 1.17549435e-38f;  // smallest normal: the scale of a row of zeros, whose reciprocal is finite
 
-template <int T>
-struct Elem {  // elements of a 16-byte vector
-    static constexpr int SIZE = T == DT_F32 ? 4 : 2;
-    static constexpr int VE = 16 / SIZE;
-    static __device__ __forceinline__ float get(const u32x4& v, int e) {
-        if constexpr (T == DT_F32) return __uint_as_float(v[e]);
-        else return to_f32<T>((uint16_t)(v[e >> 1] >> ((e & 1) * 16)));
-    }
-    static __device__ __forceinline__ u32x4 pack(const float* f) {
-        u32x4 v;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (T == DT_F32) v[i] = __float_as_uint(f[i]);
-            else v[i] = (uint32_t)from_f32<T>(f[2 * i]) | ((uint32_t)from_f32<T>(f[2 * i + 1]) << 16);
-        }
-        return v;
-    }
-};
-
 // Vector of row elements c .. c+VE-1; elements at or past `cols` are 0 and not read.
 template <int T>
 __device__ __forceinline__ u32x4 load_vec(const char* row, int c, int cols) {
@@ -167,20 +148,6 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits) {
 __device__ __forceinline__ float over_scale(float y, float s, float inv) {
     const float q = y * inv;
     return __builtin_fmaf(__builtin_fmaf(-q, s, y), inv, q);
-}
-
-// 1 / sqrt(sum / cols + eps) from the row's sum of squares.  Where that sum leaves fp32's range
-// though the row does not (|h| above 2^64 / sqrt(cols); |h| below 2^-45 with so small an eps), `again` sums
-// the squares of h * 2^-80 or h * 2^80, which stay in range for any such row.
-template <class F>
-__device__ __forceinline__ float row_rstd(float sum, int cols, float eps, F&& again) {
-    const float mean = sum / (float)cols + eps;
-    const bool high = __builtin_isinf(sum);
-    if (high || mean < 0x1p-90f) {   // the same in every thread of the row
-        const float by = high ? 0x1p-80f : 0x1p80f;
-        return by / __builtin_sqrtf(again(by) / (float)cols + eps * by * by);
-    }
-    return 1.0f / __builtin_sqrtf(mean);
 }
 
 // h = x + r in T; x alone where there is no residual.

@@ -24,6 +24,8 @@ GEMM_ROW_MAJOR, GEMM_COL_MAJOR = 0, 1
 GEMM_F32, GEMM_BF16, GEMM_F16, GEMM_F8E4M3 = 0, 1, 2, 3
 (GEMM_KERNEL_AUTO, GEMM_KERNEL_VALU_RING, GEMM_KERNEL_VALU_STAGED, GEMM_KERNEL_MFMA_RING,
  GEMM_KERNEL_MFMA_STAGED, GEMM_KERNEL_SCALE) = range(6)
+(GEMM_ACT_NONE, GEMM_ACT_RELU, GEMM_ACT_GELU, GEMM_ACT_GELU_TANH, GEMM_ACT_SILU) = range(5)
+GEMM_ROPE_HALVES, GEMM_ROPE_NEIGHBOURS = 0, 1
 GEMM_FLAG_NO_XCD_REMAP = 1
 GEMM_FLAG_EQUAL_LDS = 2
 GEMM_FLAG_POISON_LDS = 4
@@ -40,7 +42,9 @@ EXPORTS = ("gemm_f32", "gemm_bf16", "gemm_f16", "gemm_f32_ex", "gemm_bf16_ex", "
            "gemm_bf16_ws", "gemm_f16_ws", "gemm_ws_static", "gemm_workspace_size", "gemm_plan", "gemm_tune", "gemm_tune_ws",
            "gemm_schedule", "gemm_pipe_copy", "gemm_mfma_ceiling", "gemm_h2d_staged", "gemm_h2d_staged_async", "gemm_status_string",
            "gemm_last_error", "gemm_rmsnorm", "gemm_rmsnorm_bwd", "gemm_rmsnorm_bwd_workspace_size", "gemm_f8",
-           "gemm_f8_workspace_size", "gemm_w4", "gemm_w4_workspace_size")
+           "gemm_f8_workspace_size", "gemm_w4", "gemm_w4_workspace_size", "gemm_linear", "gemm_linear_workspace_size",
+           "gemm_linear_bwd", "gemm_linear_bwd_workspace_size", "gemm_qk_norm_rope", "gemm_qk_norm_rope_bwd",
+           "gemm_qk_norm_rope_bwd_workspace_size")
 
 
 class GemmOpts(ctypes.Structure):
@@ -58,6 +62,17 @@ class GemmPlan(ctypes.Structure):
         d = {f: getattr(self, f) for f, _ in self._fields_}
         d["kernel_name"] = KERNEL_NAMES.get(self.kernel, str(self.kernel))
         return d
+
+
+class GemmHeads(ctypes.Structure):
+    """tokens x heads x head_dim elements by their address and strides (elements)."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class GemmRope(ctypes.Structure):
+    """The rotation by position: addresses of positions, cos and sin, the table's pitch and rows, rot_dim, pairs."""
+    _fields_ = [("positions", ctypes.c_void_p), ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("rot_dim", ctypes.c_int), ("pairs", ctypes.c_int)]
 
 
 class GemmError(RuntimeError):
@@ -125,8 +140,22 @@ def load():
         lib.gemm_f8_workspace_size.argtypes = [i64, i64, i64, szp]
         lib.gemm_w4.argtypes = [i32, i64, i64, i64, i64, f32, vp, i64, vp, i64, vp, vp, i64, f32, vp, i32, i64, vp, sz, vp]
         lib.gemm_w4_workspace_size.argtypes = [i32, i64, i64, i64, i64, szp]
+        lib.gemm_linear.argtypes = [i32, i64, i64, i64, vp, i64, vp, i64, vp, i32, i32, vp, i64, vp, i64, vp, i32, i64, vp, sz, vp]
+        lib.gemm_linear_workspace_size.argtypes = [i32, i64, i64, i64, szp]
+        lib.gemm_linear_bwd.argtypes = [i32, i64, i64, i64, i32, vp, i32, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i32,
+                                        i64, vp, vp, sz, vp]
+        lib.gemm_linear_bwd_workspace_size.argtypes = [i32, i64, i64, i64, szp]
+        hp, rp = ctypes.POINTER(GemmHeads), ctypes.POINTER(GemmRope)
+        lib.gemm_qk_norm_rope.argtypes = [i32, i32, i64, i64, i64, i64, f32, hp, hp, vp, vp, rp, hp, hp, vp]
+        lib.gemm_qk_norm_rope_bwd.argtypes = [i32, i32, i64, i64, i64, i64, f32, hp, hp, hp, hp, vp, vp, rp, hp, hp, vp, vp, vp, sz, vp]
+        lib.gemm_qk_norm_rope_bwd_workspace_size.argtypes = [i32, i64, i64, i64, i64, szp]
+        for name in ("gemm_linear", "gemm_linear_workspace_size", "gemm_linear_bwd", "gemm_linear_bwd_workspace_size",
+                     "gemm_qk_norm_rope", "gemm_qk_norm_rope_bwd", "gemm_qk_norm_rope_bwd_workspace_size"):
+            getattr(lib, name).restype = i32
         for name in ("gemm_rmsnorm", "gemm_rmsnorm_bwd", "gemm_rmsnorm_bwd_workspace_size", "gemm_f8",
-                     "gemm_f8_workspace_size", "gemm_w4", "gemm_w4_workspace_size"):
+                     "gemm_f8_workspace_size", "gemm_w4", "gemm_w4_workspace_size", "gemm_linear", "gemm_linear_workspace_size",
+           "gemm_linear_bwd", "gemm_linear_bwd_workspace_size", "gemm_qk_norm_rope", "gemm_qk_norm_rope_bwd",
+           "gemm_qk_norm_rope_bwd_workspace_size"):
             getattr(lib, name).restype = i32
         lib.gemm_status_string.argtypes = [i32]
         lib.gemm_status_string.restype = ctypes.c_char_p
@@ -306,6 +335,45 @@ def gemm_f8_workspace_size(M, N, K):
 def gemm_w4_workspace_size(in_type, M, N, K, group):
     """(status, bytes)"""
     return _size_of(load().gemm_w4_workspace_size, in_type, M, N, K, group)
+
+
+def gemm_linear(in_type, M, N, K, A, lda, W, ldw, bias, bias_type, act, R, ldr, Z, ldz, C, c_type, ldc, workspace=0,
+                workspace_bytes=0, stream=0) -> int:
+    """C = act(A W^T + bias) + R; Z = A W^T + bias where it is wanted (see include/libgemm.h)."""
+    return load().gemm_linear(in_type, M, N, K, A, lda, W, ldw, bias, bias_type, act, R, ldr, Z, ldz, C, c_type, ldc, workspace,
+                              workspace_bytes, stream)
+
+
+def gemm_linear_bwd(in_type, M, N, K, act, dC, dc_type, lddc, Z, ldz, A, lda, W, ldw, dZ, lddz, dA, ldda, dW, dw_type, lddw, dbias,
+                    workspace=0, workspace_bytes=0, stream=0) -> int:
+    return load().gemm_linear_bwd(in_type, M, N, K, act, dC, dc_type, lddc, Z, ldz, A, lda, W, ldw, dZ, lddz, dA, ldda, dW, dw_type,
+                                  lddw, dbias, workspace, workspace_bytes, stream)
+
+
+def gemm_qk_norm_rope(in_type, w_type, tokens, q_heads, k_heads, head_dim, eps, q, k, wq, wk, rope, out_q, out_k, stream=0) -> int:
+    """Norm of each head of q and k with the rotation by position; q, k, out_q, out_k: GemmHeads, rope: GemmRope or None."""
+    return load().gemm_qk_norm_rope(in_type, w_type, tokens, q_heads, k_heads, head_dim, eps, q, k, wq, wk, rope, out_q, out_k, stream)
+
+
+def gemm_qk_norm_rope_bwd(in_type, w_type, tokens, q_heads, k_heads, head_dim, eps, dq, dk, q, k, wq, wk, rope, dxq, dxk, dwq, dwk,
+                          workspace=0, workspace_bytes=0, stream=0) -> int:
+    return load().gemm_qk_norm_rope_bwd(in_type, w_type, tokens, q_heads, k_heads, head_dim, eps, dq, dk, q, k, wq, wk, rope, dxq, dxk,
+                                        dwq, dwk, workspace, workspace_bytes, stream)
+
+
+def gemm_linear_workspace_size(in_type, M, N, K):
+    """(status, bytes)"""
+    return _size_of(load().gemm_linear_workspace_size, in_type, M, N, K)
+
+
+def gemm_linear_bwd_workspace_size(in_type, M, N, K):
+    """(status, bytes)"""
+    return _size_of(load().gemm_linear_bwd_workspace_size, in_type, M, N, K)
+
+
+def gemm_qk_norm_rope_bwd_workspace_size(in_type, tokens, q_heads, k_heads, head_dim):
+    """(status, bytes)"""
+    return _size_of(load().gemm_qk_norm_rope_bwd_workspace_size, in_type, tokens, q_heads, k_heads, head_dim)
 
 
 def gemm_status_string(s: int) -> str:

@@ -1,6 +1,7 @@
 """Torch-tensor form of the operators around the products: the root-mean-square norm and its
 backward pass (also through autograd), the product of 8-bit operands and the product with 4-bit
-weights (which have none).
+weights (which have none); and of a transformer block's dense parts, with their backward passes: the
+product with bias, activation and residual, and the norm of queries and keys with the rotation by position.
 
 As ``libgemm.matmul``, these only read shapes, strides and pointers; every step on the
 GPU runs in the library's kernels, and there is no fallback.  ``quantize_f8`` and
@@ -113,6 +114,42 @@ def _functions():
             dx = dx.to(h.dtype)
             return (dx if of_x else None, dw.to(weight.dtype) if of_weight else None, dx if of_residual else None, None, None)
 
+    class Linear(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, bias, residual, act, out_dtype, workspace):
+            keep = act != "none" and any(ctx.needs_input_grad[:3])
+            y, z = _linear(x, weight, bias, act, residual, out_dtype, keep, workspace)
+            ctx.save_for_backward(x, weight, z)
+            ctx.act, ctx.bias = act, bias.dtype if bias is not None else None
+            return y
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dy):
+            x, weight, z = ctx.saved_tensors
+            of_x, of_weight, of_bias, of_residual = ctx.needs_input_grad[:4]
+            dx = dw = db = None
+            if of_x or of_weight or of_bias:
+                dx, dw, db = linear_backward(dy.contiguous(), x, weight, z, ctx.act, (of_x, of_weight, of_bias))
+            return dx, dw, db.to(ctx.bias) if of_bias else None, dy if of_residual else None, None, None, None
+
+    class Heads(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, wq, wk, positions, cos, sin, pairs, eps):
+            ctx.save_for_backward(q, k, wq, wk, positions, cos, sin)
+            ctx.pairs, ctx.eps = pairs, eps
+            return _qk_norm_rope(q, k, wq, wk, positions, cos, sin, pairs, eps)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dq, dk):
+            q, k, wq, wk, positions, cos, sin = ctx.saved_tensors
+            of_q, of_k, of_wq, of_wk = ctx.needs_input_grad[:4]
+            gq, gk, gwq, gwk = qk_norm_rope_backward(dq.contiguous(), dk.contiguous(), q, k, wq, wk, positions, cos, sin, ctx.pairs,
+                                                     ctx.eps, of_wq or of_wk)
+            return (gq if of_q else None, gk if of_k else None, gwq.to(wq.dtype) if of_wq else None,
+                    gwk.to(wk.dtype) if of_wk else None, None, None, None, None, None)
+
     class NoBackward(torch.autograd.Function):
         @staticmethod
         def forward(ctx, name, result, *inputs):
@@ -124,7 +161,7 @@ def _functions():
         def backward(ctx, _):
             raise RuntimeError(f"{ctx.name} has no backward pass: detach its inputs")
 
-    return Norm, NoBackward
+    return Norm, NoBackward, Linear, Heads
 
 
 def rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None, stream=None) -> RmsNorm:
@@ -241,6 +278,181 @@ def matmul_w4(a, codes, scales, zeros=None, group: int = 128, C=None, alpha: flo
                             zeros.data_ptr() if zeros is not None else 0, lds, beta, C.data_ptr(), _code(C.dtype), ldc, ws,
                             nbytes, on.handle))
         return _no_gradient("matmul_w4", C, a, codes, scales, zeros)
+
+
+ACTS = {"none": lg.GEMM_ACT_NONE, "relu": lg.GEMM_ACT_RELU, "gelu": lg.GEMM_ACT_GELU, "gelu_tanh": lg.GEMM_ACT_GELU_TANH,
+        "silu": lg.GEMM_ACT_SILU}
+PAIRS = {"halves": lg.GEMM_ROPE_HALVES, "neighbours": lg.GEMM_ROPE_NEIGHBOURS}
+
+
+def _one_of(table, name: str, value) -> int:
+    if value not in table:
+        raise ValueError(f"{name} {value!r}: one of {', '.join(table)}")
+    return table[value]
+
+
+def linear(x, weight, bias=None, act: str = "none", residual=None, out_dtype=None, workspace="auto", stream=None):
+    """act(x weight^T + bias) + residual; x: M x K and weight: N x K in bf16 or f16; the result, and residual with it, in
+    their type (the default) or fp32; act: "none", "relu", "gelu", "gelu_tanh" or "silu".  Gradients reach
+    x, weight, bias and residual through ``linear_backward``."""
+    if not _wants_gradient(x, weight, bias, residual):
+        return _linear(x, weight, bias, act, residual, out_dtype, False, workspace, stream)[0]
+    with lg.Running(stream, x.device, x, weight, bias, residual, workspace) as on:   # (its backward pass runs on the same stream)
+        y = _functions()[2].apply(x, weight, bias, residual, act, out_dtype, workspace)
+        on.keep(y)
+    return y
+
+
+def linear_keeping(x, weight, bias=None, act: str = "none", residual=None, out_dtype=None, workspace="auto", stream=None):
+    """(``linear``'s result, z = x weight^T + bias in x's type, which ``linear_backward`` reads); without autograd."""
+    return _linear(x, weight, bias, act, residual, out_dtype, True, workspace, stream)
+
+
+def _linear(x, weight, bias, act, residual, out_dtype, keep, workspace, stream=None):
+    import torch
+    lda, ldw = _rows(x, "x"), _rows(weight, "weight", None, x.dtype, x.device)
+    M, K = x.shape
+    N = weight.shape[0]
+    if weight.shape[1] != K:
+        raise ValueError(f"shapes {tuple(x.shape)} and {tuple(weight.shape)}: rows of different lengths")
+    code, out_dtype, a = _code(x.dtype), out_dtype or x.dtype, _one_of(ACTS, "act", act)
+    c_code = _code(out_dtype)
+    b = _vector(bias, "bias", N, (x.dtype, torch.float32), x.device)
+    ldr = _rows(residual, "residual", (M, N), out_dtype, x.device) if residual is not None else 0
+    with lg.Running(stream, x.device, x, weight, bias, residual, workspace) as on:
+        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        z = torch.empty((M, N), dtype=x.dtype, device=x.device) if keep else None
+        on.keep(y, z)
+        held, ws, nbytes = _workspace(workspace, lambda: lg.gemm_linear_workspace_size(code, M, N, K), x.device)
+        lg.check(lg.gemm_linear(code, M, N, K, x.data_ptr(), lda, weight.data_ptr(), ldw, b, _code(bias.dtype) if b else 0, a,
+                                residual.data_ptr() if ldr else 0, ldr, z.data_ptr() if keep else 0, max(N, 1), y.data_ptr(), c_code,
+                                max(N, 1), ws, nbytes, on.handle))
+    return y, z
+
+
+def linear_backward(dy, x, weight, z=None, act: str = "none", need=(True, True, True), dw_dtype=None, workspace="auto", stream=None):
+    """(dx, dw, db) of ``linear`` from its z (None for act "none"); dx in x's type, dw in weight's or `dw_dtype`
+    (fp32), db in fp32; `need`: which of them are wanted (None for the others).  residual's gradient is dy."""
+    import torch
+    lda, ldw = _rows(x, "x"), _rows(weight, "weight", None, x.dtype, x.device)
+    M, K = x.shape
+    N = weight.shape[0]
+    if weight.shape[1] != K:
+        raise ValueError(f"shapes {tuple(x.shape)} and {tuple(weight.shape)}: rows of different lengths")
+    code, a = _code(x.dtype), _one_of(ACTS, "act", act)
+    lddy = _rows(dy, "dy", (M, N), None, x.device)
+    if z is None and act != "none":
+        raise ValueError(f"act {act!r} needs z")
+    ldz = _rows(z, "z", (M, N), x.dtype, x.device) if act != "none" else 0
+    with lg.Running(stream, x.device, dy, x, weight, z, workspace) as on:
+        new = lambda wanted, *shape, dtype: torch.empty(shape, dtype=dtype, device=x.device) if wanted else None  # noqa: E731
+        dx, dw = new(need[0], M, K, dtype=x.dtype), new(need[1], N, K, dtype=dw_dtype or weight.dtype)
+        db = new(need[2], N, dtype=torch.float32)
+        dz = new((need[0] or need[1]) and (act != "none" or dy.dtype != x.dtype), M, N, dtype=x.dtype)
+        on.keep(dx, dw, db)
+        held, ws, nbytes = _workspace(workspace, lambda: lg.gemm_linear_bwd_workspace_size(code, M, N, K), x.device)
+        at = lambda t: t.data_ptr() if t is not None else 0  # noqa: E731
+        lg.check(lg.gemm_linear_bwd(code, M, N, K, a, dy.data_ptr(), _code(dy.dtype), lddy, at(z) if ldz else 0, ldz, x.data_ptr(), lda,
+                                    weight.data_ptr(), ldw, at(dz), max(N, 1), at(dx), max(K, 1), at(dw),
+                                    _code(dw.dtype) if need[1] else 0, max(K, 1), at(db), ws, nbytes, on.handle))
+    return dx, dw, db
+
+
+def _heads(t, name: str, shape=None, dtype=None, device=None):
+    """Checks tokens x heads x dim with contiguous heads and gives what the library reads of it."""
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}" + (f", not {tuple(shape)}" if shape is not None else ", not tokens x heads x dim"))
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, not {dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    return lg.GemmHeads(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _rope(positions, cos, sin, pairs, tokens, device):
+    import torch
+    code = _one_of(PAIRS, "pairs", pairs)
+    if positions is None and cos is None and sin is None:
+        return None
+    if positions is None or cos is None or sin is None:
+        raise ValueError("positions, cos and sin come together")
+    at = _vector(positions, "positions", tokens, torch.int64, device)
+    ld = _rows(cos, "cos", None, torch.float32, device)
+    if _rows(sin, "sin", cos.shape, torch.float32, device) != ld:
+        raise ValueError("sin: the row stride of cos")
+    return lg.GemmRope(at, cos.data_ptr(), sin.data_ptr(), ld, cos.shape[0], 2 * cos.shape[1], code)
+
+
+def rope_table(rows: int, rot_dim: int, base: float = 10000.0, device=None):
+    """(cos, sin), rows x rot_dim / 2 each in fp32, of the angles position * base^(-2 i / rot_dim), taken in 64 bits."""
+    import torch
+    rate = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    angle = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * rate
+    return angle.cos().float(), angle.sin().float()
+
+
+def qk_norm_rope(q, k, wq=None, wk=None, positions=None, cos=None, sin=None, pairs: str = "halves", eps: float = 1e-6, stream=None):
+    """(q, k), each head divided by the root of its mean square, times wq or wk, and its first 2 * cos.shape[1] elements turned by
+    the token's position.  q, k: tokens x heads x dim, any strides with contiguous heads; positions: int64, a row of
+    cos and sin (``rope_table``) each; pairs: element i with i + half of those that turn ("halves") or 2 i with 2 i + 1 ("neighbours").
+    Without positions, cos and sin: the norm alone.  Gradients reach q, k, wq and wk through ``qk_norm_rope_backward``."""
+    if _wants_gradient(cos, sin):
+        raise ValueError("no gradient reaches cos and sin: detach them")
+    if not _wants_gradient(q, k, wq, wk):
+        return _qk_norm_rope(q, k, wq, wk, positions, cos, sin, pairs, eps, stream)
+    with lg.Running(stream, q.device, q, k, wq, wk, positions, cos, sin) as on:   # (its backward pass runs on the same stream)
+        out = _functions()[3].apply(q, k, wq, wk, positions, cos, sin, pairs, eps)
+        on.keep(*out)
+    return out
+
+
+def _qk(q, k, wq, wk):
+    """What both passes check of their inputs: (types' codes, weights' addresses)"""
+    import torch
+    if k.dim() != 3 or q.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError(f"q and k: shapes {tuple(q.shape)} and {tuple(k.shape)}, not tokens x heads x dim with tokens and dim alike")
+    if wq is not None and wk is not None and wq.dtype != wk.dtype:
+        raise ValueError(f"wq and wk: {wq.dtype} and {wk.dtype}")
+    w = wq if wq is not None else wk
+    at = [_vector(t, name, q.shape[2], (q.dtype, torch.float32), q.device) for t, name in ((wq, "wq"), (wk, "wk"))]
+    return _code(q.dtype), _code(w.dtype) if w is not None else 0, at
+
+
+def _qk_norm_rope(q, k, wq, wk, positions, cos, sin, pairs, eps, stream=None):
+    import torch
+    code, w_code, w = _qk(q, k, wq, wk)
+    tokens, heads, dim = q.shape
+    qh, kh = _heads(q, "q"), _heads(k, "k", None, q.dtype, q.device)
+    rope = _rope(positions, cos, sin, pairs, tokens, q.device)
+    with lg.Running(stream, q.device, q, k, wq, wk, positions, cos, sin) as on:
+        out = [torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k)]
+        on.keep(*out)
+        lg.check(lg.gemm_qk_norm_rope(code, w_code, tokens, heads, k.shape[1], dim, eps, qh, kh, *w, rope, *(_heads(t, "") for t in out),
+                                      on.handle))
+    return tuple(out)
+
+
+def qk_norm_rope_backward(dq, dk, q, k, wq=None, wk=None, positions=None, cos=None, sin=None, pairs: str = "halves", eps: float = 1e-6,
+                          need_dw: bool = True, workspace="auto", stream=None):
+    """(gradients of q, of k, of wq, of wk) of ``qk_norm_rope`` from those of its results and its inputs; the weights' in
+    fp32 (None unless `need_dw`)."""
+    import torch
+    code, w_code, w = _qk(q, k, wq, wk)
+    tokens, heads, dim = q.shape
+    given = [_heads(dq, "dq", q.shape, q.dtype, q.device), _heads(dk, "dk", k.shape, q.dtype, q.device), _heads(q, "q"),
+             _heads(k, "k", None, q.dtype, q.device)]
+    rope = _rope(positions, cos, sin, pairs, tokens, q.device)
+    with lg.Running(stream, q.device, dq, dk, q, k, wq, wk, positions, cos, sin, workspace) as on:
+        dx = [torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k)]
+        dw = [torch.empty(dim, device=q.device) if need_dw else None for _ in range(2)]
+        on.keep(*dx, *dw)
+        held, ws, nbytes = _workspace(workspace if need_dw else None,
+                                      lambda: lg.gemm_qk_norm_rope_bwd_workspace_size(code, tokens, heads, k.shape[1], dim), q.device)
+        lg.check(lg.gemm_qk_norm_rope_bwd(code, w_code, tokens, heads, k.shape[1], dim, eps, *given, *w, rope,
+                                          *(_heads(t, "") for t in dx), *(t.data_ptr() if need_dw else 0 for t in dw), ws, nbytes, on.handle))
+    return (*dx, *dw)
 
 
 def quantize_f8(t):
