@@ -22,6 +22,9 @@ gemm_status_t check_linear(int in_type, int act, int64_t M, int64_t N, int64_t K
     return GEMM_OK;
 }
 
+// Whether the kernel for few rows takes a product.
+bool linear_few(const LinearParams& p) { return p.M <= kLinearSkinnyRows && p.K > 0; }
+
 // One of the backward pass's products, through the library's own 16-bit entry points.
 gemm_status_t product(int in_type, gemm_layout_t la, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
                       int64_t ldb, void* C, int c_type, int64_t ldc, void* ws, size_t bytes, hipStream_t st) {
@@ -115,9 +118,11 @@ gemm_status_t gemm_linear(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K,
     p.lda = lda; p.ldw = ldw; p.ldr = R ? ldr : 0; p.ldz = Z ? ldz : 0; p.ldc = ldc;
     p.M = (int)M; p.N = (int)N; p.K = (int)K;
     p.act = act; p.bias_type = bias_type; p.out_type = c_type;
-    op_note("linear type %d -> %d M=%lld N=%lld K=%lld act=%d", (int)in_type, (int)c_type, (long long)M, (long long)N, (long long)K,
-            (int)act);
-    return launched(launch_linear_staged(in_type, p, stream));
+    const bool few = linear_few(p), tiles = !few && linear_tile_fits(p);
+    op_note("linear type %d -> %d M=%lld N=%lld K=%lld act=%d: %s", (int)in_type, (int)c_type, (long long)M, (long long)N, (long long)K,
+            (int)act, few ? "few rows" : tiles ? "tiles" : "128 x 128 tiles");
+    if (few) return launched(launch_linear_skinny(in_type, p, stream));
+    return launched(tiles ? launch_linear_tile(in_type, p, workspace, workspace_bytes, stream) : launch_linear_staged(in_type, p, stream));
 }
 
 gemm_status_t gemm_linear_workspace_size(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, size_t* bytes) {
@@ -125,6 +130,12 @@ gemm_status_t gemm_linear_workspace_size(gemm_dtype_t in_type, int64_t M, int64_
     REQUIRE(bytes, "bytes is NULL");
     *bytes = 0;
     TRY(check_linear(in_type, GEMM_ACT_NONE, M, N, K));
+    if (M > 0 && N > 0 && K > 0) {
+        LinearParams p = {};
+        p.M = (int)M; p.N = (int)N; p.K = (int)K;
+        p.lda = p.ldw = K;   // (of contiguous operands)
+        if (!linear_few(p) && linear_tile_fits(p)) *bytes = linear_tile_workspace(p);   // (the other kernels use none)
+    }
     return GEMM_OK;
 }
 

@@ -119,6 +119,11 @@ struct LinearParams {
     int M, N, K;
     int act, bias_type, out_type;
 };
+constexpr int kLinearSkinnyRows = 32;   // rows of A that launch_linear_skinny takes
+hipError_t launch_linear_skinny(int in_type, const LinearParams& p, hipStream_t st);
+bool linear_tile_fits(const LinearParams& p);
+size_t linear_tile_workspace(const LinearParams& p);   // of a product that fits
+hipError_t launch_linear_tile(int in_type, const LinearParams& p, void* ws, size_t ws_bytes, hipStream_t st);
 hipError_t launch_linear_staged(int in_type, const LinearParams& p, hipStream_t st);
 
 // dZ = dC * act'(Z) and its sums over the rows.
