@@ -262,9 +262,9 @@ gemm_status_t gemm_qk_norm_rope_bwd(gemm_dtype_t in_type, gemm_dtype_t w_type, i
     p.dw[0] = dwq;
     p.dw[1] = dwk;
     p.part = static_cast<float*>(workspace);
-    p.parts = heads_bwd_parts(p);
+    p.parts = heads_bwd_parts(in_type, p);
     if (dwq || dwk) {   // (partial sums are needed for dw alone)
-        const int64_t fit = workspace ? (int64_t)(workspace_bytes / (2 * (size_t)head_dim * sizeof(float))) : 0;
+        const int64_t fit = workspace ? (int64_t)(workspace_bytes / ((size_t)head_dim * sizeof(float))) : 0;
         p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(p.parts, fit));
     }
     op_note("qk_norm_rope_bwd type %d tokens=%lld heads=%lld+%lld dim=%lld rot=%d in %d parts", (int)in_type, (long long)tokens,
@@ -279,8 +279,8 @@ gemm_status_t gemm_qk_norm_rope_bwd_workspace_size(gemm_dtype_t in_type, int64_t
     *bytes = 0;
     HeadsParams p;
     TRY(check_qk(in_type, in_type, tokens, q_heads, k_heads, head_dim, 0.0f, nullptr, nullptr, nullptr, &p));
-    const int parts = heads_bwd_parts(p);
-    if (parts > 1) *bytes = (size_t)parts * 2 * (size_t)head_dim * sizeof(float);
+    const int parts = heads_bwd_most_parts(p);
+    if (parts > 1) *bytes = (size_t)parts * (size_t)head_dim * sizeof(float);
     return GEMM_OK;
 }
 

@@ -153,7 +153,7 @@ struct HeadsParams {     // [0]: queries, [1]: keys
     HeadsTensor y[2];    // what is written: y, or dx
     const char* w[2];    // NULL: ones
     float* dw[2];        // backward: NULL where not wanted
-    float* part;         // backward: parts x 2 x dim partial sums of dw (parts > 1)
+    float* part;         // backward: parts x dim partial sums of dw (parts > 1)
     const int64_t* pos;
     const float* cos;
     const float* sin;
@@ -167,7 +167,8 @@ struct HeadsParams {     // [0]: queries, [1]: keys
 };
 constexpr int kMostHeadDim = 1024;
 hipError_t launch_heads(int in_type, const HeadsParams& p, hipStream_t st);
-int heads_bwd_parts(const HeadsParams& p);
+int heads_bwd_most_parts(const HeadsParams& p);
+int heads_bwd_parts(int in_type, const HeadsParams& p);   // in_type: DT_*
 hipError_t launch_heads_bwd(int in_type, const HeadsParams& p, hipStream_t st);
 
 }  // namespace gemm
