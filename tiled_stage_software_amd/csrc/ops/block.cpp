@@ -25,11 +25,15 @@ gemm_status_t check_linear(int in_type, int act, int64_t M, int64_t N, int64_t K
 // Whether the kernel for few rows takes a product.
 bool linear_few(const LinearParams& p) { return p.M <= kLinearSkinnyRows && p.K > 0; }
 
-// One of the backward pass's products, through the library's own 16-bit entry points.
-gemm_status_t product(int in_type, gemm_layout_t la, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
+// One of the backward pass's products (rows_a: A is K x M in memory): on tiles, or, where those do not take it, through the
+// library's own 16-bit entry points.
+gemm_status_t product(int in_type, bool rows_a, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
                       int64_t ldb, void* C, int c_type, int64_t ldc, void* ws, size_t bytes, hipStream_t st) {
-    return (in_type == GEMM_BF16 ? gemm_bf16_ws : gemm_f16_ws)(la, GEMM_ROW_MAJOR, M, N, K, 1.0f, A, lda, B, ldb, 0.0f, C,
-                                                               (gemm_dtype_t)c_type, ldc, st, nullptr, ws, ws ? bytes : 0);
+    const GradParams p = {static_cast<const char*>(A), static_cast<const char*>(B), static_cast<char*>(C), lda, ldb, ldc, (int)M, (int)N,
+                          (int)K, rows_a, c_type};
+    if (M > 0 && N > 0 && linear_grad_fits(p, bytes)) return launched(launch_linear_grad(in_type, p, ws, bytes, st));
+    return (in_type == GEMM_BF16 ? gemm_bf16_ws : gemm_f16_ws)(rows_a ? GEMM_COL_MAJOR : GEMM_ROW_MAJOR, GEMM_ROW_MAJOR, M, N, K, 1.0f, A,
+                                                               lda, B, ldb, 0.0f, C, (gemm_dtype_t)c_type, ldc, st, nullptr, ws, bytes);
 }
 
 gemm_status_t check_heads(const char* what, const gemm_heads_t* h, int64_t tokens, int64_t heads, int64_t dim, HeadsTensor* to) {
@@ -199,8 +203,8 @@ gemm_status_t gemm_linear_bwd(gemm_dtype_t in_type, int64_t M, int64_t N, int64_
     const void* dz = dZ ? dZ : dC;
     const int64_t ld = dZ ? lddz : lddc;
     if (!left) rest = nullptr;
-    if (dA) TRY(product(in_type, GEMM_ROW_MAJOR, M, K, N, dz, ld, W, ldw, dA, in_type, ldda, rest, left, stream));
-    if (dW) TRY(product(in_type, GEMM_COL_MAJOR, N, K, M, dz, ld, A, lda, dW, dw_type, lddw, rest, left, stream));
+    if (dA) TRY(product(in_type, false, M, K, N, dz, ld, W, ldw, dA, in_type, ldda, rest, left, stream));
+    if (dW) TRY(product(in_type, true, N, K, M, dz, ld, A, lda, dW, dw_type, lddw, rest, left, stream));
     return GEMM_OK;
 }
 
@@ -214,12 +218,21 @@ gemm_status_t gemm_linear_bwd_workspace_size(gemm_dtype_t in_type, int64_t M, in
     const int64_t sums = parts > 1 ? round256((int64_t)parts * N * (int64_t)sizeof(float)) : 0;
     size_t most = 0;
     if (K > 0)
-        for (const gemm_dtype_t c_type : {in_type, GEMM_F32}) {
-            const void* at = reinterpret_cast<const void*>(uintptr_t(1) << 20);   // (contiguous aligned operands, wherever they are)
+        for (const bool dw : {false, true}) {
+            GradParams p = {};
+            p.M = (int)(dw ? N : M);
+            p.N = (int)K;
+            p.K = (int)(dw ? M : N);
+            p.lda = N; p.ldb = K; p.ldc = K;   // (of contiguous operands)
+            p.rows_a = dw;
             size_t b = 0;
-            TRY(gemm_workspace_size(in_type, c_type, GEMM_ROW_MAJOR, GEMM_ROW_MAJOR, M, K, N, 1.0f, at, N, at, K, 0.0f, at, K, nullptr, &b, nullptr));
-            most = std::max(most, b);
-            TRY(gemm_workspace_size(in_type, c_type, GEMM_COL_MAJOR, GEMM_ROW_MAJOR, N, K, M, 1.0f, at, N, at, K, 0.0f, at, K, nullptr, &b, nullptr));
+            if (linear_grad_fits(p, SIZE_MAX / 2)) {
+                b = linear_grad_workspace(p);
+            } else {
+                const void* at = reinterpret_cast<const void*>(uintptr_t(1) << 20);
+                TRY(gemm_workspace_size(in_type, GEMM_F32, dw ? GEMM_COL_MAJOR : GEMM_ROW_MAJOR, GEMM_ROW_MAJOR, p.M, p.N, p.K, 1.0f, at, N, at,
+                                        K, 0.0f, at, K, nullptr, &b, nullptr));
+            }
             most = std::max(most, b);
         }
     *bytes = (size_t)sums + most;

@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "linear.hpp"
+#include "linear_plan.hpp"
 #include "rows_pack.hpp"
 #include "short_loader.hpp"
 
@@ -202,27 +203,11 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const LinearEpi e, con
     finish8<T, OUT>(e, m, n, 0, v, bias, old);
 }
 
-constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-struct LinearPlan {
-    int bm, bn;    // rows and columns of a tile: 256 x 256, 192 x 256, 128 x 128 or 64 x 128
-    int splits;
-};
-
-// The tile with the least time on the fullest compute unit: a tile's elements, times kSmallCost where it is a small one.  Where small
-// tiles do not fill the card: the height and the splits of K that should be fastest.  A slab takes slab_us() on a
-// compute unit that has nothing else to hide its loads with; more workgroups than units share them at kShared; a split writes
-// and reads its fp32 sums once (at the rate of a copy) and needs one more launch.
-constexpr double kSmallCost = 1.35, kShared = 0.75, kJoinUs = 4.0, kBytesPerUs = 4.5e6;
-double slab_us(int bm) { return bm == 64 ? 0.35 : 0.5; }
 double staged_us(int bm) { return bm == 64 ? 0.4 : 0.5; }   // longer from rows of any alignment
-double rounds_of(int64_t workgroups) {
-    const int64_t cu = num_compute_units();
-    return workgroups <= cu ? 1.0 : kShared * ceil_div(workgroups, cu);
-}
 int64_t ldp_of(int64_t N) { return (N + 7) / 8 * 8; }
-LinearPlan plan_of(int64_t M, int64_t N, int64_t K, bool large) {
-    LinearPlan q = {128, 128, 1};
+// 256 x 256, 192 x 256, 128 x 128 or 64 x 128.
+TilePlan plan_of(int64_t M, int64_t N, int64_t K, bool large) {
+    TilePlan q = {128, 128, 1};
     const int64_t cu = num_compute_units();
     const int64_t t128 = ceil_div(M, 128) * ceil_div(N, 128);
     if (large && N >= 256) {
@@ -231,32 +216,18 @@ LinearPlan plan_of(int64_t M, int64_t N, int64_t K, bool large) {
             const double cost = ceil_div(ceil_div(M, bm) * ceil_div(N, 256), cu) * bm * 256.0;
             if (M >= bm && cost <= best * (q.bm == 128 ? 1.0 : 0.97)) {
                 best = cost;
-                q = LinearPlan{bm, 256, 1};
+                q = TilePlan{bm, 256, 1};
             }
         }
         if (q.bm != 128) return q;
     }
     if (t128 > cu && M > kShortRows) return q;
-    const int64_t slabs = ceil_div(K, kSlab);
-    double best = 0.0;
-    for (int bm = 128; bm >= 64; bm -= 64) {
-        const int64_t tiles = ceil_div(M, bm) * ceil_div(N, 128);
-        for (int64_t s = 1; s <= 16 && s * 4 <= slabs + 3; ++s) {
-            const double us = rounds_of(tiles * s) * ceil_div(slabs, s) * slab_us(bm) +
-                              (s > 1 ? kJoinUs + s * (double)M * ldp_of(N) * 8.0 / kBytesPerUs : 0.0);
-            if (best == 0.0 || us < best) {
-                best = us;
-                q.bm = bm;
-                q.splits = (int)s;
-            }
-        }
-    }
-    return q;
+    return small_plan(M, N, ceil_div(K, kSlab), 128, 64, 16, ldp_of(N));
 }
 
 // What a call does with the workspace it has.
 struct LinearLaunch {
-    LinearPlan q;
+    TilePlan q;
     int per_split;       // slabs of a split
     int64_t each;        // bytes of a split's sums
     RowsJob ja, jw;      // copies of the operands, behind the splits' sums ...
@@ -270,7 +241,7 @@ LinearLaunch launch_of(const LinearParams& f, size_t ws_bytes) {
     const int64_t slabs = ceil_div(f.K, kSlab), kp = slabs * kSlabBytes;
     auto with = [&](bool large) {
         LinearLaunch l;
-        LinearPlan& q = l.q;
+        TilePlan& q = l.q;
         q = plan_of(f.M, f.N, f.K, large);
         l.each = (int64_t)f.M * ldp_of(f.N) * (int64_t)sizeof(float);
         if (q.splits > 1 && ws_bytes < (size_t)(q.splits * l.each)) q.splits = (int)(ws_bytes / l.each);
@@ -305,7 +276,7 @@ hipError_t go(const GemmParams& p, const LinearEpi& e, const LinearSplit& x, int
 // Small tiles that have a compute unit to themselves: eight waves, so that two on a SIMD take turns, and four slots, so that
 // three slabs are on their way.  Else a second workgroup, which two slots leave room for, does both.
 template <int T, int OUT>
-hipError_t tile_of(const LinearPlan& q, bool direct, const GemmParams& p, const LinearEpi& e, const LinearSplit& x, hipStream_t st) {
+hipError_t tile_of(const TilePlan& q, bool direct, const GemmParams& p, const LinearEpi& e, const LinearSplit& x, hipStream_t st) {
     if (q.bm == 256) return go<T, OUT, 256, 256, 2, 4, 2>(p, e, x, q.splits, st);
     if (q.bm == 192) return go<T, OUT, 192, 256, 2, 4, 2>(p, e, x, q.splits, st);
     const bool alone = (int64_t)p.tiles_m * p.tiles_n * q.splits <= num_compute_units();
@@ -333,7 +304,7 @@ size_t linear_tile_workspace(const LinearParams& f) {
 hipError_t launch_linear_tile(int in_type, const LinearParams& f, void* ws, size_t ws_bytes, hipStream_t st) {
     if (!ws) ws_bytes = 0;
     const LinearLaunch l = launch_of(f, ws_bytes);
-    const LinearPlan& q = l.q;
+    const TilePlan& q = l.q;
     op_note("  %d x %d tiles, %d splits of K, %s loads%s", q.bm, q.bn, q.splits, l.direct ? "direct" : "staged", l.copies ? " of copied rows" : "");
     GemmParams p = {};
     p.A = f.A;

@@ -142,6 +142,20 @@ struct LinearBwdParams {
 int linear_bwd_parts(int64_t M, int64_t N);   // parts that the pass would like
 hipError_t launch_linear_bwd(int in_type, const LinearBwdParams& p, hipStream_t st);
 
+// C = A B, the products of that backward pass: B is K x N row by row; A is M x K row by row, or (rows_a) K x M row by row.
+struct GradParams {
+    const char* A;
+    const char* B;
+    char* C;
+    int64_t lda, ldb, ldc;   // elements
+    int M, N, K;
+    bool rows_a;
+    int out_type;
+};
+bool linear_grad_fits(const GradParams& p, size_t ws_bytes);
+size_t linear_grad_workspace(const GradParams& p);
+hipError_t launch_linear_grad(int in_type, const GradParams& p, void* ws, size_t ws_bytes, hipStream_t st);
+
 // ---------------------------------------------------------------- norm and rotation of heads
 struct HeadsTensor {
     const char* p;
