@@ -116,11 +116,13 @@ template <int T>
 struct Eight {
     static constexpr int Q = T == DT_F32 ? 2 : 1;
     u32x4 raw[Q];
-    __device__ __forceinline__ void load(const char* row, int n, int lo, int N) {
-        constexpr int SZ = Elem<T>::SIZE;
-        if (n >= lo && n + 8 <= N) {
+    __device__ __forceinline__ void whole(const char* row, int n) {
 #pragma unroll
-            for (int q = 0; q < Q; ++q) raw[q] = load16(row + (int64_t)n * SZ + 16 * q);
+        for (int q = 0; q < Q; ++q) raw[q] = load16(row + (int64_t)n * Elem<T>::SIZE + 16 * q);
+    }
+    __device__ __forceinline__ void load(const char* row, int n, int lo, int N) {
+        if (n >= lo && n + 8 <= N) {
+            whole(row, n);
             return;
         }
 #pragma unroll
