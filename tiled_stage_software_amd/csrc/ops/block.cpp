@@ -25,15 +25,65 @@ gemm_status_t check_linear(int in_type, int act, int64_t M, int64_t N, int64_t K
 // Whether the kernel for few rows takes a product.
 bool linear_few(const LinearParams& p) { return p.M <= kLinearSkinnyRows && p.K > 0; }
 
-// One of the backward pass's products (rows_a: A is K x M in memory): on tiles, or, where those do not take it, through the
-// library's own 16-bit entry points.
-gemm_status_t product(int in_type, bool rows_a, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
-                      int64_t ldb, void* C, int c_type, int64_t ldc, void* ws, size_t bytes, hipStream_t st) {
-    const GradParams p = {static_cast<const char*>(A), static_cast<const char*>(B), static_cast<char*>(C), lda, ldb, ldc, (int)M, (int)N,
-                          (int)K, rows_a, c_type};
-    if (M > 0 && N > 0 && linear_grad_fits(p, bytes)) return launched(launch_linear_grad(in_type, p, ws, bytes, st));
-    return (in_type == GEMM_BF16 ? gemm_bf16_ws : gemm_f16_ws)(rows_a ? GEMM_COL_MAJOR : GEMM_ROW_MAJOR, GEMM_ROW_MAJOR, M, N, K, 1.0f, A,
-                                                               lda, B, ldb, 0.0f, C, (gemm_dtype_t)c_type, ldc, st, nullptr, ws, bytes);
+// One of the backward pass's products (rows_a: A is K x M in memory), where the tiles do not take it: through the library's own
+// 16-bit entry points.
+gemm_status_t product(int in_type, const GradParams& p, void* ws, size_t bytes, hipStream_t st) {
+    return (in_type == GEMM_BF16 ? gemm_bf16_ws : gemm_f16_ws)(p.rows_a ? GEMM_COL_MAJOR : GEMM_ROW_MAJOR, GEMM_ROW_MAJOR, p.M, p.N, p.K, 1.0f,
+                                                               p.A, p.lda, p.B, p.ldb, 0.0f, p.C, (gemm_dtype_t)p.out_type, p.ldc, st, nullptr,
+                                                               bytes ? ws : nullptr, bytes);
+}
+
+bool aligned_rows(const void* at, int64_t ld, int64_t len) { return (uintptr_t)at % 16 == 0 && ld % 8 == 0 && len % 8 == 0; }
+RowsJob rows_job(const void* src, int64_t ld, int64_t rows, int64_t len) {
+    return RowsJob{static_cast<const uint8_t*>(src), nullptr, ld * 2, rows, len * 2, rows, (len + 7) / 8 * 16};
+}
+
+// What a backward pass makes of its workspace: partial sums of db; aligned copies of dZ, A and W; the products' splits.
+struct BackwardPlan {
+    GradParams f[2];     // dA, dW
+    RowsJob copies[3];   // of dZ, A, W; no source: none
+    int parts;           // of db
+    size_t sums, bytes;  // db's, all
+    bool tiles;          // the products run on tiles; else one after the other through the 16-bit entry points
+};
+BackwardPlan backward_plan(int64_t M, int64_t N, int64_t K, const void* dz, int64_t lddz, const void* A, int64_t lda, const void* W, int64_t ldw,
+                           void* dA, int64_t ldda, int in_type, void* dW, int64_t lddw, int dw_type, bool db, size_t ws) {
+    BackwardPlan b = {};
+    auto text = [](const void* p) { return static_cast<const char*>(p); };
+    b.f[0] = GradParams{text(dz), text(W), static_cast<char*>(dA), lddz, ldw, ldda, (int)M, (int)K, (int)N, false, in_type, 0, 0, 0, 1};
+    b.f[1] = GradParams{text(dz), text(A), static_cast<char*>(dW), lddz, lda, lddw, (int)N, (int)K, (int)M, true, dw_type, 0, 0, 0, 1};
+    b.parts = linear_bwd_parts(M, N);
+    if (db) {   // (partial sums are needed for db alone)
+        b.parts = (int)std::max<int64_t>(1, std::min<int64_t>(b.parts, (int64_t)(ws / ((size_t)std::max<int64_t>(N, 1) * sizeof(float)))));
+        if (b.parts > 1) b.sums = std::min(ws, (size_t)round256((int64_t)b.parts * N * (int64_t)sizeof(float)));
+    }
+    b.bytes = b.sums;
+    if (M == 0 || N == 0 || K == 0 || (!dA && !dW)) return b;
+    // tiles take aligned rows: copies of the others, where there is room for them
+    const bool copy[3] = {!aligned_rows(dz, lddz, N), dW && !aligned_rows(A, lda, K), dA && !aligned_rows(W, ldw, K)};
+    const RowsJob jobs[3] = {rows_job(dz, lddz, M, N), rows_job(A, lda, M, K), rows_job(W, ldw, N, K)};
+    size_t at = b.sums, of_copies = 0;
+    b.tiles = true;
+    for (int i = 0; i < 3; ++i)
+        if (copy[i]) of_copies += (size_t)round256(jobs[i].bytes());
+    if (at + of_copies > ws || of_copies >= (size_t(1) << 34)) b.tiles = of_copies == 0;
+    GradParams aligned[2] = {b.f[0], b.f[1]};
+    if (copy[0]) aligned[0].lda = aligned[1].lda = jobs[0].len_pad / 2;
+    if (copy[1]) aligned[1].ldb = jobs[1].len_pad / 2;
+    if (copy[2]) aligned[0].ldb = jobs[2].len_pad / 2;
+    for (const GradParams& p : aligned)
+        if (p.C && !linear_grad_fits(p)) b.tiles = false;
+    if (!b.tiles) return b;
+    for (int i = 0; i < 3; ++i)
+        if (copy[i]) {
+            b.copies[i] = jobs[i];
+            at += (size_t)round256(jobs[i].bytes());
+        }
+    b.f[0] = aligned[0];
+    b.f[1] = aligned[1];
+    linear_grad_plan(b.f, ws - at);
+    b.bytes = at + b.f[0].ws + b.f[1].ws;
+    return b;
 }
 
 gemm_status_t check_heads(const char* what, const gemm_heads_t* h, int64_t tokens, int64_t heads, int64_t dim, HeadsTensor* to) {
@@ -174,37 +224,45 @@ gemm_status_t gemm_linear_bwd(gemm_dtype_t in_type, int64_t M, int64_t N, int64_
     }
     if (!workspace) workspace_bytes = 0;
     op_note("linear_bwd type %d M=%lld N=%lld K=%lld act=%d", (int)in_type, (long long)M, (long long)N, (long long)K, (int)act);
-    char* rest = static_cast<char*>(workspace);
-    size_t left = workspace_bytes;
-    if (N > 0 && (dbias || (some && dZ))) {
-        LinearBwdParams p;
-        p.dC = static_cast<const char*>(dC);
-        p.Z = static_cast<const char*>(Z);
-        p.dZ = some ? static_cast<char*>(dZ) : nullptr;
-        p.db = dbias;
-        p.lddc = lddc; p.ldz = ldz; p.lddz = lddz;
-        p.M = M;
-        p.N = (int)N;
-        p.act = act;
-        p.dc_type = dc_type;
-        p.part = reinterpret_cast<float*>(workspace);
-        p.parts = linear_bwd_parts(M, N);
-        if (dbias) {   // (partial sums are needed for db alone)
-            p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(p.parts, (int64_t)(left / ((size_t)N * sizeof(float)))));
-            if (p.parts > 1) {
-                const size_t used = std::min(left, (size_t)round256((int64_t)p.parts * N * (int64_t)sizeof(float)));
-                rest += used;
-                left -= used;
-            }
-        }
-        TRY(launched(launch_linear_bwd(in_type, p, stream)));
-    }
-    if (!dA && !dW) return GEMM_OK;
+    if (N == 0 && (!dA || M == 0)) return GEMM_OK;
     const void* dz = dZ ? dZ : dC;
-    const int64_t ld = dZ ? lddz : lddc;
-    if (!left) rest = nullptr;
-    if (dA) TRY(product(in_type, false, M, K, N, dz, ld, W, ldw, dA, in_type, ldda, rest, left, stream));
-    if (dW) TRY(product(in_type, true, N, K, M, dz, ld, A, lda, dW, dw_type, lddw, rest, left, stream));
+    BackwardPlan b = backward_plan(M, N, K, dz, dZ ? lddz : lddc, A, lda, W, ldw, dA, ldda, in_type, dW, lddw, dw_type, dbias != nullptr, workspace_bytes);
+    char* at = static_cast<char*>(workspace) + b.sums;
+    for (RowsJob& j : b.copies)
+        if (j.src) {
+            j.dst = reinterpret_cast<uint8_t*>(at);
+            at += round256(j.bytes());
+        }
+    LinearBwdParams p = {};
+    p.dC = static_cast<const char*>(dC);
+    p.Z = static_cast<const char*>(Z);
+    p.dZ = some ? static_cast<char*>(dZ) : nullptr;
+    p.db = dbias;
+    p.lddc = lddc; p.ldz = ldz; p.lddz = lddz;
+    p.M = M;
+    p.N = (int)N;
+    p.act = act;
+    p.dc_type = dc_type;
+    p.part = static_cast<float*>(workspace);
+    p.parts = b.parts;
+    p.copy = reinterpret_cast<char*>(b.copies[0].dst);
+    p.ldcopy = b.copies[0].len_pad / 2;
+    p.jobs[0] = b.copies[1];
+    p.jobs[1] = b.copies[2];
+    if (N > 0 && (dbias || p.dZ || p.copy)) TRY(launched(launch_linear_bwd(in_type, p, stream)));
+    else if (p.jobs[0].src || p.jobs[1].src) TRY(launched(launch_rows_pack(p.jobs[0], p.jobs[1], stream)));
+    const DbJoin join = {p.part, dbias && b.parts > 1 ? dbias : nullptr, (int)N, b.parts};
+    if (b.tiles) {
+        auto copied = [](const RowsJob& j, const char* own) { return j.src ? reinterpret_cast<const char*>(j.dst) : own; };
+        b.f[0].A = b.f[1].A = copied(b.copies[0], b.f[0].A);
+        b.f[1].B = copied(b.copies[1], b.f[1].B);
+        b.f[0].B = copied(b.copies[2], b.f[0].B);
+        return launched(launch_linear_grad(in_type, b.f, join, at, stream));
+    }
+    const GradParams none[2] = {};
+    TRY(launched(launch_linear_grad(in_type, none, join, nullptr, stream)));
+    for (const GradParams& f : b.f)
+        if (f.C) TRY(product(in_type, f, static_cast<char*>(workspace) + b.sums, workspace_bytes - b.sums, stream));
     return GEMM_OK;
 }
 
@@ -214,28 +272,17 @@ gemm_status_t gemm_linear_bwd_workspace_size(gemm_dtype_t in_type, int64_t M, in
     *bytes = 0;
     TRY(check_linear(in_type, GEMM_ACT_NONE, M, N, K));
     if (M == 0 || N == 0) return GEMM_OK;
-    const int parts = linear_bwd_parts(M, N);
-    const int64_t sums = parts > 1 ? round256((int64_t)parts * N * (int64_t)sizeof(float)) : 0;
-    size_t most = 0;
-    if (K > 0)
-        for (const bool dw : {false, true}) {
-            GradParams p = {};
-            p.M = (int)(dw ? N : M);
-            p.N = (int)K;
-            p.K = (int)(dw ? M : N);
-            p.lda = N; p.ldb = K; p.ldc = K;   // (of contiguous operands)
-            p.rows_a = dw;
-            size_t b = 0;
-            if (linear_grad_fits(p, SIZE_MAX / 2)) {
-                b = linear_grad_workspace(p);
-            } else {
-                const void* at = reinterpret_cast<const void*>(uintptr_t(1) << 20);
-                TRY(gemm_workspace_size(in_type, GEMM_F32, dw ? GEMM_COL_MAJOR : GEMM_ROW_MAJOR, GEMM_ROW_MAJOR, p.M, p.N, p.K, 1.0f, at, N, at,
-                                        K, 0.0f, at, K, nullptr, &b, nullptr));
-            }
-            most = std::max(most, b);
+    // (contiguous aligned operands, wherever they are, and the larger of dW's types)
+    void* at = reinterpret_cast<void*>(uintptr_t(1) << 20);
+    const BackwardPlan b = backward_plan(M, N, K, at, N, at, K, at, K, at, K, in_type, at, K, GEMM_F32, true, SIZE_MAX / 2);
+    *bytes = b.bytes;
+    if (K > 0 && !b.tiles)
+        for (const GradParams& f : b.f) {
+            size_t more = 0;
+            TRY(gemm_workspace_size(in_type, (gemm_dtype_t)f.out_type, f.rows_a ? GEMM_COL_MAJOR : GEMM_ROW_MAJOR, GEMM_ROW_MAJOR, f.M, f.N, f.K,
+                                    1.0f, f.A, f.lda, f.B, f.ldb, 0.0f, f.C, f.ldc, nullptr, &more, nullptr));
+            *bytes = std::max(*bytes, b.sums + more);
         }
-    *bytes = (size_t)sums + most;
     return GEMM_OK;
 }
 

@@ -14,7 +14,6 @@
 
 #include "linear.hpp"
 #include "linear_plan.hpp"
-#include "rows_pack.hpp"
 
 namespace gemm {
 namespace {
@@ -195,45 +194,53 @@ struct GradOps : MfmaCompute<T, BM, BN, 64, WM, WN, 16> {
     }
 };
 
-struct GradSplit {
+struct GradSide {     // one product
+    GemmParams p;
     int per;           // slabs of K per split
     int64_t each;      // bytes between the splits' sums (in C's place)
+    int a_cols, b_cols, splits;
+    uint32_t blocks;
 };
 
-// Splits of K (blockIdx.y) store plain sums, each into its own place; the last one has what is left behind whole slabs.
+// Workgroup wg of a product.  Splits of K store plain sums, each into its own place; the last one has what is left behind whole
+// slabs.  OUT: C's type (-1: as p.out_type says, T or fp32).
 template <int T, int OUT, bool ROWS_A, int BM, int BN, int WM, int WN, int S>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)))
-void linear_grad_kernel(GemmParams p, const GradSplit x, int a_cols, int b_cols) {
+__device__ __forceinline__ void grad_tile(const GradSide& x, uint32_t wg, LDS_AS char* smem) {
     typedef half_of<T> H;
-    constexpr int NW = WM * WN, NC = NW < 4 ? NW : 4, STAGE = (BM + BN) * 128;
-    constexpr int EPI = (OUT != DT_F32 && BN == 256) ? BM * BN * 2 : 0;
-    __shared__ __attribute__((aligned(1024))) char smem_raw[S * STAGE > EPI ? S * STAGE : EPI];
-    LDS_AS char* smem = (LDS_AS char*)smem_raw;
+    constexpr int NW = WM * WN, NC = NW < 4 ? NW : 4;
+    GemmParams p = x.p;
+    const int tiles = p.tiles_m * p.tiles_n, split = (int)(wg / (uint32_t)tiles);
     int tm, tn;
-    tile_coords(p, tm, tn);
+    tile_coords_of(p, (int)(wg - (uint32_t)split * (uint32_t)tiles), tm, tn);
     const int m_keep = tm * BM, n_keep = tn * BN;
     // edge tiles shifted inward; where there are fewer rows or columns than a tile has, the operands repeat their last
-    const int m0 = max(0, min(m_keep, (ROWS_A ? a_cols : p.M) - BM)), n0 = max(0, min(n_keep, b_cols - BN));
-    const int s0 = (int)blockIdx.y * x.per, whole = p.K / 64;
-    const bool last = blockIdx.y + 1 == gridDim.y;
+    const int a_end = ROWS_A ? x.a_cols : p.M;
+    const int m0 = max(0, min(m_keep, a_end - BM)), n0 = max(0, min(n_keep, x.b_cols - BN));
+    const int s0 = split * x.per, whole = p.K / 64;
+    const bool last = split + 1 == x.splits;
     const int slabs = last ? whole - s0 : x.per, left = last ? p.K % 64 : 0;
     const char* A = p.A + (ROWS_A ? ((int64_t)s0 * 64 * p.lda + m0) * 2 : ((int64_t)m0 * p.lda + (int64_t)s0 * 64) * 2);
     const char* B = p.B + ((int64_t)s0 * 64 * p.ldb + n0) * 2;
-    p.C += blockIdx.y * x.each;
+    p.C += split * x.each;
     auto run = [&](auto& ops) {
         ops.init(smem);
-        ops.la.init(A, p.lda * 2, (ROWS_A ? a_cols : p.M) - m0);
-        ops.lb.init(B, p.ldb * 2, b_cols - n0);
+        ops.la.init(A, p.lda * 2, a_end - m0);
+        ops.lb.init(B, p.ldb * 2, x.b_cols - n0);
         gemm_sched::ring_mainloop<S, 2, 1>(ops, slabs);
         if (left > 0) ops.tail(slabs, left);
-        if constexpr (EPI > 0) {
+        if constexpr (OUT == T && BN == 256) {
             if (m0 == m_keep && n0 == n_keep && m0 + BM <= p.M && n0 + BN <= p.N && (reinterpret_cast<uintptr_t>(p.C) & 15) == 0 &&
                 (p.ldc * 2) % 16 == 0) {
                 ops.template epilogue_lds<OUT, 64 * NW>(p, m0, n0);
                 return;
             }
         }
-        ops.template epilogue<OUT>(p, m0, n0, m_keep, n_keep);
+        if constexpr (OUT >= 0) {
+            ops.template epilogue<OUT>(p, m0, n0, m_keep, n_keep);
+        } else {
+            if (p.out_type == DT_F32) ops.template epilogue<DT_F32>(p, m0, n0, m_keep, n_keep);
+            else ops.template epilogue<T>(p, m0, n0, m_keep, n_keep);
+        }
     };
     if (NC == NW || wave_id() < NC) {
         GradOps<H, ROWS_A, BM, BN, WM, WN, NC, true> ops;
@@ -243,143 +250,205 @@ void linear_grad_kernel(GemmParams p, const GradSplit x, int a_cols, int b_cols)
         run(ops);
     }
 }
-
-// C = the splits' sums, added in order.
-template <int OUT>
-__global__ __launch_bounds__(256) void linear_grad_join_kernel(const GemmParams p, const char* part, int64_t each, int ldp, int splits) {
-    const int64_t quads = ldp / 4, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= quads * p.M) return;
-    const int64_t m = id / quads;
-    const int n = (int)(id % quads) * 4;
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int i = 0; i < splits; ++i) s += *reinterpret_cast<const f32x4*>(part + i * each + (m * ldp + n) * 4);
-    store4<OUT>(p, m, n, s);
-}
-
-// 256 x 256, or 128 x 128 and (A along the sum) 64 x 128 with splits.
-TilePlan grad_plan(int64_t M, int64_t N, int64_t K, int least) {
-    const int64_t cu = num_compute_units();
-    const int64_t t128 = ceil_div(M, 128) * ceil_div(N, 128), t256 = ceil_div(M, 256) * ceil_div(N, 256);
-    if (M >= 256 && N >= 256 && ceil_div(t256, cu) * 4.0 <= ceil_div(t128, cu) * kSmallCost) return TilePlan{256, 256, 1};
-    if (t128 > cu && M >= 128) return TilePlan{128, 128, 1};
-    return small_plan(M, N, std::max<int64_t>(1, K / 64), M >= 128 || least == 128 ? 128 : 64, least, 64, (N + 7) / 8 * 8);
-}
-
-struct GradLaunch {
-    TilePlan q;
-    int per_split;
-    int64_t each, ldp;
-    RowsJob ja, jb;        // copies of what is not aligned, behind the splits' sums
-    bool copy_a, copy_b;
-    size_t used, wants;
-};
-GradLaunch launch_of(const GradParams& f, size_t ws_bytes) {
-    GradLaunch l;
-    l.q = grad_plan(f.M, f.N, f.K, f.rows_a ? 128 : 64);
-    const int64_t slabs = std::max<int64_t>(1, f.K / 64);
-    l.ldp = (f.N + 7) / 8 * 8;
-    l.each = (int64_t)f.M * l.ldp * (int64_t)sizeof(float);
-    // (an operand of the sum's length, or of the rows' or columns' that the tiles take eight at a time)
-    const int64_t a_rows = f.rows_a ? f.K : f.M, a_len = f.rows_a ? f.M : f.K;
-    l.copy_a = a_len % 8 || f.lda % 8 || (uintptr_t)f.A % 16;
-    l.copy_b = f.N % 8 || f.ldb % 8 || (uintptr_t)f.B % 16;
-    l.ja = {reinterpret_cast<const uint8_t*>(f.A), nullptr, f.lda * 2, a_rows, a_len * 2, a_rows, (a_len + 7) / 8 * 16};
-    l.jb = {reinterpret_cast<const uint8_t*>(f.B), nullptr, f.ldb * 2, f.K, (int64_t)f.N * 2, f.K, ((int64_t)f.N + 7) / 8 * 16};
-    const size_t copies = ((l.copy_a ? l.ja.bytes() : 0) + (l.copy_b ? l.jb.bytes() : 0) + 255) & ~size_t(255);
-    const size_t room = ws_bytes > copies ? ws_bytes - copies : 0;
-    if (l.q.splits > 1 && room < (size_t)(l.q.splits * l.each)) l.q.splits = (int)(room / l.each);
-    if (l.q.splits < 2) l.q.splits = 1;
-    l.per_split = (int)ceil_div(slabs, l.q.splits);
-    l.q.splits = (int)ceil_div(slabs, l.per_split);
-    l.used = copies;
-    l.wants = copies + (l.q.splits > 1 ? (size_t)(l.q.splits * l.each) : 0);
-    return l;
-}
-
 template <int T, int OUT, bool ROWS_A, int BM, int BN, int WM, int WN, int S>
-hipError_t go(const GemmParams& p, const GradSplit& x, int splits, int a_cols, int b_cols, hipStream_t st) {
-    hipLaunchKernelGGL((linear_grad_kernel<T, OUT, ROWS_A, BM, BN, WM, WN, S>), dim3((unsigned)(p.tiles_m * p.tiles_n), (unsigned)splits),
-                       dim3(64 * WM * WN), 0, st, p, x, a_cols, b_cols);
-    return hipGetLastError();
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)))
+void linear_grad_kernel(const GradSide x) {
+    constexpr int RING = S * (BM + BN) * 128, EPI = (OUT == T && BN == 256) ? BM * BN * 2 : 0;
+    __shared__ __attribute__((aligned(1024))) char smem_raw[RING > EPI ? RING : EPI];
+    grad_tile<T, OUT, ROWS_A, BM, BN, WM, WN, S>(x, blockIdx.x, (LDS_AS char*)smem_raw);
 }
-template <int T, int OUT, bool ROWS_A>
-hipError_t tile_of(const TilePlan& q, const GemmParams& p, const GradSplit& x, int a_cols, int b_cols, hipStream_t st) {
-    if (q.bm == 256) return go<T, OUT, ROWS_A, 256, 256, 2, 4, 2>(p, x, q.splits, a_cols, b_cols, st);
-    const bool alone = (int64_t)p.tiles_m * p.tiles_n * q.splits <= num_compute_units();
-    if constexpr (!ROWS_A) {
-        if (q.bm == 64)
-            return alone ? go<T, OUT, ROWS_A, 64, 128, 2, 4, 4>(p, x, q.splits, a_cols, b_cols, st)
-                         : go<T, OUT, ROWS_A, 64, 128, 2, 4, 2>(p, x, q.splits, a_cols, b_cols, st);
+// Both products in one launch, where together they leave compute units empty.
+template <int T, int BM>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2)))
+void linear_grads_kernel(const GradSide a, const GradSide w) {
+    __shared__ __attribute__((aligned(1024))) char smem_raw[4 * 256 * 128];
+    LDS_AS char* smem = (LDS_AS char*)smem_raw;
+    if (blockIdx.x < a.blocks) grad_tile<T, -1, false, BM, 128, 2, 4, 4>(a, blockIdx.x, smem);
+    else grad_tile<T, -1, true, 128, 128, 2, 4, 4>(w, blockIdx.x - a.blocks, smem);
+}
+
+// The last launch: C = the splits' sums, added in order, of either product, and db = its parts' (64 columns a workgroup, every
+// fourth part a wave).
+struct JoinSide {
+    GemmParams p;
+    const char* part;
+    int64_t each;
+    int ldp, splits;
+    uint32_t blocks;
+};
+__global__ __launch_bounds__(256) void linear_grad_join_kernel(const JoinSide a, const JoinSide w, const DbJoin d) {
+    uint32_t block = blockIdx.x;
+    if (block < a.blocks + w.blocks) {
+        const bool second = block >= a.blocks;
+        if (second) block -= a.blocks;
+        const JoinSide& x = second ? w : a;
+        const int64_t quads = x.ldp / 4, id = (int64_t)block * 256 + threadIdx.x;
+        if (id >= quads * x.p.M) return;
+        const int64_t m = id / quads;
+        const int n = (int)(id % quads) * 4;
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int i = 0; i < x.splits; ++i) s += *reinterpret_cast<const f32x4*>(x.part + i * x.each + (m * x.ldp + n) * 4);
+        if (x.p.out_type == DT_F32) store4<DT_F32>(x.p, m, n, s);
+        else if (x.p.out_type == DT_BF16) store4<DT_BF16>(x.p, m, n, s);
+        else store4<DT_F16>(x.p, m, n, s);
+        return;
     }
-    return alone ? go<T, OUT, ROWS_A, 128, 128, 2, 4, 4>(p, x, q.splits, a_cols, b_cols, st)
-                 : go<T, OUT, ROWS_A, 128, 128, 2, 2, 2>(p, x, q.splits, a_cols, b_cols, st);
+    block -= a.blocks + w.blocks;
+    __shared__ float sums[4][64];
+    const int64_t n = (int64_t)block * 64 + lane_id();
+    const int wave = wave_id();
+    float s = 0.0f;
+    if (n < d.N) {
+#pragma unroll 8
+        for (int i = wave; i < d.parts; i += 4) s += d.part[(int64_t)i * d.N + n];
+    }
+    sums[wave][lane_id()] = s;
+    __syncthreads();
+    if (wave == 0 && n < d.N) d.db[n] = sums[0][lane_id()] + sums[1][lane_id()] + sums[2][lane_id()] + sums[3][lane_id()];
+}
+
+int64_t slabs_of(const GradParams& f) { return std::max<int64_t>(1, f.K / 64); }
+int64_t ldp_of(const GradParams& f) { return ((int64_t)f.N + 7) / 8 * 8; }
+int64_t each_of(const GradParams& f) { return (int64_t)f.M * ldp_of(f) * (int64_t)sizeof(float); }
+int64_t tiles_of(const GradParams& f, int bm, int bn) { return ceil_div(f.M, bm) * ceil_div(f.N, bn); }
+size_t sums_of(const GradParams& f, int64_t splits) { return splits > 1 ? (size_t)(splits * each_of(f) + 255) & ~size_t(255) : 0; }
+
+// Large tiles, or small ones that fill the card by themselves.
+bool large(GradParams& f) {
+    const int64_t cu = num_compute_units(), t128 = tiles_of(f, 128, 128), t256 = tiles_of(f, 256, 256);
+    f.splits = 1;
+    if (f.M >= 256 && f.N >= 256 && ceil_div(t256, cu) * 4.0 <= ceil_div(t128, cu) * kSmallCost) f.bm = f.bn = 256;
+    else if (t128 > cu && (f.M >= 128 || f.rows_a)) f.bm = f.bn = 128;
+    else return false;
+    return true;
+}
+
+template <int T, bool ROWS_A>
+hipError_t alone_of(const GradParams& f, const GradSide& x, hipStream_t st) {
+    auto go = [&](auto kernel, int threads) {
+        hipLaunchKernelGGL(kernel, dim3(x.blocks), dim3(threads), 0, st, x);
+        return hipGetLastError();
+    };
+    if (f.bm == 256)
+        return x.p.out_type == DT_F32 ? go(linear_grad_kernel<T, DT_F32, ROWS_A, 256, 256, 2, 4, 2>, 512)
+                                      : go(linear_grad_kernel<T, T, ROWS_A, 256, 256, 2, 4, 2>, 512);
+    const bool alone = x.blocks <= (uint32_t)num_compute_units();
+    if constexpr (!ROWS_A) {
+        if (f.bm == 64) return alone ? go(linear_grad_kernel<T, -1, ROWS_A, 64, 128, 2, 4, 4>, 512) : go(linear_grad_kernel<T, -1, ROWS_A, 64, 128, 2, 4, 2>, 512);
+    }
+    return alone ? go(linear_grad_kernel<T, -1, ROWS_A, 128, 128, 2, 4, 4>, 512) : go(linear_grad_kernel<T, -1, ROWS_A, 128, 128, 2, 2, 2>, 256);
 }
 
 }  // namespace
 
-// Strides whose offsets 32 bits hold, and room for copies of what is not aligned.
-bool linear_grad_fits(const GradParams& f, size_t ws_bytes) {
+// Aligned operands whose strides' offsets 32 bits hold (the caller copies others).
+bool linear_grad_fits(const GradParams& f) {
     const int64_t most = int64_t(1) << 21;
-    if (f.K < 1 || f.lda > most || f.ldb > most || f.K > most * 64 || (!f.rows_a && f.K > most)) return false;
-    if (ceil_div(f.M, 64) * ceil_div(f.N, 128) >= (int64_t(1) << 22)) return false;
-    const GradLaunch l = launch_of(f, ws_bytes);
-    return l.used <= ws_bytes && l.used < (size_t(1) << 34) && (!l.copy_a || l.ja.len_pad / 2 <= most) && (!l.copy_b || l.jb.len_pad / 2 <= most);
+    const int along = f.rows_a ? f.M : f.K;
+    return f.K >= 1 && f.lda <= most && f.ldb <= most && f.K <= most * 64 && tiles_of(f, 64, 128) < (int64_t(1) << 22) && along <= most;
 }
-size_t linear_grad_workspace(const GradParams& f) { return launch_of(f, SIZE_MAX / 2).wants; }
 
-hipError_t launch_linear_grad(int in_type, const GradParams& f, void* ws, size_t ws_bytes, hipStream_t st) {
-    const GradLaunch l = launch_of(f, ws_bytes);
-    const TilePlan& q = l.q;
-    op_note("  %d x %d x %d: %d x %d tiles, %d splits of the sum%s", f.M, f.N, f.K, q.bm, q.bn, q.splits, l.copy_a || l.copy_b ? ", of copied rows" : "");
-    GemmParams p = {};
-    p.A = f.A;
-    p.B = f.B;
-    p.C = f.C;
-    p.lda = f.lda; p.ldb = f.ldb; p.ldc = f.ldc;
-    p.M = f.M; p.N = f.N; p.K = f.K;
-    p.alpha = 1.0f;
-    p.tiles_m = (int)ceil_div(f.M, q.bm);
-    p.tiles_n = (int)ceil_div(f.N, q.bn);
-    p.group_m = 8;
-    p.xcd_remap = 1;
-    if (l.copy_a || l.copy_b) {
-        uint8_t* at = static_cast<uint8_t*>(ws);
-        RowsJob ja = {}, jb = {};
-        if (l.copy_a) {
-            ja = l.ja;
-            ja.dst = at;
-            p.A = reinterpret_cast<const char*>(at);
-            p.lda = ja.len_pad / 2;
-            at += ja.bytes();
-        }
-        if (l.copy_b) {
-            jb = l.jb;
-            jb.dst = at;
-            p.B = reinterpret_cast<const char*>(at);
-            p.ldb = jb.len_pad / 2;
-        }
-        const hipError_t e = launch_rows_pack(ja, jb, st);
-        if (e != hipSuccess) return e;
+void linear_grad_plan(GradParams (&f)[2], size_t ws_bytes) {
+    GradParams *a = f[0].C ? &f[0] : nullptr, *w = f[1].C ? &f[1] : nullptr;
+    for (GradParams& x : f) {
+        x.ws = 0;
+        x.splits = 1;
+        x.bm = x.bn = 128;
     }
-    const int a_cols = (f.M + 7) / 8 * 8, b_cols = (f.N + 7) / 8 * 8;
-    const GradSplit x = {l.per_split, q.splits > 1 ? l.each : 0};
-    GemmParams s = p;
-    if (q.splits > 1) {
-        s.C = static_cast<char*>(ws) + l.used;
-        s.ldc = l.ldp;
-    }
-    auto tiles = [&](auto t, auto o) {
-        constexpr int T = decltype(t)::value, OUT = decltype(o)::value;
-        return f.rows_a ? tile_of<T, OUT, true>(q, s, x, a_cols, b_cols, st) : tile_of<T, OUT, false>(q, s, x, a_cols, b_cols, st);
+    if (a && large(*a)) a = nullptr;
+    if (w && large(*w)) w = nullptr;
+    if (!a && !w) return;
+    // the height of dA's tiles and both splits that should be fastest (together: they share a launch and its compute units)
+    constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+    double best = 0.0;
+    auto each = [&](const GradParams* x, auto&& take) {
+        for (int s : kSplits)
+            if (s == 1 || (x && 2 * s <= slabs_of(*x) + 1 && sums_of(*x, s) <= ws_bytes)) take(s);
     };
-    const hipError_t e = by_type(in_type, q.splits > 1 ? (int)DT_F32 : f.out_type, tiles);
-    if (e != hipSuccess || q.splits == 1) return e;
-    return by_type(in_type, f.out_type, [&](auto, auto o) {
-        hipLaunchKernelGGL((linear_grad_join_kernel<decltype(o)::value>), dim3((unsigned)ceil_div(f.M * (l.ldp / 4), 256)), dim3(256), 0, st, p,
-                           s.C, l.each, (int)l.ldp, q.splits);
+    for (int bm = a && a->M >= 128 ? 128 : 64; bm >= 64; bm -= 64)
+        each(a, [&](int sa) {
+            each(w, [&](int sw) {
+                const size_t bytes = (a ? sums_of(*a, sa) : 0) + (w ? sums_of(*w, sw) : 0);
+                if (bytes > ws_bytes) return;
+                const int64_t wgs = (a ? tiles_of(*a, bm, 128) * sa : 0) + (w ? tiles_of(*w, 128, 128) * sw : 0);
+                const double us = rounds_of(wgs) * std::max(a ? ceil_div(slabs_of(*a), sa) * slab_us(bm) : 0.0, w ? ceil_div(slabs_of(*w), sw) * slab_us(128) : 0.0) +
+                                  (sa > 1 || sw > 1 ? kJoinUs : 0.0) + 2.0 * bytes / kBytesPerUs;
+                if (best > 0.0 && us >= best) return;
+                best = us;
+                if (a) a->bm = bm, a->splits = sa;
+                if (w) w->splits = sw;
+            });
+        });
+    for (GradParams* x : {a, w}) {
+        if (!x) continue;
+        x->splits = (int)ceil_div(slabs_of(*x), ceil_div(slabs_of(*x), x->splits));
+        x->ws = sums_of(*x, x->splits);
+    }
+}
+
+hipError_t launch_linear_grad(int in_type, const GradParams (&f)[2], const DbJoin& db, void* ws, hipStream_t st) {
+    GradSide side[2] = {};
+    JoinSide join[2] = {};
+    char* at = static_cast<char*>(ws);
+    for (int i = 0; i < 2; ++i) {
+        const GradParams& q = f[i];
+        if (!q.C) continue;
+        GradSide& x = side[i];
+        GemmParams& p = x.p;
+        p.A = q.A;
+        p.B = q.B;
+        p.C = q.C;
+        p.lda = q.lda; p.ldb = q.ldb; p.ldc = q.ldc;
+        p.M = q.M; p.N = q.N; p.K = q.K;
+        p.alpha = 1.0f;
+        p.out_type = q.out_type;
+        p.tiles_m = (int)ceil_div(q.M, q.bm);
+        p.tiles_n = (int)ceil_div(q.N, q.bn);
+        p.group_m = 8;
+        p.xcd_remap = 1;
+        x.per = (int)ceil_div(slabs_of(q), q.splits);
+        x.a_cols = (q.M + 7) / 8 * 8;
+        x.b_cols = (q.N + 7) / 8 * 8;
+        x.splits = q.splits;
+        x.blocks = (uint32_t)(p.tiles_m * p.tiles_n * q.splits);
+        op_note("  %d x %d x %d: %d x %d tiles, %d splits of the sum", q.M, q.N, q.K, q.bm, q.bn, q.splits);
+        if (q.splits > 1) {
+            JoinSide& j = join[i];
+            j.p = p;
+            j.part = p.C = at;
+            j.each = x.each = each_of(q);
+            j.ldp = (int)(p.ldc = ldp_of(q));
+            j.splits = q.splits;
+            j.blocks = (uint32_t)ceil_div(q.M * (ldp_of(q) / 4), 256);
+            p.out_type = DT_F32;
+            at += q.ws;
+        }
+    }
+    hipError_t e = hipSuccess;
+    const bool together = side[0].blocks && side[1].blocks && f[0].bm < 256 && f[1].bm < 256 && side[0].blocks + side[1].blocks <= (uint32_t)num_compute_units();
+    auto both = [&](auto t) {
+        constexpr int T = decltype(t)::value;
+        const dim3 grid(side[0].blocks + side[1].blocks);
+        if (f[0].bm == 64) hipLaunchKernelGGL((linear_grads_kernel<T, 64>), grid, dim3(512), 0, st, side[0], side[1]);
+        else hipLaunchKernelGGL((linear_grads_kernel<T, 128>), grid, dim3(512), 0, st, side[0], side[1]);
         return hipGetLastError();
-    });
+    };
+    auto each = [&](auto t) {
+        constexpr int T = decltype(t)::value;
+        hipError_t s = hipSuccess;
+        if (side[0].blocks) s = alone_of<T, false>(f[0], side[0], st);
+        if (s == hipSuccess && side[1].blocks) s = alone_of<T, true>(f[1], side[1], st);
+        return s;
+    };
+    typedef std::integral_constant<int, DT_BF16> B;
+    typedef std::integral_constant<int, DT_F16> H;
+    if (together) e = in_type == DT_BF16 ? both(B{}) : both(H{});
+    else e = in_type == DT_BF16 ? each(B{}) : each(H{});
+    const uint32_t db_blocks = db.db ? (uint32_t)ceil_div(db.N, 64) : 0, blocks = join[0].blocks + join[1].blocks + db_blocks;
+    if (e != hipSuccess || blocks == 0) return e;
+    hipLaunchKernelGGL(linear_grad_join_kernel, dim3(blocks), dim3(256), 0, st, join[0], join[1], db);
+    return hipGetLastError();
 }
 
 }  // namespace gemm

@@ -126,35 +126,46 @@ size_t linear_tile_workspace(const LinearParams& p);   // of a product that fits
 hipError_t launch_linear_tile(int in_type, const LinearParams& p, void* ws, size_t ws_bytes, hipStream_t st);
 hipError_t launch_linear_staged(int in_type, const LinearParams& p, hipStream_t st);
 
-// dZ = dC * act'(Z) and its sums over the rows.
+// The backward pass's first launch: dZ = dC * act'(Z), its sums over the rows, and copies of rows.
 struct LinearBwdParams {
     const char* dC;      // M x N
     const char* Z;       // M x N, or NULL (act 0)
     char* dZ;            // M x N, or NULL (dC is it)
+    char* copy;          // dZ in aligned rows of whole 16 bytes, zeros behind N, or NULL
     float* db;           // N, or NULL
     float* part;         // parts x N partial sums of db (parts > 1)
-    int64_t lddc, ldz, lddz;
+    int64_t lddc, ldz, lddz, ldcopy;
     int64_t M;
     int N;
     int act, dc_type;
     int parts;           // what the rows are cut into
+    RowsJob jobs[2];
 };
 int linear_bwd_parts(int64_t M, int64_t N);   // parts that the pass would like
 hipError_t launch_linear_bwd(int in_type, const LinearBwdParams& p, hipStream_t st);
 
-// C = A B, the products of that backward pass: B is K x N row by row; A is M x K row by row, or (rows_a) K x M row by row.
+// C = A B, the products of the backward pass: B is K x N row by row; A is M x K row by row, or (rows_a) K x M row by row.
 struct GradParams {
     const char* A;
     const char* B;
-    char* C;
+    char* C;             // NULL: not wanted
     int64_t lda, ldb, ldc;   // elements
     int M, N, K;
     bool rows_a;
     int out_type;
+    size_t ws;           // what it uses of a workspace, as planned
+    int bm, bn, splits;
 };
-bool linear_grad_fits(const GradParams& p, size_t ws_bytes);
-size_t linear_grad_workspace(const GradParams& p);
-hipError_t launch_linear_grad(int in_type, const GradParams& p, void* ws, size_t ws_bytes, hipStream_t st);
+bool linear_grad_fits(const GradParams& p);
+// Tiles and splits of both products ([0] with A along the sum, [1] with rows_a) and what their splits' sums need.
+void linear_grad_plan(GradParams (&p)[2], size_t ws_bytes);
+// The sums of db's parts, which ride in the last launch.
+struct DbJoin {
+    const float* part;
+    float* db;           // NULL: nothing to join
+    int N, parts;
+};
+hipError_t launch_linear_grad(int in_type, const GradParams (&p)[2], const DbJoin& db, void* ws, hipStream_t st);
 
 // ---------------------------------------------------------------- norm and rotation of heads
 struct HeadsTensor {
