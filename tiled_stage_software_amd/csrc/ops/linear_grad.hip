@@ -235,11 +235,14 @@ __device__ __forceinline__ void grad_tile(const GradSide& x, uint32_t wg, LDS_AS
                 return;
             }
         }
+        // (rows of any alignment in whole vectors)
+        const LinearEpi e = {nullptr, nullptr, nullptr, p.C, 0, 0, p.ldc, p.M, p.N, 0, ACT_NONE};
+        constexpr int BYTES = S * (BM + BN) * 128;
         if constexpr (OUT >= 0) {
-            ops.template epilogue<OUT>(p, m0, n0, m_keep, n_keep);
+            linear_epilogue<T, OUT, BM, BN, WM, WN, 16, BYTES>(ops, e, smem, m0, n0, m_keep, n_keep);
         } else {
-            if (p.out_type == DT_F32) ops.template epilogue<DT_F32>(p, m0, n0, m_keep, n_keep);
-            else ops.template epilogue<T>(p, m0, n0, m_keep, n_keep);
+            if (p.out_type == DT_F32) linear_epilogue<T, DT_F32, BM, BN, WM, WN, 16, BYTES>(ops, e, smem, m0, n0, m_keep, n_keep);
+            else linear_epilogue<T, T, BM, BN, WM, WN, 16, BYTES>(ops, e, smem, m0, n0, m_keep, n_keep);
         }
     };
     if (NC == NW || wave_id() < NC) {
