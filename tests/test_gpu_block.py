@@ -81,7 +81,7 @@ def check_linear(a, w, b, act, r, out, **kw):
 
 
 LINEAR = [(1, 1, 1), (1, 64, 128), (3, 70, 40), (7, 129, 65), (16, 200, 512), (17, 96, 1000), (33, 300, 200), (64, 128, 640),
-          (65, 257, 333), (130, 140, 64), (200, 513, 90), (257, 256, 448), (333, 401, 2049), (512, 768, 1024)]
+          (65, 257, 333), (130, 140, 64), (200, 513, 90), (257, 256, 448), (333, 401, 2049), (512, 768, 1024), (300, 520, 1000), (260, 300, 72), (1100, 2300, 264), (129, 131, 4101)]
 
 
 @pytest.mark.parametrize("M,N,K", LINEAR)

@@ -3,10 +3,12 @@
 //
 // The ring, its loaders and the multiplication are those of the library's 16-bit products; what is new is the epilogue.  Tiles
 // of 256 x 256 and 192 x 256 (eight waves, copies by one wave of each SIMD) for large products; 128 x 128 and 64 x 128, with
-// K split over workgroups, where those leave the card empty.  Rows that the direct copies cannot take (not 16-byte aligned, K not whole
-// slabs) are copied into the workspace first where that pays, or loaded through registers.
+// K split over workgroups, where those leave the card empty.  What K has behind whole slabs is loaded through registers behind the
+// loop.  Rows that the direct copies cannot take (not 16-byte aligned) are copied into the workspace first where that
+// pays, or loaded through registers.
 #include <algorithm>
 
+#include "f8_common.hpp"
 #include "linear.hpp"
 #include "linear_plan.hpp"
 #include "rows_pack.hpp"
@@ -39,6 +41,26 @@ struct LinearRingOps : MfmaCompute<T, BM, BN, kSlab, WM, WN, 16> {
     __device__ __forceinline__ void frag(int, int slot, int ks) { C::template frag<BUF>(slot, ks); }
     template <int BUF, int HAS, int PARTS>
     __device__ __forceinline__ void math(int) { C::template math<BUF, (COPY && HAS) ? (L + PARTS - 1) / PARTS : 0>(); }
+    // The last `bytes` (fewer than a slab's) of rows that begin at A and W, once every wave is through with the slabs; zeros behind
+    // them, and the last row again where there are no more.
+    __device__ __forceinline__ void tail(const char* A, int64_t lda, int a_rows, const char* W, int64_t ldw, int w_rows, int bytes) {
+        constexpr int NT = 64 * WM * WN;
+        wait_lgkm0();
+        gemm::barrier();
+#pragma unroll
+        for (int i = 0; i < (BM + BN) * 8 / NT; ++i) {
+            const int id = (int)threadIdx.x + i * NT, row = id / 8, c = id % 8;
+            const char* at = row < BM ? A + (int64_t)min(row, a_rows - 1) * lda : W + (int64_t)min(row - BM, w_rows - 1) * ldw;
+            const u32x4 v = load_chunk(reinterpret_cast<const uint8_t*>(at), 16 * c, bytes);
+            *reinterpret_cast<LDS_AS u32x4*>(this->smem + row * kSlabBytes + ((c ^ swz<8>(row)) << 4)) = v;
+        }
+        wait_lgkm0();
+        gemm::barrier();
+        C::template frag<0>(0, 0);
+        C::template frag<1>(0, 1);
+        C::template math<0, 0>();
+        C::template math<1, 0>();
+    }
 };
 
 // Any pitch, alignment and K >= 64: 16-byte loads of any alignment into registers, two slabs ahead, written into the other
@@ -146,7 +168,7 @@ void linear_tile_kernel(GemmParams p, const LinearEpi e, const LinearSplit x) {
     const int m0 = max(0, min(m_keep, p.M - BM)), n0 = max(0, min(n_keep, p.N - BN));
     const int s0 = (int)blockIdx.y * x.per;
     const int64_t left = 2 * (int64_t)p.K - (int64_t)s0 * kSlabBytes, K = min(left, (int64_t)x.per * kSlabBytes);
-    const int slabs = (int)((K + kSlabBytes - 1) / kSlabBytes);
+    const int slabs = S > 0 ? (int)(K / kSlabBytes) : (int)((K + kSlabBytes - 1) / kSlabBytes);
     const char* A = p.A + (int64_t)s0 * kSlabBytes;
     const char* W = p.B + (int64_t)s0 * kSlabBytes;
     auto finish = [&](auto& ops) {
@@ -157,6 +179,12 @@ void linear_tile_kernel(GemmParams p, const LinearEpi e, const LinearSplit x) {
             linear_epilogue<T, OUT, BM, BN, WM, WN, 16, BYTES>(ops, e, smem, m0, n0, m_keep, n_keep);
         }
     };
+    auto behind = [&](auto& ops) {
+        const int bytes = (int)(K - (int64_t)slabs * kSlabBytes);
+        if (bytes > 0)
+            ops.tail(A + (int64_t)m0 * p.lda * 2 + (int64_t)slabs * kSlabBytes, p.lda * 2, p.M - m0, W + (int64_t)n0 * p.ldb * 2 + (int64_t)slabs * kSlabBytes,
+                     p.ldb * 2, p.N - n0, bytes);
+    };
     if constexpr (S > 0) {
         constexpr int KS = MfmaCompute<half_of<T>, BM, BN, kSlab, WM, WN, 16>::KS;
         if (NC == NW || wave_id() < NC) {
@@ -165,11 +193,13 @@ void linear_tile_kernel(GemmParams p, const LinearEpi e, const LinearSplit x) {
             init_a<BM, kSlabBytes, NC>(ops.la, A + (int64_t)m0 * p.lda * 2, p.lda * 2, kSlabBytes, p.M - m0);
             ops.lb.init(W + (int64_t)n0 * p.ldb * 2, p.ldb * 2, kSlabBytes);
             gemm_sched::ring_mainloop<S, KS, 1>(ops, slabs);
+            behind(ops);
             finish(ops);
         } else if constexpr (NC < NW) {
             LinearRingOps<half_of<T>, BM, BN, WM, WN, NC, false> ops;
             ops.init(smem);
             gemm_sched::ring_mainloop<S, KS, 1>(ops, slabs);
+            behind(ops);
             finish(ops);
         }
     } else {
@@ -203,31 +233,11 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const LinearEpi e, con
     finish8<T, OUT>(e, m, n, 0, v, bias, old);
 }
 
-double staged_us(int bm) { return bm == 64 ? 0.4 : 0.5; }   // longer from rows of any alignment
 int64_t ldp_of(int64_t N) { return (N + 7) / 8 * 8; }
-// 256 x 256, 192 x 256, 128 x 128 or 64 x 128.
-TilePlan plan_of(int64_t M, int64_t N, int64_t K, bool large) {
-    TilePlan q = {128, 128, 1};
-    const int64_t cu = num_compute_units();
-    const int64_t t128 = ceil_div(M, 128) * ceil_div(N, 128);
-    if (large && N >= 256) {
-        double best = ceil_div(t128, cu) * 128.0 * 128.0 * kSmallCost;
-        for (int bm : {256, 192}) {
-            const double cost = ceil_div(ceil_div(M, bm) * ceil_div(N, 256), cu) * bm * 256.0;
-            if (M >= bm && cost <= best * (q.bm == 128 ? 1.0 : 0.97)) {
-                best = cost;
-                q = TilePlan{bm, 256, 1};
-            }
-        }
-        if (q.bm != 128) return q;
-    }
-    if (t128 > cu && M > kShortRows) return q;
-    return small_plan(M, N, ceil_div(K, kSlab), 128, 64, 16, ldp_of(N));
-}
 
 // What a call does with the workspace it has.
 struct LinearLaunch {
-    TilePlan q;
+    TilePlan q;          // 256 x 256, 192 x 256, 128 x 128 or 64 x 128
     int per_split;       // slabs of a split
     int64_t each;        // bytes of a split's sums
     RowsJob ja, jw;      // copies of the operands, behind the splits' sums ...
@@ -237,34 +247,62 @@ struct LinearLaunch {
 };
 constexpr size_t kMostCopied = size_t(1) << 34;   // rows_pack counts chunks in 32 bits
 
+LinearLaunch with(const LinearParams& f, const TilePlan& q) {
+    const int64_t slabs = ceil_div(f.K, kSlab), kp = (int64_t)(f.K + 7) / 8 * 16;
+    LinearLaunch l = {};
+    l.q = q;
+    l.each = (int64_t)f.M * ldp_of(f.N) * (int64_t)sizeof(float);
+    l.per_split = (int)ceil_div(slabs, q.splits);
+    l.q.splits = (int)ceil_div(slabs, l.per_split);
+    const int64_t least_a = least_rows(q.bm), least_w = q.bn;
+    l.ja = {reinterpret_cast<const uint8_t*>(f.A), nullptr, f.lda * 2, f.M, (int64_t)f.K * 2, std::max<int64_t>(f.M, least_a), kp};
+    l.jw = {reinterpret_cast<const uint8_t*>(f.W), nullptr, f.ldw * 2, f.N, (int64_t)f.K * 2, std::max<int64_t>(f.N, least_w), kp};
+    l.copy_a = f.M < least_a || ((uintptr_t)f.A | (uint64_t)f.lda * 2) % 16;
+    l.copy_w = f.N < least_w || ((uintptr_t)f.W | (uint64_t)f.ldw * 2) % 16;
+    l.used = l.q.splits > 1 ? ((size_t)(l.q.splits * l.each) + 255) & ~size_t(255) : 0;
+    l.wants = l.used + (l.copy_a ? l.ja.bytes() : 0) + (l.copy_w ? l.jw.bytes() : 0);
+    l.direct = !l.copy_a && !l.copy_w;
+    return l;
+}
 LinearLaunch launch_of(const LinearParams& f, size_t ws_bytes) {
-    const int64_t slabs = ceil_div(f.K, kSlab), kp = slabs * kSlabBytes;
-    auto with = [&](bool large) {
-        LinearLaunch l;
-        TilePlan& q = l.q;
-        q = plan_of(f.M, f.N, f.K, large);
-        l.each = (int64_t)f.M * ldp_of(f.N) * (int64_t)sizeof(float);
-        if (q.splits > 1 && ws_bytes < (size_t)(q.splits * l.each)) q.splits = (int)(ws_bytes / l.each);
-        if (q.splits < 2) q.splits = 1;
-        l.per_split = (int)ceil_div(slabs, q.splits);
-        q.splits = (int)ceil_div(slabs, l.per_split);
-        const int64_t least_a = least_rows(q.bm), least_w = q.bn;
-        l.ja = {reinterpret_cast<const uint8_t*>(f.A), nullptr, f.lda * 2, f.M, (int64_t)f.K * 2, std::max<int64_t>(f.M, least_a), kp};
-        l.jw = {reinterpret_cast<const uint8_t*>(f.W), nullptr, f.ldw * 2, f.N, (int64_t)f.K * 2, std::max<int64_t>(f.N, least_w), kp};
-        l.copy_a = f.M < least_a || f.K % kSlab || ((uintptr_t)f.A | (uint64_t)f.lda * 2) % 16;
-        l.copy_w = f.N < least_w || f.K % kSlab || ((uintptr_t)f.W | (uint64_t)f.ldw * 2) % 16;
-        l.used = q.splits > 1 ? ((size_t)(q.splits * l.each) + 255) & ~size_t(255) : 0;
-        l.wants = l.used + (l.copy_a ? l.ja.bytes() : 0) + (l.copy_w ? l.jw.bytes() : 0);
-        l.copies = false;
-        if ((l.copy_a || l.copy_w) && l.wants <= ws_bytes && l.wants < kMostCopied) {
-            const double rounds = rounds_of(ceil_div(f.M, q.bm) * ceil_div(f.N, q.bn) * q.splits);
-            l.copies = q.bm > 128 || kJoinUs + 2.0 * (l.wants - l.used) / kBytesPerUs < rounds * l.per_split * staged_us(q.bm);
+    const int64_t cu = num_compute_units(), slabs = ceil_div(f.K, kSlab), t128 = ceil_div(f.M, 128) * ceil_div(f.N, 128);
+    // large tiles (of direct copies) where they are the least work for the fullest compute unit
+    double least = ceil_div(t128, cu) * 128.0 * 128.0 * kSmallCost;
+    TilePlan large = {0, 256, 1};
+    for (int bm : {256, 192}) {
+        const double cost = ceil_div(ceil_div(f.M, bm) * ceil_div(f.N, 256), cu) * bm * 256.0;
+        if (f.M >= bm && f.N >= 256 && cost <= least * (large.bm ? 0.97 : 1.0)) {
+            least = cost;
+            large.bm = bm;
         }
-        l.direct = l.copies || (!l.copy_a && !l.copy_w);
-        return l;
-    };
-    const LinearLaunch l = with(true);
-    return l.q.bm > 128 && !l.direct ? with(false) : l;   // (large tiles have no loads through registers)
+    }
+    if (large.bm) {
+        LinearLaunch l = with(f, large);
+        l.copies = !l.direct && l.wants <= ws_bytes && l.wants < kMostCopied;
+        l.direct = l.direct || l.copies;
+        if (l.direct) return l;
+    }
+    // else the height, the splits and the way of loading that should be fastest (many tiles: no splits of 128 rows)
+    LinearLaunch best = {};
+    double best_us = 0.0;
+    const bool many = t128 > cu && f.M > kShortRows;
+    for (int bm = 128; bm >= (many ? 128 : 64); bm -= 64) {
+        const int64_t tiles = ceil_div(f.M, bm) * ceil_div(f.N, 128);
+        for (int64_t s = 1; s <= (many ? 1 : 16) && s * 4 <= slabs + 3; ++s) {
+            const double sums = (double)(s * f.M * ldp_of(f.N) * 4);
+            if (s > 1 && (sums + 256 > (double)ws_bytes || ceil_div(slabs, s) == ceil_div(slabs, s - 1))) continue;
+            LinearLaunch l = with(f, TilePlan{bm, 128, (int)s});
+            const double rounds = rounds_of(tiles * l.q.splits) * l.per_split, join = s > 1 ? kJoinUs + 2.0 * sums / kBytesPerUs : 0.0;
+            const double copied = kCopyUs + 2.0 * (double)(l.wants - l.used) / kCopiedPerUs;
+            l.copies = !l.direct && l.wants <= ws_bytes && l.wants < kMostCopied && copied < rounds * staged_us(bm);
+            const double us = join + rounds * slab_us(bm) + (l.direct ? 0.0 : l.copies ? copied : rounds * staged_us(bm));
+            l.direct = l.direct || l.copies;
+            if (best_us > 0.0 && us >= best_us) continue;
+            best_us = us;
+            best = l;
+        }
+    }
+    return best;
 }
 
 template <int T, int OUT, int BM, int BN, int WM, int WN, int S>
@@ -335,7 +373,6 @@ hipError_t launch_linear_tile(int in_type, const LinearParams& f, void* ws, size
         }
         const hipError_t e = launch_rows_pack(ja, jw, st);
         if (e != hipSuccess) return e;
-        p.K = (int)kp;
     }
     const LinearEpi e = epi_of(f);
     LinearSplit x = {l.per_split, nullptr, l.each};
