@@ -317,30 +317,20 @@ int64_t each_of(const GradParams& f) { return (int64_t)f.M * ldp_of(f) * (int64_
 int64_t tiles_of(const GradParams& f, int bm, int bn) { return ceil_div(f.M, bm) * ceil_div(f.N, bn); }
 size_t sums_of(const GradParams& f, int64_t splits) { return splits > 1 ? (size_t)(splits * each_of(f) + 255) & ~size_t(255) : 0; }
 
-// Large tiles, or small ones that fill the card by themselves.
-bool large(GradParams& f) {
-    const int64_t cu = num_compute_units(), t128 = tiles_of(f, 128, 128), t256 = tiles_of(f, 256, 256);
-    f.splits = 1;
-    if (f.M >= 256 && f.N >= 256 && ceil_div(t256, cu) * 4.0 <= ceil_div(t128, cu) * kSmallCost) f.bm = f.bn = 256;
-    else if (t128 > cu && (f.M >= 128 || f.rows_a)) f.bm = f.bn = 128;
-    else return false;
-    return true;
-}
-
 template <int T, bool ROWS_A>
 hipError_t alone_of(const GradParams& f, const GradSide& x, hipStream_t st) {
-    auto go = [&](auto kernel, int threads) {
-        hipLaunchKernelGGL(kernel, dim3(x.blocks), dim3(threads), 0, st, x);
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(x.blocks), dim3(512), 0, st, x);
         return hipGetLastError();
     };
     if (f.bm == 256)
-        return x.p.out_type == DT_F32 ? go(linear_grad_kernel<T, DT_F32, ROWS_A, 256, 256, 2, 4, 2>, 512)
-                                      : go(linear_grad_kernel<T, T, ROWS_A, 256, 256, 2, 4, 2>, 512);
+        return x.p.out_type == DT_F32 ? go(linear_grad_kernel<T, DT_F32, ROWS_A, 256, 256, 2, 4, 2>)
+                                      : go(linear_grad_kernel<T, T, ROWS_A, 256, 256, 2, 4, 2>);
     const bool alone = x.blocks <= (uint32_t)num_compute_units();
     if constexpr (!ROWS_A) {
-        if (f.bm == 64) return alone ? go(linear_grad_kernel<T, -1, ROWS_A, 64, 128, 2, 4, 4>, 512) : go(linear_grad_kernel<T, -1, ROWS_A, 64, 128, 2, 4, 2>, 512);
+        if (f.bm == 64) return alone ? go(linear_grad_kernel<T, -1, ROWS_A, 64, 128, 2, 4, 4>) : go(linear_grad_kernel<T, -1, ROWS_A, 64, 128, 2, 4, 3>);
     }
-    return alone ? go(linear_grad_kernel<T, -1, ROWS_A, 128, 128, 2, 4, 4>, 512) : go(linear_grad_kernel<T, -1, ROWS_A, 128, 128, 2, 2, 2>, 256);
+    return alone ? go(linear_grad_kernel<T, -1, ROWS_A, 128, 128, 2, 4, 4>) : go(linear_grad_kernel<T, -1, ROWS_A, 128, 128, 2, 4, 2>);
 }
 
 }  // namespace
@@ -352,42 +342,72 @@ bool linear_grad_fits(const GradParams& f) {
     return f.K >= 1 && f.lda <= most && f.ldb <= most && f.K <= most * 64 && tiles_of(f, 64, 128) < (int64_t(1) << 22) && along <= most;
 }
 
+// A small product's splits, the launch that joins them not counted: it is one for both.
+double grad_us(int64_t cu, const GradParams& f, int bm, int splits) {
+    return slabs_us(cu, bm, tiles_of(f, bm, bm == 256 ? 256 : 128) * splits, ceil_div(slabs_of(f), splits), DIRECT);
+}
+double sums_us(const GradParams& f, int splits) { return 2.0 * (double)sums_of(f, splits) / kBytesPerUs; }
+
 void linear_grad_plan(GradParams (&f)[2], size_t ws_bytes) {
-    GradParams *a = f[0].C ? &f[0] : nullptr, *w = f[1].C ? &f[1] : nullptr;
+    // each for itself: the tile and splits that should be fastest
+    const int64_t cu = num_compute_units();
+    size_t left = ws_bytes;
+    double alone = 0.0;
+    int joins = 0;
     for (GradParams& x : f) {
         x.ws = 0;
         x.splits = 1;
         x.bm = x.bn = 128;
+        if (!x.C) continue;
+        double best = 0.0;
+        auto take = [&](int bm, int s) {
+            const double us = grad_us(cu, x, bm, s) + (s > 1 ? kJoinUs + sums_us(x, s) : 0.0);
+            if (best > 0.0 && us >= best) return;
+            best = us;
+            x.bm = bm;
+            x.bn = bm == 256 ? 256 : 128;
+            x.splits = s;
+        };
+        if (x.M >= 256 && x.N >= 256) take(256, 1);
+        for (int bm : {128, 64}) {
+            if (bm == 64 && (x.rows_a || tiles_of(x, 64, 128) > 16 * cu)) continue;
+            for (int s : kSplits)
+                if (s == 1 || (2 * s <= slabs_of(x) + 1 && tiles_of(x, bm, 128) * (s - 1) <= 2 * cu && sums_of(x, s) <= left)) take(bm, s);
+        }
+        x.ws = sums_of(x, x.splits);
+        left -= x.ws;
+        alone += best + 2.5;   // (a launch)
+        joins += x.splits > 1;
     }
-    if (a && large(*a)) a = nullptr;
-    if (w && large(*w)) w = nullptr;
-    if (!a && !w) return;
-    // the height of dA's tiles and both splits that should be fastest (together: they share a launch and its compute units)
-    constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
-    double best = 0.0;
-    auto each = [&](const GradParams* x, auto&& take) {
-        for (int s : kSplits)
-            if (s == 1 || (x && 2 * s <= slabs_of(*x) + 1 && sums_of(*x, s) <= ws_bytes)) take(s);
-    };
-    for (int bm = a && a->M >= 128 ? 128 : 64; bm >= 64; bm -= 64)
-        each(a, [&](int sa) {
-            each(w, [&](int sw) {
-                const size_t bytes = (a ? sums_of(*a, sa) : 0) + (w ? sums_of(*w, sw) : 0);
-                if (bytes > ws_bytes) return;
-                const int64_t wgs = (a ? tiles_of(*a, bm, 128) * sa : 0) + (w ? tiles_of(*w, 128, 128) * sw : 0);
-                const double us = rounds_of(wgs) * std::max(a ? ceil_div(slabs_of(*a), sa) * slab_us(bm) : 0.0, w ? ceil_div(slabs_of(*w), sw) * slab_us(128) : 0.0) +
-                                  (sa > 1 || sw > 1 ? kJoinUs : 0.0) + 2.0 * bytes / kBytesPerUs;
-                if (best > 0.0 && us >= best) return;
-                best = us;
-                if (a) a->bm = bm, a->splits = sa;
-                if (w) w->splits = sw;
-            });
-        });
-    for (GradParams* x : {a, w}) {
-        if (!x) continue;
-        x->splits = (int)ceil_div(slabs_of(*x), ceil_div(slabs_of(*x), x->splits));
-        x->ws = sums_of(*x, x->splits);
+    if (joins == 2) alone -= kJoinUs;
+    // or both in one launch, where together they fill the compute units once at most
+    if (f[0].C && f[1].C) {
+        const GradParams &a = f[0], &w = f[1];
+        double best = alone;
+        int bm_a = 0, sa = 1, sw = 1;
+        for (int bm : {128, 64})
+            for (int s0 : kSplits) {
+                if ((s0 > 1 && 2 * s0 > slabs_of(a) + 1) || tiles_of(a, bm, 128) * s0 >= cu) break;
+                for (int s1 : kSplits) {
+                    if ((s1 > 1 && 2 * s1 > slabs_of(w) + 1) || sums_of(a, s0) + sums_of(w, s1) > ws_bytes || tiles_of(a, bm, 128) * s0 + tiles_of(w, 128, 128) * s1 > cu) break;
+                    const double us = 2.5 + std::max(grad_us(cu, a, bm, s0), grad_us(cu, w, 128, s1)) + (s0 > 1 || s1 > 1 ? kJoinUs : 0.0) + sums_us(a, s0) + sums_us(w, s1);
+                    if (us >= best) continue;
+                    best = us;
+                    bm_a = bm, sa = s0, sw = s1;
+                }
+            }
+        if (bm_a) {
+            f[0].bm = bm_a;
+            f[0].bn = f[1].bm = f[1].bn = 128;
+            f[0].splits = sa;
+            f[1].splits = sw;
+        }
     }
+    for (GradParams& x : f)
+        if (x.C) {
+            x.splits = (int)ceil_div(slabs_of(x), ceil_div(slabs_of(x), x.splits));
+            x.ws = sums_of(x, x.splits);
+        }
 }
 
 hipError_t launch_linear_grad(int in_type, const GradParams (&f)[2], const DbJoin& db, void* ws, hipStream_t st) {

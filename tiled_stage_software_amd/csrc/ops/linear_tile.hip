@@ -264,39 +264,31 @@ LinearLaunch with(const LinearParams& f, const TilePlan& q) {
     l.direct = !l.copy_a && !l.copy_w;
     return l;
 }
+// The tile, the splits and the way of loading that should be fastest.
 LinearLaunch launch_of(const LinearParams& f, size_t ws_bytes) {
-    const int64_t cu = num_compute_units(), slabs = ceil_div(f.K, kSlab), t128 = ceil_div(f.M, 128) * ceil_div(f.N, 128);
-    // large tiles (of direct copies) where they are the least work for the fullest compute unit
-    double least = ceil_div(t128, cu) * 128.0 * 128.0 * kSmallCost;
-    TilePlan large = {0, 256, 1};
-    for (int bm : {256, 192}) {
-        const double cost = ceil_div(ceil_div(f.M, bm) * ceil_div(f.N, 256), cu) * bm * 256.0;
-        if (f.M >= bm && f.N >= 256 && cost <= least * (large.bm ? 0.97 : 1.0)) {
-            least = cost;
-            large.bm = bm;
-        }
-    }
-    if (large.bm) {
-        LinearLaunch l = with(f, large);
-        l.copies = !l.direct && l.wants <= ws_bytes && l.wants < kMostCopied;
-        l.direct = l.direct || l.copies;
-        if (l.direct) return l;
-    }
-    // else the height, the splits and the way of loading that should be fastest (many tiles: no splits of 128 rows)
+    const int64_t slabs = ceil_div(f.K, kSlab), cu = num_compute_units();
     LinearLaunch best = {};
     double best_us = 0.0;
-    const bool many = t128 > cu && f.M > kShortRows;
-    for (int bm = 128; bm >= (many ? 128 : 64); bm -= 64) {
-        const int64_t tiles = ceil_div(f.M, bm) * ceil_div(f.N, 128);
-        for (int64_t s = 1; s <= (many ? 1 : 16) && s * 4 <= slabs + 3; ++s) {
-            const double sums = (double)(s * f.M * ldp_of(f.N) * 4);
-            if (s > 1 && (sums + 256 > (double)ws_bytes || ceil_div(slabs, s) == ceil_div(slabs, s - 1))) continue;
-            LinearLaunch l = with(f, TilePlan{bm, 128, (int)s});
-            const double rounds = rounds_of(tiles * l.q.splits) * l.per_split, join = s > 1 ? kJoinUs + 2.0 * sums / kBytesPerUs : 0.0;
+    for (int bm : {256, 192, 128, 64}) {
+        const bool large = bm > 128;   // (no loads through registers, and no splits: small tiles fill the card better)
+        const int bn = large ? 256 : 128;
+        if (large && (f.M < bm || f.N < bn)) continue;
+        const int64_t tiles = ceil_div(f.M, bm) * ceil_div(f.N, bn);
+        if (bm == 64 && tiles > 16 * cu) continue;
+        for (int s : kSplits) {
+            const double sums = (double)(s * (int64_t)f.M * ldp_of(f.N) * 4);
+            if (s > 1 && (large || tiles > 2 * cu || s > 16 || s * 4 > slabs + 3 || tiles * s > 4 * cu || sums + 256 > (double)ws_bytes)) break;
+            LinearLaunch l = with(f, TilePlan{bm, bn, s});
             const double copied = kCopyUs + 2.0 * (double)(l.wants - l.used) / kCopiedPerUs;
-            l.copies = !l.direct && l.wants <= ws_bytes && l.wants < kMostCopied && copied < rounds * staged_us(bm);
-            const double us = join + rounds * slab_us(bm) + (l.direct ? 0.0 : l.copies ? copied : rounds * staged_us(bm));
-            l.direct = l.direct || l.copies;
+            const double staged = slabs_us(cu, bm, tiles * l.q.splits, l.per_split, STAGED);
+            double us = slabs_us(cu, bm, tiles * l.q.splits, l.per_split, DIRECT);
+            if (!l.direct) {
+                l.copies = l.wants <= ws_bytes && l.wants < kMostCopied && (large || us + copied < staged);
+                if (large && !l.copies) continue;
+                us = l.copies ? us + copied : staged;
+                l.direct = l.copies;
+            }
+            if (s > 1) us += kJoinUs + 2.0 * sums / kBytesPerUs;
             if (best_us > 0.0 && us >= best_us) continue;
             best_us = us;
             best = l;
@@ -311,8 +303,8 @@ hipError_t go(const GemmParams& p, const LinearEpi& e, const LinearSplit& x, int
                        dim3(64 * WM * WN), 0, st, p, e, x);
     return hipGetLastError();
 }
-// Small tiles that have a compute unit to themselves: eight waves, so that two on a SIMD take turns, and four slots, so that
-// three slabs are on their way.  Else a second workgroup, which two slots leave room for, does both.
+// Small tiles that have a compute unit to themselves: four slots, so that three slabs are on their way.  Else a second workgroup, which
+// fewer slots leave room for, hides the waits (eight waves either way: four measured 52.6 us instead of 48.4 on 264 tiles of 128 rows).
 template <int T, int OUT>
 hipError_t tile_of(const TilePlan& q, bool direct, const GemmParams& p, const LinearEpi& e, const LinearSplit& x, hipStream_t st) {
     if (q.bm == 256) return go<T, OUT, 256, 256, 2, 4, 2>(p, e, x, q.splits, st);
@@ -320,10 +312,10 @@ hipError_t tile_of(const TilePlan& q, bool direct, const GemmParams& p, const Li
     const bool alone = (int64_t)p.tiles_m * p.tiles_n * q.splits <= num_compute_units();
     if (q.bm == 64) {
         if (!direct) return go<T, OUT, 64, 128, 2, 4, 0>(p, e, x, q.splits, st);
-        return alone ? go<T, OUT, 64, 128, 2, 4, 4>(p, e, x, q.splits, st) : go<T, OUT, 64, 128, 2, 4, 2>(p, e, x, q.splits, st);
+        return alone ? go<T, OUT, 64, 128, 2, 4, 4>(p, e, x, q.splits, st) : go<T, OUT, 64, 128, 2, 4, 3>(p, e, x, q.splits, st);
     }
     if (!direct) return go<T, OUT, 128, 128, 2, 4, 0>(p, e, x, q.splits, st);
-    return alone ? go<T, OUT, 128, 128, 2, 4, 4>(p, e, x, q.splits, st) : go<T, OUT, 128, 128, 2, 2, 2>(p, e, x, q.splits, st);
+    return alone ? go<T, OUT, 128, 128, 2, 4, 4>(p, e, x, q.splits, st) : go<T, OUT, 128, 128, 2, 4, 2>(p, e, x, q.splits, st);
 }
 
 }  // namespace
