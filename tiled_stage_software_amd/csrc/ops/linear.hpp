@@ -111,7 +111,8 @@ __device__ __forceinline__ void act_all(int act, float (&v)[N]) {
 }
 
 // ------------------------------------------------------------------ eight columns of a row
-// Columns n .. n+7 of a row that starts at `row`: whole, or those within [lo, N) one by one (others: 0, not read).
+// Columns n .. n+7 of a row that starts at `row`; those from N on are 0 and not read (n < N).  Where they are not whole they come one
+// by one, none behind a branch: waits between them would be a load's latency each.
 template <int T>
 struct Eight {
     static constexpr int Q = T == DT_F32 ? 2 : 1;
@@ -120,22 +121,29 @@ struct Eight {
 #pragma unroll
         for (int q = 0; q < Q; ++q) raw[q] = load16(row + (int64_t)n * Elem<T>::SIZE + 16 * q);
     }
-    __device__ __forceinline__ void load(const char* row, int n, int lo, int N) {
-        if (n >= lo && n + 8 <= N) {
+    __device__ __forceinline__ void load(const char* row, int n, int N) {
+        if (n + 8 <= N) {
             whole(row, n);
             return;
         }
+        uint32_t x[8];
 #pragma unroll
-        for (int q = 0; q < Q; ++q) raw[q] = u32x4{0u, 0u, 0u, 0u};
+        for (int e = 0; e < 8; ++e) {
+            const int at = min(n + e, N - 1);
+            if constexpr (T == DT_F32) x[e] = reinterpret_cast<const uint32_t*>(row)[at];
+            else x[e] = reinterpret_cast<const uint16_t*>(row)[at];
+        }
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (n + e >= lo && n + e < N) {
-                if constexpr (T == DT_F32) raw[e >> 2][e & 3] = reinterpret_cast<const uint32_t*>(row)[n + e];
-                else raw[0][e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[n + e] << ((e & 1) * 16);
-            }
+        for (int e = 0; e < 8; ++e) x[e] = n + e < N ? x[e] : 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (T == DT_F32) raw[0][e] = x[e], raw[1][e] = x[4 + e];
+            else raw[0][e] = x[2 * e] | x[2 * e + 1] << 16;
+        }
     }
     __device__ __forceinline__ float get(int e) const { return Elem<T>::get(raw[e / Elem<T>::VE], e % Elem<T>::VE); }
 };
+// Eight values to columns n .. n+7, those within [lo, N).
 template <int T>
 __device__ __forceinline__ void store8(char* row, int n, int lo, int N, const float* v) {
     constexpr int SZ = Elem<T>::SIZE, VE = Elem<T>::VE;
@@ -154,18 +162,18 @@ __device__ __forceinline__ void store8(char* row, int n, int lo, int N, const fl
 
 // Bias of columns n .. n+7 (0 where there is none).
 template <int T>
-__device__ __forceinline__ void load_bias(const LinearEpi& e, int n, int lo, float* b) {
+__device__ __forceinline__ void load_bias(const LinearEpi& e, int n, float* b) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) b[i] = 0.0f;
-    if (!e.bias) return;
+    if (!e.bias || n >= e.N) return;
     if (e.bias_type == DT_F32) {
         Eight<DT_F32> v;
-        v.load(e.bias, n, lo, e.N);
+        v.load(e.bias, n, e.N);
 #pragma unroll
         for (int i = 0; i < 8; ++i) b[i] = v.get(i);
     } else {
         Eight<T> v;
-        v.load(e.bias, n, lo, e.N);
+        v.load(e.bias, n, e.N);
 #pragma unroll
         for (int i = 0; i < 8; ++i) b[i] = v.get(i);
     }
@@ -200,7 +208,7 @@ __device__ __forceinline__ void linear_epilogue(Compute& ops, const LinearEpi& e
     const int w = wave_id(), wm = w / WN, wn = w % WN, lane = lane_id();
     const int c8 = (int)threadIdx.x % TPR, n = n0 + 8 * c8;
     float bias[8];
-    load_bias<T>(e, n, n_keep, bias);
+    load_bias<T>(e, n, bias);
 #pragma unroll
     for (int i0 = 0; i0 < TM; i0 += BLK) {
         constexpr int ROWS = WM * BLK * MI;
@@ -236,7 +244,7 @@ __device__ __forceinline__ void linear_epilogue(Compute& ops, const LinearEpi& e
 #pragma unroll
                 for (int a = 0; a < AHEAD; ++a) {
                     const int s = s0 + a * RPI;
-                    if (mine(s)) old[a].load(e.R + (int64_t)row_of(s) * e.ldr * Elem<OUT>::SIZE, n, n_keep, e.N);
+                    if (mine(s)) old[a].load(e.R + (int64_t)row_of(s) * e.ldr * Elem<OUT>::SIZE, n, e.N);
                 }
             }
 #pragma unroll

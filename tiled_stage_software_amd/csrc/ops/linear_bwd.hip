@@ -30,10 +30,10 @@ __device__ __forceinline__ void rows_of(const LinearBwdParams& p, int64_t m, int
     auto load = [&](int a, int64_t i) {   // (past the last row: the last again)
         const int64_t r = i < rows ? i : rows - 1;
         if constexpr (WHOLE) dc[a].whole(dc_at + r * dc_step, n);
-        else dc[a].load(dc_at + r * dc_step, n, 0, p.N);
+        else dc[a].load(dc_at + r * dc_step, n, p.N);
         if constexpr (ACT != ACT_NONE) {
             if constexpr (WHOLE) z[a].whole(z_at + r * z_step, n);
-            else z[a].load(z_at + r * z_step, n, 0, p.N);
+            else z[a].load(z_at + r * z_step, n, p.N);
         }
     };
     if (rows == 0) return;

@@ -114,8 +114,8 @@ __global__ __launch_bounds__(64 * WAVES) void linear_skinny_kernel(const LinearP
     float bias[8];
     Eight<OUT> old;
     if (mine) {
-        load_bias<T>(e, n, 0, bias);
-        if (e.R) old.load(e.R + m * e.ldr * Elem<OUT>::SIZE, n, 0, p.N);
+        load_bias<T>(e, n, bias);
+        if (e.R) old.load(e.R + m * e.ldr * Elem<OUT>::SIZE, n, p.N);
     }
     lds_barrier();
     if (!mine) return;

@@ -220,9 +220,9 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const LinearEpi e, con
     const int64_t m = id / eights;
     const int n = (int)(id % eights) * 8;
     float bias[8], v[8];
-    load_bias<T>(e, n, 0, bias);
+    load_bias<T>(e, n, bias);
     Eight<OUT> old;
-    if (e.R) old.load(e.R + m * e.ldr * Elem<OUT>::SIZE, n, 0, e.N);
+    if (e.R) old.load(e.R + m * e.ldr * Elem<OUT>::SIZE, n, e.N);
     f32x4 s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll 4
     for (int i = 0; i < splits; ++i)
