@@ -23,7 +23,19 @@ gemm_status_t check_linear(int in_type, int act, int64_t M, int64_t N, int64_t K
 }
 
 // Whether the kernel for few rows takes a product.
-bool linear_few(const LinearParams& p) { return p.M <= kLinearSkinnyRows && p.K > 0; }
+// Whether the kernel for few rows takes a product.  Its workgroups' waves are bound by the steps of K that a compute unit has to take, and
+// more so from rows that do not start at cache lines, where tiles have splits of K and fewer bytes of A to load.  Measured
+// (bf16, microseconds, few rows / tiles): 32 rows 4096 x 4096 (64 steps) 10.5 / 12.6, 1152 x 12608 (197) 19.3 / 13.7, 4096 x 14336
+// (224) 31.9 / 27.2, 32768 x 2048 (256) 49 / 33; 16 rows 14336 x 4096 (224) 27.7 / 31.8, 352 x 16000 (250) 15.0 / 11.4, rows 16 bytes
+// further apart 35.8 / 28.9 and 20.1 / 12.7; one row 8044 x 15920 (490) 49 / 51.  Without the workspace that tiles ask for, always.
+bool linear_few(const LinearParams& p, bool lines, size_t ws_bytes) {   // lines: W's rows start at cache lines
+    if (p.M > kLinearSkinnyRows || p.K < 1) return false;
+    const double steps = std::max(1.0, p.N / 16.0 / num_compute_units()) * p.K / 64.0;
+    if (p.M <= 4 || steps <= (p.M <= 16 && lines ? 224.0 : 128.0) || !linear_tile_fits(p)) return true;
+    LinearParams q = p;
+    q.lda = q.ldw = p.K;
+    return ws_bytes < linear_tile_workspace(q);
+}
 
 // One of the backward pass's products (rows_a: A is K x M in memory), where the tiles do not take it: through the library's own
 // 16-bit entry points.
@@ -172,7 +184,8 @@ gemm_status_t gemm_linear(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K,
     p.lda = lda; p.ldw = ldw; p.ldr = R ? ldr : 0; p.ldz = Z ? ldz : 0; p.ldc = ldc;
     p.M = (int)M; p.N = (int)N; p.K = (int)K;
     p.act = act; p.bias_type = bias_type; p.out_type = c_type;
-    const bool few = linear_few(p), tiles = !few && linear_tile_fits(p);
+    if (!workspace) workspace_bytes = 0;
+    const bool few = linear_few(p, ldw % 64 == 0, workspace_bytes), tiles = !few && linear_tile_fits(p);
     op_note("linear type %d -> %d M=%lld N=%lld K=%lld act=%d: %s", (int)in_type, (int)c_type, (long long)M, (long long)N, (long long)K,
             (int)act, few ? "few rows" : tiles ? "tiles" : "128 x 128 tiles");
     if (few) return launched(launch_linear_skinny(in_type, p, stream));
@@ -188,7 +201,7 @@ gemm_status_t gemm_linear_workspace_size(gemm_dtype_t in_type, int64_t M, int64_
         LinearParams p = {};
         p.M = (int)M; p.N = (int)N; p.K = (int)K;
         p.lda = p.ldw = K;   // (of contiguous operands)
-        if (!linear_few(p) && linear_tile_fits(p)) *bytes = linear_tile_workspace(p);   // (the other kernels use none)
+        if (!linear_few(p, false, SIZE_MAX) && linear_tile_fits(p)) *bytes = linear_tile_workspace(p);   // (the other kernels use none)
     }
     return GEMM_OK;
 }
