@@ -489,8 +489,8 @@ typedef enum gemm_act {
  * Sums, bias, activation and residual are in fp32; C and Z are rounded once, each from the unrounded sums.  An activation is
  * good to a few 2^-21 of its value for |z| up to 8, and to z^2 2^-23 beyond.  NaN stays NaN; infinite
  * sums have the activations' limits.  K == 0: C = act(bias) + R.  M == 0 or N == 0: nothing is written.
- * workspace: as gemm_f8 uses one, for splits of a long K and for copies of operands whose rows are not 16-byte aligned or not
- * whole slabs of 64; gemm_linear_workspace_size gives the bytes for contiguous aligned operands.  With less (or NULL) the call
+ * workspace: as gemm_f8 uses one, for splits of a long K and for copies of operands whose rows are not 16-byte aligned;
+ * gemm_linear_workspace_size gives the bytes for contiguous aligned operands.  With less (or NULL) the call
  * does without, with the same result up to the order of sums.
  * Errors: GEMM_ERR_INVALID_ARG for a negative or too large size, a leading dimension too small, a type or an activation not
  * offered, NULL A, W or C, a workspace not 256-byte aligned. */
@@ -508,8 +508,9 @@ gemm_status_t gemm_linear_workspace_size(gemm_dtype_t in_type, int64_t M, int64_
  * dA: M x K of in_type, or NULL (not computed; W is not read).  dW: N x K of dw_type (in_type or GEMM_F32), or NULL (A is not
  * read).  dbias: N floats, summed in fp32 from unrounded values in a fixed order, or NULL.  M == 0: dW = 0, dbias = 0.
  * The derivative of relu at 0 is 0.
- * workspace: partial sums of dbias and rewritten operands of the two products, one after the other;
- * gemm_linear_bwd_workspace_size gives the bytes for contiguous aligned operands.  With less (or NULL) the call does without.
+ * workspace: partial sums of dbias, copies of dZ, A and W where their rows are not 16-byte aligned, splits of the products' sums;
+ * gemm_linear_bwd_workspace_size gives the bytes for contiguous operands.  With less (or NULL) the call does
+ * without, with the same results up to the order of sums.
  * Errors: as gemm_linear, plus GEMM_ERR_INVALID_ARG for a NULL Z or dZ that is needed. */
 gemm_status_t gemm_linear_bwd(gemm_dtype_t in_type, int64_t M, int64_t N, int64_t K, gemm_act_t act, const void* dC,
                               gemm_dtype_t dc_type, int64_t lddc, const void* Z, int64_t ldz, const void* A, int64_t lda,

@@ -22,7 +22,6 @@ gemm_status_t check_linear(int in_type, int act, int64_t M, int64_t N, int64_t K
     return GEMM_OK;
 }
 
-// Whether the kernel for few rows takes a product.
 // Whether the kernel for few rows takes a product.  Its workgroups' waves are bound by the steps of K that a compute unit has to take, and
 // more so from rows that do not start at cache lines, where tiles have splits of K and fewer bytes of A to load.  Measured
 // (bf16, microseconds, few rows / tiles): 32 rows 4096 x 4096 (64 steps) 10.5 / 12.6, 1152 x 12608 (197) 19.3 / 13.7, 4096 x 14336

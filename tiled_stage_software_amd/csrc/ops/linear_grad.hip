@@ -346,6 +346,8 @@ bool linear_grad_fits(const GradParams& f) {
 double grad_us(int64_t cu, const GradParams& f, int bm, int splits) {
     return slabs_us(cu, bm, tiles_of(f, bm, bm == 256 ? 256 : 128) * splits, ceil_div(slabs_of(f), splits), DIRECT);
 }
+// Splits, which are fewer where as many would leave some empty.
+int64_t splits_of(const GradParams& f, int splits) { return ceil_div(slabs_of(f), ceil_div(slabs_of(f), splits)); }
 double sums_us(const GradParams& f, int splits) { return 2.0 * (double)sums_of(f, splits) / kBytesPerUs; }
 
 void linear_grad_plan(GradParams (&f)[2], size_t ws_bytes) {
@@ -372,10 +374,9 @@ void linear_grad_plan(GradParams (&f)[2], size_t ws_bytes) {
         for (int bm : {128, 64}) {
             if (bm == 64 && (x.rows_a || tiles_of(x, 64, 128) > 16 * cu)) continue;
             for (int s : kSplits)
-                if (s == 1 || (2 * s <= slabs_of(x) + 1 && tiles_of(x, bm, 128) * (s - 1) <= 2 * cu && sums_of(x, s) <= left)) take(bm, s);
+                if (s == 1 || (2 * s <= slabs_of(x) + 1 && tiles_of(x, bm, 128) * (s - 1) <= 2 * cu && sums_of(x, splits_of(x, s)) <= left)) take(bm, s);
         }
-        x.ws = sums_of(x, x.splits);
-        left -= x.ws;
+        left -= sums_of(x, splits_of(x, x.splits));
         alone += best + 2.5;   // (a launch)
         joins += x.splits > 1;
     }
@@ -389,7 +390,7 @@ void linear_grad_plan(GradParams (&f)[2], size_t ws_bytes) {
             for (int s0 : kSplits) {
                 if ((s0 > 1 && 2 * s0 > slabs_of(a) + 1) || tiles_of(a, bm, 128) * s0 >= cu) break;
                 for (int s1 : kSplits) {
-                    if ((s1 > 1 && 2 * s1 > slabs_of(w) + 1) || sums_of(a, s0) + sums_of(w, s1) > ws_bytes || tiles_of(a, bm, 128) * s0 + tiles_of(w, 128, 128) * s1 > cu) break;
+                    if ((s1 > 1 && 2 * s1 > slabs_of(w) + 1) || sums_of(a, splits_of(a, s0)) + sums_of(w, splits_of(w, s1)) > ws_bytes || tiles_of(a, bm, 128) * s0 + tiles_of(w, 128, 128) * s1 > cu) break;
                     const double us = 2.5 + std::max(grad_us(cu, a, bm, s0), grad_us(cu, w, 128, s1)) + (s0 > 1 || s1 > 1 ? kJoinUs : 0.0) + sums_us(a, s0) + sums_us(w, s1);
                     if (us >= best) continue;
                     best = us;
@@ -405,7 +406,7 @@ void linear_grad_plan(GradParams (&f)[2], size_t ws_bytes) {
     }
     for (GradParams& x : f)
         if (x.C) {
-            x.splits = (int)ceil_div(slabs_of(x), ceil_div(slabs_of(x), x.splits));
+            x.splits = (int)splits_of(x, x.splits);
             x.ws = sums_of(x, x.splits);
         }
 }

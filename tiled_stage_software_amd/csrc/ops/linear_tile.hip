@@ -276,9 +276,9 @@ LinearLaunch launch_of(const LinearParams& f, size_t ws_bytes) {
         const int64_t tiles = ceil_div(f.M, bm) * ceil_div(f.N, bn);
         if (bm == 64 && tiles > 16 * cu) continue;
         for (int s : kSplits) {
-            const double sums = (double)(s * (int64_t)f.M * ldp_of(f.N) * 4);
-            if (s > 1 && (large || tiles > 2 * cu || s > 16 || s * 4 > slabs + 3 || tiles * s > 4 * cu || sums + 256 > (double)ws_bytes)) break;
+            if (s > 1 && (large || tiles > 2 * cu || s > 16 || s * 4 > slabs + 3 || tiles * s > 4 * cu)) break;
             LinearLaunch l = with(f, TilePlan{bm, bn, s});
+            if (l.used > ws_bytes) break;
             const double copied = kCopyUs + 2.0 * (double)(l.wants - l.used) / kCopiedPerUs;
             const double staged = slabs_us(cu, bm, tiles * l.q.splits, l.per_split, STAGED);
             double us = slabs_us(cu, bm, tiles * l.q.splits, l.per_split, DIRECT);
@@ -288,7 +288,7 @@ LinearLaunch launch_of(const LinearParams& f, size_t ws_bytes) {
                 us = l.copies ? us + copied : staged;
                 l.direct = l.copies;
             }
-            if (s > 1) us += kJoinUs + 2.0 * sums / kBytesPerUs;
+            if (l.q.splits > 1) us += kJoinUs + 2.0 * (double)l.used / kBytesPerUs;
             if (best_us > 0.0 && us >= best_us) continue;
             best_us = us;
             best = l;

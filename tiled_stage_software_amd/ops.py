@@ -446,7 +446,7 @@ def qk_norm_rope_backward(dq, dk, q, k, wq=None, wk=None, positions=None, cos=No
     rope = _rope(positions, cos, sin, pairs, tokens, q.device)
     with lg.Running(stream, q.device, dq, dk, q, k, wq, wk, positions, cos, sin, workspace) as on:
         dx = [torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k)]
-        dw = [torch.empty(dim, device=q.device) if need_dw else None for _ in range(2)]
+        dw = [torch.empty(dim, dtype=torch.float32, device=q.device) if need_dw else None for _ in range(2)]
         on.keep(*dx, *dw)
         held, ws, nbytes = _workspace(workspace if need_dw else None,
                                       lambda: lg.gemm_qk_norm_rope_bwd_workspace_size(code, tokens, heads, k.shape[1], dim), q.device)
