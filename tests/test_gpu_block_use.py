@@ -1,0 +1,427 @@
+"""The product with bias, activation and residual, and the norm and rotation of heads, as programs use them: through autograd, on
+other streams, captured into graphs, far apart in memory, few rows on tiles, and together in a block."""
+import importlib.util
+import os
+
+import pytest
+import torch
+
+from block_util import ACTS
+from gpu_util import DEV, say
+from ops_util import DT
+from test_gpu_block import EPS, at, check_heads, check_heads_bwd, check_linear, check_linear_bwd, gen, gh, heads_inputs, linear_inputs, stream
+from tiled_stage_software_amd import libgemm as lg, ops
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    lg.load()  # fails loudly if the library is missing
+    torch.zeros(1, device=DEV)
+
+
+@pytest.fixture(scope="module")
+def workspace():
+    return torch.full((96 << 20,), 0x7F, dtype=torch.uint8, device=DEV)
+
+
+def on_gpu(ts):
+    return [t.to(DEV) if t is not None else None for t in ts]
+
+
+# ------------------------------------------------------------------ few rows on tiles
+@pytest.mark.parametrize("M,N,K", [(5, 352, 16000), (16, 640, 15001), (32, 352, 16000), (17, 4100, 8200), (32, 16500, 1024), (9, 33000, 512)])
+def test_linear_of_few_rows_on_tiles(M, N, K, workspace):
+    """The sizes where tiles with splits of K take few rows, with a workspace and without."""
+    for i, (pad, ws) in enumerate(((0, workspace), (8, workspace), (3, workspace), (0, None))):
+        out = ("bf16", "f32")[i % 2]
+        a, w, b, r = linear_inputs(M, N, K, ("bf16", "f16")[i // 2] if out == "f32" else "bf16", out, M + N + i)
+        check_linear(a, w, b, ACTS[i], r, out, pads=(pad, pad, pad), ws=ws, keep=i % 2 == 0)
+
+
+# ------------------------------------------------------------------ autograd
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_linear_gradients_through_autograd(act, out):
+    """What linear_backward gives, to the bit, in the types of the leaves."""
+    a, w, b, r = on_gpu(linear_inputs(70, 136, 100, "bf16", out, 3, "f32" if act == "relu" else "in"))
+    y0, z = ops.linear_keeping(a, w, b, act, r, DT[out])
+    leaves = [t.clone().requires_grad_() for t in (a, w, b, r)]
+    y = ops.linear(leaves[0], leaves[1], leaves[2], act, leaves[3], DT[out])
+    assert torch.equal(y, y0) and torch.equal(ops.linear(a, w, b, act, r, DT[out]), y0)
+    g = torch.randn(136, 70, generator=gen(4)).to(DEV, DT[out]).t()          # rows that are not contiguous
+    want = ops.linear_backward(g.contiguous(), a, w, z if act != "none" else None, act)
+    got = torch.autograd.grad(y, leaves, g, retain_graph=True)
+    for t, leaf, ref in zip(got, leaves, (want[0], want[1], want[2].to(b.dtype), g)):
+        assert t.dtype == leaf.dtype and torch.equal(t, ref)
+    one = torch.ones((), device=DEV, dtype=DT[out]).expand(70, 136)          # what a sum hands back
+    want = ops.linear_backward(one.contiguous(), a, w, z if act != "none" else None, act)
+    for _ in range(2):
+        got = torch.autograd.grad(y.sum(), leaves[:2], retain_graph=True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for some in ((0,), (1,), (2,), (3,), (0, 2), (1, 3)):                    # leaves that want gradients
+        mixed = [t.clone().requires_grad_(i in some) for i, t in enumerate((a, w, b, r))]
+        y = ops.linear(mixed[0], mixed[1], mixed[2], act, mixed[3], DT[out])
+        full = ops.linear_backward(g.contiguous(), a, w, z if act != "none" else None, act)
+        got = torch.autograd.grad(y, [mixed[i] for i in some], g)
+        for i, t in zip(some, got):
+            assert torch.equal(t, (full[0], full[1], full[2].to(b.dtype), g)[i])
+
+
+def test_linear_without_bias_and_residual_through_autograd():
+    a, w, _, _ = on_gpu(linear_inputs(40, 72, 64, "f16", "f16", 5, None, False))
+    x, v = a.clone().requires_grad_(), w.clone().requires_grad_()
+    y = ops.linear(x, v, act="silu")
+    z = ops.linear_keeping(a, w, act="silu")[1]
+    g = torch.randn(40, 72, device=DEV).half()
+    want = ops.linear_backward(g, a, w, z, "silu")
+    got = torch.autograd.grad(y, (x, v), g)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with torch.no_grad():
+        assert not ops.linear(x, v).requires_grad
+    y = ops.linear(x, v)                                                     # a second derivative is refused
+    (d,) = torch.autograd.grad(y, x, g, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(d.sum(), v)
+    y = ops.linear(x[:0], v)                                                 # no rows
+    assert y.shape == (0, 72)
+    got = torch.autograd.grad(y, (x, v), y.detach())
+    assert bool((got[0] == 0).all()) and bool((got[1] == 0).all())
+
+
+@pytest.mark.parametrize("pairs", ["halves", "neighbours"])
+def test_heads_gradients_through_autograd(pairs):
+    q, k, w, pos, angles = heads_inputs(37, 5, 2, 64, 32, "bf16", "bf16", 6)
+    qkv = torch.cat([q, k, k.flip(0)], 1).to(DEV)
+    w, pos, (cos, sin) = on_gpu(w), pos.to(DEV), on_gpu(angles)
+    leaf = qkv.clone().requires_grad_()
+    ws = [t.clone().requires_grad_() for t in w]
+    out = ops.qk_norm_rope(leaf[:, :5], leaf[:, 5:7], *ws, pos, cos, sin, pairs, EPS)
+    plain = ops.qk_norm_rope(qkv[:, :5], qkv[:, 5:7], *w, pos, cos, sin, pairs, EPS)
+    assert all(torch.equal(a, b) for a, b in zip(out, plain))
+    dq = torch.randn(5, 37, 64, device=DEV).bfloat16().transpose(0, 1)
+    dk = torch.randn(1, device=DEV).bfloat16().expand(37, 2, 64)
+    want = ops.qk_norm_rope_backward(dq.contiguous(), dk.contiguous(), qkv[:, :5], qkv[:, 5:7], *w, pos, cos, sin, pairs, EPS)
+    got = torch.autograd.grad(out, [leaf, *ws], (dq, dk), retain_graph=True)
+    assert torch.equal(got[0][:, :5], want[0]) and torch.equal(got[0][:, 5:7], want[1]) and bool((got[0][:, 7:] == 0).all())
+    assert torch.equal(got[1], want[2].bfloat16()) and torch.equal(got[2], want[3].bfloat16())
+    # one result used, one weight wanted
+    got = torch.autograd.grad(out[0], ws, dq, retain_graph=True)
+    zero = torch.zeros(37, 2, 64, device=DEV, dtype=BF)
+    want = ops.qk_norm_rope_backward(dq.contiguous(), zero, qkv[:, :5], qkv[:, 5:7], *w, pos, cos, sin, pairs, EPS)
+    assert torch.equal(got[0], want[2].bfloat16()) and bool((got[1] == 0).all())
+    # one weight for both, and none
+    both = w[0].clone().requires_grad_()
+    a = ops.qk_norm_rope(qkv[:, :5], qkv[:, 5:7], both, both, pos, cos, sin, pairs, EPS)
+    (got,) = torch.autograd.grad(a, both, (dq, dk))
+    want = ops.qk_norm_rope_backward(dq.contiguous(), dk.contiguous(), qkv[:, :5], qkv[:, 5:7], w[0], w[0], pos, cos, sin, pairs, EPS)
+    assert torch.equal(got, want[2].bfloat16() + want[3].bfloat16())
+    leaf = qkv.clone().requires_grad_()
+    a = ops.qk_norm_rope(leaf[:, :5], leaf[:, 5:7], eps=EPS)
+    (got,) = torch.autograd.grad(a, leaf, (dq, dk))
+    want = ops.qk_norm_rope_backward(dq.contiguous(), dk.contiguous(), qkv[:, :5], qkv[:, 5:7], eps=EPS, need_dw=False)
+    assert torch.equal(got[:, :5], want[0]) and want[2] is None
+    with pytest.raises(ValueError):
+        ops.qk_norm_rope(leaf[:, :5], leaf[:, 5:7], positions=pos, cos=cos.clone().requires_grad_(), sin=sin)
+
+
+# ------------------------------------------------------------------ streams and graphs
+def part_inputs(rows, seed):
+    """x, residual, weights and positions of a block's dense parts."""
+    g = gen(seed)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    return on_gpu([r(rows, 256).bfloat16(), r(rows, 256).bfloat16(), (r(7 * 64, 256) / 16).bfloat16(), r(7 * 64), 1 + 0.1 * r(64), 1 + 0.1 * r(64),
+                   (r(256, 320) / 18).bfloat16(), torch.randint(0, 90, (rows,), generator=g), r(rows, 256).bfloat16(), r(rows, 5, 64).bfloat16(),
+                   r(rows, 2, 64).bfloat16()])
+
+
+TABLE = {}
+
+
+def parts(x, res, wqkv, bias, wq, wk, wo, pos, dy, dq, dk, ws="auto", stream=None):
+    """QKV product, norm and rotation, a product with activation and residual, and the backward passes of all."""
+    if not TABLE:
+        TABLE["at"] = ops.rope_table(90, 48, device=DEV)
+    cos, sin = TABLE["at"]
+    on = dict(workspace=ws, stream=stream)
+    qkv = ops.linear(x, wqkv, bias, out_dtype=BF, **on)
+    heads = qkv.unflatten(1, (7, 64))
+    q, k = ops.qk_norm_rope(heads[:, :5], heads[:, 5:], wq, wk, pos, cos, sin, stream=stream)
+    y, z = ops.linear_keeping(q.flatten(1), wo, None, "gelu", res, **on)
+    back = ops.linear_backward(dy, q.flatten(1), wo, z, "gelu", **on)
+    of_heads = ops.qk_norm_rope_backward(dq, dk, heads[:, :5], heads[:, 5:], wq, wk, pos, cos, sin, **on)
+    last = ops.linear_backward(qkv, x, wqkv, dw_dtype=torch.float32, **on)
+    return (qkv, q, k, y, z, *back, *of_heads, *last)
+
+
+@pytest.mark.parametrize("rows", [1, 70, 600])
+def test_other_streams_and_the_same_bits(rows, workspace):
+    args = part_inputs(rows, 1)
+    want = parts(*args)
+    again = parts(*args)
+    kept = parts(*args, ws=workspace)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    by_handle = parts(*args, stream=side.cuda_stream)
+    with torch.cuda.stream(side):
+        current = parts(*args)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    for i, (a, *others) in enumerate(zip(want, again, kept, by_handle, current)):
+        for b in others:
+            assert torch.equal(a, b), i
+
+
+def test_tensors_dropped_while_another_stream_still_reads_them():
+    """Inputs and results of a call on another stream may be dropped at once: what the caller's stream allocates next does
+    not lie in them before that stream has passed."""
+    side = torch.cuda.Stream()
+    a, w, b, _ = on_gpu(linear_inputs(2048, 4096, 4096, "bf16", "bf16", 2))
+    want = ops.linear(a, w, b, act="gelu")
+    torch.cuda.synchronize()
+    for _ in range(3):
+        x = a.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        y = ops.linear(x, w, b, act="gelu", stream=side.cuda_stream)
+        del x
+        junk = torch.full((2048, 4096), float("nan"), device=DEV, dtype=BF)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(y, want)
+        del y, junk
+
+
+@pytest.mark.parametrize("rows", [1, 70, 600])
+def test_graph_replays(rows):
+    """Captured once, replayed with new inputs and eager work between: the eager results."""
+    args = part_inputs(rows, 1)
+    parts(*args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = parts(*args)
+    for seed in (2, 3, 4):
+        for t, v in zip(args, part_inputs(rows, seed)):
+            t.copy_(v)
+        want = parts(*args)
+        torch.cuda.synchronize()
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(out, want)):
+            assert torch.equal(a, b), (seed, i)
+
+
+def test_two_graphs_share_a_workspace(workspace):
+    """Nothing in a workspace outlives its call: graphs replayed in turn on one stream may have one between them."""
+    sizes = (70, 600)
+    args = [part_inputs(n, n) for n in sizes]
+    want = [parts(*a) for a in args]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for a in args:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(parts(*a, ws=workspace))
+    for turn in (0, 1, 0, 0, 1):
+        for t in outs[turn]:
+            t.zero_()
+        workspace.fill_(0x7F)
+        graphs[turn].replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(outs[turn], want[turn])):
+            assert torch.equal(a, b), (turn, i)
+
+
+def step(x, wqkv, bias, wq, wk, wo, res, pos):
+    """Gradients of a loss by autograd, from leaves of its own."""
+    leaves = [t.detach().requires_grad_() for t in (x, wqkv, bias, wq, wk, wo, res)]
+    heads = ops.linear(leaves[0], leaves[1], leaves[2]).unflatten(1, (7, 64))
+    q, k = ops.qk_norm_rope(heads[:, :5], heads[:, 5:], leaves[3], leaves[4], pos, *TABLE["at"])
+    y = ops.linear(q.flatten(1), leaves[5], None, "gelu_tanh", leaves[6])
+    return torch.autograd.grad((y, k), leaves, (y.detach(), k.detach()))
+
+
+def test_training_step_in_a_graph():
+    """The backward pass through autograd, captured with its forward pass and replayed."""
+    x, res, wqkv, bias, wq, wk, wo, pos, *_ = args = part_inputs(70, 5)
+    parts(*args)   # (the table)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(x, wqkv, bias, wq, wk, wo, res, pos)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(x, wqkv, bias, wq, wk, wo, res, pos)
+    for seed in (6, 7, 8):
+        for t, v in zip(args, part_inputs(70, seed)):
+            t.copy_(v)
+        want = step(x, wqkv, bias, wq, wk, wo, res, pos)
+        torch.cuda.synchronize()
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(out, want)):
+            assert torch.equal(a, b), (seed, i)
+
+
+# ------------------------------------------------------------------ far apart and large
+def far(rows, cols, ld, dtype, fill=None):
+    """rows x cols with rows ld elements apart, which nothing between them is read or written for."""
+    t = torch.empty((rows - 1) * ld + cols, dtype=dtype, device=DEV).as_strided((rows, cols), (ld, 1))
+    t.copy_(fill.to(DEV) if fill is not None else torch.zeros(rows, cols, dtype=dtype))
+    return t
+
+
+@pytest.mark.parametrize("M,N,K,ld", [(70, 40, 100, (1 << 25) + 8), (3, 40, 200, (1 << 31) + 8), (300, 260, 128, 1 << 21), (300, 260, 136, (1 << 21) + 3)])
+def test_linear_of_rows_far_apart(M, N, K, ld):
+    """Pitches with which offsets pass 32 bits: what the same rows give close together."""
+    a, w, b, r = linear_inputs(M, N, K, "bf16", "bf16", 9)
+    check_linear(a, w, b, "gelu", r, "bf16")
+    A, R, C, Z = far(M, K, ld, BF, a), far(M, N, ld, BF, r), far(M, N, ld, BF), far(M, N, ld, BF)
+    W = far(N, K, ld, BF, w) if ld < 1 << 26 else w.to(DEV)
+    call = lambda A, W, R, Z, C: lg.check(lg.gemm_linear(lg.GEMM_BF16, M, N, K, at(A), A.stride(0), at(W), W.stride(0), at(B), lg.GEMM_BF16, 2, at(R),  # noqa: E731
+                                                         R.stride(0), at(Z), Z.stride(0), at(C), lg.GEMM_BF16, C.stride(0), 0, 0, stream()))
+    B = b.to(DEV)
+    call(A, W, R, Z, C)
+    near = [t.contiguous() for t in (A, W, R, Z, C)]
+    call(*near)
+    # (the kernels may differ in the order of their sums: within the roundings of the results)
+    for got, ref in ((C, near[4]), (Z, near[3])):
+        assert bool(((got.float() - ref.float()).abs() <= 2.0 ** -7 * ref.float().abs() + 1e-5).all())
+    dA, dW, db = far(M, K, ld, BF), torch.empty(N, K, device=DEV), torch.empty(N, device=DEV)
+    lg.check(lg.gemm_linear_bwd(lg.GEMM_BF16, M, N, K, 2, at(C), lg.GEMM_BF16, ld, at(Z), ld, at(A), ld, at(W), W.stride(0), at(R), ld, at(dA), ld,
+                                at(dW), lg.GEMM_F32, K, at(db), 0, 0, stream()))
+    want = ops.linear_backward(C.contiguous(), A.contiguous(), W.contiguous(), Z.contiguous(), "gelu", dw_dtype=torch.float32)
+    # (sums of the same rounded dZ in another order: of M or N terms, each rounding 2^-24 of their magnitudes)
+    for got, ref, terms in ((dA, want[0], N), (dW, want[1], M), (db, want[2], M)):
+        size = float(ref.float().abs().max())
+        assert float((got.float() - ref.float()).abs().max()) <= size * (2.0 ** -8 + terms * 2.0 ** -20)
+
+
+def test_linear_of_more_elements_than_32_bits_count():
+    """C, Z, dZ and the residual have more than 2^31 elements: small whole numbers, exact in every step."""
+    M, N, K = 40008, 60000, 64
+    g = torch.Generator(DEV).manual_seed(1)
+    a = torch.randint(-2, 3, (M, K), generator=g, device=DEV).bfloat16()
+    w = torch.randint(-1, 2, (N, K), generator=g, device=DEV).bfloat16()
+    y, z = ops.linear_keeping(a, w, act="relu")
+    rows = torch.tensor([0, 1, 35791, 35792, 39999, M - 1], device=DEV)
+    want = a[rows].float() @ w.float().t()
+    assert torch.equal(z[rows].float(), want) and torch.equal(y[rows].float(), want.relu())
+    y = ops.linear(a, w, residual=y)
+    assert torch.equal(y[rows].float(), want + want.relu())
+    del y
+    dy = torch.ones((), device=DEV, dtype=BF).expand(M, N).contiguous()
+    dx, dw, db = ops.linear_backward(dy, a, w, z, "relu", dw_dtype=torch.float32)
+    assert torch.equal(dx[rows], ((want > 0).float() @ w.float()).bfloat16())
+    for c0 in (0, 30000, N - 500):
+        d = (a.float() @ w[c0:c0 + 500].float().t() > 0).float()
+        assert torch.equal(db[c0:c0 + 500], d.sum(0)) and torch.equal(dw[c0:c0 + 500], d.t().contiguous() @ a.float())
+
+
+@pytest.mark.parametrize("hs,ld", [((1 << 24) + 8, 72), (1 << 26, 64), (64, (1 << 31) + 64), (80, 1 << 30)])
+def test_heads_far_apart(hs, ld):
+    """Heads and tokens whose offsets pass 32 bits: the bits of the same ones close together."""
+    T, HQ, HK, D = 3, 5, 2, 64
+    q, k, w, pos, angles = heads_inputs(T, HQ, HK, D, 32, "bf16", "f32", 8)
+    w, pos, (cos, sin) = on_gpu(w), pos.to(DEV), on_gpu(angles)
+
+    def place(v):
+        n = (T - 1) * ld + (v.shape[1] - 1) * hs + D
+        t = torch.empty(n, dtype=BF, device=DEV).as_strided(v.shape, (ld, hs, 1))
+        t.copy_(v)
+        return t
+
+    near = ops.qk_norm_rope(q.to(DEV), k.to(DEV), *w, pos, cos, sin)
+    Q, K, OQ, OK = place(q), place(k), place(torch.zeros_like(q)), place(torch.zeros_like(k))
+    rope = lg.GemmRope(at(pos), at(cos), at(sin), cos.stride(0), cos.shape[0], 32, 0)
+    lg.check(lg.gemm_qk_norm_rope(lg.GEMM_BF16, lg.GEMM_F32, T, HQ, HK, D, 1e-6, gh(Q), gh(K), at(w[0]), at(w[1]), rope, gh(OQ), gh(OK), stream()))
+    tol = lambda got, ref: bool(((got.float() - ref.float()).abs() <= 2.0 ** -7 * ref.float().abs() + 1e-5).all())  # noqa: E731
+    assert tol(OQ, near[0]) and tol(OK, near[1])   # (the lanes of a head differ, and the order of its sum: a rounding of the result)
+    dq, dk = torch.randn(T, HQ, D, device=DEV).bfloat16(), torch.randn(T, HK, D, device=DEV).bfloat16()
+    want = ops.qk_norm_rope_backward(dq, dk, q.to(DEV), k.to(DEV), *w, pos, cos, sin)
+    DQ, DK, dw = place(dq), place(dk), torch.empty(2, D, device=DEV)
+    lg.check(lg.gemm_qk_norm_rope_bwd(lg.GEMM_BF16, lg.GEMM_F32, T, HQ, HK, D, 1e-6, gh(DQ), gh(DK), gh(Q), gh(K), at(w[0]), at(w[1]), rope, gh(OQ),
+                                      gh(OK), at(dw[0]), at(dw[1]), 0, 0, stream()))
+    assert tol(OQ, want[0]) and tol(OK, want[1])
+    assert torch.allclose(dw[0], want[2], rtol=1e-4, atol=1e-4) and torch.allclose(dw[1], want[3], rtol=1e-4, atol=1e-4)
+
+
+def test_heads_of_more_elements_than_32_bits_count():
+    T, H, D = 140000, 120, 128
+    q = torch.randn(T, H, D, device=DEV, dtype=BF)
+    k = torch.randn(T, 1, D, device=DEV, dtype=BF)
+    pos = torch.arange(T, device=DEV) % 1000
+    cos, sin = ops.rope_table(1000, D, device=DEV)
+    w = 1 + 0.1 * torch.randn(D, device=DEV)
+    out = ops.qk_norm_rope(q, k, w, w, pos, cos, sin)
+    rows = torch.tensor([0, 1, 69905, 69906, 139809, 139811, T - 1], device=DEV)
+    some = ops.qk_norm_rope(q[rows], k[rows], w, w, pos[rows], cos, sin)
+    assert torch.equal(out[0][rows], some[0]) and torch.equal(out[1][rows], some[1])
+    back = ops.qk_norm_rope_backward(out[0], out[1], q, k, w, w, pos, cos, sin)
+    of = ops.qk_norm_rope_backward(some[0], some[1], q[rows], k[rows], w, w, pos[rows], cos, sin)
+    assert torch.equal(back[0][rows], of[0]) and torch.equal(back[1][rows], of[1])
+
+
+def test_small_pieces_of_a_workspace(workspace):
+    """Whatever bytes there are, the results stay within their tolerances."""
+    for nbytes in (256, 4096, 1 << 16, 1 << 20):
+        ws = workspace[:nbytes]
+        a, w, b, r = linear_inputs(100, 140, 1003, "bf16", "f32", 1)
+        check_linear(a, w, b, "silu", r, "f32", ws=ws)
+        check_linear_bwd(100, 140, 1003, "bf16", "gelu", ws=ws)
+        q, k, wt, pos, angles = heads_inputs(50, 4, 2, 80, 40, "f16", "f32", 2)
+        check_heads_bwd(q, k, wt, pos, angles, "halves", ws=ws)
+        check_heads(q, k, wt, pos, angles, "halves")
+
+
+# ------------------------------------------------------------------ together
+def plain_block(block, x):
+    """The example's block in 64 bits."""
+    p = {n: t.detach().double().requires_grad_() for n, t in block.parameters.items()}
+    D, H, G = block.dim, block.heads, block.groups
+    x = x.detach().double().requires_grad_()
+    T = x.shape[0]
+    norm = lambda v, w: v * (v.square().mean(-1, keepdim=True) + 1e-6).rsqrt() * w  # noqa: E731
+    cos, sin = block.cos[:T, None].double(), block.sin[:T, None].double()
+
+    def turn(v):
+        a, b = v.split(D // 2, -1)
+        return torch.cat([a * cos - b * sin, b * cos + a * sin], -1)
+
+    qkv = (norm(x, p["norm1"]) @ p["qkv"].t() + p["qkv_bias"]).unflatten(1, (-1, D))
+    q, k, v = qkv.split([H, G, G], 1)
+    q, k = turn(norm(q, p["q_norm"])), turn(norm(k, p["k_norm"])).repeat_interleave(H // G, 1)
+    s = torch.einsum("thd,shd->hts", q, k) / D ** 0.5
+    s = s.masked_fill(torch.ones(T, T, dtype=torch.bool, device=x.device).triu(1), float("-inf")).softmax(2)
+    y = x + torch.einsum("hts,shd->thd", s, v.repeat_interleave(H // G, 1)).flatten(1) @ p["proj"].t()
+    y = y + torch.nn.functional.gelu(norm(y, p["norm2"]) @ p["up"].t() + p["up_bias"]) @ p["down"].t()
+    return y, dict(x=x, **p)
+
+
+def test_example_block():
+    """The example runs, and its gradients are the formulas'.  A path from the loss to a leaf passes at most 24 tensors that
+    are rounded to bf16, each off by up to 2^-8 of its values, and sums of branches whose errors add up to at most twice
+    their result's: 24 * 2^-8 * 2 < 0.2 of a gradient's norm.  A token served alone passes other kernels, whose sums
+    have another order: the same roundings, of 16 tensors on the way to the result."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "dense_block.py")
+    spec = importlib.util.spec_from_file_location("dense_block", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    block, x, dy, out, served, of = example.main(["--width", "256", "--wide", "520", "--heads", "4", "--groups", "2", "--prompt", "45", "--tokens", "3"])
+    y, leaves = plain_block(block, x)
+    off = lambda a, b: float((a.double() - b).norm() / b.norm())  # noqa: E731
+    assert off(out, y.detach()) < 16 * 2.0 ** -8
+    assert off(served, out.double()) < 16 * 2.0 ** -8
+    want = dict(zip(leaves, torch.autograd.grad(y, list(leaves.values()), dy.double())))
+    for name, g in of.items():
+        say(f"[block] d{name}: {off(g, want[name]):.4f} from 64 bits")
+        assert off(g, want[name]) < 0.2, name
