@@ -91,11 +91,13 @@ __global__ __launch_bounds__(kCols / 8 * kLanes) void linear_bwd_kernel(const Li
 
 }  // namespace
 
-// Runs of 32 rows at least (four rounds of a thread's loads), and no more than fill the card a few times over.
+// Runs of 32 rows at least (four rounds of a thread's loads), of half as many while that leaves compute units empty, and no more than fill
+// the card a few times over.
 int linear_bwd_parts(int64_t M, int64_t N) {
-    const int64_t strips = (N + kCols - 1) / kCols, most = 8 * (int64_t)num_compute_units();
-    const int64_t want = std::max<int64_t>(1, most / std::max<int64_t>(1, strips)), rows = (M + 31) / 32;
-    return (int)std::max<int64_t>(1, std::min(want, rows));
+    const int64_t strips = std::max<int64_t>(1, (N + kCols - 1) / kCols), cu = num_compute_units();
+    int64_t run = 32;
+    while (run > kLanes && strips * ((M + run / 2 - 1) / (run / 2)) <= cu * 3 / 4) run /= 2;
+    return (int)std::max<int64_t>(1, std::min(8 * cu / strips, (M + run - 1) / run));
 }
 
 hipError_t launch_linear_bwd(int in_type, const LinearBwdParams& p, hipStream_t st) {
