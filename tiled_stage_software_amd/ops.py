@@ -4,7 +4,9 @@ weights (which have none); and of a transformer block's dense parts, with their 
 product with bias, activation and residual, and the norm of queries and keys with the rotation by position.
 
 As ``libgemm.matmul``, these only read shapes, strides and pointers; every step on the
-GPU runs in the library's kernels, and there is no fallback.  ``quantize_f8`` and
+GPU runs in the library's kernels, and there is no fallback.  Calls may be captured into graphs; a
+backward pass through autograd with its forward pass, from leaves that no graph made before still
+holds (torch ties a leaf's gradient to that one's stream, which a capture must not meet).  ``quantize_f8`` and
 ``quantize_w4`` prepare weights once, in plain torch, on any device.
 """
 from __future__ import annotations
