@@ -425,3 +425,43 @@ def test_example_block():
     for name, g in of.items():
         say(f"[block] d{name}: {off(g, want[name]):.4f} from 64 bits")
         assert off(g, want[name]) < 0.2, name
+
+
+# ------------------------------------------------------------------ the ends of the sizes
+@pytest.mark.parametrize("M,N,K", [(2, (1 << 24) + 40, 16), ((1 << 18) + 300, 40, 32), (50, (1 << 18) + 72, 32), (3, (1 << 24) + 9, 5)])
+def test_linear_in_several_launches(M, N, K):
+    """Sizes that a launch's grid or counts do not hold: small whole numbers, exact."""
+    g = torch.Generator(DEV).manual_seed(N)
+    draw = lambda *s: torch.randint(-3, 4, s, generator=g, device=DEV).bfloat16()  # noqa: E731
+    a, w, b, r = draw(M, K), draw(N, K), draw(N), draw(M, N)
+    y, z = ops.linear_keeping(a, w, b, "relu", r)
+    want = a.float() @ w.float().t() + b.float()
+    assert torch.equal(z, want.bfloat16()) and torch.equal(y, (want.relu() + r.float()).bfloat16())
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 0, 7), (5, 40, 0), (0, 40, 24), (0, 0, 0), (5, 0, 0)])
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_linear_backward_of_empty_sides(M, N, K, act):
+    new = lambda *s: torch.randn(*s, device=DEV).bfloat16()  # noqa: E731
+    a, w, b = (new(*s).requires_grad_() for s in ((M, K), (N, K), (N,)))
+    y = ops.linear(a, w, b, act)
+    dy = new(M, N)
+    da, dw, db = torch.autograd.grad(y, (a, w, b), dy)
+    assert da.shape == a.shape and dw.shape == w.shape and bool((da == 0).all()) and bool((dw == 0).all())
+    z = b.detach().double().expand(M, N).requires_grad_()
+    f = torch.nn.functional.gelu(z) if act == "gelu" else z * 1
+    (dz,) = torch.autograd.grad(f, z, dy.double())
+    assert bool(((db.double() - dz.sum(0)).abs() <= 2.0 ** -8 * dz.sum(0).abs() + 2.0 ** -16 * dz.abs().sum(0)).all())
+
+
+def test_heads_of_empty_sides():
+    cos, sin = ops.rope_table(4, 8, device=DEV)
+    for T, HQ, HK in ((0, 3, 2), (4, 0, 2), (4, 3, 0), (4, 0, 0)):
+        q, k = torch.randn(T, HQ, 16, device=DEV), torch.randn(T, HK, 16, device=DEV)
+        w = [torch.ones(16, device=DEV, requires_grad=True) for _ in range(2)]
+        pos = torch.arange(T, device=DEV)
+        out = ops.qk_norm_rope(q, k, *w, pos, cos, sin)
+        assert out[0].shape == q.shape and out[1].shape == k.shape
+        dw = torch.autograd.grad(out, w, (torch.ones_like(q), torch.ones_like(k)))
+        for t, heads in zip(dw, (HQ, HK)):
+            assert bool((t == 0).all()) == (T * heads == 0)
