@@ -25,8 +25,8 @@ gemm_status_t check_linear(int in_type, int act, int64_t M, int64_t N, int64_t K
 // Whether the kernel for few rows takes a product.  Its workgroups' waves are bound by the steps of K that a compute unit has to take, and
 // more so from rows that do not start at cache lines, where tiles have splits of K and fewer bytes of A to load.  Measured
 // (bf16, microseconds, few rows / tiles): 32 rows 4096 x 4096 (64 steps) 10.5 / 12.6, 1152 x 12608 (197) 19.3 / 13.7, 4096 x 14336
-// (224) 31.9 / 27.2, 32768 x 2048 (256) 49 / 33; 16 rows 14336 x 4096 (224) 27.7 / 31.8, 352 x 16000 (250) 15.0 / 11.4, rows 16 bytes
-// further apart 35.8 / 28.9 and 20.1 / 12.7; one row 8044 x 15920 (490) 49 / 51.  Without the workspace that tiles ask for, always.
+// (224) 31.9 / 27.2, 14336 x 4096 (224) 39 / 27, 32768 x 2048 (256) 49 / 29; 16 rows 14336 x 4096 about even, 352 x 16000 (250) 15.0 /
+// 11.4, rows 16 bytes further apart 35.8 / 28.9 and 20.1 / 12.7; one row 8044 x 15920 (490) 49 / 51.  Without the workspace that tiles ask for, always.
 bool linear_few(const LinearParams& p, bool lines, size_t ws_bytes) {   // lines: W's rows start at cache lines
     if (p.M > kLinearSkinnyRows || p.K < 1) return false;
     const double steps = std::max(1.0, p.N / 16.0 / num_compute_units()) * p.K / 64.0;
