@@ -194,6 +194,26 @@ def test_tensors_dropped_while_another_stream_still_reads_them():
         del y, junk
 
 
+def test_gradients_on_another_stream():
+    """Forward on a stream given by its handle: the backward pass runs there too, and the caller's stream waits for it."""
+    x, res, wqkv, bias, wq, wk, wo, pos, dy, dq, dk = part_inputs(600, 3)
+    cos, sin = ops.rope_table(90, 48, device=DEV)
+
+    def grads(stream):
+        leaves = [t.clone().requires_grad_() for t in (x, wqkv, bias, wq, wk)]
+        torch.cuda.synchronize()
+        heads = ops.linear(leaves[0], leaves[1], leaves[2], "silu", stream=stream).unflatten(1, (7, 64))
+        out = ops.qk_norm_rope(heads[:, :5], heads[:, 5:], leaves[3], leaves[4], pos, cos, sin, stream=stream)
+        return torch.autograd.grad(out, leaves, (dq, dk))
+
+    side = torch.cuda.Stream()
+    want = grads(None)
+    got = grads(side.cuda_stream)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("rows", [1, 70, 600])
 def test_graph_replays(rows):
     """Captured once, replayed with new inputs and eager work between: the eager results."""
