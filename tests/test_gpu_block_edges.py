@@ -1,0 +1,56 @@
+"""Ends of a transformer block's dense parts on the GPU: infinite weights where the depth ends inside a slab."""
+import pytest
+import torch
+
+from gpu_util import DEV
+from test_gpu_block import gen, run_linear
+from tiled_stage_software_amd import libgemm as lg
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    lg.load()  # fails loudly if the library is missing
+    torch.zeros(1, device=DEV)
+
+
+@pytest.fixture(scope="module")
+def workspace():
+    return torch.full((96 << 20,), 0x7F, dtype=torch.uint8, device=DEV)
+
+
+#          few rows (one to four, a block, two blocks; eight waves and sixteen), tiles of 64 and of 128 rows, depths below a slab
+INFINITE = [(3, 70, 72), (3, 70, 2049), (13, 96, 72), (13, 96, 1100), (20, 96, 72), (20, 96, 2049), (20, 9000, 130), (40, 96, 72),
+            (64, 300, 1000), (200, 260, 72), (333, 401, 2049), (260, 300, 129), (200, 96, 40)]
+
+
+@pytest.mark.parametrize("M,N,K", INFINITE)
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_infinite_weights_reach_their_columns_alone(M, N, K, t, workspace):
+    """Elements that a last slab reads for the second time count once: an infinite weight among them makes its column's sums
+    infinite (not NaN), a NaN makes them NaN, and the other columns keep their bits."""
+    dtype = torch.bfloat16 if t == "bf16" else torch.float16
+    g = gen(M + N + K)
+    a = (torch.rand(M, K, generator=g) + 0.1).to(dtype)
+    w = (torch.randn(N, K, generator=g) / K ** 0.5).to(dtype)
+    inf = float("inf")
+    odd = {5: (max(K // 64 * 64 - 1, 0), inf), 6: (max(K - 64, 0), -inf), 17: (max(K - 60, 0), float("nan")), 33: (K - 1, inf), 34: (0, -inf)}
+    v = w.clone()
+    for n, (k, x) in odd.items():
+        v[n, k] = x
+    keep = [n for n in range(N) if n not in odd]
+    for pad in (0, 8, 3):
+        for ws in (workspace, None):
+            for act in ("none", "silu"):
+                clean, clean_z = run_linear(a, w, None, act, None, t, pads=(pad, pad, 0), ws=ws)
+                C, Z = run_linear(a, v, None, act, None, t, pads=(pad, pad, 0), ws=ws)
+                assert torch.equal(C[:, keep], clean[:, keep]) and torch.equal(Z[:, keep], clean_z[:, keep])
+                for n, (k, x) in odd.items():
+                    if x != x:
+                        assert bool(torch.isnan(C[:, n].float()).all() and torch.isnan(Z[:, n].float()).all()), (n, pad, act, ws is None)
+                    else:
+                        limit = x if act == "none" or x > 0 else 0.0
+                        assert bool((Z[:, n] == x).all() and (C[:, n] == limit).all()), (n, pad, act, ws is None)

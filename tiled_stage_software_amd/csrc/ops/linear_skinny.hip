@@ -8,8 +8,8 @@
 //
 // 1 x 14336 x 4096 bf16 with gelu: 23.3 us, 5.0 TB/s.
 //
-// A last step that K does not fill is the row's last 128 bytes, with zeros in A for what earlier steps had.  The waves' sums
-// meet in LDS in wave order.
+// A last step that K does not fill is the row's last 128 bytes, with zeros in A and in W for what earlier steps had (an infinity
+// there times a zero would be NaN).  The waves' sums meet in LDS in wave order.
 #include "f8_common.hpp"
 #include "linear.hpp"
 
@@ -61,13 +61,16 @@ __global__ __launch_bounds__(64 * WAVES) void linear_skinny_kernel(const LinearP
     auto multiply = [&](int d, int64_t s) {
         const int had = (int)(s * kStep - first_byte(s));   // bytes that earlier steps had
         if (had > 0) {
+            u32x4 mask;   // the same chunk of every row
 #pragma unroll
-            for (int h = 0; h < AL; ++h)
+            for (int q = 0; q < 4; ++q) {
+                const int o = had - 16 * lc - 4 * q;
+                mask[q] = o >= 4 ? 0u : o <= 0 ? ~0u : ~0u << (8 * o);
+            }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int o = had - 16 * lc - 4 * q;
-                    a[d][h][q] &= o >= 4 ? 0u : o <= 0 ? ~0u : ~0u << (8 * o);
-                }
+            for (int h = 0; h < 2; ++h) b[d][h] &= mask;
+#pragma unroll
+            for (int h = 0; h < AL; ++h) a[d][h] &= mask;
         }
         wave_fence();
 #pragma unroll

@@ -77,7 +77,7 @@ struct LinearRingOps : MfmaCompute<T, BM, BN, kSlab, WM, WN, 16> {
 
 // Any pitch, alignment and K >= 64: 16-byte loads of any alignment into registers, two slabs ahead, written into the other
 // slot under the first half of a slab's products.  A last slab that K does not fill is the row's last 128 bytes, with zeros in
-// A for what earlier slabs had.  Rows past the end repeat the last.
+// A and in W for what earlier slabs had (an infinity there times a zero would be NaN).  Rows past the end repeat the last.
 template <typename T, int BM, int BN, int WM, int WN>
 struct LinearStagedOps : MfmaCompute<T, BM, BN, kSlab, WM, WN, 16> {
     typedef MfmaCompute<T, BM, BN, kSlab, WM, WN, 16> C;
@@ -119,7 +119,7 @@ struct LinearStagedOps : MfmaCompute<T, BM, BN, kSlab, WM, WN, 16> {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             u32x4 x = v[V][i];
-            if (i < CA && last) x &= mask;
+            if (last) x &= mask;
             *reinterpret_cast<LDS_AS u32x4*>(this->smem + slot * C::STAGE + dst + i * STEP * kSlabBytes) = x;
         }
     }
