@@ -235,10 +235,14 @@ gemm_status_t gemm_linear_bwd(gemm_dtype_t in_type, int64_t M, int64_t N, int64_
         REQUIRE(!dW || A || K == 0, "A is NULL");
     }
     if (!workspace) workspace_bytes = 0;
-    op_note("linear_bwd type %d M=%lld N=%lld K=%lld act=%d", (int)in_type, (long long)M, (long long)N, (long long)K, (int)act);
     if (N == 0 && (!dA || M == 0)) return GEMM_OK;
     const void* dz = dZ ? dZ : dC;
     BackwardPlan b = backward_plan(M, N, K, dz, dZ ? lddz : lddc, A, lda, W, ldw, dA, ldda, in_type, dW, lddw, dw_type, dbias != nullptr, workspace_bytes);
+    op_note("linear_bwd type %d M=%lld N=%lld K=%lld act=%d: dZ in %d parts%s%s%s", (int)in_type, (long long)M, (long long)N, (long long)K, (int)act,
+            b.parts, b.copies[0].src ? ", dZ copied" : "", b.copies[1].src ? ", A copied" : "", b.copies[2].src ? ", W copied" : "");
+    for (const GradParams& f : b.f)
+        if (f.C && b.tiles) op_note("  %d x %d x %d: %d x %d tiles, %d splits of the sum", f.M, f.N, f.K, f.bm, f.bn, f.splits);
+        else if (f.C) op_note("  %d x %d x %d: as a 16-bit product", f.M, f.N, f.K);
     char* at = static_cast<char*>(workspace) + b.sums;
     for (RowsJob& j : b.copies)
         if (j.src) {

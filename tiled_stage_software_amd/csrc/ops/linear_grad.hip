@@ -439,7 +439,6 @@ hipError_t launch_linear_grad(int in_type, const GradParams (&f)[2], const DbJoi
         x.b_cols = (q.N + 7) / 8 * 8;
         x.splits = q.splits;
         x.blocks = (uint32_t)(p.tiles_m * p.tiles_n * q.splits);
-        op_note("  %d x %d x %d: %d x %d tiles, %d splits of the sum", q.M, q.N, q.K, q.bm, q.bn, q.splits);
         if (q.splits > 1) {
             JoinSide& j = join[i];
             j.p = p;
