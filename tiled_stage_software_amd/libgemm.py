@@ -405,9 +405,14 @@ class Running:
     stream's memory, not from blocks that earlier work of the caller's stream may still use.  The
     tensors that the call is given are marked for that stream, and by ``keep`` its results for the
     caller's: either may be dropped at once."""
+    tangents = True   # False: inputs with forward-mode tangents are refused (``requires_grad`` says nothing of those)
 
     def __init__(self, stream, device, *given):
         import torch
+        if not self.tangents and getattr(torch.autograd.forward_ad, "_current_level", 0) >= 0:   # (hardly ever: a question takes 0.3 us)
+            for t in given:
+                if isinstance(t, torch.Tensor) and torch.autograd.forward_ad.unpack_dual(t).tangent is not None:
+                    raise NotImplementedError("the operators have no forward-mode derivatives: detach their inputs")
         if device.type != "cuda":
             raise ValueError(f"tensors on {device}: the kernels run on the GPU")
         self.caller = torch.cuda.current_stream(device)

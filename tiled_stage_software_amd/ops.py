@@ -6,8 +6,8 @@ product with bias, activation and residual, and the norm of queries and keys wit
 As ``libgemm.matmul``, these only read shapes, strides and pointers; every step on the
 GPU runs in the library's kernels, and there is no fallback.  Calls may be captured into graphs; a
 backward pass through autograd with its forward pass, from leaves that no graph made before still
-holds (torch ties a leaf's gradient to that one's stream, which a capture must not meet).  ``quantize_f8`` and
-``quantize_w4`` prepare weights once, in plain torch, on any device.
+holds (torch ties a leaf's gradient to that one's stream, which a capture must not meet).  Inputs with forward-mode
+tangents are refused.  ``quantize_f8`` and ``quantize_w4`` prepare weights once, in plain torch, on any device.
 """
 from __future__ import annotations
 
@@ -80,6 +80,11 @@ def _workspace(workspace, size, device):
             return None, 0, 0
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return workspace, *lg.workspace_of(workspace, device)
+
+
+class _Running(lg.Running):
+    """No operator has a forward-mode derivative, and kernels that read a dual tensor's memory would lose its tangent."""
+    tangents = False
 
 
 def _wants_gradient(*tensors) -> bool:
@@ -172,7 +177,7 @@ def rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None, st
     8-bit codes) and h reach x, weight and residual through ``rmsnorm_backward``."""
     if not _wants_gradient(x, weight, residual):
         return _rmsnorm(x, weight, residual, eps, out_dtype, stream)
-    with lg.Running(stream, x.device, x, weight, residual) as on:   # (its backward pass runs on the same stream)
+    with _Running(stream, x.device, x, weight, residual) as on:   # (its backward pass runs on the same stream)
         y, scale, h, rstd = _functions()[0].apply(x, weight, residual, eps, out_dtype)
         on.keep(y, scale, h, rstd)
     return RmsNorm(y, scale, x if h is None else h, rstd)
@@ -186,7 +191,7 @@ def _rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None, s
     w = _vector(weight, "weight", cols, (x.dtype, torch.float32), x.device)
     y_code = _code(out_dtype)
     ldr = _rows(residual, "residual", x.shape, x.dtype, x.device) if residual is not None else 0
-    with lg.Running(stream, x.device, x, weight, residual) as on:
+    with _Running(stream, x.device, x, weight, residual) as on:
         h, ldh = x, 0
         if ldr:
             h, ldh = torch.empty((rows, cols), dtype=x.dtype, device=x.device), max(cols, 1)
@@ -210,7 +215,7 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, need_dw: bool = True, workspa
     lddh = _rows(dh, "dh", h.shape, h.dtype, h.device) if dh is not None else 0
     w = _vector(weight, "weight", cols, (h.dtype, torch.float32), h.device)
     r = _vector(rstd, "rstd", rows, torch.float32, h.device)
-    with lg.Running(stream, h.device, dy, h, weight, rstd, dh, workspace) as on:
+    with _Running(stream, h.device, dy, h, weight, rstd, dh, workspace) as on:
         dx = torch.empty((rows, cols), dtype=h.dtype, device=h.device)
         dw = torch.empty(cols, device=h.device) if need_dw else None
         on.keep(dx, dw)
@@ -250,7 +255,7 @@ def matmul_f8(a, b, scale_a=None, scale_b=None, C=None, alpha: float = 1.0, beta
         raise ValueError(f"shapes {tuple(a.shape)} and {tuple(b.shape)}: rows of different lengths")
     sa = _vector(scale_a, "scale_a", M, torch.float32, a.device)
     sb = _vector(scale_b, "scale_b", N, torch.float32, a.device)
-    with lg.Running(stream, a.device, a, b, scale_a, scale_b, C, workspace) as on:
+    with _Running(stream, a.device, a, b, scale_a, scale_b, C, workspace) as on:
         C, ldc = _result(on, C, M, N, beta, out_dtype or torch.bfloat16, a.device)
         held, ws, nbytes = _workspace(workspace, lambda: lg.gemm_f8_workspace_size(M, N, K), a.device)
         lg.check(lg.gemm_f8(M, N, K, alpha, a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb, beta, C.data_ptr(), _code(C.dtype),
@@ -273,7 +278,7 @@ def matmul_w4(a, codes, scales, zeros=None, group: int = 128, C=None, alpha: flo
     if zeros is not None and _rows(zeros, "zeros", (N, groups), a.dtype, a.device) != lds:
         raise ValueError("zeros: the row stride of scales")
     code = _code(a.dtype)
-    with lg.Running(stream, a.device, a, codes, scales, zeros, C, workspace) as on:
+    with _Running(stream, a.device, a, codes, scales, zeros, C, workspace) as on:
         C, ldc = _result(on, C, M, N, beta, out_dtype or a.dtype, a.device)
         held, ws, nbytes = _workspace(workspace, lambda: lg.gemm_w4_workspace_size(code, M, N, K, group), a.device)
         lg.check(lg.gemm_w4(code, M, N, K, group, alpha, a.data_ptr(), lda, codes.data_ptr(), ldw, scales.data_ptr(),
@@ -299,7 +304,7 @@ def linear(x, weight, bias=None, act: str = "none", residual=None, out_dtype=Non
     x, weight, bias and residual through ``linear_backward``."""
     if not _wants_gradient(x, weight, bias, residual):
         return _linear(x, weight, bias, act, residual, out_dtype, False, workspace, stream)[0]
-    with lg.Running(stream, x.device, x, weight, bias, residual, workspace) as on:   # (its backward pass runs on the same stream)
+    with _Running(stream, x.device, x, weight, bias, residual, workspace) as on:   # (its backward pass runs on the same stream)
         y = _functions()[2].apply(x, weight, bias, residual, act, out_dtype, workspace)
         on.keep(y)
     return y
@@ -321,7 +326,7 @@ def _linear(x, weight, bias, act, residual, out_dtype, keep, workspace, stream=N
     c_code = _code(out_dtype)
     b = _vector(bias, "bias", N, (x.dtype, torch.float32), x.device)
     ldr = _rows(residual, "residual", (M, N), out_dtype, x.device) if residual is not None else 0
-    with lg.Running(stream, x.device, x, weight, bias, residual, workspace) as on:
+    with _Running(stream, x.device, x, weight, bias, residual, workspace) as on:
         y = torch.empty((M, N), dtype=out_dtype, device=x.device)
         z = torch.empty((M, N), dtype=x.dtype, device=x.device) if keep else None
         on.keep(y, z)
@@ -346,7 +351,7 @@ def linear_backward(dy, x, weight, z=None, act: str = "none", need=(True, True, 
     if z is None and act != "none":
         raise ValueError(f"act {act!r} needs z")
     ldz = _rows(z, "z", (M, N), x.dtype, x.device) if act != "none" else 0
-    with lg.Running(stream, x.device, dy, x, weight, z, workspace) as on:
+    with _Running(stream, x.device, dy, x, weight, z, workspace) as on:
         new = lambda wanted, *shape, dtype: torch.empty(shape, dtype=dtype, device=x.device) if wanted else None  # noqa: E731
         dx, dw = new(need[0], M, K, dtype=x.dtype), new(need[1], N, K, dtype=dw_dtype or weight.dtype)
         db = new(need[2], N, dtype=torch.float32)
@@ -404,7 +409,7 @@ def qk_norm_rope(q, k, wq=None, wk=None, positions=None, cos=None, sin=None, pai
         raise ValueError("no gradient reaches cos and sin: detach them")
     if not _wants_gradient(q, k, wq, wk):
         return _qk_norm_rope(q, k, wq, wk, positions, cos, sin, pairs, eps, stream)
-    with lg.Running(stream, q.device, q, k, wq, wk, positions, cos, sin) as on:   # (its backward pass runs on the same stream)
+    with _Running(stream, q.device, q, k, wq, wk, positions, cos, sin) as on:   # (its backward pass runs on the same stream)
         out = _functions()[3].apply(q, k, wq, wk, positions, cos, sin, pairs, eps)
         on.keep(*out)
     return out
@@ -428,7 +433,7 @@ def _qk_norm_rope(q, k, wq, wk, positions, cos, sin, pairs, eps, stream=None):
     tokens, heads, dim = q.shape
     qh, kh = _heads(q, "q"), _heads(k, "k", None, q.dtype, q.device)
     rope = _rope(positions, cos, sin, pairs, tokens, q.device)
-    with lg.Running(stream, q.device, q, k, wq, wk, positions, cos, sin) as on:
+    with _Running(stream, q.device, q, k, wq, wk, positions, cos, sin) as on:
         out = [torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k)]
         on.keep(*out)
         lg.check(lg.gemm_qk_norm_rope(code, w_code, tokens, heads, k.shape[1], dim, eps, qh, kh, *w, rope, *(_heads(t, "") for t in out),
@@ -446,7 +451,7 @@ def qk_norm_rope_backward(dq, dk, q, k, wq=None, wk=None, positions=None, cos=No
     given = [_heads(dq, "dq", q.shape, q.dtype, q.device), _heads(dk, "dk", k.shape, q.dtype, q.device), _heads(q, "q"),
              _heads(k, "k", None, q.dtype, q.device)]
     rope = _rope(positions, cos, sin, pairs, tokens, q.device)
-    with lg.Running(stream, q.device, dq, dk, q, k, wq, wk, positions, cos, sin, workspace) as on:
+    with _Running(stream, q.device, dq, dk, q, k, wq, wk, positions, cos, sin, workspace) as on:
         dx = [torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k)]
         dw = [torch.empty(dim, dtype=torch.float32, device=q.device) if need_dw else None for _ in range(2)]
         on.keep(*dx, *dw)
