@@ -103,11 +103,14 @@ gemm_status_t check_heads(const char* what, const gemm_heads_t* h, int64_t token
     REQUIRE(h && h->data, "%s is NULL", what);
     const int64_t ld = h->token_stride, hs = h->head_stride, most = int64_t(1) << 40;
     const bool one_token = tokens == 1, one_head = heads == 1;
+    // from the first token (head) to the last: strides below 2^40 times up to 2^30 tokens do not fit 64 bits
+    const __int128 token_span = one_token ? 0 : (__int128)(tokens - 1) * ld, head_span = one_head ? 0 : (__int128)(heads - 1) * hs;
     // tokens outermost or heads outermost: nothing of one lies within another
     const bool fine = (one_token || (ld > 0 && ld < most)) && (one_head || (hs > 0 && hs < most)) &&
-                      ((one_head || hs >= dim) && (one_token || ld >= (one_head ? dim : (heads - 1) * hs + dim)) ||
-                       (one_token || ld >= dim) && (one_head || hs >= (one_token ? dim : (tokens - 1) * ld + dim)));
+                      ((one_head || hs >= dim) && (one_token || ld >= head_span + dim) || (one_token || ld >= dim) && (one_head || hs >= token_span + dim));
     REQUIRE(fine, "%s: heads overlap (token stride %lld, head stride %lld)", what, (long long)ld, (long long)hs);
+    REQUIRE(token_span + head_span < (int64_t(1) << 60), "%s: offsets past 64 bits (token stride %lld, head stride %lld)", what, (long long)ld,
+            (long long)hs);
     *to = HeadsTensor{static_cast<const char*>(h->data), one_token ? 0 : ld, one_head ? 0 : hs};
     return GEMM_OK;
 }
