@@ -395,6 +395,8 @@ def _rope(positions, cos, sin, pairs, tokens, device):
 def rope_table(rows: int, rot_dim: int, base: float = 10000.0, device=None):
     """(cos, sin), rows x rot_dim / 2 each in fp32, of the angles position * base^(-2 i / rot_dim), taken in 64 bits."""
     import torch
+    if rows < 0 or rot_dim < 0 or rot_dim % 2:
+        raise ValueError(f"rows {rows}, rot_dim {rot_dim}: not negative, rot_dim even")
     rate = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
     angle = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * rate
     return angle.cos().float(), angle.sin().float()
