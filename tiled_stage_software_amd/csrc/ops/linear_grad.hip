@@ -24,8 +24,8 @@ namespace {
 // Row r's place for its 32-byte pieces, by width C: rows r, r + 1, r + 2, r + 3 and r + 16, ... r + 19 (r a multiple of 4) differ.
 template <int C>
 __device__ __forceinline__ int tr_swz(int r) {
-    if constexpr (C == 64) return (r >> 1 & 1) | (r >> 4 & 1) << 1;   // (four pieces a row, two rows in the banks' width)
-    else return (r & 3) | (r >> 4 & 1) << 2;
+    static_assert(C >= 128, "eight pieces a row");
+    return (r & 3) | (r >> 4 & 1) << 2;
 }
 __device__ __forceinline__ void copy16(const char* base, uint32_t off, LDS_AS char* to) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" :: "v"(off), "s"(base), "s"((uint32_t)(uintptr_t)to) : "m0");
