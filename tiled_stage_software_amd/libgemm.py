@@ -149,13 +149,10 @@ def load():
         lib.gemm_qk_norm_rope.argtypes = [i32, i32, i64, i64, i64, i64, f32, hp, hp, vp, vp, rp, hp, hp, vp]
         lib.gemm_qk_norm_rope_bwd.argtypes = [i32, i32, i64, i64, i64, i64, f32, hp, hp, hp, hp, vp, vp, rp, hp, hp, vp, vp, vp, sz, vp]
         lib.gemm_qk_norm_rope_bwd_workspace_size.argtypes = [i32, i64, i64, i64, i64, szp]
-        for name in ("gemm_linear", "gemm_linear_workspace_size", "gemm_linear_bwd", "gemm_linear_bwd_workspace_size",
-                     "gemm_qk_norm_rope", "gemm_qk_norm_rope_bwd", "gemm_qk_norm_rope_bwd_workspace_size"):
-            getattr(lib, name).restype = i32
         for name in ("gemm_rmsnorm", "gemm_rmsnorm_bwd", "gemm_rmsnorm_bwd_workspace_size", "gemm_f8",
                      "gemm_f8_workspace_size", "gemm_w4", "gemm_w4_workspace_size", "gemm_linear", "gemm_linear_workspace_size",
-           "gemm_linear_bwd", "gemm_linear_bwd_workspace_size", "gemm_qk_norm_rope", "gemm_qk_norm_rope_bwd",
-           "gemm_qk_norm_rope_bwd_workspace_size"):
+                     "gemm_linear_bwd", "gemm_linear_bwd_workspace_size", "gemm_qk_norm_rope", "gemm_qk_norm_rope_bwd",
+                     "gemm_qk_norm_rope_bwd_workspace_size"):
             getattr(lib, name).restype = i32
         lib.gemm_status_string.argtypes = [i32]
         lib.gemm_status_string.restype = ctypes.c_char_p
