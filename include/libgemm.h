@@ -487,7 +487,8 @@ typedef enum gemm_act {
  * leading dimension.  C: M x N of c_type (in_type or GEMM_F32).  Z: where it is stored (NULL: it is not), M x N of in_type:
  * what gemm_linear_bwd reads.  No other overlap.
  * Sums, bias, activation and residual are in fp32; C and Z are rounded once, each from the unrounded sums.  An activation is
- * good to 2^-20 + q 2^-22 of its value, q what its exponential takes (z^2 / 2 for GEMM_ACT_GELU, |z| for GEMM_ACT_SILU).  NaN stays
+ * good to 2^-20 + q 2^-22 of its value, q what its exponential takes (z^2 / 2 for GEMM_ACT_GELU, sqrt(8 / pi) * |z + 0.044715 z^3| for
+ * GEMM_ACT_GELU_TANH, |z| for GEMM_ACT_SILU), or to 2^-119 where that is more: far tails underflow to 0 (silu from -87.3 on).  NaN stays
  * NaN; infinite sums have the activations' limits.  K == 0: C = act(bias) + R.  M == 0 or N == 0: nothing is written.
  * workspace: as gemm_f8 uses one, for splits of a long K and for copies of operands whose rows are not 16-byte aligned;
  * gemm_linear_workspace_size gives the bytes for contiguous aligned operands.  With less (or NULL) the call

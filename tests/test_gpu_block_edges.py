@@ -1,8 +1,12 @@
-"""Ends of a transformer block's dense parts on the GPU: infinite weights where the depth ends inside a slab."""
+"""Ends of a transformer block's dense parts on the GPU: infinite weights where the depth ends inside a slab, far tails of the
+activations."""
+import math
+
 import pytest
 import torch
 
-from gpu_util import DEV
+from block_util import ACTS, act64
+from gpu_util import DEV, say
 from test_gpu_block import gen, run_linear
 from tiled_stage_software_amd import libgemm as lg
 
@@ -54,3 +58,19 @@ def test_infinite_weights_reach_their_columns_alone(M, N, K, t, workspace):
                     else:
                         limit = x if act == "none" or x > 0 else 0.0
                         assert bool((Z[:, n] == x).all() and (C[:, n] == limit).all()), (n, pad, act, ws is None)
+
+
+@pytest.mark.parametrize("act", ACTS[2:])
+def test_activations_keep_their_bound_in_far_tails(act):
+    """Any fp32 sum (a bias on sums of zeros): 2^-20 + q 2^-22 of the value, or 2^-119 where exp2 has underflown, and the roundings of C
+    and of the last sum."""
+    b = torch.cat([torch.linspace(-140, 20, 40000), torch.linspace(-15, -5, 20000), torch.tensor([-1e4, -3e4, -1e30, 1e30])])
+    b = torch.nn.functional.pad(b, (0, -len(b) % 64))
+    a, w = torch.zeros(1, 64, dtype=torch.bfloat16), torch.zeros(len(b), 64, dtype=torch.bfloat16)
+    C, _ = run_linear(a, w, b, act, None, "f32", keep=False)
+    z = b.double()
+    q = {"gelu": z * z / 2, "gelu_tanh": math.sqrt(8 / math.pi) * (z + 0.044715 * z ** 3).abs(), "silu": z.abs()}[act]
+    want = act64(z, act)
+    e = ((C[0].double() - want).abs() / ((want.abs() * (2.0 ** -20 + q * 2.0 ** -22 + 2.0 ** -24)).clamp_min(2.0 ** -119))).max()
+    say(f"[linear] {act} to its tail: {float(e):.3f} of the bound")
+    assert float(e) <= 1
