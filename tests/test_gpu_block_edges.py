@@ -1,5 +1,5 @@
 """Ends of a transformer block's dense parts on the GPU: infinite weights where the depth ends inside a slab, far tails of the
-activations."""
+activations, the same bits from many parts."""
 import math
 
 import pytest
@@ -7,8 +7,8 @@ import torch
 
 from block_util import ACTS, act64
 from gpu_util import DEV, say
-from test_gpu_block import gen, run_linear
-from tiled_stage_software_amd import libgemm as lg
+from test_gpu_block import EPS, gen, heads_inputs, run_linear
+from tiled_stage_software_amd import libgemm as lg, ops
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +74,21 @@ def test_activations_keep_their_bound_in_far_tails(act):
     e = ((C[0].double() - want).abs() / ((want.abs() * (2.0 ** -20 + q * 2.0 ** -22 + 2.0 ** -24)).clamp_min(2.0 ** -119))).max()
     say(f"[linear] {act} to its tail: {float(e):.3f} of the bound")
     assert float(e) <= 1
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+@pytest.mark.parametrize("T,HQ,HK,D,rot", [(3001, 6, 2, 64, 64), (513, 5, 1, 72, 36), (2049, 3, 3, 40, 10)])
+def test_heads_backward_gives_the_same_bits_again(T, HQ, HK, D, rot, t, workspace):
+    """Many parts of dw: in the same order whatever the workspace holds."""
+    q, k, w, pos, angles = heads_inputs(T, HQ, HK, D, rot, t, t, 4)
+    g = gen(T)
+    dq, dk = (torch.randn(x.shape, generator=g).to(x.dtype) for x in (q, k))
+    args = [x.to(DEV) for x in (dq, dk, q, k, *w, pos, *angles)]
+    runs = []
+    for fill in (0x7F, 0x00, 0x3C):
+        workspace.fill_(fill)
+        runs.append(ops.qk_norm_rope_backward(*args, eps=EPS, workspace=workspace))
+    for again in runs[1:]:
+        for x, y in zip(runs[0], again):
+            assert torch.equal(x, y)
+    assert lg.gemm_qk_norm_rope_bwd_workspace_size(lg.GEMM_F32, T, HQ, HK, D)[1] > 64 * D * 4
