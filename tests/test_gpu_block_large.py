@@ -159,3 +159,25 @@ def test_linear_backward_exact_integers_on_large_tiles(M, N, K, dw_type, workspa
         got = run_backward(dc, z, a, w, "relu", dw_type, pads, ws)
         assert torch.equal(got[0].double(), dz) and torch.equal(got[3].double(), dz.sum(0)), pads
         assert torch.equal(got[1], da.to(torch.bfloat16)) and torch.equal(got[2], dw.to(DT[dw_type])), pads
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 513, 333), (513, 1001, 643), GRAD_A[0], GRAD_W[0], GRAD_BOTH[0]])
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_backward_rounds_dz_once_and_nothing_else(M, N, K, t, workspace):
+    """The one rounding to 16 bits inside the backward pass is dZ's: dA and dW are the products of the dZ that is stored, to fp32
+    sums and their own rounding, and db is the sum of the unrounded values."""
+    T = DT[t]
+    g = gen(M + N + K)
+    dc, z = torch.randn(M, N, generator=g).to(T), (1.5 * torch.randn(M, N, generator=g)).to(T)
+    a, w = torch.randn(M, K, generator=g).to(T), (torch.randn(N, K, generator=g) / K ** 0.5).to(T)
+    dZ, dA, dW, db = run_backward(dc, z, a, w, "gelu", "f32", (0, 0), workspace)
+    A, W, dz = a.to(DEV).double(), w.to(DEV).double(), dc.to(DEV).double() * slope64(z.to(DEV).double(), "gelu")
+    kept, slope = dZ.double(), dc.to(DEV).double().abs() * SLOPE + U32 * dz.abs()
+    assert worst(dZ, dz, rounding(dz, T) + slope) <= 1
+    da, dw = kept @ W, kept.t() @ A
+    assert worst(dA, da, rounding(da, T) + (N + 6) * U32 * (kept.abs() @ W.abs())) <= 1
+    assert worst(dW, dw, rounding(dw, torch.float32) + (M + 6) * U32 * (kept.abs().t() @ A.abs())) <= 1
+    far = lambda got, want: float((got.double() - want).norm() / want.norm())  # noqa: E731
+    say(f"[linear backward] {t} {M}x{N}x{K}: dA {far(dA, dz @ W):.1e}, dW (fp32) {far(dW, dz.t() @ A):.1e}, db {far(db, dz.sum(0)):.1e} "
+        f"from 64 bits; from the products of the rounded dZ {far(dA, da):.1e}, {far(dW, dw):.1e}")
+    assert worst(db, dz.sum(0), rounding(dz.sum(0), torch.float32) + slope.sum(0) + (M + 6) * U32 * (dz.abs() + slope).sum(0)) <= 1
