@@ -446,7 +446,7 @@ def _qk_norm_rope(q, k, wq, wk, positions, cos, sin, pairs, eps, stream=None):
 def qk_norm_rope_backward(dq, dk, q, k, wq=None, wk=None, positions=None, cos=None, sin=None, pairs: str = "halves", eps: float = 1e-6,
                           need_dw: bool = True, workspace="auto", stream=None):
     """(gradients of q, of k, of wq, of wk) of ``qk_norm_rope`` from those of its results and its inputs; the weights' in
-    fp32 (None unless `need_dw`)."""
+    fp32 (None unless `need_dw`, which without a workspace leaves one workgroup for all)."""
     import torch
     code, w_code, w = _qk(q, k, wq, wk)
     tokens, heads, dim = q.shape
