@@ -505,7 +505,8 @@ gemm_status_t gemm_linear_workspace_size(gemm_dtype_t in_type, int64_t M, int64_
  *     dZ = dC * act'(Z),  dA = dZ * W,  dW = dZ^T * A,  dbias = sum over the rows of dZ
  * dC: M x N of dc_type (in_type or GEMM_F32).  Z: M x N of in_type, what gemm_linear stored; NULL allowed for GEMM_ACT_NONE (not read then).  dZ:
  * M x N of in_type, written, and what both products read: it is rounded once, also from an fp32 dC, and dA and dW, in fp32 too, are
- * good to that rounding of their terms; it may be the same memory as dC (of in_type) or Z with the same leading dimension.  With GEMM_ACT_NONE and a dC of in_type it may be NULL: dC is then read in its place.
+ * good to that rounding of their terms; it may be the same memory as dC (of in_type) or Z with the same leading dimension.  With
+ * GEMM_ACT_NONE and a dC of in_type it may be NULL: dC is then read in its place.
  * dA: M x K of in_type, or NULL (not computed; W is not read).  dW: N x K of dw_type (in_type or GEMM_F32), or NULL (A is not
  * read).  dbias: N floats, summed in fp32 from unrounded values in a fixed order, or NULL.  M == 0: dW = 0, dbias = 0.
  * The derivative of relu at 0 is 0.
@@ -565,8 +566,9 @@ gemm_status_t gemm_qk_norm_rope(gemm_dtype_t in_type, gemm_dtype_t w_type, int64
  * dq, dk: gradients of the outputs; q, k: the forward pass's inputs; dxq, dxk: written, may be the same memory as dq or q (dk or
  * k) with the same strides.  dwq, dwk: head_dim floats, or NULL (not computed); zeros where there is nothing to sum.
  * The sums run in fp32, in parts that meet in `workspace` in a fixed order: gemm_qk_norm_rope_bwd_workspace_size gives the bytes
- * for full speed; with less there are fewer parts, head_dim floats each, and as many workgroups, which compute dx too.  Without any (or NULL) one
- * workgroup does it all where dwq or dwk is wanted (8192 x 40 heads of 128: 10 ms instead of 0.06).  Errors: as gemm_qk_norm_rope, plus a workspace not 256-byte aligned. */
+ * for full speed; with less there are fewer parts, head_dim floats each, and as few workgroups, which compute dx too: without any
+ * (or NULL) one does it all where dwq or dwk is wanted (8192 x 40 heads of 128: 10 ms instead of 0.06).
+ * Errors: as gemm_qk_norm_rope, plus a workspace not 256-byte aligned. */
 gemm_status_t gemm_qk_norm_rope_bwd(gemm_dtype_t in_type, gemm_dtype_t w_type, int64_t tokens, int64_t q_heads, int64_t k_heads,
                                     int64_t head_dim, float eps, const gemm_heads_t* dq, const gemm_heads_t* dk,
                                     const gemm_heads_t* q, const gemm_heads_t* k, const void* wq, const void* wk,

@@ -21,7 +21,7 @@
 namespace gemm {
 namespace {
 
-// Row r's place for its 32-byte pieces, by width C: rows r, r + 1, r + 2, r + 3 and r + 16, ... r + 19 (r a multiple of 4) differ.
+// Row r's place for its 32-byte pieces (rows of C columns): r, r + 1, r + 2, r + 3 and r + 16, ... r + 19 (r a multiple of 4) differ.
 template <int C>
 __device__ __forceinline__ int tr_swz(int r) {
     static_assert(C >= 128, "eight pieces a row");

@@ -1,6 +1,8 @@
 // linear_staged.hip -- the product with bias, activation and residual for operands of any size, pitch and
 // alignment: 128 x 128 tiles, slabs of 64 in two LDS slots, loads through registers, zeros past the edges (no K at all
-// leaves act(bias) + R).  For what the other kernels do not take: K below 64, where C's bytes bound it, and pitches above 2^21.
+// leaves act(bias) + R).  For what the other kernels do not take: K below 64 and pitches above 2^21.  K below 64 takes three times its
+// bytes (4096 x 4096 x 32 bf16 21.8 us, floor 6.6; 8192 x 14336 x 32 124, floor 46; the same from K = 8 to 48): a workgroup's loads, products
+// and epilogue run in turn, and LDS holds two of them a compute unit.
 #include "linear.hpp"
 
 namespace gemm {

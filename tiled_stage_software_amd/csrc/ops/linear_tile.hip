@@ -167,8 +167,8 @@ struct LinearSplit {
 };
 
 // Columns of small tiles start a slab apart in K.  Workgroups run side by side, and where W's pitch is a power of two all of them would read
-// the same few lines of every row at a time, which lie in few of the memory's channels: 64 x 14336 x 4096 34.8 us instead of 29.0, 128 rows
-// 37.0 and 33.6.  Large tiles are not bound by W's bytes (no difference).
+// the same few lines of every row at a time, which lie in few of the memory's channels: 64 x 14336 x 4096 34.8 us instead of 28.5, 128 rows
+// 37.0 and 34.2.  Large tiles are not bound by W's bytes (no difference).
 // S: slots of the ring (0: loads through registers, two slots).  Splits of K (blockIdx.y) store plain sums.
 template <int T, int OUT, int BM, int BN, int WM, int WN, int S>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)))
