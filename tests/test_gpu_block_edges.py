@@ -8,6 +8,7 @@ import torch
 from block_util import ACTS, act64
 from gpu_util import DEV, say
 from test_gpu_block import EPS, gen, heads_inputs, run_linear
+from test_gpu_block_large import run_backward
 from tiled_stage_software_amd import libgemm as lg, ops
 
 pytestmark = pytest.mark.gpu
@@ -92,3 +93,30 @@ def test_heads_backward_gives_the_same_bits_again(T, HQ, HK, D, rot, t, workspac
         for x, y in zip(runs[0], again):
             assert torch.equal(x, y)
     assert lg.gemm_qk_norm_rope_bwd_workspace_size(lg.GEMM_F32, T, HQ, HK, D)[1] > 64 * D * 4
+
+
+@pytest.mark.parametrize("M,N,K", [(70, 96, 88), (33, 40, 129), (300, 513, 333), (513, 200, 643), (4001, 328, 4090)])
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_infinite_operands_of_the_backward_pass_reach_their_columns_alone(M, N, K, t, workspace):
+    """An infinity in W or A reaches its column of dA or dW, a NaN in dC its row of dA and of dW: wherever sums end inside a slab."""
+    dtype = torch.bfloat16 if t == "bf16" else torch.float16
+    g = gen(M + N + K)
+    dc = (torch.rand(M, N, generator=g) + 0.1).to(dtype)
+    a, w = (torch.randn(*s, generator=g).to(dtype) / 16 for s in ((M, K), (N, K)))
+    inf, kept = float("inf"), [k for k in range(K) if k not in (0, 5, K - 1)]
+    a2, w2, dc2 = a.clone(), w.clone(), dc.clone()
+    w2[N - 1, 0], w2[0, 5], w2[N // 64 * 64 - 1, K - 1] = inf, -inf, inf
+    a2[M - 1, 0], a2[0, 5], a2[M // 64 * 64 - 1, K - 1] = inf, -inf, inf
+    dc2[M - 1, N - 1] = float("nan")
+    rows, cols = list(range(M - 1)), list(range(N - 1))
+    for pad in (0, 8, 3):
+        for ws in (workspace, None):
+            clean = run_backward(dc, None, a, w, "none", "f32", (pad, pad), ws)
+            _, dA, dW, _ = run_backward(dc, None, a2, w2, "none", "f32", (pad, pad), ws)
+            for got, ref in ((dA, clean[1]), (dW, clean[2])):
+                assert torch.equal(got[:, kept], ref[:, kept]), (pad, ws is None)
+                for k, x in ((0, inf), (5, -inf), (K - 1, inf)):
+                    assert bool((got[:, k] == x).all()), (pad, ws is None, k)
+            _, dA, dW, db = run_backward(dc2, None, a, w, "none", "f32", (pad, pad), ws)
+            assert torch.equal(dA[rows], clean[1][rows]) and torch.equal(dW[cols], clean[2][cols]) and torch.equal(db[cols], clean[3][cols])
+            assert bool(torch.isnan(dA[M - 1].float()).all() and torch.isnan(dW[N - 1]).all() and torch.isnan(db[N - 1])), (pad, ws is None)
